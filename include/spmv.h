@@ -602,6 +602,158 @@ spmv_status spgemm_compute(spgemm_t h, int32_t *rp_c, int32_t *ci_c, float *v_c,
 spmv_status spgemm_destroy(spgemm_t h);
 
 /* ======================================================================== */
+/* Operators of many tokens beside the matrix-vector products: the pruned     */
+/* projection for a batch of tokens (or for experts' groups of tokens), tokens */
+/* sorted by group and back, and low-rank adapters of many requests.          */
+/* Matrices of activations are row-major [tokens, width] with a row stride    */
+/* (ld*) in elements, at least the width.                                     */
+/* ======================================================================== */
+typedef enum { SPMV_F16 = 0, SPMV_BF16 = 1, SPMV_F32 = 2 } spmv_dtype;
+
+/* ------------------------------------------------------------------------ */
+/* MACKO for many tokens: for every token t                                   */
+/*   y[t, i] = alpha * (row_scale[i]) * sum_j W[i, j] x[t, j] + beta * y[t, i]  */
+/* with W's values and x in fp16, exact products, fp32 sums, and y in fp32 or */
+/* fp16 (rounded once).  With n_groups > 1 there is one W per group: their    */
+/* encodings stacked, n_groups * n_rows rows behind one mrow_ptr (group g owns */
+/* rows g n_rows ..), and group g's tokens are rows tok_offsets[g] ..          */
+/* tok_offsets[g+1]-1 of x and y (device int32[n_groups+1], non-decreasing, as */
+/* route_plan writes it; values are clamped to [0, n_tok]).  Rows of y outside */
+/* every group are not touched.  tok_offsets may be NULL for one group.       */
+/* W's pruned positions count as zeros, so a token with an infinity or NaN    */
+/* gets unspecified outputs; other tokens are not affected.                   */
+/* The gradient in x is the same call on the encoding of W's transpose.       */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of the plan of a weight of n_rows rows (all groups together): for each
+ * row and 256 columns where its entries start.  Host only.  More than 2^20
+ * columns are SPMV_ERR_UNSUPPORTED. */
+spmv_status macko_spmm_plan_size(int32_t n_rows, int32_t n_cols, size_t *bytes);
+
+/* Builds the plan (device, 4-byte aligned, >= macko_spmm_plan_size bytes) from
+ * the encoding; it holds while mrow_ptr and codes stay as they are, and values
+ * may change.  Asynchronous. */
+spmv_status macko_spmm_plan(int32_t n_rows, int32_t n_cols, int32_t bdelta, const int32_t *mrow_ptr,
+                            const uint32_t *codes, void *plan, size_t plan_bytes, void *stream);
+
+/* Bytes of the workspace macko_spmm needs when x cannot be read 16 bytes at a
+ * time: n_cols or ldx not a multiple of 8, or x not 16-byte aligned (x is
+ * copied there first).  Otherwise the workspace may be NULL.  Host only. */
+spmv_status macko_spmm_workspace_size(int32_t n_tok, int32_t n_cols, size_t *bytes);
+
+/* The product.  All pointers device; alignments of mvals and codes as for
+ * macko_spmv; workspace 16-byte aligned, not shared by calls that may overlap.
+ * y_dtype: SPMV_F32 or SPMV_F16.  y and x must not overlap.  Asynchronous. */
+spmv_status macko_spmm(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t bdelta,
+                       const int32_t *mrow_ptr, const uint32_t *codes, const uint16_t *mvals,
+                       const void *plan, const int32_t *tok_offsets, int32_t n_tok, float alpha,
+                       const uint16_t *x_f16, int64_t ldx, float beta, void *y, int32_t y_dtype,
+                       int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with int8 values and row scales (macko_quantize_i8). */
+spmv_status macko_spmm_i8(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t bdelta,
+                          const int32_t *mrow_ptr, const uint32_t *codes, const int8_t *q,
+                          const float *row_scale, const void *plan, const int32_t *tok_offsets,
+                          int32_t n_tok, float alpha, const uint16_t *x_f16, int64_t ldx, float beta,
+                          void *y, int32_t y_dtype, int64_t ldy, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Tokens sorted by group and back.  Token t has top_k choices; slot          */
+/* s = t * top_k + c is its choice c, with the group keys[s].  The plan is a   */
+/* stable sort of the slots by group:                                         */
+/*   offsets int32[n_groups+1]: slots of groups < g; offsets[n_groups] = the   */
+/*       number of sorted rows                                               */
+/*   order int32[n_slots]: the slot of each sorted row, ascending in a group;   */
+/*       slots whose key is outside [0, n_groups) are dropped: they come last  */
+/*   pos int32[n_slots]: the sorted row of each slot, -1 if dropped            */
+/*   tiles int32[4 * n_tiles], 16-byte aligned: {group, begin, end, group's    */
+/*       begin} for every 16 sorted rows of a group; the dropped ones' tiles   */
+/*       have group -1, unused tiles {-1, 0, 0, 0}                            */
+/* A key may occur twice among a token's choices.                             */
+/* ------------------------------------------------------------------------ */
+
+/* Number of tiles: (n_slots + 15 * min(n_groups + 1, n_slots)) / 16.  Host only.
+ * At most 2048 groups and 2^22 slots (SPMV_ERR_UNSUPPORTED). */
+spmv_status route_tile_count(int32_t n_slots, int32_t n_groups, int32_t *n_tiles);
+
+/* Bytes of route_plan's workspace (0 where it needs none).  Host only. */
+spmv_status route_workspace_size(int32_t n_slots, int32_t n_groups, size_t *bytes);
+
+/* Builds the plan.  keys int32[n_slots]; all pointers device.  Asynchronous. */
+spmv_status route_plan(int32_t n_slots, int32_t n_groups, const int32_t *keys, int32_t *offsets,
+                       int32_t *order, int32_t *pos, int32_t *tiles, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* xs[i] = weights[order[i]] * x[order[i] / top_k] for the sorted rows
+ * i < offsets[n_groups]; later rows of xs stay as they are.  weights: fp32
+ * [n_tok * top_k] or NULL (1: a copy).  x [n_tok, dim] and xs [n_tok * top_k,
+ * dim] of type dtype, not overlapping.  Asynchronous. */
+spmv_status route_gather(int32_t n_tok, int32_t top_k, int32_t dim, int32_t dtype, int32_t n_groups,
+                         const int32_t *offsets, const int32_t *order, const float *weights,
+                         const void *x, int64_t ldx, void *xs, int64_t ldxs, void *stream);
+
+/* y[t] = sum over c of weights[t, c] * ys[pos[t, c]], dropped choices left out,
+ * in fp32 in ascending c and rounded once (0 if all are dropped).  weights as
+ * above; with NULL this is the gradient of an unweighted gather.
+ * Asynchronous. */
+spmv_status route_combine(int32_t n_tok, int32_t top_k, int32_t dim, int32_t dtype, const int32_t *pos,
+                          const float *weights, const void *ys, int64_t ldys, void *y, int64_t ldy,
+                          void *stream);
+
+/* Gradients of route_combine: dys[pos[t, c]] = weights[t, c] * dy[t] (other rows
+ * of dys stay as they are) and dw[t, c] = sum_j ys[pos[t, c], j] * dy[t, j] in
+ * fp32, 0 for a dropped choice.  dys must not overlap dy or ys.  Asynchronous. */
+spmv_status route_combine_grad(int32_t n_tok, int32_t top_k, int32_t dim, int32_t dtype, const void *dy,
+                               int64_t lddy, const void *ys, int64_t ldys, const int32_t *pos,
+                               const float *weights, void *dys, int64_t lddys, float *dw,
+                               void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters of many requests beside a shared projection:             */
+/*   y[t, :] = y_in[t, :] + scale[a] * sum_{j < ranks[a]} (A[a, j, :] . x[t, :]) B[a, j, :]  */
+/* where a is token t's adapter.  A [n_adapters, max_rank, n_in] and            */
+/* B [n_adapters, max_rank, n_out] are contiguous and both rank-major, so the   */
+/* gradient in x is lora_apply with A and B exchanged and dy for x.  Rows at or */
+/* past an adapter's rank are not used.  ranks: device int32[n_adapters]       */
+/* (clamped to [0, max_rank]; NULL: max_rank); scale: device fp32[n_adapters]  */
+/* (NULL: 1).  order, offsets, tiles: the plan route_plan wrote for n_tok keys  */
+/* (one choice per token) and n_adapters groups; tokens whose key is dropped    */
+/* have no adapter: y[t] = y_in[t].  n_tiles: route_tile_count's value.         */
+/* Sums over n_in, n_out and tokens are fp32; the rank vector A x is not        */
+/* rounded to 16 bits.  Results are the same bits on every call.               */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of the workspace of the two calls below.  Host only.  Ranks above 128
+ * are SPMV_ERR_UNSUPPORTED. */
+spmv_status lora_workspace_size(int32_t n_tok, int32_t max_rank, size_t *bytes);
+
+/* dtype: SPMV_F16 or SPMV_BF16, of x, A and B; y_dtype: the same, or SPMV_F32.
+ * y_in may be y (in place, same stride; rows without an adapter are then not
+ * touched) or NULL (zeros); otherwise x, y_in and y must not overlap.
+ * workspace: 16-byte aligned, not shared by calls that may overlap.
+ * Asynchronous. */
+spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adapters, int32_t max_rank,
+                       const int32_t *ranks, const float *scale, const void *A, const void *B,
+                       int32_t dtype, const int32_t *order, const int32_t *offsets,
+                       const int32_t *tiles, int32_t n_tiles, const void *x, int64_t ldx,
+                       const void *y_in, int64_t ldyin, void *y, int32_t y_dtype, int64_t ldy,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of the adapters' weights from x and dy (the gradient of y, of x's
+ * type), fp32, written whole (zeros for ranks not used and for adapters
+ * without tokens):
+ *   dA[a, j, :] = scale[a] * sum_t (B[a, j, :] . dy[t, :]) x[t, :]
+ *   dB[a, j, :] = scale[a] * sum_t (A[a, j, :] . x[t, :]) dy[t, :]
+ * over the tokens t of adapter a.  Asynchronous. */
+spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adapters, int32_t max_rank,
+                      const int32_t *ranks, const float *scale, const void *A, const void *B,
+                      int32_t dtype, const int32_t *order, const int32_t *offsets,
+                      const int32_t *tiles, int32_t n_tiles, const void *x, int64_t ldx,
+                      const void *dy, int64_t lddy, float *dA, float *dB, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* ======================================================================== */
 /* Reference streams: the measured bandwidth a plain kernel reaches, beside  */
 /* the HBM peak, as the second denominator of the roofline figures.          */
 /* ======================================================================== */

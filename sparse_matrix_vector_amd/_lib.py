@@ -79,6 +79,24 @@ SIGNATURES = {
     "spgemm_info": [vp, P_i64, P_i64, P_i32],
     "spgemm_compute": [vp, vp, vp, vp, vp],
     "spgemm_destroy": [vp],
+    "macko_spmm_plan_size": [c_i32, c_i32, P_sz],
+    "macko_spmm_plan": [c_i32, c_i32, c_i32, vp, vp, vp, c_sz, vp],
+    "macko_spmm_workspace_size": [c_i32, c_i32, P_sz],
+    "macko_spmm": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32, c_i64,
+                   vp, c_sz, vp],
+    "macko_spmm_i8": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp, vp, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32,
+                      c_i64, vp, c_sz, vp],
+    "route_tile_count": [c_i32, c_i32, P_i32],
+    "route_workspace_size": [c_i32, c_i32, P_sz],
+    "route_plan": [c_i32, c_i32, vp, vp, vp, vp, vp, vp, c_sz, vp],
+    "route_gather": [c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, c_i64, vp, c_i64, vp],
+    "route_combine": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, c_i64, vp, c_i64, vp],
+    "route_combine_grad": [c_i32, c_i32, c_i32, c_i32, vp, c_i64, vp, c_i64, vp, vp, vp, c_i64, vp, vp],
+    "lora_workspace_size": [c_i32, c_i32, P_sz],
+    "lora_apply": [c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, c_i32, vp, vp, vp, c_i32, vp, c_i64, vp, c_i64,
+                   vp, c_i32, c_i64, vp, c_sz, vp],
+    "lora_grad": [c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, c_i32, vp, vp, vp, c_i32, vp, c_i64, vp, c_i64,
+                  vp, vp, vp, c_sz, vp],
     "fem_jacobi_diagonal": [c_i32, c_i32, vp, vp, c_i32, vp, vp, vp],
     "fem_solver_workspace_size": [c_i32, c_i32, P_sz],
     "fem_pcg_solve": [c_i32, c_i32, vp, vp, c_i32, vp, vp, vp, c_f32, c_i32, vp, c_sz, P_i32, P_f64, vp],
