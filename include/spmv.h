@@ -636,10 +636,13 @@ spmv_status macko_spmm_plan_size(int32_t n_rows, int32_t n_cols, size_t *bytes);
 spmv_status macko_spmm_plan(int32_t n_rows, int32_t n_cols, int32_t bdelta, const int32_t *mrow_ptr,
                             const uint32_t *codes, void *plan, size_t plan_bytes, void *stream);
 
-/* Bytes of the workspace macko_spmm needs when x cannot be read 16 bytes at a
- * time: n_cols or ldx not a multiple of 8, or x not 16-byte aligned (x is
- * copied there first).  Otherwise the workspace may be NULL.  Host only. */
-spmv_status macko_spmm_workspace_size(int32_t n_tok, int32_t n_cols, size_t *bytes);
+/* Bytes of the workspace of macko_spmm at this shape: room for x where it cannot
+ * be read 16 bytes at a time (n_cols or ldx not a multiple of 8, or x not
+ * 16-byte aligned: it is copied there first), and for partial sums where the
+ * columns are split over workgroups.  A call that needs neither also takes
+ * NULL.  Not monotone in n_tok.  Host only. */
+spmv_status macko_spmm_workspace_size(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t n_tok,
+                                      size_t *bytes);
 
 /* The product.  All pointers device; alignments of mvals and codes as for
  * macko_spmv; workspace 16-byte aligned, not shared by calls that may overlap.

@@ -104,6 +104,15 @@ def _stream(stream, like=None):
     return stream.cuda_stream
 
 
+def _stream_scope(stream, device):
+    """The context whose current stream is `stream` (None: as it is)."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+
+
 def _i32_dtype():
     import torch
     return torch.int32
@@ -646,9 +655,9 @@ def macko_spmm_plan(n_rows, n_cols, mrow_ptr, codes, plan, stream=None, bdelta=4
     return plan
 
 
-def macko_spmm_workspace_size(n_tok, n_cols) -> int:
+def macko_spmm_workspace_size(n_groups, n_rows, n_cols, n_tok) -> int:
     out = ctypes.c_size_t()
-    _call("macko_spmm_workspace_size", int(n_tok), int(n_cols), ctypes.byref(out))
+    _call("macko_spmm_workspace_size", int(n_groups), int(n_rows), int(n_cols), int(n_tok), ctypes.byref(out))
     return out.value
 
 
@@ -706,14 +715,18 @@ class MackoMatrix:
         macko_spmm_plan(self.n_groups * self.n_rows, n_cols, mrow_ptr, codes, self.plan, stream, bdelta)
 
     def workspace(self, n_tok):
-        """A workspace for calls of up to n_tok tokens with any alignment."""
+        """A workspace for calls of n_tok tokens."""
         import torch
-        return torch.empty(macko_spmm_workspace_size(n_tok, self.n_cols), dtype=torch.uint8, device=self.plan.device)
+        return torch.empty(macko_spmm_workspace_size(self.n_groups, self.n_rows, self.n_cols, n_tok), dtype=torch.uint8,
+                           device=self.plan.device)
 
     def apply(self, x, y, alpha=1.0, beta=0.0, tok_offsets=None, workspace=None, stream=None):
         if (self.n_groups > 1 or tok_offsets is not None) and (
                 tok_offsets is None or tok_offsets.numel() != self.n_groups + 1):
             raise ValueError(f"tok_offsets must have {self.n_groups + 1} elements")
+        if workspace is None and x.dim() == 2:
+            with _stream_scope(stream, self.plan.device):      # torch's allocator orders it with that stream's work
+                workspace = self.workspace(x.shape[0])
         if self.row_scale is None:
             return macko_spmm(self.n_rows, self.n_cols, self.mrow_ptr, self.codes, self.vals, self.plan, alpha, x, beta,
                               y, workspace, tok_offsets, stream, self.bdelta)

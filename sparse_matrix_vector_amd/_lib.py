@@ -81,7 +81,7 @@ SIGNATURES = {
     "spgemm_destroy": [vp],
     "macko_spmm_plan_size": [c_i32, c_i32, P_sz],
     "macko_spmm_plan": [c_i32, c_i32, c_i32, vp, vp, vp, c_sz, vp],
-    "macko_spmm_workspace_size": [c_i32, c_i32, P_sz],
+    "macko_spmm_workspace_size": [c_i32, c_i32, c_i32, c_i32, P_sz],
     "macko_spmm": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32, c_i64,
                    vp, c_sz, vp],
     "macko_spmm_i8": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp, vp, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32,

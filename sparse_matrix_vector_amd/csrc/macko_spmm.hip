@@ -33,6 +33,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 constexpr int SM_SLAB = 256;            // columns of a slab
 constexpr int SM_LDW = SM_SLAB + 8;     // halfs per tile row: the spare columns also spread rows over the banks
 constexpr int SM_ROWS = 16;
+constexpr int SM_FRONT = 8;             // halfs before the first tile: spare columns of its first row
 constexpr int SM_UNIT_BITS = 18;        // plan word: unit in the row, and how far back its predecessor's column lies
 constexpr int SM_MAX_COLS = 1 << 20;    // (n_cols + 1024) / 8 units fit SM_UNIT_BITS
 
@@ -42,14 +43,12 @@ template <int BD>
 struct Codes {
     typedef typename std::conditional<BD == 8, u32x2, unsigned int>::type lane_t;
     // the 8 codes of unit u (a word shared with 4 / BD - 1 neighbours for BD < 4)
-    static __device__ __forceinline__ lane_t load(const unsigned int *__restrict__ codes, int64_t u) {
-        if constexpr (BD == 8)
-            return reinterpret_cast<const u32x2 *>(codes)[u];
-        else
-            return codes[(u * BD) >> 2];
+    static __device__ __forceinline__ lane_t load(const unsigned int *__restrict__ codes, unsigned int u) {
+        const char *p = reinterpret_cast<const char *>(codes) + (BD < 4 ? (u * BD) & ~3u : u * BD);
+        return *reinterpret_cast<const lane_t *>(p);
     }
     // inclusive prefix of (code + 1) over the unit's entries
-    static __device__ __forceinline__ void prefix(lane_t w, int64_t u, int (&p)[8]) {
+    static __device__ __forceinline__ void prefix(lane_t w, unsigned int u, int (&p)[8]) {
         int run = 0;
         if constexpr (BD == 8) {
 #pragma unroll
@@ -58,7 +57,7 @@ struct Codes {
                 p[t] = run;
             }
         } else {
-            const unsigned int ws = BD < 4 ? w >> ((8 * BD * (unsigned)u) & 31u) : w;
+            const unsigned int ws = BD < 4 ? w >> ((8 * BD * u) & 31u) : w;
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 run += (int)((ws >> (BD * t)) & ((1u << BD) - 1u)) + 1;
@@ -68,9 +67,14 @@ struct Codes {
     }
 };
 
-// the unit's 8 values: 16 bytes of fp16 or 8 bytes of int8
+// the unit's 8 values: 16 bytes of fp16 or 8 bytes of int8 (fewer than 2^31
+// entries: byte offsets fit 32 bits)
 template <bool I8>
 using vals_t = typename std::conditional<I8, u32x2, u32x4>::type;
+template <bool I8>
+__device__ __forceinline__ vals_t<I8> load_vals(const void *__restrict__ vals, unsigned int u) {
+    return *reinterpret_cast<const vals_t<I8> *>(static_cast<const char *>(vals) + u * (unsigned)sizeof(vals_t<I8>));
+}
 
 // Values t, t + 1 (t even) as the bits of two fp16; int8 exactly, as 1024 + (q + 128) - 1152.
 template <bool I8>
@@ -118,8 +122,8 @@ __global__ __launch_bounds__(256) void k_macko_spmm_plan(int n_rows, int n_slabs
     for (int b = 0; b < n; b += 64) {
         const bool in = b + lane < n;
         int p[8];
-        Codes<BD>::prefix(in ? Codes<BD>::load(codes, (int64_t)u0 + b + lane) : typename Codes<BD>::lane_t{},
-                          (int64_t)u0 + b + lane, p);
+        Codes<BD>::prefix(in ? Codes<BD>::load(codes, (unsigned)(u0 + b + lane)) : typename Codes<BD>::lane_t{},
+                          (unsigned)(u0 + b + lane), p);
         const int tot = in ? p[7] : 0;
         const int incl = wave_inclusive_scan(tot);
         const int before = carry + incl - tot;
@@ -158,51 +162,216 @@ struct SpmmArg {
     int y_f32, vec_y;
 };
 
-// Decodes the slab `k` of the 16 rows from `row0` on into the wave's tile.
-template <int BD, bool I8>
-__device__ __forceinline__ void decode_slab(const SpmmArg &a, int64_t row0, int rows, int k, int lane,
-                                            unsigned short *tile) {
-    typedef vals_t<I8> V;
-    const int odd = lane & 1 ? -1 : 0, high = lane & 2 ? -1 : 0;
+// y[tok, r .. r + 3] from the sums v of those rows (global rows `row` ..).
+template <bool I8>
+__device__ __forceinline__ void finish(const SpmmArg &a, int tok, int r, int64_t row, f32x4 v) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int r = 8 * half + (lane >> 3), l = lane & 7;
-        int u = 0, end = 0, carry = 0;
-        int64_t base = 0;
-        if (r < rows) {
-            const unsigned int *p = a.plan + (row0 + r) * (a.n_slabs + 1) + k;
-            const unsigned int p0 = p[0], p1 = p[1];
-            const int m0 = a.mrp[row0 + r], m1 = a.mrp[row0 + r + 1];
-            base = m0 / 8;
-            u = (int)(p0 & ((1u << SM_UNIT_BITS) - 1u));
-            end = min((int)(p1 & ((1u << SM_UNIT_BITS) - 1u)) + 1, (m1 - m0) / 8);
-            carry = -1 - (int)(p0 >> SM_UNIT_BITS);      // relative to the slab's first column
+    for (int j = 0; j < 4; ++j) v[j] *= I8 && r + j < a.n_rows ? a.alpha * a.row_scale[row + j] : a.alpha;
+    if (a.y_f32) {
+        float *y = static_cast<float *>(a.y) + (int64_t)tok * a.ldy + r;
+        if (a.vec_y && r + 3 < a.n_rows) {
+            if (a.beta != 0.0f) {
+                const f32x4 o = *reinterpret_cast<const f32x4 *>(y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = fmaf(a.beta, o[j], v[j]);
+            }
+            *reinterpret_cast<f32x4 *>(y) = v;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r + j < a.n_rows) y[j] = a.beta != 0.0f ? fmaf(a.beta, y[j], v[j]) : v[j];
         }
-        unsigned short *dst = tile + r * SM_LDW;
-        for (; __any(u < end); u += 8) {
-            const bool in = u + l < end;
-            typename Codes<BD>::lane_t w = {};
-            V v = {};
-            if (in) {
-                w = Codes<BD>::load(a.codes, base + u + l);
-                v = reinterpret_cast<const V *>(a.vals)[base + u + l];
-            }
-            int p[8];
-            Codes<BD>::prefix(w, base + u + l, p);
-            const int tot = in ? p[7] : 0;
-            const int incl = scan8(tot, odd, high);
-            const int before = carry + incl - tot;
-            carry += last8(incl);
-            if (in) {
+    } else {
+        _Float16 *y = static_cast<_Float16 *>(a.y) + (int64_t)tok * a.ldy + r;
+        if (a.vec_y && r + 3 < a.n_rows) {
+            Vec<F16, 4> o;
+            if (a.beta != 0.0f) {
+                o = load_vec<F16, 4>(y);
 #pragma unroll
-                for (int t = 0; t < 8; t += 2) {
-                    const unsigned int h = value_pair<I8>(v, t);
-                    dst[min((unsigned)(before + p[t]), (unsigned)SM_SLAB)] = (unsigned short)h;
-                    dst[min((unsigned)(before + p[t + 1]), (unsigned)SM_SLAB)] = (unsigned short)(h >> 16);
-                }
+                for (int j = 0; j < 4; ++j) v[j] = fmaf(a.beta, (float)o.v[j], v[j]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o.v[j] = (_Float16)v[j];
+            store_vec<F16, 4>(y, o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r + j < a.n_rows) y[j] = (_Float16)(a.beta != 0.0f ? fmaf(a.beta, (float)y[j], v[j]) : v[j]);
         }
     }
+}
+
+// A wave's 16 rows, 8 at a time (h = 0, 1); lane l of a row's 8 lanes takes
+// every eighth unit of the row's piece of a slab.
+struct RowPair {
+    int base[2], units[2];      // first unit (a valid one also for empty rows) and number of units of the rows
+    const unsigned int *plan[2];
+};
+
+// `last`: the matrix's last unit; rows past the end of the group count as empty.
+__device__ __forceinline__ RowPair load_rows(const SpmmArg &a, int64_t row0, int rows, int last, int lane) {
+    RowPair rp;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = 8 * h + (lane >> 3);
+        const int64_t row = row0 + max(min(r, rows - 1), 0);
+        const int b = a.mrp[row] / 8, e = a.mrp[row + 1] / 8;
+        rp.units[h] = r < rows ? e - b : 0;
+        rp.base[h] = min(b, last);
+        rp.plan[h] = a.plan + row * (a.n_slabs + 1);
+    }
+    return rp;
+}
+
+// The units of one slab in registers: SM_STEPS of 8 lanes cover a slab of a
+// half pruned row, further ones are loaded while decoding.  Lanes past the end
+// read the piece's last unit, so no load hides behind a branch and loads
+// stay in flight over other work.
+constexpr int SM_STEPS = 3;
+template <int BD, bool I8>
+struct Stage {
+    int u[2], end[2], carry[2];
+    typename Codes<BD>::lane_t w[2][SM_STEPS];
+    vals_t<I8> v[2][SM_STEPS];
+};
+
+struct PlanWords {
+    unsigned int p0[2], p1[2];
+};
+
+__device__ __forceinline__ PlanWords load_plan(const RowPair &rp, int k) {
+    PlanWords w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        w.p0[h] = rp.plan[h][k];
+        w.p1[h] = rp.plan[h][k + 1];
+    }
+    return w;
+}
+
+template <int BD, bool I8>
+__device__ __forceinline__ void load_half(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, const PlanWords &w, int l,
+                                          int h) {
+    {
+        st.u[h] = (int)(w.p0[h] & ((1u << SM_UNIT_BITS) - 1u)) + l;
+        st.end[h] = min((int)(w.p1[h] & ((1u << SM_UNIT_BITS) - 1u)) + 1, rp.units[h]);
+        st.carry[h] = -1 - (int)(w.p0[h] >> SM_UNIT_BITS);      // relative to the slab's first column
+        const int stop = max(st.end[h] - 1, 0);
+#pragma unroll
+        for (int i = 0; i < SM_STEPS; ++i) {
+            const unsigned int u = (unsigned)(rp.base[h] + min(st.u[h] + 8 * i, stop));
+            st.w[h][i] = Codes<BD>::load(a.codes, u);
+            st.v[h][i] = load_vals<I8>(a.vals, u);
+        }
+    }
+}
+
+template <int BD, bool I8>
+__device__ __forceinline__ void load_stage(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, const PlanWords &w,
+                                           int l) {
+    load_half<BD, I8>(st, a, rp, w, l, 0);
+    load_half<BD, I8>(st, a, rp, w, l, 1);
+}
+
+// Byte offsets 2 * (code sums + entries so far) of the unit's 8 entries, and
+// the unit's whole advance in columns.  4-bit codes are summed as bytes: even
+// and odd codes apart, doubled, then two shifted adds give all prefix sums
+// (at most 240, so no carries; the last entry's offset, up to 256, is the total).
+template <int BD>
+__device__ __forceinline__ int unit_offsets(typename Codes<BD>::lane_t w, unsigned int unit, int (&o)[8]) {
+    if constexpr (BD == 4) {
+        const unsigned int lo = (w << 1) & 0x1E1E1E1Eu, hi = (w >> 3) & 0x1E1E1E1Eu;
+        unsigned int P = lo + hi;
+        asm volatile("" : "+v"(P));           // shifted adds stay adds (not quarter-rate multiplies)
+        P += P << 8;
+        asm volatile("" : "+v"(P));
+        P += P << 16;
+        asm volatile("" : "+v"(P));
+        const unsigned int E = (P << 8) + lo + 0x0E0A0602u;   // entries 0, 2, 4, 6
+        const unsigned int Q = P + 0x000C0804u;               // entries 1, 3, 5
+        const int tot = (int)(P >> 25) + 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[2 * k] = (int)((E >> (8 * k)) & 255u);
+            o[2 * k + 1] = k < 3 ? (int)((Q >> (8 * k)) & 255u) : 2 * tot;
+        }
+        return tot;
+    } else {
+        Codes<BD>::prefix(w, unit, o);
+        const int tot = o[7];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) o[t] *= 2;
+        return tot;
+    }
+}
+
+typedef __attribute__((address_space(3))) unsigned short lds_half;
+__device__ __forceinline__ int lds_offset(const unsigned short *p) {
+    return (int)(uintptr_t)(const __attribute__((address_space(3))) unsigned short *)p;
+}
+__device__ __forceinline__ int clamp3(int v, int lo, int hi) {
+    int r;
+    asm("v_med3_i32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "v"(lo), "v"(hi));
+    return r;
+}
+
+// One step: the 8 lanes of each row decode 8 units into the tile row at `row`
+// (LDS byte offset).  Entries of neighbouring slabs are clamped into the spare
+// columns on both sides of the row.
+template <int BD, bool I8>
+__device__ __forceinline__ void decode_step(typename Codes<BD>::lane_t w, const vals_t<I8> &v, unsigned int unit, bool in,
+                                            int &carry, int odd, int high, int row) {
+    int o[8];
+    const int all = unit_offsets<BD>(w, unit, o);
+    const int tot = in ? all : 0;
+    int incl = scan8(tot, odd, high);
+    asm volatile("" : "+v"(incl));
+    const int before = row + 2 * (carry + incl - tot);
+    carry += last8(incl);
+    if (in) {
+        const int lo = row - 2, hi = row + 2 * SM_SLAB;
+#pragma unroll
+        for (int t = 0; t < 8; t += 2) {
+            const unsigned int h = value_pair<I8>(v, t);
+            *(lds_half *)(uintptr_t)(unsigned)clamp3(before + o[t], lo, hi) = (unsigned short)h;
+            *(lds_half *)(uintptr_t)(unsigned)clamp3(before + o[t + 1], lo, hi) = (unsigned short)(h >> 16);
+        }
+    }
+}
+
+// Eight of the wave's rows of a slab into its tile at `tile` (LDS byte offset).
+template <int BD, bool I8>
+__device__ __forceinline__ void decode_half(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, int lane, int tile,
+                                            int h) {
+    const int odd = lane & 1 ? -1 : 0, high = lane & 2 ? -1 : 0;
+    {
+        const int row = tile + 2 * (8 * h + (lane >> 3)) * SM_LDW;
+#pragma unroll
+        for (int i = 0; i < SM_STEPS; ++i) {
+            const int u = st.u[h] + 8 * i;
+            if (i > 0 && !__any(u < st.end[h])) break;
+            decode_step<BD, I8>(st.w[h][i], st.v[h][i], (unsigned)(rp.base[h] + u), u < st.end[h], st.carry[h], odd, high,
+                                row);
+        }
+        for (int u = st.u[h] + 8 * SM_STEPS; __any(u < st.end[h]); u += 8) {
+            const unsigned int at = (unsigned)(rp.base[h] + min(u, max(st.end[h] - 1, 0)));
+            decode_step<BD, I8>(Codes<BD>::load(a.codes, at), load_vals<I8>(a.vals, at), (unsigned)(rp.base[h] + u),
+                                u < st.end[h], st.carry[h], odd, high, row);
+        }
+    }
+}
+
+template <int BD, bool I8>
+__device__ __forceinline__ void decode_stage(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, int lane, int tile) {
+    decode_half<BD, I8>(st, a, rp, lane, tile, 0);
+    decode_half<BD, I8>(st, a, rp, lane, tile, 1);
+}
+
+// Clears the 256 columns of a wave's 16 rows: each half wave a row per store.
+__device__ __forceinline__ void clear_tile(unsigned short *tile, int lane) {
+    unsigned short *p = tile + (lane >> 5) * SM_LDW + 8 * (lane & 31);
+#pragma unroll
+    for (int i = 0; i < SM_ROWS; i += 2) *reinterpret_cast<u32x4 *>(p + i * SM_LDW) = u32x4{0u, 0u, 0u, 0u};
 }
 
 __device__ __forceinline__ void wave_lds_order() {
@@ -229,42 +398,70 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
     const int r0 = blockIdx.y * SM_ROWS;
     const int rows = min(SM_ROWS, a.n_rows - r0);
     const int64_t row0 = (int64_t)blockIdx.z * a.n_rows + r0;
-    unsigned short *tile = lds + wv * SM_ROWS * SM_LDW;
+    unsigned short *tile = lds + SM_FRONT + wv * SM_ROWS * SM_LDW;
     const unsigned short *xr[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xr[i] = a.x + (int64_t)min(t0 + 16 * i + n, t1 - 1) * a.ldx + 16 * q;
+    for (int i = 0; i < NT; ++i) xr[i] = a.x + (int64_t)min(t0 + 16 * i + n, t1 - 1) * a.ldx;
     f32x4 acc[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int k = wv; k < a.n_slabs; k += WAVES) {
-        for (int i = lane; i < SM_ROWS * SM_LDW / 8; i += 64)
-            *reinterpret_cast<u32x4 *>(tile + 8 * i) = u32x4{0u, 0u, 0u, 0u};
-        wave_lds_order();
-        decode_slab<BD, I8>(a, row0, rows, k, lane, tile);
-        wave_lds_order();
-        const int c0 = k * SM_SLAB;
+    const int last_unit = a.mrp[(int64_t)gridDim.z * a.n_rows] / 8 - 1;
+    const RowPair rp = load_rows(a, row0, rows, last_unit, lane);
+    // one slab: its units are in st; next gets those of slab k + WAVES, whose
+    // plan words are in pw, and pw those of the slab after that
+    PlanWords pw;
+    const int top = wv + (a.n_slabs - 1 - wv) / WAVES * WAVES;   // the wave's last slab, read again at the end
+    auto slab = [&](int k, Stage<BD, I8> &st, Stage<BD, I8> &next) {
+        // loads are waited for in the order of their issue: what is needed
+        // first goes first, and the next slab's units last
+        // columns past the last are read as the row's last ones: W is zero there
+        const int c0 = k * SM_SLAB + 16 * q, cm = a.n_cols - 8;
+        u32x4 x[NT < 4 ? NT : 1][8];
+        if constexpr (NT < 4) {
 #pragma unroll
-        for (int s = 0; s < SM_SLAB; s += 64) {
-            if (c0 + s >= a.n_cols) break;              // uniform
-            const u32x4 w0 = *reinterpret_cast<const u32x4 *>(tile + n * SM_LDW + s + 16 * q);
-            const u32x4 w1 = *reinterpret_cast<const u32x4 *>(tile + n * SM_LDW + s + 16 * q + 8);
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    x[i][s] = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 64 * (s >> 1) + 8 * (s & 1), cm));
+        }
+        const PlanWords after = load_plan(rp, min(k + 2 * WAVES, top));
+        __builtin_amdgcn_sched_barrier(0);
+        load_stage<BD, I8>(next, a, rp, pw, lane & 7);
+        __builtin_amdgcn_sched_barrier(0);
+        pw = after;
+        clear_tile(tile, lane);
+        wave_lds_order();
+        decode_stage<BD, I8>(st, a, rp, lane, lds_offset(tile));
+        wave_lds_order();
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const h8 w = __builtin_bit_cast(
+                h8, *reinterpret_cast<const u32x4 *>(tile + n * SM_LDW + 64 * (s >> 1) + 16 * q + 8 * (s & 1)));
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                if (i < live) {                          // uniform
-                    // columns past the last are zeros, not what follows the row of x
-                    const int c = c0 + s + 16 * q;
-                    u32x4 x0 = {0u, 0u, 0u, 0u}, x1 = {0u, 0u, 0u, 0u};
-                    if (c < a.n_cols) x0 = *reinterpret_cast<const u32x4 *>(xr[i] + c0 + s);
-                    if (c + 8 < a.n_cols) x1 = *reinterpret_cast<const u32x4 *>(xr[i] + c0 + s + 8);
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w0), __builtin_bit_cast(h8, x0),
-                                                                    acc[i], 0, 0, 0);
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w1), __builtin_bit_cast(h8, x1),
-                                                                    acc[i], 0, 0, 0);
+                if constexpr (NT < 4) {
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, x[i][s]), acc[i], 0, 0, 0);
+                } else if (i < live) {                   // uniform
+                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 64 * (s >> 1) + 8 * (s & 1), cm));
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, xv), acc[i], 0, 0, 0);
                 }
             }
         }
         wave_lds_order();
+    };
+    if (last_unit >= 0 && wv < a.n_slabs) {              // an empty matrix has no unit to read
+        Stage<BD, I8> s0, s1;
+        const PlanWords first = load_plan(rp, wv);
+        pw = load_plan(rp, min(wv + WAVES, top));
+        __builtin_amdgcn_sched_barrier(0);
+        load_stage<BD, I8>(s0, a, rp, first, lane & 7);
+        int k = wv;
+        for (; k + WAVES < a.n_slabs; k += 2 * WAVES) {
+            slab(k, s0, s1);
+            slab(k + WAVES, s1, s0);
+        }
+        if (k < a.n_slabs) slab(k, s0, s1);
     }
     // the waves' sums, added in wave order; the tile is free now
     float *sums = reinterpret_cast<float *>(lds);        // [WAVES][NT][64] of f32x4
@@ -275,42 +472,186 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
     for (int i = wv; i < live; i += WAVES) {
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int w = 0; w < WAVES; ++w) v += *reinterpret_cast<const f32x4 *>(sums + ((w * NT + i) * 64 + lane) * 4);
-        const int tok = t0 + 16 * i + n, r = r0 + 4 * q;   // D: row 4 q + j, column (token) n
+        const int tok = t0 + 16 * i + n;                 // D: row 4 q + j, column (token) n
+        if (tok < t1) finish<I8>(a, tok, r0 + 4 * q, row0 + 4 * q, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: 64 rows of W per workgroup, each of 4 waves decoding 16 of them
+// into a common tile and multiplying all 64 by tokens of its own, so x goes
+// from memory straight to the registers of the one wave that uses it, and a W
+// operand read from LDS serves all of the wave's tokens.  With fewer than four
+// token tiles the waves of one tile share out its columns instead.
+// ---------------------------------------------------------------------------
+template <int NT>
+struct BlockShape {
+    static constexpr int WAVES = 4;
+    static constexpr int ROWS = WAVES * SM_ROWS;
+    static constexpr int TILE = ROWS * SM_LDW;              // halfs
+    static constexpr int KW = NT < 4 ? 4 / NT : 1;          // waves that share a token tile's columns
+    static constexpr int TW = NT < 4 ? 1 : NT / 4;          // token tiles of a wave
+    static constexpr int STEPS = 8 / KW;                    // 32-column steps of a wave per slab
+    static constexpr int AHEAD = STEPS * TW <= 16 ? STEPS : 16 / TW;   // steps of x in registers
+    static constexpr int OCC = NT < 8 ? 4 : 2;              // waves per SIMD that the registers allow
+    static constexpr size_t LDS = (size_t)(SM_FRONT + TILE) * 2;
+};
+
+// an LDS-only barrier: loads issued before it stay in flight
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Workgroup: rows ROWS * blockIdx.y .., group blockIdx.z / split, slabs of part
+// blockIdx.z % split, and `width` 16-token tiles from width * blockIdx.x on.
+template <int BD, bool I8, int NT>
+__global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) void k_macko_spmm_block(SpmmArg a, int width, int split,
+                                                                       float *__restrict__ partial, int ldp) {
+    typedef BlockShape<NT> B;
+    extern __shared__ __attribute__((aligned(16))) unsigned short lds[];
+    const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int group = blockIdx.z / split, part = blockIdx.z - group * split;
+    int t0 = 0, t1 = a.n_tok;
+    if (a.tok_offsets) {
+        t0 = min(max(a.tok_offsets[group], 0), a.n_tok);
+        t1 = min(max(a.tok_offsets[group + 1], t0), a.n_tok);
+    }
+    t0 += blockIdx.x * 16 * width;
+    if (t0 >= t1) return;
+    t1 = min(t1, t0 + 16 * width);
+    const int r0 = blockIdx.y * B::ROWS;
+    const int64_t row0 = (int64_t)group * a.n_rows + r0;
+    // the wave's token tiles: every fourth (NT >= 4), or one and a part of its columns
+    const int kp = NT < 4 ? wv / NT : 0, tw0 = NT < 4 ? wv % NT : wv;
+    constexpr int TSTEP = NT < 4 ? 1 : 4;
+    const int live = (t1 - t0 + 15) / 16;                   // token tiles in use
+    const int mine = NT < 4 ? (tw0 < live ? 1 : 0) : min(B::TW, max(0, (live - tw0 + 3) / 4));
+    const int wrow = wv * SM_ROWS;                          // the wave's rows in the decoding
+    unsigned short *tile = lds + SM_FRONT + wrow * SM_LDW;
+    f32x4 acc[4][B::TW];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < B::TW; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int last_unit = a.mrp[(int64_t)(gridDim.z / split) * a.n_rows] / 8 - 1;
+    const RowPair rp = load_rows(a, row0 + min(wrow, a.n_rows - 1 - r0), a.n_rows - r0 - wrow, last_unit, lane);
+    const unsigned short *xr[B::TW];
+#pragma unroll
+    for (int t = 0; t < B::TW; ++t)
+        xr[t] = a.x + (int64_t)min(t0 + 16 * (tw0 + TSTEP * t) + n, t1 - 1) * a.ldx;
+    const int lo = (int)((int64_t)a.n_slabs * part / split), hi = (int)((int64_t)a.n_slabs * (part + 1) / split);
+    const int cm = a.n_cols - 8;
+    if (last_unit >= 0 && lo < hi) {                        // an empty matrix has no unit to read
+        const int col = kp * 32 * B::STEPS + 16 * q;        // the lane's first column in a slab
+        u32x4 x[B::AHEAD][B::TW];
+        // columns past the last are read as the row's last ones: W is zero there
+        auto load_x = [&](int k, int s, int slot) {
+#pragma unroll
+            for (int t = 0; t < B::TW; ++t)
+                x[slot][t] = *reinterpret_cast<const u32x4 *>(xr[t] + min(k * SM_SLAB + col + 64 * (s >> 1) + 8 * (s & 1), cm));
+        };
+        Stage<BD, I8> st;
+        const PlanWords first = load_plan(rp, lo);
+        PlanWords pw = load_plan(rp, min(lo + 1, hi - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        load_stage<BD, I8>(st, a, rp, first, lane & 7);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < B::AHEAD; ++s) load_x(lo, s, s);
+        for (int k = lo; k < hi; ++k) {
+            clear_tile(tile, lane);
+            wave_lds_order();
+            // half by half, the next slab's units are loaded as soon as their
+            // registers are free; the next x is in flight over the decoding
+            const PlanWords after = load_plan(rp, min(k + 2, hi - 1));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                decode_half<BD, I8>(st, a, rp, lane, lds_offset(tile), h);
+                __builtin_amdgcn_sched_barrier(0);
+                load_half<BD, I8>(st, a, rp, pw, lane & 7, h);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            pw = after;
+            lds_barrier();
+#pragma unroll
+            for (int s = 0; s < B::STEPS; ++s) {
+                h8 w[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    w[r] = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4 *>(lds + SM_FRONT + (16 * r + n) * SM_LDW +
+                                                                                   kp * B::STEPS * 32 + 64 * (s >> 1) + 16 * q + 8 * (s & 1)));
+#pragma unroll
+                for (int t = 0; t < B::TW; ++t) {
+                    if (t < mine) {                         // uniform
+                        const h8 xv = __builtin_bit_cast(h8, x[s % B::AHEAD][t]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[r], xv, acc[r][t], 0, 0, 0);
+                    }
+                }
+                if (s + B::AHEAD < B::STEPS)
+                    load_x(k, s + B::AHEAD, s % B::AHEAD);
+                else
+                    load_x(min(k + 1, hi - 1), (s + B::AHEAD) % B::STEPS, s % B::AHEAD);
+            }
+            lds_barrier();
+        }
+    }
+    if (B::KW > 1) {                                        // the column parts, in order
+        f32x4 *sums = reinterpret_cast<f32x4 *>(lds);       // [KW - 1][NT][4][64]
+        __syncthreads();
+        if (kp > 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[(((kp - 1) * NT + tw0) * 4 + r) * 64 + lane] = acc[r][0];
+        }
+        __syncthreads();
+        if (kp > 0) return;
+        for (int p = 0; p < B::KW - 1; ++p)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r][0] += sums[((p * NT + tw0) * 4 + r) * 64 + lane];
+    }
+#pragma unroll
+    for (int t = 0; t < B::TW; ++t) {
+        const int tok = t0 + 16 * (tw0 + TSTEP * t) + n;
         if (tok >= t1) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] *= I8 && r + j < a.n_rows ? a.alpha * a.row_scale[row0 + 4 * q + j] : a.alpha;
-        if (a.y_f32) {
-            float *y = static_cast<float *>(a.y) + (int64_t)tok * a.ldy + r;
-            if (a.vec_y && r + 3 < a.n_rows) {
-                if (a.beta != 0.0f) {
-                    const f32x4 o = *reinterpret_cast<const f32x4 *>(y);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = fmaf(a.beta, o[j], v[j]);
-                }
-                *reinterpret_cast<f32x4 *>(y) = v;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r + j < a.n_rows) y[j] = a.beta != 0.0f ? fmaf(a.beta, y[j], v[j]) : v[j];
-            }
-        } else {
-            _Float16 *y = static_cast<_Float16 *>(a.y) + (int64_t)tok * a.ldy + r;
-            if (a.vec_y && r + 3 < a.n_rows) {
-                Vec<F16, 4> o;
-                if (a.beta != 0.0f) {
-                    o = load_vec<F16, 4>(y);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = fmaf(a.beta, (float)o.v[j], v[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o.v[j] = (_Float16)v[j];
-                store_vec<F16, 4>(y, o);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r + j < a.n_rows) y[j] = (_Float16)(a.beta != 0.0f ? fmaf(a.beta, (float)y[j], v[j]) : v[j]);
-            }
+        for (int r = 0; r < 4; ++r) {
+            const int row = r0 + 16 * r + 4 * q;
+            if (row >= a.n_rows) continue;
+            if (split > 1)
+                *reinterpret_cast<f32x4 *>(partial + ((int64_t)part * a.n_tok + tok) * ldp + row) = acc[r][t];
+            else
+                finish<I8>(a, tok, row, row0 - r0 + row, acc[r][t]);
         }
+    }
+}
+
+// Adds the parts of k_macko_spmm_block in order.
+template <bool I8>
+__global__ __launch_bounds__(256) void k_macko_spmm_join(SpmmArg a, int n_groups, int split,
+                                                         const float *__restrict__ partial, int ldp) {
+    const int r = 4 * (blockIdx.x * 256 + threadIdx.x);
+    if (r >= a.n_rows) return;
+    int t0 = 0, t1 = a.n_tok;
+    if (a.tok_offsets) {
+        t0 = min(max(a.tok_offsets[0], 0), a.n_tok);
+        t1 = min(max(a.tok_offsets[n_groups], t0), a.n_tok);
+    }
+    for (int tok = t0 + blockIdx.y; tok < t1; tok += gridDim.y) {
+        f32x4 v = *reinterpret_cast<const f32x4 *>(partial + (int64_t)tok * ldp + r);
+        for (int s = 1; s < split; ++s)
+            v += *reinterpret_cast<const f32x4 *>(partial + ((int64_t)s * a.n_tok + tok) * ldp + r);
+        int64_t row = r;
+        if (I8 && n_groups > 1) {                           // the token's group
+            int g = 0;
+            while (g + 1 < n_groups && a.tok_offsets[g + 1] <= tok) ++g;
+            row += (int64_t)g * a.n_rows;
+        }
+        finish<I8>(a, tok, r, row, v);
     }
 }
 
@@ -327,22 +668,75 @@ spmv_status check_size(int64_t n_rows, int64_t n_cols) {
 
 template <int BD, bool I8, int NT, int WAVES>
 void launch(const SpmmArg &a, dim3 grid, hipStream_t st) {
-    const size_t lds = std::max<size_t>((size_t)WAVES * SM_ROWS * SM_LDW * 2, (size_t)WAVES * NT * 64 * 16);
+    const size_t lds = std::max<size_t>((size_t)(SM_FRONT + WAVES * SM_ROWS * SM_LDW) * 2, (size_t)WAVES * NT * 64 * 16);
     k_macko_spmm<BD, I8, NT, WAVES><<<grid, 64 * WAVES, lds, st>>>(a);
 }
 
+// How the tokens and columns of a product are cut.
+struct Cut {
+    bool block;       // k_macko_spmm_block, else k_macko_spmm
+    int nt;           // token tiles a workgroup can hold
+    int width;        // token tiles it takes
+    int tiles;        // workgroups over the tokens (of the largest possible group)
+    int split;        // workgroups over the columns
+};
+
+Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok) {
+    Cut c = {};
+    const int64_t t16 = std::max<int64_t>(1, ceil_div(n_tok, 16));
+    c.block = n_tok > 16;
+    // a group's share of the tokens is not known here: room for twice the mean
+    const int64_t room = n_groups > 1 ? std::min(t16, ceil_div(2 * n_tok, 16 * n_groups)) : t16;
+    c.nt = room > 8 ? 16 : room > 4 ? 8 : room > 2 ? 4 : 2;
+    c.tiles = (int)ceil_div(t16, c.nt);
+    c.width = n_groups > 1 ? c.nt : (int)ceil_div(t16, c.tiles);
+    c.split = 1;
+    if (c.block) {
+        // parts of the columns: fewest rounds of slabs over the resident
+        // workgroups, each further part costing the traffic of its sums
+        const int64_t slabs = ceil_div(n_cols, SM_SLAB), wgs = n_groups * ceil_div(n_rows, BlockShape<4>::ROWS) * c.tiles;
+        double best = 1e30;
+        for (int s = 1; s <= 16 && s <= slabs; ++s) {
+            const double cost = (double)ceil_div(wgs * s, 256 * (c.nt < 8 ? 4 : 2)) * (double)ceil_div(slabs, s) +
+                                (s > 1 ? 1.0 + s * (double)n_tok * (double)n_rows * 4e-7 : 0.0);
+            if (cost < best) best = cost, c.split = s;
+        }
+    }
+    return c;
+}
+
+int64_t partial_ld(int64_t n_rows) { return ceil_div(n_rows, 4) * 4; }
+
+size_t packed_bytes(int64_t n_tok, int64_t n_cols) {
+    return ((size_t)n_tok * (size_t)(ceil_div(n_cols, 8) * 8) * 2 + 15) & ~size_t(15);
+}
+
+template <int BD, bool I8, int NT>
+void launch_block(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
+    const dim3 grid(c.tiles, (unsigned)ceil_div(a.n_rows, BlockShape<NT>::ROWS), n_groups * c.split);
+    k_macko_spmm_block<BD, I8, NT><<<grid, 64 * BlockShape<NT>::WAVES, BlockShape<NT>::LDS, st>>>(a, c.width, c.split, partial,
+                                                                                    (int)partial_ld(a.n_rows));
+}
+
 template <int BD, bool I8>
-spmv_status launch_shape(const SpmmArg &a, int n_groups, hipStream_t st) {
-    // token tiles per workgroup; groups share n_tok among them, so any of them may have all
-    const int nt = n_groups > 1 || a.n_tok > 32 ? 4 : a.n_tok > 16 ? 2 : 1;
-    const dim3 grid((unsigned)ceil_div(a.n_tok, 16 * nt), (unsigned)ceil_div(a.n_rows, SM_ROWS), n_groups);
-    if (nt == 1)
-        launch<BD, I8, 1, 4>(a, grid, st);
-    else if (nt == 2)
-        launch<BD, I8, 2, 4>(a, grid, st);
-    else
-        launch<BD, I8, 4, 4>(a, grid, st);
-    SPMV_LAUNCHED("k_macko_spmm");
+spmv_status launch_shape(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
+    if (!c.block) {
+        launch<BD, I8, 1, 4>(a, dim3(1, (unsigned)ceil_div(a.n_rows, SM_ROWS), n_groups), st);
+        SPMV_LAUNCHED("k_macko_spmm");
+        return SPMV_OK;
+    }
+    switch (c.nt) {
+        case 2: launch_block<BD, I8, 2>(a, c, n_groups, partial, st); break;
+        case 4: launch_block<BD, I8, 4>(a, c, n_groups, partial, st); break;
+        case 8: launch_block<BD, I8, 8>(a, c, n_groups, partial, st); break;
+        default: launch_block<BD, I8, 16>(a, c, n_groups, partial, st); break;
+    }
+    SPMV_LAUNCHED("k_macko_spmm_block");
+    if (c.split > 1) {
+        k_macko_spmm_join<I8><<<dim3((unsigned)ceil_div(a.n_rows, 1024), (unsigned)std::min(a.n_tok, 65535)), 256, 0, st>>>(
+            a, n_groups, c.split, partial, (int)partial_ld(a.n_rows));
+        SPMV_LAUNCHED("k_macko_spmm_join");
+    }
     return SPMV_OK;
 }
 
@@ -358,8 +752,8 @@ spmv_status spmm_apply(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t
     if (!width_ok(bdelta)) return fail(SPMV_ERR_INVALID_VALUE, "code width %d is not 1, 2, 4 or 8", bdelta);
     if (y_dtype != SPMV_F32 && y_dtype != SPMV_F16)
         return fail(dtype_ok(y_dtype) ? SPMV_ERR_UNSUPPORTED : SPMV_ERR_INVALID_VALUE, "y must be fp32 or fp16");
-    if (n_groups > 65535 || ceil_div(n_rows, SM_ROWS) > 65535)
-        return fail(SPMV_ERR_UNSUPPORTED, "more than 65535 groups or %d rows are not supported", 65535 * SM_ROWS);
+    if (n_groups > 4095 || ceil_div(n_rows, SM_ROWS) > 65535)
+        return fail(SPMV_ERR_UNSUPPORTED, "more than 4095 groups or %d rows are not supported", 65535 * SM_ROWS);
     if ((int64_t)n_groups * n_rows > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "n_groups * n_rows does not fit int32");
     if (ldx < n_cols || ldy < n_rows) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
     if (n_groups > 1 && !tok_offsets) return fail(SPMV_ERR_INVALID_VALUE, "tok_offsets is NULL with several groups");
@@ -377,13 +771,16 @@ spmv_status spmm_apply(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t
                  static_cast<const unsigned int *>(plan), tok_offsets, x, ldx, y, ldy, alpha, beta, y_dtype == SPMV_F32, 0};
     const size_t ysize = dtype_size(y_dtype);
     a.vec_y = ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (4 * ysize - 1)) == 0;
-    if (!aligned16(x) || ldx % 8 != 0 || n_cols % 8 != 0) {
+    const Cut cut = cut_of(n_groups, n_rows, n_cols, n_tok);
+    const bool pack = !aligned16(x) || ldx % 8 != 0 || n_cols % 8 != 0;
+    if (pack || cut.split > 1) {
         size_t need = 0;
-        macko_spmm_workspace_size(n_tok, n_cols, &need);
+        macko_spmm_workspace_size(n_groups, n_rows, n_cols, n_tok, &need);
         if (!workspace || workspace_bytes < need || !aligned16(workspace))
-            return fail(SPMV_ERR_INVALID_VALUE,
-                        "rows of x that are not 16-byte aligned, or n_cols not a multiple of 8, need a 16-byte aligned "
-                        "workspace of %zu bytes", need);
+            return fail(SPMV_ERR_INVALID_VALUE, "this product needs a 16-byte aligned workspace of %zu bytes", need);
+    }
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + packed_bytes(n_tok, n_cols));
+    if (pack) {
         const int ldp = (int)(ceil_div(n_cols, 8) * 8);
         k_macko_spmm_pack<<<dim3((unsigned)ceil_div(ldp, 256), (unsigned)std::min(n_tok, 65535)), 256, 0, s>>>(
             n_tok, n_cols, ldp, x, ldx, static_cast<unsigned short *>(workspace));
@@ -393,10 +790,10 @@ spmv_status spmm_apply(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t
         a.n_cols = ldp;
     }
     switch (bdelta) {
-        case 1: return launch_shape<1, I8>(a, n_groups, s);
-        case 2: return launch_shape<2, I8>(a, n_groups, s);
-        case 4: return launch_shape<4, I8>(a, n_groups, s);
-        default: return launch_shape<8, I8>(a, n_groups, s);
+        case 1: return launch_shape<1, I8>(a, cut, n_groups, partial, s);
+        case 2: return launch_shape<2, I8>(a, cut, n_groups, partial, s);
+        case 4: return launch_shape<4, I8>(a, cut, n_groups, partial, s);
+        default: return launch_shape<8, I8>(a, cut, n_groups, partial, s);
     }
 }
 
@@ -439,12 +836,15 @@ extern "C" spmv_status macko_spmm_plan(int32_t n_rows, int32_t n_cols, int32_t b
     return SPMV_OK;
 }
 
-extern "C" spmv_status macko_spmm_workspace_size(int32_t n_tok, int32_t n_cols, size_t *bytes) {
+extern "C" spmv_status macko_spmm_workspace_size(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t n_tok,
+                                                 size_t *bytes) {
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
-    if (n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "n_tok < 0");
-    const spmv_status st = check_size(0, n_cols);
+    if (n_groups < 1 || n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "n_groups must be >= 1 and n_tok >= 0");
+    const spmv_status st = check_size(n_rows, n_cols);
     if (st != SPMV_OK) return st;
-    *bytes = (size_t)n_tok * (size_t)(ceil_div(n_cols, 8) * 8) * 2;
+    const Cut c = cut_of(n_groups, n_rows, n_cols, n_tok);
+    *bytes = packed_bytes(n_tok, n_cols) +
+             (c.split > 1 ? (size_t)c.split * (size_t)n_tok * (size_t)partial_ld(n_rows) * 4 : 0);
     return SPMV_OK;
 }
 

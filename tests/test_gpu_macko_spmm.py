@@ -116,6 +116,44 @@ def test_token_counts(T):
         assert (yb[0] == -7).all() and (yb[T + 1] == -7).all()
 
 
+@pytest.mark.parametrize("shape", [(64, 2304, 20), (200, 5000, 40), (1000, 2560, 300), (70, 12288, 65)])
+@pytest.mark.parametrize("i8", [False, True])
+def test_columns_split_over_workgroups(shape, i8):
+    """Few rows and many columns: partial sums in the workspace, joined in order (same bits on every call)."""
+    rows, cols, T = shape
+    w = _weight(rows, cols, "0.8", 4, 8, i8)
+    m = _matrix(w, rows, cols, 4)
+    assert S.macko_spmm_workspace_size(1, rows, cols, T) > S.macko_spmm_workspace_size(1, rows, cols, 1) * T
+    x = _x(T, cols, T)
+    y0 = torch.randn(T, rows, device="cuda").half()
+    ys = []
+    for fill in (255, 0):
+        ws = m.workspace(T).fill_(fill)
+        y = y0.clone()
+        m.apply(x, y, 0.5, -2.0, workspace=ws)
+        ys.append(y)
+    ref, bound = R.spmm(w[4], x, 0.5, -2.0, y0, torch.float16)
+    R.check(ys[0], ref, bound, "split")
+    assert torch.equal(*ys)
+
+
+def test_split_groups_and_streams():
+    """Two groups, columns split, on a stream of its own with a workspace of its own."""
+    groups, rows, cols, T = 2, 96, 4096, 50
+    w = _weight(groups * rows, cols, "0.8", 4, 9, True)
+    m = _matrix(w, rows, cols, 4, groups)
+    x = _x(T, cols, 2)
+    off = torch.tensor([0, 19, 50], dtype=torch.int32, device="cuda")
+    y = torch.zeros(T, rows, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    m.apply(x, y, tok_offsets=off, stream=side)
+    side.synchronize()
+    for g, a, b in ((0, 0, 19), (1, 19, 50)):
+        ref, bound = R.spmm(w[4][g * rows:(g + 1) * rows], x[a:b], 1.0, 0.0, None, torch.float32)
+        R.check(y[a:b], ref, bound, f"group {g}")
+
+
 def test_full_size_against_the_vector_product():
     """12288 x 12288 at 50 %: each token against macko_spmv, same bound for both."""
     W = gen.pruned_weight(0.5, seed=3)
@@ -149,8 +187,8 @@ def test_strides_and_alignment():
         m.apply(x, y, workspace=m.workspace(T))
         R.check(y, ref, bound, f"{extra} {off}")
         assert (yb[:, :off] == -7).all() and (yb[:, off + rows:] == -7).all()
-    with pytest.raises(S.SpmvError):
-        m.apply(xb[:, 3:3 + cols], y)                                          # needs a workspace
+    with pytest.raises(S.SpmvError):                                           # needs a workspace
+        S.macko_spmm(rows, cols, m.mrow_ptr, m.codes, m.vals, m.plan, 1.0, xb[:, 3:3 + cols], 0.0, y)
 
 
 @pytest.mark.parametrize("i8", [False, True])

@@ -135,8 +135,8 @@ def test_spmm_refusals(i8):
     assert call(g=0) == VALUE and call(n=-1) == VALUE and call(rows=-1) == VALUE and call(cols=-1) == VALUE
     assert call(b=3) == VALUE and call(ydt=1) == UNSUPPORTED and call(ydt=5) == VALUE
     assert call(cols=(1 << 20) + 1, ldx=1 << 21) == UNSUPPORTED
-    assert call(rows=16 * 65535 + 1, ldy=1 << 21) == UNSUPPORTED and call(g=65536, off=P) == UNSUPPORTED
-    assert call(g=65535, rows=40000, ldy=40000, off=P) == OVERFLOW
+    assert call(rows=16 * 65535 + 1, ldy=1 << 21) == UNSUPPORTED and call(g=4096, off=P) == UNSUPPORTED
+    assert call(g=4095, rows=600000, ldy=600000, off=P) == OVERFLOW
     assert call(ldx=63) == VALUE and call(ldy=31) == VALUE
     assert call(g=2) == VALUE                                   # several groups without offsets
     for k in ("mrp", "codes", "vals", "plan", "x", "y"):
@@ -144,8 +144,8 @@ def test_spmm_refusals(i8):
     assert call(cols=0, ldx=0) == VALUE
     assert call(vals=P + 4) == UNSUPPORTED and call(codes=P + 2) == UNSUPPORTED and call(b=8, codes=P + 4) == UNSUPPORTED
     # x that needs packing: no workspace, too small, misaligned
-    need = S.macko_spmm_workspace_size(4, 64)
-    assert need == 4 * 64 * 2 and S.macko_spmm_workspace_size(3, 9) == 3 * 16 * 2
+    need = S.macko_spmm_workspace_size(1, 32, 64, 4)
+    assert need == 4 * 64 * 2 and S.macko_spmm_workspace_size(1, 32, 9, 3) == 3 * 16 * 2
     for kw in (dict(x=P + 2), dict(ldx=65), dict(cols=63, ldx=64)):
         assert call(**kw) == VALUE
         assert b"workspace" in S.lib().spmv_last_error()
@@ -162,7 +162,9 @@ def test_spmm_plan_sizes_and_refusals():
     assert S.macko_spmm_plan_size(0, 100) == 0
     assert L.macko_spmm_plan_size(-1, 4, ctypes.byref(z)) == VALUE and L.macko_spmm_plan_size(4, 4, None) == VALUE
     assert L.macko_spmm_plan_size(4, (1 << 20) + 1, ctypes.byref(z)) == UNSUPPORTED
-    assert L.macko_spmm_workspace_size(-1, 4, ctypes.byref(z)) == VALUE
+    assert L.macko_spmm_workspace_size(1, 4, 4, -1, ctypes.byref(z)) == VALUE
+    assert L.macko_spmm_workspace_size(0, 4, 4, 1, ctypes.byref(z)) == VALUE
+    assert L.macko_spmm_workspace_size(1, 4, 4, 1, None) == VALUE
     assert L.macko_spmm_plan(8, 64, 5, P, P, P, 1 << 20, None) == VALUE
     assert L.macko_spmm_plan(8, 64, 4, P, P, P, 8, None) == VALUE
     assert L.macko_spmm_plan(8, 64, 4, None, P, P, 1 << 20, None) == VALUE
