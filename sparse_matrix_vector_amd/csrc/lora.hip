@@ -58,17 +58,18 @@ struct Frag<BF16> {
     }
 };
 
-// Elements c .. c + 7 of a row as 16 bytes; those at or past n are zero.
-// VEC: n is a multiple of 8 and the row 16-byte aligned.
+// Elements c .. c + 7 of a row of n as 16 bytes.  VEC (n a multiple of 8, the
+// row 16-byte aligned): no branch, past the end the row's last 8 elements;
+// otherwise elements past the end are zero.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load8(const unsigned short *__restrict__ row, int c, int n) {
-    if (VEC) return c < n ? *reinterpret_cast<const u32x4 *>(row + c) : u32x4{0u, 0u, 0u, 0u};
-    unsigned short v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? row[c + i] : (unsigned short)0;
+    if (VEC) return *reinterpret_cast<const u32x4 *>(row + min(c, n - 8));
     u32x4 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (unsigned int)v[2 * i] | ((unsigned int)v[2 * i + 1] << 16);
+    for (int i = 0; i < 4; ++i) {
+        const unsigned int lo = row[min(c + 2 * i, n - 1)], hi = row[min(c + 2 * i + 1, n - 1)];
+        r[i] = (c + 2 * i < n ? lo : 0u) | (c + 2 * i + 1 < n ? hi << 16 : 0u);
+    }
     return r;
 }
 
@@ -87,71 +88,40 @@ struct ShrinkArg {
     int64_t ldx;
     int dim;
     float *h;                      // [split][n_tok][16 NJ], rows in sorted order
+    unsigned short *terms;         // the weight gradients' operand (below), or NULL
+    int *exps;
 };
 
 __device__ __forceinline__ int rank_of(const int *ranks, int a, int max_rank) {
     return ranks ? min(max(ranks[a], 0), max_rank) : max_rank;
 }
 
-// One workgroup: tile blockIdx.x, k range blockIdx.y of gridDim.y, product
-// blockIdx.z (the gradient needs A x and B dy).  Each of the 4 waves takes a
-// quarter of the range in steps of 64 (lane group q owns k = 16 q .. 16 q + 15
-// of a step, in x and W alike), and wave 0 adds the four sums.
-template <typename E, int NJ, bool VEC>
-__global__ __launch_bounds__(256) void k_lora_shrink(int n_tok, int n_adapters, int max_rank,
-                                                     const int *__restrict__ ranks,
-                                                     const int *__restrict__ order,
-                                                     const int4 *__restrict__ tiles, ShrinkArg a0, ShrinkArg a1) {
-    typedef typename Frag<E>::V V;
-    __shared__ f32x4 part[3][NJ][64];
-    const ShrinkArg &a = blockIdx.z ? a1 : a0;
-    const int4 tile = tiles[blockIdx.x];
-    if ((unsigned)tile.x >= (unsigned)n_adapters) return;
-    const int rank = rank_of(ranks, tile.x, max_rank);
-    const int nj = (rank + 15) / 16;
-    if (nj == 0) return;
-    const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int tok = order[min(tile.y + n, tile.z - 1)];
-    const unsigned short *xr = a.x + (int64_t)tok * a.ldx;
-    const unsigned short *wr[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-        wr[j] = a.W + ((int64_t)tile.x * max_rank + min(16 * j + n, max_rank - 1)) * a.dim;
-    // steps of this wave: waves of all splits take turns over 64-wide steps in contiguous runs
-    const int steps = (a.dim + 63) / 64, parts = gridDim.y * 4, mine = blockIdx.y * 4 + wv;
-    const int lo = (int)((int64_t)steps * mine / parts), hi = (int)((int64_t)steps * (mine + 1) / parts);
-    f32x4 acc[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = lo; s < hi; ++s) {
-        const int k = s * 64 + q * 16;
-        const u32x4 x0 = load8<VEC>(xr, k, a.dim), x1 = load8<VEC>(xr, k + 8, a.dim);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            if (j < nj) {
-                const u32x4 w0 = load8<VEC>(wr[j], k, a.dim), w1 = load8<VEC>(wr[j], k + 8, a.dim);
-                acc[j] = Frag<E>::mma(__builtin_bit_cast(V, x0), __builtin_bit_cast(V, w0), acc[j]);
-                acc[j] = Frag<E>::mma(__builtin_bit_cast(V, x1), __builtin_bit_cast(V, w1), acc[j]);
-            }
-        }
+constexpr int SHRINK_WAVES = 4;
+
+// The rows of one workgroup: a plan tile, or MT tiles of a group from every
+// MT-th one on (the others of the group have nothing to do).  Workgroup `id`
+// takes tile MT * (id % n) + id / n, n = tiles / MT: those with work come first
+// and without gaps, or they would fall on the same compute units again and again.
+struct Block {
+    int group, begin, end;
+};
+template <int MT>
+__device__ __forceinline__ Block block_of(const int4 *__restrict__ tiles, int n_tiles, int id,
+                                          const int *__restrict__ offsets, int n_tok, int n_adapters) {
+    if (MT > 1) {
+        const int n = (n_tiles + MT - 1) / MT;
+        id = MT * (id % n) + id / n;
     }
-    if (wv > 0) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) part[wv - 1][j][lane] = acc[j];
+    if (id >= n_tiles) return {-1, 0, 0};
+    const int4 t = tiles[id];
+    Block b = {(unsigned)t.x < (unsigned)n_adapters ? t.x : -1, t.y, t.z};
+    if (MT > 1) {
+        if ((t.y - t.w) % (LR_TILE * MT) != 0)
+            b.end = b.begin;
+        else if (t.z > t.y)
+            b.end = min(t.y + LR_TILE * MT, b.group >= 0 ? offsets[b.group + 1] : n_tok);
     }
-    __syncthreads();
-    if (wv > 0) return;
-    float *h = a.h + (int64_t)blockIdx.y * n_tok * (16 * NJ);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const f32x4 v = (acc[j] + part[0][j][lane]) + (part[1][j][lane] + part[2][j][lane]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = tile.y + 4 * q + i;     // D: row 4 q + i, column n
-            if (row < tile.z) h[(int64_t)row * (16 * NJ) + 16 * j + n] = 16 * j + n < rank ? v[i] : 0.0f;
-        }
-    }
+    return b;
 }
 
 // v as a sum of NT numbers of type E.
@@ -171,20 +141,236 @@ __device__ __forceinline__ int scale_exponent(float m) {
     return e == 0 || e == 255 ? 0 : 127 - e;
 }
 
-// Eight neighbouring results of one token.
+// Operands of the weight gradients: h as NT terms, transposed to
+// [term][rank][n_tok + LR_PAD] so that 8 tokens of a rank are one load; fp16
+// terms scaled by a power of two per tile, whose exponent is kept at the
+// tile's first row.
+constexpr int LR_PAD = 8;
+template <typename E, int NT, int R>
+__device__ __forceinline__ void store_terms(unsigned short *__restrict__ terms, int n_tok, int row, int end, int rank,
+                                            const float (&v)[4], int e) {
+    unsigned short t[4][NT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(v[i], e) : v[i], t[i]);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+        unsigned short *p = terms + ((int64_t)k * R + rank) * (n_tok + LR_PAD) + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row + i < end) p[i] = t[i][k];
+    }
+}
+
+template <typename E>
+constexpr int grad_terms() { return E::CODE == SPMV_BF16 ? 3 : 2; }
+
+// The 64-wide steps lo .. hi - 1 of MT token tiles and the first N rank tiles.
+// Two register sets take turns, so a step's loads are in flight over the
+// previous step's products; past the end the last step is read again.
+template <typename E, int N, int MT, bool VEC, int NJ>
+__device__ __forceinline__ void shrink_steps(const unsigned short *const (&xr)[MT], const unsigned short *const (&wr)[NJ],
+                                             int dim, int lo, int hi, int q, f32x4 (&acc)[MT][NJ]) {
+    typedef typename Frag<E>::V V;
+    struct Step {
+        u32x4 x[MT][2], w[N][2];
+    };
+    auto load = [&](Step &st, int s) {
+        const int k = min(s, hi - 1) * 64 + q * 16;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            st.x[m][0] = load8<VEC>(xr[m], k, dim);
+            st.x[m][1] = load8<VEC>(xr[m], k + 8, dim);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            st.w[j][0] = load8<VEC>(wr[j], k, dim);
+            st.w[j][1] = load8<VEC>(wr[j], k + 8, dim);
+        }
+    };
+    auto multiply = [&](Step &st, int s) {
+        if (VEC && s * 64 + 64 > dim) {          // uniform: columns past the end count nothing
+            const int k = s * 64 + q * 16;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) st.x[m][i][d] = k + 8 * i < dim ? st.x[m][i][d] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    acc[m][j] = Frag<E>::mma(__builtin_bit_cast(V, st.x[m][i]), __builtin_bit_cast(V, st.w[j][i]), acc[m][j]);
+    };
+    if (lo >= hi) return;
+    Step s0, s1;
+    load(s0, lo);
+    int s = lo;
+    for (; s + 1 < hi; s += 2) {
+        load(s1, s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s0, s);
+        load(s0, s + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s1, s + 1);
+    }
+    if (s < hi) multiply(s0, s);
+}
+
+// One workgroup: a block of tokens, one of `split` parts of the contraction, and
+// one of `products` (the gradient needs A x and B dy).  The parts of a block are
+// neighbours in the launch, so that together they read whole rows of x:
+// with the blocks in front, all workgroups read the same columns of rows a
+// power of two apart, which lie on few memory channels.  The waves share the range in
+// runs of 64-wide steps (lane group q owns k = 16 q .. 16 q + 15 of a step, in
+// x and W alike), and wave 0 adds their sums in order.
+template <typename E, int NJ, int MT, bool VEC>
+__global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(int n_tok, int n_adapters, int max_rank,
+                                                     const int *__restrict__ ranks,
+                                                     const int *__restrict__ order, const int *__restrict__ offsets,
+                                                     const int4 *__restrict__ tiles, int n_tiles, int split, int products,
+                                                     ShrinkArg a0, ShrinkArg a1) {
+    constexpr int NT = grad_terms<E>(), WAVES = SHRINK_WAVES;
+    __shared__ f32x4 part[WAVES - 1][MT][NJ][64];
+    const int id = blockIdx.x / split, spl = blockIdx.x - id * split;
+    const int tile = products > 1 ? id >> 1 : id;
+    const ShrinkArg &a = products > 1 && (id & 1) ? a1 : a0;
+    const Block blk = block_of<MT>(tiles, n_tiles, tile, offsets, n_tok, n_adapters);
+    if (blk.group < 0 || blk.begin >= blk.end) return;
+    const int rank = rank_of(ranks, blk.group, max_rank);
+    const int nj = (rank + 15) / 16;
+    if (nj == 0) return;
+    const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const unsigned short *xr[MT], *wr[NJ];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xr[m] = a.x + (int64_t)order[min(blk.begin + 16 * m + n, blk.end - 1)] * a.ldx;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        wr[j] = a.W + ((int64_t)blk.group * max_rank + min(16 * j + n, max_rank - 1)) * a.dim;
+    // steps of this wave: waves of all splits take contiguous runs of 64-wide steps
+    const int steps = (a.dim + 63) / 64, parts = split * WAVES, mine = spl * WAVES + wv;
+    const int lo = (int)((int64_t)steps * mine / parts), hi = (int)((int64_t)steps * (mine + 1) / parts);
+    f32x4 acc[MT][NJ];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[m][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // the rank tiles in use decide the loop, so that no load is conditional
+    if (NJ <= 4 || nj <= NJ / 2) {
+        if (NJ >= 4 && nj > 3)
+            shrink_steps<E, NJ < 4 ? NJ : 4, MT, VEC>(xr, wr, a.dim, lo, hi, q, acc);
+        else if (NJ >= 4 && nj > 2)
+            shrink_steps<E, NJ < 3 ? NJ : 3, MT, VEC>(xr, wr, a.dim, lo, hi, q, acc);
+        else if (NJ >= 2 && nj > 1)
+            shrink_steps<E, NJ < 2 ? NJ : 2, MT, VEC>(xr, wr, a.dim, lo, hi, q, acc);
+        else
+            shrink_steps<E, 1, MT, VEC>(xr, wr, a.dim, lo, hi, q, acc);
+    } else {
+        shrink_steps<E, NJ, MT, VEC>(xr, wr, a.dim, lo, hi, q, acc);
+    }
+    if (wv > 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) part[wv - 1][m][j][lane] = acc[m][j];
+    }
+    __syncthreads();
+    if (wv > 0) return;
+    float *h = a.h + (int64_t)spl * n_tok * (16 * NJ);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int row0 = blk.begin + 16 * m + 4 * q;    // D: row 4 q + i, column n
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+            for (int w = 0; w < WAVES - 1; ++w) acc[m][j] += part[w][m][j][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (16 * j + n >= rank || row0 + i >= blk.end) acc[m][j][i] = 0.0f;
+                top = fmaxf(top, fabsf(acc[m][j][i]));
+            }
+        }
+        if (!a.terms) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row0 + i < blk.end) h[(int64_t)(row0 + i) * (16 * NJ) + 16 * j + n] = acc[m][j][i];
+            continue;
+        }
+        int e = 0;
+        if (E::CODE == SPMV_F16) {
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            e = scale_exponent(top);
+            if (lane == 0 && blk.begin + 16 * m < blk.end) a.exps[blk.begin + 16 * m] = e;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const float v[4] = {acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]};
+            store_terms<E, NT, 16 * NJ>(a.terms, n_tok, row0, blk.end, 16 * j + n, v, e);
+        }
+    }
+}
+
+// Adds a split shrink's parts in order and writes the gradients' operands:
+// one wave per tile and product.
+template <typename E, int NJ>
+__global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, int max_rank, int split,
+                                                   const int *__restrict__ ranks,
+                                                   const int4 *__restrict__ tiles, ShrinkArg a0, ShrinkArg a1) {
+    constexpr int R = 16 * NJ, NT = grad_terms<E>();
+    const ShrinkArg &a = blockIdx.y ? a1 : a0;
+    const int4 tile = tiles[blockIdx.x];
+    if ((unsigned)tile.x >= (unsigned)n_adapters || tile.y >= tile.z) return;
+    if (rank_of(ranks, tile.x, max_rank) == 0) return;
+    const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
+    const int row0 = tile.y + 4 * q;
+    float v[NJ][4], top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = min(row0 + i, tile.z - 1);
+            float t = 0.0f;
+            for (int s = 0; s < split; ++s) t += a.h[((int64_t)s * n_tok + row) * R + 16 * j + n];
+            v[j][i] = row0 + i < tile.z ? t : 0.0f;
+            top = fmaxf(top, fabsf(v[j][i]));
+        }
+    int e = 0;
+    if (E::CODE == SPMV_F16) {
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        e = scale_exponent(top);
+        if (lane == 0) a.exps[tile.y] = e;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) store_terms<E, NT, R>(a.terms, n_tok, row0, tile.z, 16 * j + n, v[j], e);
+}
+
+// Eight neighbouring results of one token (past the end the row's last ones).
+template <typename Y>
+struct RowPiece {
+    typename Y::T v[8];
+};
 template <typename Y, bool VEC>
-__device__ __forceinline__ void load_row8(const typename Y::T *p, int c, int n, float (&v)[8]) {
+__device__ __forceinline__ void load_piece(RowPiece<Y> &r, const typename Y::T *p, int c, int n) {
     if (VEC) {
         constexpr int PER = 16 / (int)sizeof(typename Y::T);
 #pragma unroll
         for (int i = 0; i < 8; i += PER) {
-            const Vec<Y, PER> r = load_vec<Y, PER>(p + c + i);
+            const Vec<Y, PER> t = load_vec<Y, PER>(p + min(c, n - 8) + i);
 #pragma unroll
-            for (int k = 0; k < PER; ++k) v[i + k] = (float)r.v[k];
+            for (int k = 0; k < PER; ++k) r.v[i + k] = t.v[k];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < n ? (float)p[c + i] : 0.0f;
+        for (int i = 0; i < 8; ++i) r.v[i] = p[min(c + i, n - 1)];
     }
 }
 template <typename Y, bool VEC>
@@ -205,122 +391,165 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
     }
 }
 
-// One workgroup: tile blockIdx.x, columns 512 blockIdx.y ..; 128 per wave.
-template <typename E, typename Y, int NJ, int NT, bool VEC>
+// One workgroup: a block of tokens and 512 columns, 128 per wave; the columns
+// of a block are neighbours in the launch and together move whole rows of y.
+template <typename E, typename Y, int NJ, int NT, int MT, bool VEC>
 __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, int max_rank, int split,
                                                      const int *__restrict__ ranks,
                                                      const float *__restrict__ scale,
-                                                     const int *__restrict__ order,
-                                                     const int4 *__restrict__ tiles, const float *__restrict__ h,
-                                                     const unsigned short *__restrict__ B, int dim,
+                                                     const int *__restrict__ order, const int *__restrict__ offsets,
+                                                     const int4 *__restrict__ tiles, int n_tiles, const float *__restrict__ h,
+                                                     const unsigned short *__restrict__ B, int dim, int pieces,
                                                      const typename Y::T *y_in, int64_t ldyin,
                                                      typename Y::T *y, int64_t ldy) {
     typedef typename Frag<E>::V V;
     constexpr int R = 16 * NJ, LD = R + 8;
-    __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE][LD];
-    __shared__ float unscale[LR_TILE];
-    const int4 tile = tiles[blockIdx.x];
-    if (tile.y >= tile.z) return;
-    const bool adapted = (unsigned)tile.x < (unsigned)n_adapters;
-    const int rank = adapted ? rank_of(ranks, tile.x, max_rank) : 0;
+    __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE * MT][LD];
+    __shared__ float unscale[LR_TILE * MT];
+    const int id = blockIdx.x / pieces, piece = blockIdx.x - id * pieces;
+    const Block blk = block_of<MT>(tiles, n_tiles, id, offsets, n_tok, n_adapters);
+    if (blk.begin >= blk.end) return;
+    const int rank = blk.group >= 0 ? rank_of(ranks, blk.group, max_rank) : 0;
     if (rank == 0 && y_in == y) return;
     const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int c0 = blockIdx.y * (4 * LR_WAVE_COLS) + wv * LR_WAVE_COLS + 8 * n;
+    const int c0 = piece * (4 * LR_WAVE_COLS) + wv * LR_WAVE_COLS + 8 * n;
 
+    // y_in of the lane's rows is in flight over everything else
+    int64_t tok[MT][4];
+    RowPiece<Y> base[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tok[m][i] = order[min(blk.begin + 16 * m + 4 * q + i, blk.end - 1)];
+    if (y_in) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_piece<Y, VEC>(base[m][i], y_in + tok[m][i] * ldyin, c0, dim);
+    } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) base[m][i].v[c] = (typename Y::T)0.0f;
+    }
+    f32x4 acc[MT][8];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (rank > 0) {
+        const unsigned short *Br = B + (int64_t)blk.group * max_rank * dim;
+        u32x4 r[8];
+        auto load_b = [&](int jb) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = load8<VEC>(Br + (int64_t)min(jb + i, max_rank - 1) * dim, c0, dim);
+        };
+        load_b(NJ == 1 ? 8 * (q & 1) : 8 * q);
         // 16 lanes per token: the partial sums of h in order, the token's
         // largest |h|, and the scaled terms
-        const int t = threadIdx.x >> 4, l = threadIdx.x & 15;
-        const int64_t row = min(tile.y + t, tile.z - 1);
-        float v[NJ], m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) v[j] = 0.0f;
-        for (int s = 0; s < split; ++s)
+        for (int m = 0; m < MT; ++m) {
+            const int t = 16 * m + (threadIdx.x >> 4), l = threadIdx.x & 15;
+            const int64_t row = min(blk.begin + t, blk.end - 1);
+            float v[NJ], top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) v[j] += h[((int64_t)s * n_tok + row) * R + 16 * j + l];
+            for (int j = 0; j < NJ; ++j) v[j] = 0.0f;
+            const float *hr = h + row * R + l;
+#pragma unroll 4
+            for (int s = 0; s < split; ++s)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) m = fmaxf(m, fabsf(v[j]));
+                for (int j = 0; j < NJ; ++j)
+                    if (16 * j < rank) v[j] += hr[(int64_t)s * n_tok * R + 16 * j];
 #pragma unroll
-        for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-        const int e = E::CODE == SPMV_F16 ? scale_exponent(m) : 0;
+            for (int j = 0; j < NJ; ++j) top = fmaxf(top, fabsf(v[j]));
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            unsigned short terms[NT];
-            split_terms<E, NT>(ldexpf(v[j], e), terms);
+            for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            const int e = E::CODE == SPMV_F16 ? scale_exponent(top) : 0;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) hs[i][t][16 * j + l] = terms[i];
+            for (int j = 0; j < NJ; ++j) {
+                unsigned short terms[NT];
+                split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(v[j], e) : v[j], terms);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) hs[i][t][16 * j + l] = terms[i];
+            }
+            if (l == 0) unscale[t] = ldexpf(scale ? scale[blk.group] : 1.0f, -e);
         }
-        if (l == 0) unscale[t] = ldexpf(scale ? scale[tile.x] : 1.0f, -e);
         __syncthreads();
-    }
-    f32x4 acc[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (rank > 0) {
-        const unsigned short *Br = B + (int64_t)tile.x * max_rank * dim;
         if constexpr (NJ == 1) {
             // up to 16 ranks: the terms share the contraction, eight ranks
             // of one term per lane group and step
             constexpr int STEPS = (2 * NT + 3) / 4;
-            u32x4 r[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[i] = load8<VEC>(Br + (int64_t)min(8 * (q & 1) + i, max_rank - 1) * dim, c0, dim);
             const int live = rank - 8 * (q & 1);
+            if (rank < 16) {                                // rows past the rank may hold anything
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i >= live) r[i] = u32x4{0u, 0u, 0u, 0u};   // rows past the rank may hold anything
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) r[i][d] = i < live ? r[i][d] : 0u;
+            }
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int term = 2 * s + (q >> 1);
-                u32x4 a = u32x4{0u, 0u, 0u, 0u};
-                if (term < NT) a = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][n][8 * (q & 1)]);
+                u32x4 a[MT];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    acc[c] = Frag<E>::mma(__builtin_bit_cast(V, a), __builtin_bit_cast(V, column_of(r, c)), acc[c]);
-            }
-        } else {
-            for (int j0 = 0; j0 < rank; j0 += 32) {
-                const int jb = j0 + 8 * q;
-                u32x4 r[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    r[i] = load8<VEC>(Br + (int64_t)min(jb + i, max_rank - 1) * dim, c0, dim);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (jb + i >= rank) r[i] = u32x4{0u, 0u, 0u, 0u};
-                V a[NT];
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    a[i] = __builtin_bit_cast(V, *reinterpret_cast<const u32x4 *>(&hs[i][n][jb]));
+                for (int m = 0; m < MT; ++m) {
+                    a[m] = u32x4{0u, 0u, 0u, 0u};
+                    if (term < NT)
+                        a[m] = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][16 * m + n][8 * (q & 1)]);
+                }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const V b = __builtin_bit_cast(V, column_of(r, c));
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) acc[c] = Frag<E>::mma(a[i], b, acc[c]);
+                    for (int m = 0; m < MT; ++m) acc[m][c] = Frag<E>::mma(__builtin_bit_cast(V, a[m]), b, acc[m][c]);
+                }
+            }
+        } else {
+            for (int j0 = 0; j0 < rank; j0 += 32) {
+                const int jb = j0 + 8 * q;
+                if (j0 > 0) load_b(jb);
+                if (j0 + 32 > rank) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) r[i][d] = jb + i < rank ? r[i][d] : 0u;
+                }
+                V a[MT][NT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        a[m][i] = __builtin_bit_cast(V, *reinterpret_cast<const u32x4 *>(&hs[i][16 * m + n][jb]));
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const V b = __builtin_bit_cast(V, column_of(r, c));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) acc[m][c] = Frag<E>::mma(a[m][i], b, acc[m][c]);
                 }
             }
         }
     }
     if (c0 >= dim) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = tile.y + 4 * q + i;
-        if (row >= tile.z) break;
-        const int64_t tok = order[row];
-        float v[8];
-        if (y_in)
-            load_row8<Y, VEC>(y_in + tok * ldyin, c0, dim, v);
-        else
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = 0.0f;
-        const float f = rank > 0 ? unscale[4 * q + i] : 0.0f;
-        if (rank > 0) {
+        for (int i = 0; i < 4; ++i) {
+            const int t = 16 * m + 4 * q + i;
+            if (blk.begin + t >= blk.end) break;
+            float v[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = fmaf(f, acc[c][i], v[c]);
+            for (int c = 0; c < 8; ++c) v[c] = (float)base[m][i].v[c];
+            if (rank > 0) {
+                const float f = unscale[t];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] = fmaf(f, acc[m][c][i], v[c]);
+            }
+            store_row8<Y, VEC>(y + tok[m][i] * ldy, c0, dim, v);
         }
-        store_row8<Y, VEC>(y + tok * ldy, c0, dim, v);
     }
 }
 
@@ -328,21 +557,25 @@ struct OuterArg {
     const unsigned short *x;   // x or dy
     int64_t ldx;
     int dim, blocks;           // columns, and their 128-column blocks
-    const float *h;            // [split][n_tok][16 NJ]
+    const unsigned short *terms;
+    const int *exps;
     float *out;                // [n_adapters, max_rank, dim]
 };
 
 // One workgroup: 128 columns of adapter blockIdx.y's gradient; blockIdx.x
 // counts the column blocks of the first product, then of the second, and
 // blockIdx.z blocks of NJ rank tiles out of the R / 16 of h.  The 8 waves take
-// turns over 32-token steps and their sums are added in order.
-template <typename E, int NJ, int R, int NT, bool VEC>
-__global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank, int split,
+// turns over 32-token steps (two plan tiles), the next step's rows loading
+// over the current one's products, and their sums are added in order.
+template <typename E, int NJ, int R, bool VEC>
+__global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
                                                     const int *__restrict__ ranks,
                                                     const float *__restrict__ scale,
                                                     const int *__restrict__ order,
                                                     const int *__restrict__ offsets, OuterArg a0, OuterArg a1) {
     typedef typename Frag<E>::V V;
+    constexpr int NT = grad_terms<E>();
+    constexpr bool F = E::CODE == SPMV_F16;
     __shared__ f32x4 sum[8][64];
     const int r0 = blockIdx.z * 16 * NJ;   // first rank of this workgroup
     const bool second = (int)blockIdx.x >= a0.blocks;
@@ -352,55 +585,64 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank, int
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int c0 = (blockIdx.x - (second ? a0.blocks : 0)) * LR_WAVE_COLS + 8 * n;
     const int rank = rank_of(ranks, ad, max_rank);
-    const int t0 = min(max(offsets[ad], 0), n_tok), t1 = min(max(offsets[ad + 1], t0), n_tok);
+    const int t0 = min(max(offsets[ad], 0), n_tok), t1 = rank > r0 ? min(max(offsets[ad + 1], t0), n_tok) : t0;
     f32x4 acc[NJ][8];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[j][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int t = t0 + 32 * wv; t < t1; t += 32 * 8) {
-        u32x4 r[8];
+    int tok[8];
+    auto load_tok = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t tok = order[min(t + 8 * q + i, t1 - 1)];
-            r[i] = load8<VEC>(a.x + tok * a.ldx, c0, a.dim);
-        }
-        float g[NJ][8], m = 0.0f;
+        for (int i = 0; i < 8; ++i) tok[i] = order[min(t + 8 * q + i, t1 - 1)];
+    };
+    auto load_rows = [&](u32x4(&r)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = load8<VEC>(a.x + (int64_t)tok[i] * a.ldx, c0, a.dim);
+    };
+    auto step = [&](int t, u32x4(&r)[8], u32x4(&next)[8]) {
+        // the next step's rows, and the tokens of the one after (past the end
+        // the last ones again)
+        load_rows(next);
+        load_tok(t + 512);
+        __builtin_amdgcn_sched_barrier(0);
+        const int at = min(t + 8 * q, t1 - 1), valid = t1 - (t + 8 * q);   // tokens of this lane
+        u32x4 op[NJ][NT];
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t row = min(t + 8 * q + i, t1 - 1);
-                float v = 0.0f;
-                for (int s = 0; s < split; ++s) v += a.h[((int64_t)s * n_tok + row) * R + r0 + 16 * j + n];
-                g[j][i] = t + 8 * q + i < t1 && r0 + 16 * j + n < rank ? v : 0.0f;
-                m = fmaxf(m, fabsf(g[j][i]));
-            }
-        int e = 0;
-        if (E::CODE == SPMV_F16) {
+            for (int k = 0; k < NT; ++k)
+                __builtin_memcpy(&op[j][k], a.terms + ((int64_t)k * R + r0 + 16 * j + n) * (n_tok + LR_PAD) + at, 16);
+        float back = 1.0f;
+        if (F) {
+            // the two tiles' terms on the scale of the larger: its exponent is the smaller
+            const int e = a.exps[min(t + 16 * (q >> 1), t0 + (t1 - 1 - t0) / 16 * 16)];
+            const int both = min(e, __shfl_xor(e, 32));
+            const _Float16 f = (_Float16)ldexpf(1.0f, max(both - e, -40));   // 0 below 2^-25
+            back = ldexpf(1.0f, -both);
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-            e = scale_exponent(m);
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int k = 0; k < NT; ++k) op[j][k] = __builtin_bit_cast(u32x4, __builtin_bit_cast(h8, op[j][k]) * f);
+        }
+        if (t + 32 > t1) {                 // uniform: tokens past the end count nothing
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        op[j][k][d] = valid > 2 * d + 1 ? op[j][k][d] : valid > 2 * d ? op[j][k][d] & 0xFFFFu : 0u;
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            u32x4 op[NT];
+        for (int c = 0; c < 8; ++c) {
+            const V b = __builtin_bit_cast(V, column_of(r, c));
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                unsigned short lo[NT], hi[NT];
-                split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(g[j][i], e) : g[j][i], lo);
-                split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(g[j][i + 1], e) : g[j][i + 1], hi);
+            for (int j = 0; j < NJ; ++j) {
+                f32x4 d = F ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j][c];
 #pragma unroll
-                for (int k = 0; k < NT; ++k) op[k][i / 2] = (unsigned int)lo[k] | ((unsigned int)hi[k] << 16);
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const V b = __builtin_bit_cast(V, column_of(r, c));
-                f32x4 d = E::CODE == SPMV_F16 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j][c];
-#pragma unroll
-                for (int k = 0; k < NT; ++k) d = Frag<E>::mma(__builtin_bit_cast(V, op[k]), b, d);
-                if (E::CODE == SPMV_F16) {
-                    const float back = ldexpf(1.0f, -e);
+                for (int k = 0; k < NT; ++k) d = Frag<E>::mma(__builtin_bit_cast(V, op[j][k]), b, d);
+                if (F) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][c][i] = fmaf(back, d[i], acc[j][c][i]);
                 } else {
@@ -408,31 +650,41 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank, int
                 }
             }
         }
+    };
+    int t = t0 + 32 * wv;
+    if (t < t1) {
+        u32x4 ra[8], rb[8];
+        load_tok(t);
+        load_rows(ra);
+        load_tok(t + 256);
+        for (; t < t1; t += 512) {
+            step(t, ra, rb);
+            if (t + 256 < t1) step(t + 256, rb, ra);
+        }
     }
     // waves add their sums one after the other, so the order is fixed
     const float f = scale ? scale[ad] : 1.0f;
+#pragma unroll
     for (int j = 0; j < NJ; ++j) {
+        for (int w = 0; w < 8; ++w) {
+            if (wv == w) {
 #pragma unroll
-        for (int jj = 0; jj < NJ; ++jj) {
-            if (jj != j) continue;
-            for (int w = 0; w < 8; ++w) {
-                if (wv == w) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) sum[c][lane] = w == 0 ? acc[jj][c] : sum[c][lane] + acc[jj][c];
-                }
-                __syncthreads();
+                for (int c = 0; c < 8; ++c) sum[c][lane] = w == 0 ? acc[j][c] : sum[c][lane] + acc[j][c];
             }
+            __syncthreads();
         }
-        if (wv == 0 && c0 < a.dim) {
+        // all 8 waves write: wave w the rows 4 q + (w & 3) of half the lanes' groups
+        const int i = wv & 3;
+        const int row = r0 + 16 * j + 4 * q + i;
+        if ((q & 1) == (wv >> 2) && row < max_rank && c0 < a.dim) {
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = r0 + 16 * j + 4 * q + i;
-                if (row >= max_rank) break;
-                float v[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] = row < rank ? f * sum[c][lane][i] : 0.0f;
-                store_row8<F32, VEC>(a.out + ((int64_t)ad * max_rank + row) * a.dim, c0, a.dim, v);
+            for (int c = 0; c < 8; ++c) {
+                const f32x4 s4 = sum[c][lane];
+                const float s1 = i == 0 ? s4[0] : i == 1 ? s4[1] : i == 2 ? s4[2] : s4[3];
+                v[c] = row < rank ? f * s1 : 0.0f;
             }
+            store_row8<F32, VEC>(a.out + ((int64_t)ad * max_rank + row) * a.dim, c0, a.dim, v);
         }
         __syncthreads();
     }
@@ -443,20 +695,31 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank, int
 // ---------------------------------------------------------------------------
 int rank_tiles(int max_rank) { return max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : max_rank <= 64 ? 4 : 8; }
 
-// Workgroups that share a tile's contraction: enough for 2048 workgroups in
-// all, at most LR_MAX_SPLIT (the workspace's bound, which knows n_tok alone).
+// Blocks of 4 tiles where adapters have 64 tokens or more on average: an
+// operand of A or B then serves 4 tiles.
+bool wide_blocks(int64_t n_tok, int64_t n_adapters, int max_rank) { return max_rank <= 32 && n_tok >= 64 * n_adapters && n_tok >= 512; }
+
+// Workgroups that share a block's contraction.  Whoever reads h adds the parts,
+// once per 512 columns of the result, so there are only as many as it takes to
+// have LR_FILL workgroups, each wave with at least two 64-wide steps.  The
+// workspace holds the most that n_tok alone allows.
+constexpr int LR_FILL = 256;
 int max_split(int64_t n_tok) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(LR_MAX_SPLIT, 2048 / std::max<int64_t>(1, ceil_div(n_tok, LR_TILE))));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(LR_MAX_SPLIT, LR_FILL / std::max<int64_t>(1, ceil_div(n_tok, LR_TILE))));
 }
-// ... and so that each of a workgroup's 4 waves keeps two 64-wide steps.
-int split_of(int64_t n_tok, int64_t dim) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(max_split(n_tok), dim / 512));
+int split_of(int64_t n_tok, int64_t blocks, int64_t dim) {
+    const int64_t fill = std::min<int64_t>(max_split(n_tok), ceil_div(LR_FILL, std::max<int64_t>(1, blocks)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(fill, dim / (128 * SHRINK_WAVES)));
 }
 
 size_t h_bytes(int64_t n_tok, int max_rank) {
     return ((size_t)max_split(n_tok) * (size_t)n_tok * (size_t)(16 * rank_tiles(max_rank)) * 4 + 255) & ~size_t(255);
 }
-
+// terms of one product (three at most), and the tiles' exponents behind them
+size_t terms_bytes(int64_t n_tok, int max_rank) {
+    return (((size_t)3 * (size_t)(16 * rank_tiles(max_rank)) * (size_t)(n_tok + LR_PAD) * 2 + 255) & ~size_t(255)) +
+           (((size_t)n_tok + 63) & ~size_t(63)) * 4;
+}
 spmv_status check_common(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adapters, int32_t max_rank,
                          int32_t dtype, const void *A, const void *B, const int32_t *order, const int32_t *offsets,
                          const int32_t *tiles, int32_t n_tiles, const void *workspace, size_t workspace_bytes) {
@@ -482,6 +745,8 @@ spmv_status check_common(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_a
     if (!aligned16(workspace)) return fail(SPMV_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
     return SPMV_OK;
 }
+
+constexpr int shrink_tiles(int nj) { return nj == 8 ? 2 : 4; }   // the waves' sums in LDS: 3 KB per tile and 16 ranks
 
 bool rows16(const void *p, int64_t ld, int64_t dim, int64_t per = 8) {
     return aligned16(p) && ld % per == 0 && dim % 8 == 0;
@@ -514,7 +779,7 @@ extern "C" spmv_status lora_workspace_size(int32_t n_tok, int32_t max_rank, size
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
     if (n_tok < 0 || max_rank < 1) return fail(SPMV_ERR_INVALID_VALUE, "n_tok must be >= 0 and max_rank positive");
     if (max_rank > LR_MAX_RANK) return fail(SPMV_ERR_UNSUPPORTED, "ranks above %d are not supported", LR_MAX_RANK);
-    *bytes = 2 * h_bytes(n_tok, max_rank);
+    *bytes = 2 * (h_bytes(n_tok, max_rank) + terms_bytes(n_tok, max_rank));
     return SPMV_OK;
 }
 
@@ -535,15 +800,23 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
     if (n_tok == 0) return SPMV_OK;
     if (!x || !y) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
     hipStream_t s = as_stream(stream);
-    const int split = split_of(n_tok, n_in);
+    const bool wide = wide_blocks(n_tok, n_adapters, max_rank);
+    const int split = split_of(n_tok, n_tiles / (wide ? 4 : 1), n_in);
     const int4 *tl = reinterpret_cast<const int4 *>(tiles);
     const ShrinkArg sa = {static_cast<const unsigned short *>(x), static_cast<const unsigned short *>(A), ldx, n_in,
-                          static_cast<float *>(workspace)};
+                          static_cast<float *>(workspace), nullptr, nullptr};
     st = by_half(dtype, [&](auto e) {
         return by_rank(max_rank, [&](auto nj) {
             return by_bool(rows16(x, ldx, n_in) && aligned16(A), [&](auto vec) {
-                k_lora_shrink<decltype(e), decltype(nj)::value, decltype(vec)::value>
-                    <<<dim3(n_tiles, split, 1), 256, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, tl, sa, sa);
+                constexpr int NJ = decltype(nj)::value;
+                constexpr bool VEC = decltype(vec)::value;
+                const int grid = (n_tiles + 3) / 4 * 4 * split;
+                if (wide)
+                    k_lora_shrink<decltype(e), NJ, shrink_tiles(NJ), VEC>
+                        <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 1, sa, sa);
+                else
+                    k_lora_shrink<decltype(e), NJ, 1, VEC>
+                        <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 1, sa, sa);
                 SPMV_LAUNCHED("k_lora_shrink");
                 return SPMV_OK;
             });
@@ -552,7 +825,9 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
     if (st != SPMV_OK) return st;
     const int64_t yper = 16 / (int64_t)dtype_size(y_dtype);
     const bool vec_y = rows16(y, ldy, n_out, yper) && (!y_in || rows16(y_in, ldyin, n_out, yper)) && aligned16(B);
-    const dim3 grid(n_tiles, (unsigned)ceil_div(n_out, 4 * LR_WAVE_COLS));
+    const int64_t pieces = ceil_div(n_out, 4 * LR_WAVE_COLS);
+    if (n_tiles * pieces > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "the launch does not fit int32");
+    const int grid = (int)(n_tiles * pieces);
     return by_half(dtype, [&](auto e) {
         typedef decltype(e) E;
         return by_rank(max_rank, [&](auto nj) {
@@ -561,10 +836,14 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
                 constexpr bool VEC = decltype(vec)::value;
                 auto go = [&](auto yt, auto nt) {
                     typedef decltype(yt) Y;
-                    k_lora_expand<E, Y, NJ, decltype(nt)::value, VEC><<<grid, 256, 0, s>>>(
-                        n_tok, n_adapters, max_rank, split, ranks, scale, order, tl, static_cast<const float *>(workspace),
-                        static_cast<const unsigned short *>(B), n_out, static_cast<const typename Y::T *>(y_in), ldyin,
-                        static_cast<typename Y::T *>(y), ldy);
+                    auto run = [&](auto mt) {
+                        k_lora_expand<E, Y, NJ, decltype(nt)::value, decltype(mt)::value, VEC><<<grid, 256, 0, s>>>(
+                            n_tok, n_adapters, max_rank, split, ranks, scale, order, offsets, tl, n_tiles,
+                            static_cast<const float *>(workspace), static_cast<const unsigned short *>(B), n_out,
+                            (int)pieces,
+                            static_cast<const typename Y::T *>(y_in), ldyin, static_cast<typename Y::T *>(y), ldy);
+                    };
+                    run(std::integral_constant<int, 1>{});
                 };
                 if (y_dtype == SPMV_F32)
                     go(F32{}, std::integral_constant<int, E::CODE == SPMV_BF16 ? 3 : 2>{});
@@ -588,16 +867,25 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
     if (ldx < n_in || lddy < n_out) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
     if (!dA || !dB || (n_tok > 0 && (!x || !dy))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
     hipStream_t s = as_stream(stream);
-    const int split = split_of(n_tok, std::min(n_in, n_out));
-    float *h = static_cast<float *>(workspace);
-    float *g = reinterpret_cast<float *>(static_cast<char *>(workspace) + h_bytes(n_tok, max_rank));
+    const bool wide = wide_blocks(n_tok, n_adapters, max_rank);
+    const int split = split_of(n_tok, 2 * n_tiles / (wide ? 4 : 1), std::min(n_in, n_out));
+    const size_t hb = h_bytes(n_tok, max_rank), tb = terms_bytes(n_tok, max_rank);
+    char *w = static_cast<char *>(workspace);
     const auto *xs = static_cast<const unsigned short *>(x), *dys = static_cast<const unsigned short *>(dy);
     const bool vec = rows16(x, ldx, n_in) && rows16(dy, lddy, n_out) && aligned16(A) && aligned16(B) && aligned16(dA) &&
                      aligned16(dB);
-    const ShrinkArg hx = {xs, static_cast<const unsigned short *>(A), ldx, n_in, h};
-    const ShrinkArg gy = {dys, static_cast<const unsigned short *>(B), lddy, n_out, g};
-    const OuterArg oa = {xs, ldx, n_in, (int)ceil_div(n_in, LR_WAVE_COLS), g, dA};
-    const OuterArg ob = {dys, lddy, n_out, (int)ceil_div(n_out, LR_WAVE_COLS), h, dB};
+    const int4 *tl = reinterpret_cast<const int4 *>(tiles);
+    unsigned short *terms[2];
+    int *exps[2];
+    for (int i = 0; i < 2; ++i) {
+        terms[i] = reinterpret_cast<unsigned short *>(w + 2 * hb + i * tb);
+        exps[i] = reinterpret_cast<int *>(w + 2 * hb + (i + 1) * tb) - ((n_tok + 63) & ~63);
+    }
+    ShrinkArg hx = {xs, static_cast<const unsigned short *>(A), ldx, n_in, reinterpret_cast<float *>(w), terms[0], exps[0]};
+    ShrinkArg gy = {dys, static_cast<const unsigned short *>(B), lddy, n_out, reinterpret_cast<float *>(w + hb), terms[1],
+                    exps[1]};
+    const OuterArg oa = {xs, ldx, n_in, (int)ceil_div(n_in, LR_WAVE_COLS), terms[1], exps[1], dA};
+    const OuterArg ob = {dys, lddy, n_out, (int)ceil_div(n_out, LR_WAVE_COLS), terms[0], exps[0], dB};
     return by_half(dtype, [&](auto e) {
         typedef decltype(e) E;
         return by_rank(max_rank, [&](auto nj) {
@@ -605,14 +893,31 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
                 constexpr int NJ = decltype(nj)::value;
                 constexpr bool VEC = decltype(v)::value;
                 if (n_tok > 0) {
-                    k_lora_shrink<E, NJ, VEC><<<dim3(n_tiles, split, 2), 256, 0, s>>>(
-                        n_tok, n_adapters, max_rank, ranks, order, reinterpret_cast<const int4 *>(tiles), hx, gy);
+                    ShrinkArg s0 = hx, s1 = gy;
+                    if (split > 1) s0.terms = s1.terms = nullptr;
+                    const int grid = (n_tiles + 3) / 4 * 4 * split * 2;
+                    if (wide)
+                        k_lora_shrink<E, NJ, shrink_tiles(NJ), VEC>
+                            <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 2, s0, s1);
+                    else
+                        k_lora_shrink<E, NJ, 1, VEC>
+                            <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 2, s0, s1);
                     SPMV_LAUNCHED("k_lora_shrink");
+                    if (split > 1) {
+                        k_lora_terms<E, NJ><<<dim3(n_tiles, 2), 64, 0, s>>>(n_tok, n_adapters, max_rank, split, ranks, tl, hx,
+                                                                           gy);
+                        SPMV_LAUNCHED("k_lora_terms");
+                    }
                 }
-                constexpr int JB = NJ < 4 ? NJ : 4;
-                k_lora_outer<E, JB, 16 * NJ, E::CODE == SPMV_BF16 ? 3 : 2, VEC>
-                    <<<dim3(oa.blocks + ob.blocks, n_adapters, NJ / JB), 512, 0, s>>>(n_tok, max_rank, split, ranks, scale, order,
-                                                                             offsets, oa, ob);
+                // few column blocks (one adapter): fewer rank tiles each, x read again from the caches
+                constexpr int JB = NJ < 2 ? NJ : 2;
+                const int64_t blocks = (int64_t)(oa.blocks + ob.blocks) * n_adapters;
+                if (blocks < 192)
+                    k_lora_outer<E, 1, 16 * NJ, VEC><<<dim3(oa.blocks + ob.blocks, n_adapters, NJ), 512, 0, s>>>(
+                        n_tok, max_rank, ranks, scale, order, offsets, oa, ob);
+                else
+                    k_lora_outer<E, JB, 16 * NJ, VEC><<<dim3(oa.blocks + ob.blocks, n_adapters, NJ / JB), 512, 0, s>>>(
+                        n_tok, max_rank, ranks, scale, order, offsets, oa, ob);
                 SPMV_LAUNCHED("k_lora_outer");
                 return SPMV_OK;
             });

@@ -96,8 +96,9 @@ def lora_grad(keys, ranks, scale, A, B, x, dy):
             W, u, v = W[a, :r], u[at], v[at]
             g = u @ W.t()
             dg = (u.abs() @ W.abs().t()) * ((u.shape[1] / 32 + 72) * ADD)
-            # two 16-bit terms: 22 bits, and 2^-25 of the largest of 32 tokens
-            dg = dg + g.abs() * 2.0 ** -22 + g.abs().max() * 2.0 ** -25
+            # two 16-bit terms: 22 bits; brought to the scale of the largest of 32
+            # tokens, each term is rounded to a multiple of 2^-24 of it, or dropped below 2^-24
+            dg = dg + g.abs() * 2.0 ** -22 + g.abs().max() * 2.0 ** -23
             s = abs(scale[a])
             out[2 * k][a, :r] = scale[a] * (g.t() @ v)
             mag = (g.abs() + dg).t() @ v.abs()

@@ -62,7 +62,8 @@ def _bits(dt, ydt):
 
 SHAPES = [(1, 64, 64, 1, 1), (1, 4096, 512, 4, 16), (3, 8, 8, 2, 8), (17, 1000, 1504, 3, 8), (40, 136, 648, 5, 24),
           (61, 2048, 1024, 40, 64), (200, 33, 77, 3, 5), (150, 515, 130, 2, 33), (70, 256, 264, 2, 128),
-          (33, 264, 1032, 9, 100), (16, 64, 1, 2, 4), (31, 1, 64, 2, 4)]
+          (33, 264, 1032, 9, 100), (16, 64, 1, 2, 4), (31, 1, 64, 2, 4), (700, 1032, 520, 4, 16), (600, 200, 1048, 2, 64),
+          (520, 129, 130, 1, 100), (513, 4096, 64, 8, 24)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -162,7 +163,8 @@ def test_bad_token_stays_alone():
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 64, 64, 1, 1), (300, 1000, 1504, 3, 8), (500, 136, 520, 4, 24), (77, 33, 70, 2, 5),
-                                   (260, 512, 128, 1, 64), (90, 128, 264, 3, 128), (600, 64, 64, 20, 16)])
+                                   (260, 512, 128, 1, 64), (90, 128, 264, 3, 128), (600, 64, 64, 20, 16),
+                                   (2100, 1040, 1096, 2, 32), (1500, 72, 64, 3, 48), (700, 2560, 2056, 1, 16)])
 def test_grad(shape, dt):
     T, K, N, n, r = shape
     s = _make(T, K, N, n, r, dt, seed=T)
@@ -185,6 +187,24 @@ def test_grad(shape, dt):
     _apply(s, dy, None, dx, A=s["B"], B=s["A"])
     ref, bound = R.lora(s["keys"], s["ranks"], sc, B, A, dy, None, _bits(dt, dx.dtype), dx.dtype)
     R.check(dx, ref, bound, f"dx {shape} {dt}")
+
+
+def test_grad_of_tiny_and_large_tokens_together():
+    """fp16: tokens whose rank vectors differ by 2^40 share one adapter."""
+    T, K, N, r = 96, 256, 128, 8
+    s = _make(T, K, N, 1, r, "f16", seed=21, ranks="full", keys="one")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dy = torch.randn(T, N, device="cuda", generator=g)
+    dy[::2] *= 2.0 ** -20
+    dy[32:48] *= 2.0 ** -14
+    dy[48:64] *= 2.0 ** 8
+    dy = dy.half()
+    dA, dB = torch.empty(1, r, K, device="cuda"), torch.empty(1, r, N, device="cuda")
+    p = s["plan"]
+    S.lora_grad(s["ranks_t"], s["scale"], s["A"], s["B"], p.order, p.offsets, p.tiles, s["x"], dy, dA, dB, s["ws"])
+    ra, ba, rb, bb = R.lora_grad(s["keys"], [r], R.f64(s["scale"]).tolist(), s["A"], s["B"], s["x"], dy)
+    R.check(dA, ra, ba, "dA")
+    R.check(dB, rb, bb, "dB")
 
 
 def test_grad_without_tokens():
