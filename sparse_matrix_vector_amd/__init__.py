@@ -41,6 +41,8 @@ __all__ = [
     "route_combine", "route_combine_grad", "RoutePlan", "lora_workspace_size", "lora_apply", "lora_grad",
 ]
 
+_TOKENS = frozenset(__all__[__all__.index("macko_spmm_plan_size"):])
+
 STATUS = {0: "SPMV_OK", 1: "SPMV_ERR_INVALID_VALUE", 2: "SPMV_ERR_INVALID_MATRIX",
           3: "SPMV_ERR_UNSORTED", 4: "SPMV_ERR_OVERFLOW", 5: "SPMV_ERR_UNSUPPORTED", 6: "SPMV_ERR_HIP"}
 CSR_AUTO, CSR_SCALAR, CSR_VECTOR, CSR_BINNED = 0, 1, 2, 3
@@ -102,15 +104,6 @@ def _stream(stream, like=None):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _stream_scope(stream, device):
-    """The context whose current stream is `stream` (None: as it is)."""
-    import contextlib
-    import torch
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 
 def _i32_dtype():
@@ -573,319 +566,6 @@ def dense_gemv_f16(m, n, W, x_f16, alpha, beta, y, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# Operators of many tokens: shared argument checks
-# ---------------------------------------------------------------------------
-def _dtype_code(t, name):
-    """spmv_dtype of a tensor."""
-    import torch
-    code = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
-    return code
-
-
-def _vec(t, dtype, name, n, device, allow_none=False):
-    """Device pointer of a contiguous tensor of at least n elements on `device`."""
-    p = _dev(t, dtype, name, allow_none)
-    if p is not None:
-        if t.numel() < n:
-            raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return p
-
-
-def _rows(t, dtype, name, n, width, device):
-    """(device pointer, row stride) of an [n, width] tensor whose rows are contiguous."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
-        raise ValueError(f"{name} must have shape ({n}, {width}), got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    ld = t.stride(0)
-    if width > 1 and t.stride(1) != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    if n <= 1:
-        ld = width
-    elif ld < width:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return t.data_ptr(), ld
-
-
-def _call_on(device, name, *args):
-    """The call with `device` current (kernels and streams belong to one)."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        _call(name, *args)
-    else:
-        with torch.cuda.device(device):
-            _call(name, *args)
-
-
-def _ws(workspace, device):
-    """(pointer, bytes) of a workspace tensor (None: NULL, 0)."""
-    if workspace is None:
-        return None, 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-# ---------------------------------------------------------------------------
-# MACKO for many tokens
-# ---------------------------------------------------------------------------
-def macko_spmm_plan_size(n_rows, n_cols) -> int:
-    out = ctypes.c_size_t()
-    _call("macko_spmm_plan_size", int(n_rows), int(n_cols), ctypes.byref(out))
-    return out.value
-
-
-def macko_spmm_plan(n_rows, n_cols, mrow_ptr, codes, plan, stream=None, bdelta=4):
-    """Fills `plan` (a uint8 CUDA tensor of macko_spmm_plan_size bytes) for
-    the n_rows rows of all groups together."""
-    d = mrow_ptr.device
-    pp, pb = _ws(plan, d)
-    _call_on(d, "macko_spmm_plan", int(n_rows), int(n_cols), int(bdelta),
-             _vec(mrow_ptr, _i32_dtype(), "mrow_ptr", n_rows + 1, d), _vec(codes, _u32_dtype(), "codes", 0, d), pp, pb,
-             _stream(stream, mrow_ptr))
-    return plan
-
-
-def macko_spmm_workspace_size(n_groups, n_rows, n_cols, n_tok) -> int:
-    out = ctypes.c_size_t()
-    _call("macko_spmm_workspace_size", int(n_groups), int(n_rows), int(n_cols), int(n_tok), ctypes.byref(out))
-    return out.value
-
-
-def _spmm_args(n_rows, n_cols, mrow_ptr, codes, plan, x, y, workspace, tok_offsets):
-    import torch
-    d, n = y.device, int(x.shape[0])
-    n_groups = 1 if tok_offsets is None else tok_offsets.numel() - 1
-    xp, ldx = _rows(x, _u16_dtype(), "x", n, n_cols, d)
-    yp, ldy = _rows(y, (torch.float16, torch.float32), "y", n, n_rows, d)
-    pp, pb = _ws(plan, d)
-    if pb < macko_spmm_plan_size(n_groups * n_rows, n_cols):
-        raise ValueError("plan is smaller than macko_spmm_plan_size")
-    wp, wb = _ws(workspace, d)
-    return (d, n_groups, _vec(mrow_ptr, _i32_dtype(), "mrow_ptr", n_groups * n_rows + 1, d),
-            _vec(codes, _u32_dtype(), "codes", 0, d), pp,
-            _vec(tok_offsets, _i32_dtype(), "tok_offsets", 1, d, allow_none=True), n, xp, ldx, yp,
-            F16 if y.dtype == torch.float16 else F32, ldy, wp, wb)
-
-
-def macko_spmm(n_rows, n_cols, mrow_ptr, codes, mvals, plan, alpha, x, beta, y, workspace=None, tok_offsets=None,
-               stream=None, bdelta=4):
-    """y = alpha * x W^T + beta * y for x [tokens, n_cols] fp16 and y [tokens,
-    n_rows] fp32 or fp16; tok_offsets (int32 [groups + 1]): one stacked weight
-    per group of tokens."""
-    d, g, mp, cp, pp, op, n, xp, ldx, yp, yd, ldy, wp, wb = _spmm_args(n_rows, n_cols, mrow_ptr, codes, plan, x, y,
-                                                                       workspace, tok_offsets)
-    _call_on(d, "macko_spmm", g, int(n_rows), int(n_cols), int(bdelta), mp, cp, _vec(mvals, _u16_dtype(), "mvals", 0, d),
-             pp, op, n, float(alpha), xp, ldx, float(beta), yp, yd, ldy, wp, wb, _stream(stream, y))
-    return y
-
-
-def macko_spmm_i8(n_rows, n_cols, mrow_ptr, codes, q, row_scale, plan, alpha, x, beta, y, workspace=None,
-                  tok_offsets=None, stream=None, bdelta=4):
-    import torch
-    d, g, mp, cp, pp, op, n, xp, ldx, yp, yd, ldy, wp, wb = _spmm_args(n_rows, n_cols, mrow_ptr, codes, plan, x, y,
-                                                                       workspace, tok_offsets)
-    _call_on(d, "macko_spmm_i8", g, int(n_rows), int(n_cols), int(bdelta), mp, cp,
-             _vec(q, (torch.int8, torch.uint8), "q", 0, d), _vec(row_scale, _f32_dtype(), "row_scale", g * n_rows, d), pp,
-             op, n, float(alpha), xp, ldx, float(beta), yp, yd, ldy, wp, wb, _stream(stream, y))
-    return y
-
-
-class MackoMatrix:
-    """One MACKO weight (or n_groups stacked ones) with its many-token plan.
-    row_scale: the int8 values' scales, or None for fp16 values."""
-
-    def __init__(self, n_rows, n_cols, mrow_ptr, codes, vals, row_scale=None, n_groups=1, bdelta=4, stream=None):
-        import torch
-        self.n_rows, self.n_cols, self.n_groups, self.bdelta = int(n_rows), int(n_cols), int(n_groups), int(bdelta)
-        self.mrow_ptr, self.codes, self.vals, self.row_scale = mrow_ptr, codes, vals, row_scale
-        if mrow_ptr.numel() != self.n_groups * self.n_rows + 1:
-            raise ValueError(f"mrow_ptr must have {self.n_groups * self.n_rows + 1} elements")
-        self.plan = torch.empty(max(macko_spmm_plan_size(self.n_groups * self.n_rows, n_cols), 4), dtype=torch.uint8,
-                                device=mrow_ptr.device)
-        macko_spmm_plan(self.n_groups * self.n_rows, n_cols, mrow_ptr, codes, self.plan, stream, bdelta)
-
-    def workspace(self, n_tok):
-        """A workspace for calls of n_tok tokens."""
-        import torch
-        return torch.empty(macko_spmm_workspace_size(self.n_groups, self.n_rows, self.n_cols, n_tok), dtype=torch.uint8,
-                           device=self.plan.device)
-
-    def apply(self, x, y, alpha=1.0, beta=0.0, tok_offsets=None, workspace=None, stream=None):
-        if (self.n_groups > 1 or tok_offsets is not None) and (
-                tok_offsets is None or tok_offsets.numel() != self.n_groups + 1):
-            raise ValueError(f"tok_offsets must have {self.n_groups + 1} elements")
-        if workspace is None and x.dim() == 2:
-            with _stream_scope(stream, self.plan.device):      # torch's allocator orders it with that stream's work
-                workspace = self.workspace(x.shape[0])
-        if self.row_scale is None:
-            return macko_spmm(self.n_rows, self.n_cols, self.mrow_ptr, self.codes, self.vals, self.plan, alpha, x, beta,
-                              y, workspace, tok_offsets, stream, self.bdelta)
-        return macko_spmm_i8(self.n_rows, self.n_cols, self.mrow_ptr, self.codes, self.vals, self.row_scale, self.plan,
-                             alpha, x, beta, y, workspace, tok_offsets, stream, self.bdelta)
-
-
-# ---------------------------------------------------------------------------
-# Tokens sorted by group and back
-# ---------------------------------------------------------------------------
-def route_tile_count(n_slots, n_groups) -> int:
-    out = ctypes.c_int32()
-    _call("route_tile_count", int(n_slots), int(n_groups), ctypes.byref(out))
-    return out.value
-
-
-def route_workspace_size(n_slots, n_groups) -> int:
-    out = ctypes.c_size_t()
-    _call("route_workspace_size", int(n_slots), int(n_groups), ctypes.byref(out))
-    return out.value
-
-
-def route_plan(n_groups, keys, offsets, order, pos, tiles, workspace=None, stream=None):
-    """Fills offsets [n_groups + 1], order and pos [slots] and tiles
-    [route_tile_count, 4] (int32 CUDA tensors) from keys (int32, any shape)."""
-    d, n, i32 = keys.device, keys.numel(), _i32_dtype()
-    wp, wb = _ws(workspace, d)
-    _call_on(d, "route_plan", n, int(n_groups), _vec(keys, i32, "keys", n, d),
-             _vec(offsets, i32, "offsets", n_groups + 1, d), _vec(order, i32, "order", n, d), _vec(pos, i32, "pos", n, d),
-             _vec(tiles, i32, "tiles", 4 * route_tile_count(n, n_groups), d), wp, wb, _stream(stream, keys))
-
-
-def route_gather(top_k, x, order, offsets, xs, weights=None, stream=None):
-    """xs[i] = weights[order[i]] * x[order[i] // top_k] for the sorted rows."""
-    d, (n, dim), k = x.device, x.shape, int(top_k)
-    xp, ldx = _rows(x, x.dtype, "x", n, dim, d)
-    sp, lds = _rows(xs, x.dtype, "xs", n * k, dim, d)
-    _call_on(d, "route_gather", n, k, dim, _dtype_code(x, "x"), offsets.numel() - 1,
-             _vec(offsets, _i32_dtype(), "offsets", 2, d), _vec(order, _i32_dtype(), "order", n * k, d),
-             _vec(weights, _f32_dtype(), "weights", n * k, d, allow_none=True), xp, ldx, sp, lds, _stream(stream, x))
-    return xs
-
-
-def route_combine(ys, pos, y, weights=None, stream=None):
-    """y[t] = sum_c weights[t, c] * ys[pos[t, c]]; pos: [tokens, top_k]."""
-    d, (n, dim) = y.device, y.shape
-    k = _top_k(pos, n)
-    sp, lds = _rows(ys, y.dtype, "ys", n * k, dim, d)
-    yp, ldy = _rows(y, y.dtype, "y", n, dim, d)
-    _call_on(d, "route_combine", n, k, dim, _dtype_code(y, "y"), _vec(pos, _i32_dtype(), "pos", n * k, d),
-             _vec(weights, _f32_dtype(), "weights", n * k, d, allow_none=True), sp, lds, yp, ldy, _stream(stream, y))
-    return y
-
-
-def route_combine_grad(dy, ys, pos, weights, dys, dw, stream=None):
-    """dys[pos[t, c]] = weights[t, c] * dy[t]; dw[t, c] = <ys[pos[t, c]], dy[t]>."""
-    d, (n, dim) = dy.device, dy.shape
-    k = _top_k(pos, n)
-    gp, ldg = _rows(dy, dy.dtype, "dy", n, dim, d)
-    sp, lds = _rows(ys, dy.dtype, "ys", n * k, dim, d)
-    op, ldo = _rows(dys, dy.dtype, "dys", n * k, dim, d)
-    _call_on(d, "route_combine_grad", n, k, dim, _dtype_code(dy, "dy"), gp, ldg, sp, lds,
-             _vec(pos, _i32_dtype(), "pos", n * k, d), _vec(weights, _f32_dtype(), "weights", n * k, d, allow_none=True),
-             op, ldo, _vec(dw, _f32_dtype(), "dw", n * k, d), _stream(stream, dy))
-    return dys, dw
-
-
-def _top_k(pos, n_tok):
-    if pos.dim() != 2 or pos.shape[0] != n_tok or pos.shape[1] < 1:
-        raise ValueError(f"pos must have shape ({n_tok}, top_k), got {tuple(pos.shape)}")
-    return int(pos.shape[1])
-
-
-class RoutePlan:
-    """The plan of a batch of n_tok tokens with top_k choices of n_groups
-    groups each: build() sorts, gather() and combine() move rows there and
-    back.  One plan serves every layer that shares the batch's keys."""
-
-    def __init__(self, n_tok, top_k, n_groups, device="cuda"):
-        import torch
-        self.n_tok, self.top_k, self.n_groups = int(n_tok), int(top_k), int(n_groups)
-        n = self.n_tok * self.top_k
-        new = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=device)  # noqa: E731
-        self.offsets, self.order, self.pos = new(self.n_groups + 1), new(n), new(self.n_tok, self.top_k)
-        self.tiles = new(route_tile_count(n, n_groups), 4)
-        self.workspace = torch.empty(route_workspace_size(n, n_groups), dtype=torch.uint8, device=device)
-
-    def build(self, keys, stream=None):
-        """keys: int32 [n_tok, top_k] (or flat); outside [0, n_groups): dropped."""
-        if keys.numel() != self.n_tok * self.top_k:
-            raise ValueError(f"keys must have {self.n_tok * self.top_k} elements, got {keys.numel()}")
-        route_plan(self.n_groups, keys, self.offsets, self.order, self.pos, self.tiles, self.workspace, stream)
-        return self
-
-    def gather(self, x, xs, weights=None, stream=None):
-        return route_gather(self.top_k, x, self.order, self.offsets, xs, weights, stream)
-
-    def combine(self, ys, y, weights=None, stream=None):
-        return route_combine(ys, self.pos, y, weights, stream)
-
-    def combine_grad(self, dy, ys, weights, dys, dw, stream=None):
-        return route_combine_grad(dy, ys, self.pos, weights, dys, dw, stream)
-
-
-# ---------------------------------------------------------------------------
-# Low-rank adapters of many requests
-# ---------------------------------------------------------------------------
-def lora_workspace_size(n_tok, max_rank) -> int:
-    out = ctypes.c_size_t()
-    _call("lora_workspace_size", int(n_tok), int(max_rank), ctypes.byref(out))
-    return out.value
-
-
-def _lora_args(ranks, scale, A, B, order, offsets, tiles, x, workspace):
-    import torch
-    d, dt = x.device, x.dtype
-    if dt not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"x must be float16 or bfloat16, got {dt}")
-    if A.dim() != 3 or B.dim() != 3 or A.shape[:2] != B.shape[:2]:
-        raise ValueError(f"A and B must be [adapters, rank, width], got {tuple(A.shape)} and {tuple(B.shape)}")
-    n_ad, r, n_in = A.shape
-    n_out, n = B.shape[2], x.shape[0]
-    if offsets.numel() != n_ad + 1 or order.numel() != n:
-        raise ValueError("the plan is not one of x's tokens and A's adapters")
-    xp, ldx = _rows(x, dt, "x", n, n_in, d)
-    i32 = _i32_dtype()
-    wp, wb = _ws(workspace, d)
-    return (d, (n, n_in, n_out, n_ad, r, _vec(ranks, i32, "ranks", n_ad, d, allow_none=True),
-                _vec(scale, _f32_dtype(), "scale", n_ad, d, allow_none=True), _vec(A, dt, "A", 0, d),
-                _vec(B, dt, "B", 0, d), F16 if dt == torch.float16 else BF16, _vec(order, i32, "order", n, d),
-                _vec(offsets, i32, "offsets", n_ad + 1, d), _vec(tiles, i32, "tiles", 0, d), tiles.numel() // 4, xp,
-                ldx), wp, wb)
-
-
-def lora_apply(ranks, scale, A, B, order, offsets, tiles, x, y_in, y, workspace, stream=None):
-    """y[t] = y_in[t] + scale[a] * B[a]^T (A[a] x[t]) for token t's adapter a
-    (y_in: None for zeros, or y itself).  A [adapters, rank, n_in] and
-    B [adapters, rank, n_out]; order, offsets, tiles: a RoutePlan's, of one
-    choice per token.  The gradient in x: A and B exchanged, dy for x."""
-    import torch
-    d, a, wp, wb = _lora_args(ranks, scale, A, B, order, offsets, tiles, x, workspace)
-    yp, ldy = _rows(y, (x.dtype, torch.float32), "y", a[0], a[2], d)
-    ip, ldi = (None, 0) if y_in is None else _rows(y_in, y.dtype, "y_in", a[0], a[2], d)
-    _call_on(d, "lora_apply", *a, ip, ldi, yp, F32 if y.dtype == torch.float32 else a[9], ldy, wp, wb, _stream(stream, y))
-    return y
-
-
-def lora_grad(ranks, scale, A, B, order, offsets, tiles, x, dy, dA, dB, workspace, stream=None):
-    """Weight gradients of lora_apply, fp32: dA like A, dB like B."""
-    d, a, wp, wb = _lora_args(ranks, scale, A, B, order, offsets, tiles, x, workspace)
-    if dA.shape != A.shape or dB.shape != B.shape:
-        raise ValueError("dA and dB must have the shapes of A and B")
-    gp, ldg = _rows(dy, x.dtype, "dy", a[0], a[2], d)
-    _call_on(d, "lora_grad", *a, gp, ldg, _vec(dA, _f32_dtype(), "dA", 0, d), _vec(dB, _f32_dtype(), "dB", 0, d), wp, wb,
-             _stream(stream, x))
-    return dA, dB
-
-
-# ---------------------------------------------------------------------------
 # Finite-element matvec
 # ---------------------------------------------------------------------------
 def fem_matvec_apply(n_elem, n_dof, edof, rho, penalty, Ke, alpha, x, beta, y, stream=None):
@@ -1119,3 +799,13 @@ def fem_assemble_csr(n_elem, n_dof, edof, rho, penalty, Ke, stream=None):
     v = torch.empty(max(nnz, 1), dtype=torch.float32, device=dev)[:nnz]
     fem_assemble_values(n_elem, n_dof, edof, rho, penalty, Ke, rp, ci, v, ws, stream)
     return rp, ci, v
+
+
+# ---------------------------------------------------------------------------
+# Operators of many tokens (tokens.py, which imports torch: loaded on first use)
+# ---------------------------------------------------------------------------
+def __getattr__(name):
+    if name in _TOKENS:
+        from . import tokens
+        return getattr(tokens, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
