@@ -688,13 +688,13 @@ spmv_status route_plan(int32_t n_slots, int32_t n_groups, const int32_t *keys, i
                        int32_t *order, int32_t *pos, int32_t *tiles, void *workspace,
                        size_t workspace_bytes, void *stream);
 
-/* xs[i] = weights[order[i]] * x[order[i] / top_k] for the sorted rows
- * i < offsets[n_groups]; later rows of xs stay as they are.  weights: fp32
- * [n_tok * top_k] or NULL (1: a copy).  x [n_tok, dim] and xs [n_tok * top_k,
- * dim] of type dtype, not overlapping.  Asynchronous. */
-spmv_status route_gather(int32_t n_tok, int32_t top_k, int32_t dim, int32_t dtype, int32_t n_groups,
-                         const int32_t *offsets, const int32_t *order, const float *weights,
-                         const void *x, int64_t ldx, void *xs, int64_t ldxs, void *stream);
+/* xs[pos[t, c]] = weights[t, c] * x[t]: the tokens' rows in sorted order (row i
+ * is token order[i] / top_k).  Rows from offsets[n_groups] on stay as they
+ * are.  weights: fp32 [n_tok * top_k] or NULL (1: a copy).  x [n_tok, dim] and
+ * xs [n_tok * top_k, dim] of type dtype, not overlapping.  Asynchronous. */
+spmv_status route_gather(int32_t n_tok, int32_t top_k, int32_t dim, int32_t dtype, const int32_t *pos,
+                         const float *weights, const void *x, int64_t ldx, void *xs, int64_t ldxs,
+                         void *stream);
 
 /* y[t] = sum over c of weights[t, c] * ys[pos[t, c]], dropped choices left out,
  * in fp32 in ascending c and rounded once (0 if all are dropped).  weights as

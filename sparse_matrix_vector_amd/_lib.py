@@ -89,7 +89,7 @@ SIGNATURES = {
     "route_tile_count": [c_i32, c_i32, P_i32],
     "route_workspace_size": [c_i32, c_i32, P_sz],
     "route_plan": [c_i32, c_i32, vp, vp, vp, vp, vp, vp, c_sz, vp],
-    "route_gather": [c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, c_i64, vp, c_i64, vp],
+    "route_gather": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, c_i64, vp, c_i64, vp],
     "route_combine": [c_i32, c_i32, c_i32, c_i32, vp, vp, vp, c_i64, vp, c_i64, vp],
     "route_combine_grad": [c_i32, c_i32, c_i32, c_i32, vp, c_i64, vp, c_i64, vp, vp, vp, c_i64, vp, vp],
     "lora_workspace_size": [c_i32, c_i32, P_sz],

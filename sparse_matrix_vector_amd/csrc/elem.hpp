@@ -41,4 +41,37 @@ __device__ __forceinline__ void store_vec(typename E::T *p, const Vec<E, N> &v) 
     *reinterpret_cast<Vec<E, N> *>(p) = v;
 }
 
+// The same for 16 bytes at an address aligned to one element only (global
+// memory takes such accesses on gfx950), and for data that is read or written
+// once and need not stay in the caches.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+template <typename E, int N>
+__device__ __forceinline__ Vec<E, N> load_any(const typename E::T *p) {
+    if constexpr (sizeof(Vec<E, N>) == 16)
+        return __builtin_bit_cast(Vec<E, N>, (u32x4) * reinterpret_cast<const u32x4_any *>(p));
+    else
+        return load_vec<E, N>(p);
+}
+template <typename E, int N>
+__device__ __forceinline__ Vec<E, N> load_once(const typename E::T *p) {
+    if constexpr (sizeof(Vec<E, N>) == 16)
+        return __builtin_bit_cast(Vec<E, N>, (u32x4)__builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p)));
+    else
+        return load_vec<E, N>(p);
+}
+template <typename E, int N>
+__device__ __forceinline__ void store_any(typename E::T *p, const Vec<E, N> &v) {
+    if constexpr (sizeof(Vec<E, N>) == 16)
+        *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4, v);
+    else
+        store_vec<E, N>(p, v);
+}
+template <typename E, int N>
+__device__ __forceinline__ void store_once(typename E::T *p, const Vec<E, N> &v) {
+    if constexpr (sizeof(Vec<E, N>) == 16)
+        __builtin_nontemporal_store((u32x4_any)__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4_any *>(p));
+    else
+        store_vec<E, N>(p, v);
+}
+
 }  // namespace spmv

@@ -252,22 +252,21 @@ def route_plan(n_groups, keys, offsets, order, pos, tiles, workspace=None, strea
             _ptr(tiles, _I32, "tiles", 4 * n_tiles, d), wp, wb)
 
 
-def route_gather(top_k, x, order, offsets, xs, weights=None, stream=None):
-    """xs[i] = weights[order[i]] * x[order[i] // top_k] for the sorted rows."""
-    d, n, dim = _matrix(x, "x")
-    slots = n * top_k
-    xp, ldx = _rows(x, x.dtype, "x", n, dim, d)
-    sp, lds = _rows(xs, x.dtype, "xs", slots, dim, d)
-    _launch(d, stream, "route_gather", n, top_k, dim, _code(x, "x"), offsets.numel() - 1,
-            _ptr(offsets, _I32, "offsets", 2, d), _ptr(order, _I32, "order", slots, d),
-            _opt(weights, _F32, "weights", slots, d), xp, ldx, sp, lds)
-    return xs
-
-
 def _top_k(pos, n_tok):
     if pos.dim() != 2 or pos.shape[0] != n_tok or pos.shape[1] < 1:
         raise ValueError(f"pos must have shape ({n_tok}, top_k), got {tuple(pos.shape)}")
     return pos.shape[1]
+
+
+def route_gather(x, pos, xs, weights=None, stream=None):
+    """xs[pos[t, c]] = weights[t, c] * x[t]; pos: [tokens, top_k]."""
+    k = _top_k(pos, x.shape[0])
+    d, n, dim = _matrix(x, "x")
+    xp, ldx = _rows(x, x.dtype, "x", n, dim, d)
+    sp, lds = _rows(xs, x.dtype, "xs", n * k, dim, d)
+    _launch(d, stream, "route_gather", n, k, dim, _code(x, "x"), _ptr(pos, _I32, "pos", n * k, d),
+            _opt(weights, _F32, "weights", n * k, d), xp, ldx, sp, lds)
+    return xs
 
 
 def route_combine(ys, pos, y, weights=None, stream=None):
@@ -314,7 +313,7 @@ class RoutePlan:
         return self
 
     def gather(self, x, xs, weights=None, stream=None):
-        return route_gather(self.top_k, x, self.order, self.offsets, xs, weights, stream)
+        return route_gather(x, self.pos, xs, weights, stream)
 
     def combine(self, ys, y, weights=None, stream=None):
         return route_combine(ys, self.pos, y, weights, stream)

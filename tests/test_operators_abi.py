@@ -52,14 +52,13 @@ def test_route_sizes_and_refusals():
 
 def test_route_data_refusals():
     L = S.lib()
-    # gather(n_tok, top_k, dim, dtype, n_groups, offsets, order, weights, x, ldx, xs, ldxs)
-    def gather(n=4, k=2, dim=8, dt=0, g=3, off=P, order=P, w=None, x=P, ldx=8, xs=P, ldxs=8):
-        return L.route_gather(n, k, dim, dt, g, off, order, w, x, ldx, xs, ldxs, None)
+    def gather(n=4, k=2, dim=8, dt=0, pos=P, w=None, x=P, ldx=8, xs=P, ldxs=8):
+        return L.route_gather(n, k, dim, dt, pos, w, x, ldx, xs, ldxs, None)
     assert gather(n=-1) == VALUE and gather(k=0) == VALUE and gather(dim=-1) == VALUE and gather(dt=3) == VALUE
-    assert gather(g=0) == VALUE and gather(ldx=7) == VALUE and gather(ldxs=7) == VALUE
-    assert gather(off=None) == VALUE and gather(order=None) == VALUE and gather(x=None) == VALUE
+    assert gather(ldx=7) == VALUE and gather(ldxs=7) == VALUE
+    assert gather(pos=None) == VALUE and gather(xs=None) == VALUE and gather(x=None) == VALUE
     assert gather(n=1 << 30, k=4) == OVERFLOW
-    assert gather(n=0, x=None, xs=None, off=None, order=None) == OK
+    assert gather(n=0, x=None, xs=None, pos=None) == OK
     assert gather(dim=0, ldx=0, ldxs=0, x=None, xs=None) == OK
 
     def combine(n=4, k=2, dim=8, dt=0, pos=P, w=None, ys=P, ldys=8, y=P, ldy=8):
