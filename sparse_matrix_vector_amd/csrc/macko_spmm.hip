@@ -71,11 +71,6 @@ struct Codes {
 // entries: byte offsets fit 32 bits)
 template <bool I8>
 using vals_t = typename std::conditional<I8, u32x2, u32x4>::type;
-template <bool I8>
-__device__ __forceinline__ vals_t<I8> load_vals(const void *__restrict__ vals, unsigned int u) {
-    return *reinterpret_cast<const vals_t<I8> *>(static_cast<const char *>(vals) + u * (unsigned)sizeof(vals_t<I8>));
-}
-
 // Values t, t + 1 (t even) as the bits of two fp16; int8 exactly, as 1024 + (q + 128) - 1152.
 template <bool I8>
 __device__ __forceinline__ unsigned int value_pair(const vals_t<I8> &v, int t) {
@@ -87,6 +82,38 @@ __device__ __forceinline__ unsigned int value_pair(const vals_t<I8> &v, int t) {
             unsigned int, as_h2(__builtin_amdgcn_perm(0x64646464u, w, (t & 2) ? 0x04030402u : 0x04010400u)) -
                               f16x2{(_Float16)1152.0f, (_Float16)1152.0f});
     }
+}
+
+// The streamed arrays as buffers: a lane whose offset lies past the end reads
+// zeros without a memory access, so lanes without a unit cost nothing and need
+// no branch.  (Sizes are below 4 GB: fewer than 2^31 entries, in units of 128.)
+struct Streams {
+    __amdgpu_buffer_rsrc_t codes, vals;
+};
+constexpr unsigned int SM_NO_UNIT = 0xFFFFFFF0u;
+
+template <int BD, bool I8>
+__device__ __forceinline__ Streams streams_of(const unsigned int *codes, const void *vals, int units) {
+    constexpr int FLAGS = 0x00027000;
+    return {__builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned int *>(codes), 0, (int)((unsigned)units * BD), FLAGS),
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(vals), 0,
+                                              (int)((unsigned)units * (unsigned)sizeof(vals_t<I8>)), FLAGS)};
+}
+template <int BD>
+__device__ __forceinline__ typename Codes<BD>::lane_t stream_codes(const Streams &s, bool in, unsigned int u) {
+    const int at = (int)(in ? (BD < 4 ? (u * BD) & ~3u : u * BD) : SM_NO_UNIT);
+    if constexpr (BD == 8)
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(s.codes, at, 0, 0));
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(s.codes, at, 0, 0);
+}
+template <bool I8>
+__device__ __forceinline__ vals_t<I8> stream_vals(const Streams &s, bool in, unsigned int u) {
+    const int at = (int)(in ? u * (unsigned)sizeof(vals_t<I8>) : SM_NO_UNIT);
+    if constexpr (I8)
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(s.vals, at, 0, 0));
+    else
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s.vals, at, 0, 0));
 }
 
 // Inclusive sum over groups of 8 lanes: within pairs, within quads, then the
@@ -204,12 +231,12 @@ __device__ __forceinline__ void finish(const SpmmArg &a, int tok, int r, int64_t
 // A wave's 16 rows, 8 at a time (h = 0, 1); lane l of a row's 8 lanes takes
 // every eighth unit of the row's piece of a slab.
 struct RowPair {
-    int base[2], units[2];      // first unit (a valid one also for empty rows) and number of units of the rows
+    int base[2], units[2];      // first unit and number of units of the rows
     const unsigned int *plan[2];
 };
 
-// `last`: the matrix's last unit; rows past the end of the group count as empty.
-__device__ __forceinline__ RowPair load_rows(const SpmmArg &a, int64_t row0, int rows, int last, int lane) {
+// Rows past the end of the group count as empty.
+__device__ __forceinline__ RowPair load_rows(const SpmmArg &a, int64_t row0, int rows, int lane) {
     RowPair rp;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -217,16 +244,15 @@ __device__ __forceinline__ RowPair load_rows(const SpmmArg &a, int64_t row0, int
         const int64_t row = row0 + max(min(r, rows - 1), 0);
         const int b = a.mrp[row] / 8, e = a.mrp[row + 1] / 8;
         rp.units[h] = r < rows ? e - b : 0;
-        rp.base[h] = min(b, last);
+        rp.base[h] = b;
         rp.plan[h] = a.plan + row * (a.n_slabs + 1);
     }
     return rp;
 }
 
 // The units of one slab in registers: SM_STEPS of 8 lanes cover a slab of a
-// half pruned row, further ones are loaded while decoding.  Lanes past the end
-// read the piece's last unit, so no load hides behind a branch and loads
-// stay in flight over other work.
+// half pruned row, further ones are loaded while decoding.  No load hides
+// behind a branch, so they stay in flight over other work.
 constexpr int SM_STEPS = 3;
 template <int BD, bool I8>
 struct Stage {
@@ -250,24 +276,24 @@ __device__ __forceinline__ PlanWords load_plan(const RowPair &rp, int k) {
 }
 
 template <int BD, bool I8>
-__device__ __forceinline__ void load_half(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, const PlanWords &w, int l,
+__device__ __forceinline__ void load_half(Stage<BD, I8> &st, const Streams &a, const RowPair &rp, const PlanWords &w, int l,
                                           int h) {
     {
         st.u[h] = (int)(w.p0[h] & ((1u << SM_UNIT_BITS) - 1u)) + l;
         st.end[h] = min((int)(w.p1[h] & ((1u << SM_UNIT_BITS) - 1u)) + 1, rp.units[h]);
         st.carry[h] = -1 - (int)(w.p0[h] >> SM_UNIT_BITS);      // relative to the slab's first column
-        const int stop = max(st.end[h] - 1, 0);
 #pragma unroll
         for (int i = 0; i < SM_STEPS; ++i) {
-            const unsigned int u = (unsigned)(rp.base[h] + min(st.u[h] + 8 * i, stop));
-            st.w[h][i] = Codes<BD>::load(a.codes, u);
-            st.v[h][i] = load_vals<I8>(a.vals, u);
+            const bool in = st.u[h] + 8 * i < st.end[h];
+            const unsigned int u = (unsigned)(rp.base[h] + st.u[h] + 8 * i);
+            st.w[h][i] = stream_codes<BD>(a, in, u);
+            st.v[h][i] = stream_vals<I8>(a, in, u);
         }
     }
 }
 
 template <int BD, bool I8>
-__device__ __forceinline__ void load_stage(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, const PlanWords &w,
+__device__ __forceinline__ void load_stage(Stage<BD, I8> &st, const Streams &a, const RowPair &rp, const PlanWords &w,
                                            int l) {
     load_half<BD, I8>(st, a, rp, w, l, 0);
     load_half<BD, I8>(st, a, rp, w, l, 1);
@@ -341,7 +367,7 @@ __device__ __forceinline__ void decode_step(typename Codes<BD>::lane_t w, const 
 
 // Eight of the wave's rows of a slab into its tile at `tile` (LDS byte offset).
 template <int BD, bool I8>
-__device__ __forceinline__ void decode_half(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, int lane, int tile,
+__device__ __forceinline__ void decode_half(Stage<BD, I8> &st, const Streams &a, const RowPair &rp, int lane, int tile,
                                             int h) {
     const int odd = lane & 1 ? -1 : 0, high = lane & 2 ? -1 : 0;
     {
@@ -354,15 +380,15 @@ __device__ __forceinline__ void decode_half(Stage<BD, I8> &st, const SpmmArg &a,
                                 row);
         }
         for (int u = st.u[h] + 8 * SM_STEPS; __any(u < st.end[h]); u += 8) {
-            const unsigned int at = (unsigned)(rp.base[h] + min(u, max(st.end[h] - 1, 0)));
-            decode_step<BD, I8>(Codes<BD>::load(a.codes, at), load_vals<I8>(a.vals, at), (unsigned)(rp.base[h] + u),
-                                u < st.end[h], st.carry[h], odd, high, row);
+            const unsigned int at = (unsigned)(rp.base[h] + u);
+            const bool in = u < st.end[h];
+            decode_step<BD, I8>(stream_codes<BD>(a, in, at), stream_vals<I8>(a, in, at), at, in, st.carry[h], odd, high, row);
         }
     }
 }
 
 template <int BD, bool I8>
-__device__ __forceinline__ void decode_stage(Stage<BD, I8> &st, const SpmmArg &a, const RowPair &rp, int lane, int tile) {
+__device__ __forceinline__ void decode_stage(Stage<BD, I8> &st, const Streams &a, const RowPair &rp, int lane, int tile) {
     decode_half<BD, I8>(st, a, rp, lane, tile, 0);
     decode_half<BD, I8>(st, a, rp, lane, tile, 1);
 }
@@ -406,8 +432,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int last_unit = a.mrp[(int64_t)gridDim.z * a.n_rows] / 8 - 1;
-    const RowPair rp = load_rows(a, row0, rows, last_unit, lane);
+    const Streams str = streams_of<BD, I8>(a.codes, a.vals, a.mrp[(int64_t)gridDim.z * a.n_rows] / 8);
+    const RowPair rp = load_rows(a, row0, rows, lane);
     // one slab: its units are in st; next gets those of slab k + WAVES, whose
     // plan words are in pw, and pw those of the slab after that
     PlanWords pw;
@@ -416,46 +442,46 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
         // loads are waited for in the order of their issue: what is needed
         // first goes first, and the next slab's units last
         // columns past the last are read as the row's last ones: W is zero there
-        const int c0 = k * SM_SLAB + 16 * q, cm = a.n_cols - 8;
+        const int c0 = k * SM_SLAB + 8 * q, cm = a.n_cols - 8;
         u32x4 x[NT < 4 ? NT : 1][8];
         if constexpr (NT < 4) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    x[i][s] = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 64 * (s >> 1) + 8 * (s & 1), cm));
+                    x[i][s] = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 32 * s, cm));
         }
         const PlanWords after = load_plan(rp, min(k + 2 * WAVES, top));
         __builtin_amdgcn_sched_barrier(0);
-        load_stage<BD, I8>(next, a, rp, pw, lane & 7);
+        load_stage<BD, I8>(next, str, rp, pw, lane & 7);
         __builtin_amdgcn_sched_barrier(0);
         pw = after;
         clear_tile(tile, lane);
         wave_lds_order();
-        decode_stage<BD, I8>(st, a, rp, lane, lds_offset(tile));
+        decode_stage<BD, I8>(st, str, rp, lane, lds_offset(tile));
         wave_lds_order();
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             const h8 w = __builtin_bit_cast(
-                h8, *reinterpret_cast<const u32x4 *>(tile + n * SM_LDW + 64 * (s >> 1) + 16 * q + 8 * (s & 1)));
+                h8, *reinterpret_cast<const u32x4 *>(tile + n * SM_LDW + 32 * s + 8 * q));
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 if constexpr (NT < 4) {
                     acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, x[i][s]), acc[i], 0, 0, 0);
                 } else if (i < live) {                   // uniform
-                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 64 * (s >> 1) + 8 * (s & 1), cm));
+                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 32 * s, cm));
                     acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, xv), acc[i], 0, 0, 0);
                 }
             }
         }
         wave_lds_order();
     };
-    if (last_unit >= 0 && wv < a.n_slabs) {              // an empty matrix has no unit to read
+    if (wv < a.n_slabs) {
         Stage<BD, I8> s0, s1;
         const PlanWords first = load_plan(rp, wv);
         pw = load_plan(rp, min(wv + WAVES, top));
         __builtin_amdgcn_sched_barrier(0);
-        load_stage<BD, I8>(s0, a, rp, first, lane & 7);
+        load_stage<BD, I8>(s0, str, rp, first, lane & 7);
         int k = wv;
         for (; k + WAVES < a.n_slabs; k += 2 * WAVES) {
             slab(k, s0, s1);
@@ -489,12 +515,14 @@ struct BlockShape {
     static constexpr int WAVES = 4;
     static constexpr int ROWS = WAVES * SM_ROWS;
     static constexpr int TILE = ROWS * SM_LDW;              // halfs
-    static constexpr int KW = NT < 4 ? 4 / NT : 1;          // waves that share a token tile's columns
-    static constexpr int TW = NT < 4 ? 1 : NT / 4;          // token tiles of a wave
+    static constexpr int KW = NT < 4 ? 4 / NT : 1;          // waves that share out a token tile's columns
+    static constexpr int GROUPS = 4 / KW;                   // of KW waves, each with every GROUPS-th token tile
+    static constexpr int TW = NT / GROUPS;                  // token tiles of a wave
     static constexpr int STEPS = 8 / KW;                    // 32-column steps of a wave per slab
     static constexpr int AHEAD = STEPS * TW <= 16 ? STEPS : 16 / TW;   // steps of x in registers
     static constexpr int OCC = NT < 8 ? 4 : 2;              // waves per SIMD that the registers allow
-    static constexpr size_t LDS = (size_t)(SM_FRONT + TILE) * 2;
+    // the tile, or the column parts' sums
+    static constexpr size_t LDS = std::max<size_t>((size_t)(SM_FRONT + TILE) * 2, (size_t)(KW - 1) * NT * 4 * 64 * 16);
 };
 
 // an LDS-only barrier: loads issued before it stay in flight
@@ -504,31 +532,34 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Workgroup: rows ROWS * blockIdx.y .., group blockIdx.z / split, slabs of part
-// blockIdx.z % split, and `width` 16-token tiles from width * blockIdx.x on.
+// A workgroup takes 64 rows of a group, one of `split` parts of its slabs, and
+// `width` 16-token tiles; row blocks first, so that workgroups that run together
+// share the piece of x.  (Runs of row blocks per XCD measured 2 % slower.)
 template <int BD, bool I8, int NT>
-__global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) void k_macko_spmm_block(SpmmArg a, int width, int split,
+__global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) void k_macko_spmm_block(SpmmArg a, int n_groups, int row_blocks, int tiles, int width, int split,
                                                                        float *__restrict__ partial, int ldp) {
     typedef BlockShape<NT> B;
     extern __shared__ __attribute__((aligned(16))) unsigned short lds[];
     const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int group = blockIdx.z / split, part = blockIdx.z - group * split;
+    const int rb = (int)(blockIdx.x % (unsigned)row_blocks);
+    int rest = (int)(blockIdx.x / (unsigned)row_blocks);
+    const int tt = rest % tiles;
+    rest /= tiles;
+    const int part = rest % split, group = rest / split;
     int t0 = 0, t1 = a.n_tok;
     if (a.tok_offsets) {
         t0 = min(max(a.tok_offsets[group], 0), a.n_tok);
         t1 = min(max(a.tok_offsets[group + 1], t0), a.n_tok);
     }
-    t0 += blockIdx.x * 16 * width;
+    t0 += tt * 16 * width;
     if (t0 >= t1) return;
     t1 = min(t1, t0 + 16 * width);
-    const int r0 = blockIdx.y * B::ROWS;
+    const int r0 = rb * B::ROWS;
     const int64_t row0 = (int64_t)group * a.n_rows + r0;
-    // the wave's token tiles: every fourth (NT >= 4), or one and a part of its columns
-    const int kp = NT < 4 ? wv / NT : 0, tw0 = NT < 4 ? wv % NT : wv;
-    constexpr int TSTEP = NT < 4 ? 1 : 4;
+    const int kp = wv / B::GROUPS, tw0 = wv % B::GROUPS;    // the wave's part of the columns, first token tile
     const int live = (t1 - t0 + 15) / 16;                   // token tiles in use
-    const int mine = NT < 4 ? (tw0 < live ? 1 : 0) : min(B::TW, max(0, (live - tw0 + 3) / 4));
+    const int mine = min(B::TW, max(0, (live - tw0 + B::GROUPS - 1) / B::GROUPS));
     const int wrow = wv * SM_ROWS;                          // the wave's rows in the decoding
     unsigned short *tile = lds + SM_FRONT + wrow * SM_LDW;
     f32x4 acc[4][B::TW];
@@ -537,28 +568,28 @@ __global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) vo
 #pragma unroll
         for (int t = 0; t < B::TW; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int last_unit = a.mrp[(int64_t)(gridDim.z / split) * a.n_rows] / 8 - 1;
-    const RowPair rp = load_rows(a, row0 + min(wrow, a.n_rows - 1 - r0), a.n_rows - r0 - wrow, last_unit, lane);
+    const Streams str = streams_of<BD, I8>(a.codes, a.vals, a.mrp[(int64_t)n_groups * a.n_rows] / 8);
+    const RowPair rp = load_rows(a, row0 + min(wrow, a.n_rows - 1 - r0), a.n_rows - r0 - wrow, lane);
     const unsigned short *xr[B::TW];
 #pragma unroll
     for (int t = 0; t < B::TW; ++t)
-        xr[t] = a.x + (int64_t)min(t0 + 16 * (tw0 + TSTEP * t) + n, t1 - 1) * a.ldx;
+        xr[t] = a.x + (int64_t)min(t0 + 16 * (tw0 + B::GROUPS * t) + n, t1 - 1) * a.ldx;
     const int lo = (int)((int64_t)a.n_slabs * part / split), hi = (int)((int64_t)a.n_slabs * (part + 1) / split);
     const int cm = a.n_cols - 8;
-    if (last_unit >= 0 && lo < hi) {                        // an empty matrix has no unit to read
-        const int col = kp * 32 * B::STEPS + 16 * q;        // the lane's first column in a slab
+    if (lo < hi) {
+        const int col = kp * 32 * B::STEPS + 8 * q;         // the lane's first column in a slab
         u32x4 x[B::AHEAD][B::TW];
         // columns past the last are read as the row's last ones: W is zero there
         auto load_x = [&](int k, int s, int slot) {
 #pragma unroll
             for (int t = 0; t < B::TW; ++t)
-                x[slot][t] = *reinterpret_cast<const u32x4 *>(xr[t] + min(k * SM_SLAB + col + 64 * (s >> 1) + 8 * (s & 1), cm));
+                x[slot][t] = *reinterpret_cast<const u32x4 *>(xr[t] + min(k * SM_SLAB + col + 32 * s, cm));
         };
         Stage<BD, I8> st;
         const PlanWords first = load_plan(rp, lo);
         PlanWords pw = load_plan(rp, min(lo + 1, hi - 1));
         __builtin_amdgcn_sched_barrier(0);
-        load_stage<BD, I8>(st, a, rp, first, lane & 7);
+        load_stage<BD, I8>(st, str, rp, first, lane & 7);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < B::AHEAD; ++s) load_x(lo, s, s);
@@ -570,9 +601,9 @@ __global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) vo
             const PlanWords after = load_plan(rp, min(k + 2, hi - 1));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                decode_half<BD, I8>(st, a, rp, lane, lds_offset(tile), h);
+                decode_half<BD, I8>(st, str, rp, lane, lds_offset(tile), h);
                 __builtin_amdgcn_sched_barrier(0);
-                load_half<BD, I8>(st, a, rp, pw, lane & 7, h);
+                load_half<BD, I8>(st, str, rp, pw, lane & 7, h);
                 __builtin_amdgcn_sched_barrier(0);
             }
             pw = after;
@@ -583,7 +614,7 @@ __global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) vo
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     w[r] = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4 *>(lds + SM_FRONT + (16 * r + n) * SM_LDW +
-                                                                                   kp * B::STEPS * 32 + 64 * (s >> 1) + 16 * q + 8 * (s & 1)));
+                                                                                   (kp * B::STEPS + s) * 32 + 8 * q));
 #pragma unroll
                 for (int t = 0; t < B::TW; ++t) {
                     if (t < mine) {                         // uniform
@@ -602,21 +633,27 @@ __global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) vo
         }
     }
     if (B::KW > 1) {                                        // the column parts, in order
-        f32x4 *sums = reinterpret_cast<f32x4 *>(lds);       // [KW - 1][NT][4][64]
+        f32x4 *sums = reinterpret_cast<f32x4 *>(lds) + tw0 * (4 * B::TW * 64) + lane;   // [KW - 1][GROUPS][TW][4][64]
+        constexpr int PART = B::GROUPS * B::TW * 4 * 64;
         __syncthreads();
         if (kp > 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sums[(((kp - 1) * NT + tw0) * 4 + r) * 64 + lane] = acc[r][0];
+            for (int t = 0; t < B::TW; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sums[(kp - 1) * PART + (t * 4 + r) * 64] = acc[r][t];
         }
         __syncthreads();
         if (kp > 0) return;
+#pragma unroll
         for (int p = 0; p < B::KW - 1; ++p)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r][0] += sums[((p * NT + tw0) * 4 + r) * 64 + lane];
+            for (int t = 0; t < B::TW; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r][t] += sums[p * PART + (t * 4 + r) * 64];
     }
 #pragma unroll
     for (int t = 0; t < B::TW; ++t) {
-        const int tok = t0 + 16 * (tw0 + TSTEP * t) + n;
+        const int tok = t0 + 16 * (tw0 + B::GROUPS * t) + n;
         if (tok >= t1) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -675,6 +712,7 @@ void launch(const SpmmArg &a, dim3 grid, hipStream_t st) {
 // How the tokens and columns of a product are cut.
 struct Cut {
     bool block;       // k_macko_spmm_block, else k_macko_spmm
+    int waves;        // of a workgroup of k_macko_spmm
     int nt;           // token tiles a workgroup can hold
     int width;        // token tiles it takes
     int tiles;        // workgroups over the tokens (of the largest possible group)
@@ -684,23 +722,36 @@ struct Cut {
 Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok) {
     Cut c = {};
     const int64_t t16 = std::max<int64_t>(1, ceil_div(n_tok, 16));
-    c.block = n_tok > 16;
+    // Up to 32 tokens, as long as the traffic of x (every 16 rows read all of it)
+    // is small: 12288 x 12288 at 70 % measured 41.5 against 45.9 us in 64-row
+    // workgroups for 8 tokens (151 MB of x), 53.0 against 48.4 us for 16 (302 MB).
+    // Above 16 tokens only up to 24 slabs: 4096 x 4096 times 32 takes 14.5 against
+    // 19.6 us, but 1024 x 12288 takes 31 against 15.5 us with its columns split.
+    const int64_t slabs = ceil_div(n_cols, SM_SLAB);
+    c.block = n_tok > 32 || (n_tok > 16 && slabs > 24) || ceil_div(n_rows, SM_ROWS) * n_tok * n_cols * 2 > (200 << 20);
+    if (!c.block) {
+        // few row tiles: more waves share a tile's slabs (2048 x 2048 times 5:
+        // 5.3 us with 8, 6.7 us with 4; 8192 x 8192 times 2: 23.1 and 20.9 us)
+        c.waves = n_groups * ceil_div(n_rows, SM_ROWS) <= 256 && slabs >= 8 ? 8 : 4;
+        c.nt = (int)t16;
+        c.tiles = c.split = 1;
+        c.width = c.nt;
+        return c;
+    }
     // a group's share of the tokens is not known here: room for twice the mean
     const int64_t room = n_groups > 1 ? std::min(t16, ceil_div(2 * n_tok, 16 * n_groups)) : t16;
     c.nt = room > 8 ? 16 : room > 4 ? 8 : room > 2 ? 4 : 2;
     c.tiles = (int)ceil_div(t16, c.nt);
     c.width = n_groups > 1 ? c.nt : (int)ceil_div(t16, c.tiles);
     c.split = 1;
-    if (c.block) {
-        // parts of the columns: fewest rounds of slabs over the resident
-        // workgroups, each further part costing the traffic of its sums
-        const int64_t slabs = ceil_div(n_cols, SM_SLAB), wgs = n_groups * ceil_div(n_rows, BlockShape<4>::ROWS) * c.tiles;
-        double best = 1e30;
-        for (int s = 1; s <= 16 && s <= slabs; ++s) {
-            const double cost = (double)ceil_div(wgs * s, 256 * (c.nt < 8 ? 4 : 2)) * (double)ceil_div(slabs, s) +
-                                (s > 1 ? 1.0 + s * (double)n_tok * (double)n_rows * 4e-7 : 0.0);
-            if (cost < best) best = cost, c.split = s;
-        }
+    // parts of the columns: fewest rounds of slabs over the resident
+    // workgroups, each further part costing the traffic of its sums
+    const int64_t wgs = n_groups * ceil_div(n_rows, BlockShape<4>::ROWS) * c.tiles;
+    double best = 1e30;
+    for (int s = 1; s <= 16 && s <= slabs; ++s) {
+        const double cost = (double)ceil_div(wgs * s, 256 * (c.nt < 8 ? 4 : 2)) * (double)ceil_div(slabs, s) +
+                            (s > 1 ? 1.0 + s * (double)n_tok * (double)n_rows * 4e-7 : 0.0);
+        if (cost < best) best = cost, c.split = s;
     }
     return c;
 }
@@ -712,26 +763,43 @@ size_t packed_bytes(int64_t n_tok, int64_t n_cols) {
 }
 
 template <int BD, bool I8, int NT>
-void launch_block(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
-    const dim3 grid(c.tiles, (unsigned)ceil_div(a.n_rows, BlockShape<NT>::ROWS), n_groups * c.split);
-    k_macko_spmm_block<BD, I8, NT><<<grid, 64 * BlockShape<NT>::WAVES, BlockShape<NT>::LDS, st>>>(a, c.width, c.split, partial,
-                                                                                    (int)partial_ld(a.n_rows));
+spmv_status launch_block(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
+    const int row_blocks = (int)ceil_div(a.n_rows, BlockShape<NT>::ROWS);
+    const int64_t grid = (int64_t)row_blocks * c.tiles * c.split * n_groups;
+    if (grid > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "the launch does not fit int32");
+    k_macko_spmm_block<BD, I8, NT><<<(unsigned)grid, 64 * BlockShape<NT>::WAVES, BlockShape<NT>::LDS, st>>>(
+        a, n_groups, row_blocks, c.tiles, c.width, c.split, partial, (int)partial_ld(a.n_rows));
+    SPMV_LAUNCHED("k_macko_spmm_block");
+    return SPMV_OK;
+}
+
+template <int BD, bool I8, int NT>
+void launch_waves(const SpmmArg &a, const Cut &c, dim3 grid, hipStream_t st) {
+    if (c.waves == 8)
+        launch<BD, I8, NT, 8>(a, grid, st);
+    else
+        launch<BD, I8, NT, 4>(a, grid, st);
 }
 
 template <int BD, bool I8>
 spmv_status launch_shape(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
     if (!c.block) {
-        launch<BD, I8, 1, 4>(a, dim3(1, (unsigned)ceil_div(a.n_rows, SM_ROWS), n_groups), st);
+        const dim3 grid(c.tiles, (unsigned)ceil_div(a.n_rows, SM_ROWS), n_groups);
+        if (c.nt == 1)
+            launch_waves<BD, I8, 1>(a, c, grid, st);
+        else
+            launch_waves<BD, I8, 2>(a, c, grid, st);
         SPMV_LAUNCHED("k_macko_spmm");
         return SPMV_OK;
     }
+    spmv_status s;
     switch (c.nt) {
-        case 2: launch_block<BD, I8, 2>(a, c, n_groups, partial, st); break;
-        case 4: launch_block<BD, I8, 4>(a, c, n_groups, partial, st); break;
-        case 8: launch_block<BD, I8, 8>(a, c, n_groups, partial, st); break;
-        default: launch_block<BD, I8, 16>(a, c, n_groups, partial, st); break;
+        case 2: s = launch_block<BD, I8, 2>(a, c, n_groups, partial, st); break;
+        case 4: s = launch_block<BD, I8, 4>(a, c, n_groups, partial, st); break;
+        case 8: s = launch_block<BD, I8, 8>(a, c, n_groups, partial, st); break;
+        default: s = launch_block<BD, I8, 16>(a, c, n_groups, partial, st); break;
     }
-    SPMV_LAUNCHED("k_macko_spmm_block");
+    if (s != SPMV_OK) return s;
     if (c.split > 1) {
         k_macko_spmm_join<I8><<<dim3((unsigned)ceil_div(a.n_rows, 1024), (unsigned)std::min(a.n_tok, 65535)), 256, 0, st>>>(
             a, n_groups, c.split, partial, (int)partial_ld(a.n_rows));
@@ -771,6 +839,16 @@ spmv_status spmm_apply(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t
                  static_cast<const unsigned int *>(plan), tok_offsets, x, ldx, y, ldy, alpha, beta, y_dtype == SPMV_F32, 0};
     const size_t ysize = dtype_size(y_dtype);
     a.vec_y = ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (4 * ysize - 1)) == 0;
+    // one token is the vector product, whose gather of x needs no dense tile
+    // (12288 x 12288 at 70 %: 20.5 us against 38)
+    if (n_tok == 1 && !tok_offsets && y_dtype == SPMV_F32) {
+        if constexpr (I8)
+            return macko_spmv_i8(n_rows, n_cols, bdelta, mrow_ptr, codes, static_cast<const int8_t *>(vals), row_scale, alpha,
+                                 x, beta, static_cast<float *>(y), stream);
+        else
+            return macko_spmv(n_rows, n_cols, bdelta, mrow_ptr, codes, static_cast<const uint16_t *>(vals), alpha, x, beta,
+                              static_cast<float *>(y), stream);
+    }
     const Cut cut = cut_of(n_groups, n_rows, n_cols, n_tok);
     const bool pack = !aligned16(x) || ldx % 8 != 0 || n_cols % 8 != 0;
     if (pack || cut.split > 1) {

@@ -116,14 +116,15 @@ def test_token_counts(T):
         assert (yb[0] == -7).all() and (yb[T + 1] == -7).all()
 
 
-@pytest.mark.parametrize("shape", [(64, 2304, 20), (200, 5000, 40), (1000, 2560, 300), (70, 12288, 65)])
+@pytest.mark.parametrize("shape", [(64, 2304, 20), (200, 5000, 40), (1000, 2560, 300), (70, 12288, 65), (33, 8000, 24)])
 @pytest.mark.parametrize("i8", [False, True])
 def test_columns_split_over_workgroups(shape, i8):
-    """Few rows and many columns: partial sums in the workspace, joined in order (same bits on every call)."""
+    """Few rows and many columns: partial sums in the workspace (but for the
+    first shape), joined in order (same bits on every call)."""
     rows, cols, T = shape
     w = _weight(rows, cols, "0.8", 4, 8, i8)
     m = _matrix(w, rows, cols, 4)
-    assert S.macko_spmm_workspace_size(1, rows, cols, T) > S.macko_spmm_workspace_size(1, rows, cols, 1) * T
+    assert (S.macko_spmm_workspace_size(1, rows, cols, T) > S.macko_spmm_workspace_size(1, rows, cols, 1) * T) == (T != 20)
     x = _x(T, cols, T)
     y0 = torch.randn(T, rows, device="cuda").half()
     ys = []
