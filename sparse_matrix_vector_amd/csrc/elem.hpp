@@ -44,7 +44,7 @@ __device__ __forceinline__ void store_vec(typename E::T *p, const Vec<E, N> &v) 
 // The same for 16 bytes at an address aligned to one element only (global
 // memory takes such accesses on gfx950), and for data that is read or written
 // once and need not stay in the caches.
-typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <typename E, int N>
 __device__ __forceinline__ Vec<E, N> load_any(const typename E::T *p) {
     if constexpr (sizeof(Vec<E, N>) == 16)

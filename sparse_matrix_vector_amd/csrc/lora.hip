@@ -58,12 +58,12 @@ struct Frag<BF16> {
     }
 };
 
-// Elements c .. c + 7 of a row of n as 16 bytes.  VEC (n a multiple of 8, the
-// row 16-byte aligned): no branch, past the end the row's last 8 elements;
-// otherwise elements past the end are zero.
+// Elements c .. c + 7 of a row of n as 16 bytes.  VEC (n >= 8): one access of
+// any alignment and no branch; near or past the end the row's last 8 elements,
+// from n - 8 on.  Otherwise elements past the end are zero.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load8(const unsigned short *__restrict__ row, int c, int n) {
-    if (VEC) return *reinterpret_cast<const u32x4 *>(row + min(c, n - 8));
+    if (VEC) return *reinterpret_cast<const u32x4_any *>(row + min(c, n - 8));
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -188,14 +188,21 @@ __device__ __forceinline__ void shrink_steps(const unsigned short *const (&xr)[M
         }
     };
     auto multiply = [&](Step &st, int s) {
-        if (VEC && s * 64 + 64 > dim) {          // uniform: columns past the end count nothing
+        if (VEC && s * 64 + 64 > dim) {
+            // uniform: near the end both operands hold elements dim - 8 + e; those
+            // of them that belong to an earlier piece, or that lie before this
+            // one, count nothing
             const int k = s * 64 + q * 16;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int i = 0; i < 2; ++i) {
+                const int skip = k + 8 * i - min(k + 8 * i, dim - 8);   // elements to leave out
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int d = 0; d < 4; ++d) {
+                    const unsigned int keep = (2 * d >= skip ? 0xFFFFu : 0u) | (2 * d + 1 >= skip ? 0xFFFF0000u : 0u);
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) st.x[m][i][d] = k + 8 * i < dim ? st.x[m][i][d] : 0u;
+                    for (int m = 0; m < MT; ++m) st.x[m][i][d] &= keep;
+                }
+            }
         }
 #pragma unroll
         for (int j = 0; j < N; ++j)
@@ -353,7 +360,8 @@ __global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, in
     for (int j = 0; j < NJ; ++j) store_terms<E, NT, R>(a.terms, n_tok, row0, tile.z, 16 * j + n, v[j], e);
 }
 
-// Eight neighbouring results of one token (past the end the row's last ones).
+// Eight neighbouring results of one token.  VEC (n >= 8): near the end the
+// row's last 8; a lane whose columns overlap its neighbour's stores its own only.
 template <typename Y>
 struct RowPiece {
     typename Y::T v[8];
@@ -364,7 +372,7 @@ __device__ __forceinline__ void load_piece(RowPiece<Y> &r, const typename Y::T *
         constexpr int PER = 16 / (int)sizeof(typename Y::T);
 #pragma unroll
         for (int i = 0; i < 8; i += PER) {
-            const Vec<Y, PER> t = load_vec<Y, PER>(p + min(c, n - 8) + i);
+            const Vec<Y, PER> t = load_any<Y, PER>(p + min(c, n - 8) + i);
 #pragma unroll
             for (int k = 0; k < PER; ++k) r.v[i + k] = t.v[k];
         }
@@ -375,19 +383,20 @@ __device__ __forceinline__ void load_piece(RowPiece<Y> &r, const typename Y::T *
 }
 template <typename Y, bool VEC>
 __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const float (&v)[8]) {
-    if (VEC) {
+    if (VEC && c + 8 <= n) {
         constexpr int PER = 16 / (int)sizeof(typename Y::T);
 #pragma unroll
         for (int i = 0; i < 8; i += PER) {
             Vec<Y, PER> r;
 #pragma unroll
             for (int k = 0; k < PER; ++k) r.v[k] = (typename Y::T)v[i + k];
-            store_vec<Y, PER>(p + c + i, r);
+            store_any<Y, PER>(p + c + i, r);
         }
     } else {
+        const int at = VEC ? n - 8 : c;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < n) p[c + i] = (typename Y::T)v[i];
+            if (at + i >= c && at + i < n) p[at + i] = (typename Y::T)v[i];
     }
 }
 
@@ -748,10 +757,6 @@ spmv_status check_common(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_a
 
 constexpr int shrink_tiles(int nj) { return nj == 8 ? 2 : 4; }   // the waves' sums in LDS: 3 KB per tile and 16 ranks
 
-bool rows16(const void *p, int64_t ld, int64_t dim, int64_t per = 8) {
-    return aligned16(p) && ld % per == 0 && dim % 8 == 0;
-}
-
 template <typename F>
 spmv_status by_rank(int max_rank, F f) {
     switch (rank_tiles(max_rank)) {
@@ -807,7 +812,7 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
                           static_cast<float *>(workspace), nullptr, nullptr};
     st = by_half(dtype, [&](auto e) {
         return by_rank(max_rank, [&](auto nj) {
-            return by_bool(rows16(x, ldx, n_in) && aligned16(A), [&](auto vec) {
+            return by_bool(n_in >= 8, [&](auto vec) {
                 constexpr int NJ = decltype(nj)::value;
                 constexpr bool VEC = decltype(vec)::value;
                 const int grid = (n_tiles + 3) / 4 * 4 * split;
@@ -823,15 +828,13 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
         });
     });
     if (st != SPMV_OK) return st;
-    const int64_t yper = 16 / (int64_t)dtype_size(y_dtype);
-    const bool vec_y = rows16(y, ldy, n_out, yper) && (!y_in || rows16(y_in, ldyin, n_out, yper)) && aligned16(B);
     const int64_t pieces = ceil_div(n_out, 4 * LR_WAVE_COLS);
     if (n_tiles * pieces > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "the launch does not fit int32");
     const int grid = (int)(n_tiles * pieces);
     return by_half(dtype, [&](auto e) {
         typedef decltype(e) E;
         return by_rank(max_rank, [&](auto nj) {
-            return by_bool(vec_y, [&](auto vec) {
+            return by_bool(n_out >= 8, [&](auto vec) {
                 constexpr int NJ = decltype(nj)::value;
                 constexpr bool VEC = decltype(vec)::value;
                 auto go = [&](auto yt, auto nt) {
@@ -872,8 +875,7 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
     const size_t hb = h_bytes(n_tok, max_rank), tb = terms_bytes(n_tok, max_rank);
     char *w = static_cast<char *>(workspace);
     const auto *xs = static_cast<const unsigned short *>(x), *dys = static_cast<const unsigned short *>(dy);
-    const bool vec = rows16(x, ldx, n_in) && rows16(dy, lddy, n_out) && aligned16(A) && aligned16(B) && aligned16(dA) &&
-                     aligned16(dB);
+    const bool vec = n_in >= 8 && n_out >= 8;
     const int4 *tl = reinterpret_cast<const int4 *>(tiles);
     unsigned short *terms[2];
     int *exps[2];

@@ -63,7 +63,8 @@ def _bits(dt, ydt):
 SHAPES = [(1, 64, 64, 1, 1), (1, 4096, 512, 4, 16), (3, 8, 8, 2, 8), (17, 1000, 1504, 3, 8), (40, 136, 648, 5, 24),
           (61, 2048, 1024, 40, 64), (200, 33, 77, 3, 5), (150, 515, 130, 2, 33), (70, 256, 264, 2, 128),
           (33, 264, 1032, 9, 100), (16, 64, 1, 2, 4), (31, 1, 64, 2, 4), (700, 1032, 520, 4, 16), (600, 200, 1048, 2, 64),
-          (520, 129, 130, 1, 100), (513, 4096, 64, 8, 24)]
+          (520, 129, 130, 1, 100), (513, 4096, 64, 8, 24), (45, 9, 131, 2, 8), (45, 7, 515, 2, 8), (45, 515, 7, 2, 8),
+          (45, 1031, 129, 2, 20), (40, 8, 8, 2, 3)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -164,7 +165,8 @@ def test_bad_token_stays_alone():
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 64, 64, 1, 1), (300, 1000, 1504, 3, 8), (500, 136, 520, 4, 24), (77, 33, 70, 2, 5),
                                    (260, 512, 128, 1, 64), (90, 128, 264, 3, 128), (600, 64, 64, 20, 16),
-                                   (2100, 1040, 1096, 2, 32), (1500, 72, 64, 3, 48), (700, 2560, 2056, 1, 16)])
+                                   (2100, 1040, 1096, 2, 32), (1500, 72, 64, 3, 48), (700, 2560, 2056, 1, 16), (200, 1031, 515, 2, 16), (80, 9, 7, 2, 4),
+                                   (600, 517, 135, 2, 32)])
 def test_grad(shape, dt):
     T, K, N, n, r = shape
     s = _make(T, K, N, n, r, dt, seed=T)
