@@ -98,6 +98,11 @@ __device__ __forceinline__ int rank_of(const int *ranks, int a, int max_rank) {
 
 constexpr int SHRINK_WAVES = 4;
 
+// The token of sorted row i; whatever the plan holds, one of the batch's.
+__device__ __forceinline__ int token_of(const int *__restrict__ order, int i, int n_tok) {
+    return (int)min((unsigned)order[i], (unsigned)(n_tok - 1));
+}
+
 // The rows of one workgroup: a plan tile, or MT tiles of a group from every
 // MT-th one on (the others of the group have nothing to do).  Workgroup `id`
 // takes tile MT * (id % n) + id / n, n = tiles / MT: those with work come first
@@ -113,13 +118,15 @@ __device__ __forceinline__ Block block_of(const int4 *__restrict__ tiles, int n_
         id = MT * (id % n) + id / n;
     }
     if (id >= n_tiles) return {-1, 0, 0};
-    const int4 t = tiles[id];
+    int4 t = tiles[id];
+    t.y = min(max(t.y, 0), n_tok);
+    t.z = min(min(t.z, t.y + LR_TILE), n_tok);
     Block b = {(unsigned)t.x < (unsigned)n_adapters ? t.x : -1, t.y, t.z};
     if (MT > 1) {
-        if ((t.y - t.w) % (LR_TILE * MT) != 0)
+        if ((unsigned)(t.y - t.w) % (LR_TILE * MT) != 0)
             b.end = b.begin;
         else if (t.z > t.y)
-            b.end = min(t.y + LR_TILE * MT, b.group >= 0 ? offsets[b.group + 1] : n_tok);
+            b.end = min(min(t.y + LR_TILE * MT, n_tok), b.group >= 0 ? offsets[b.group + 1] : n_tok);
     }
     return b;
 }
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(int n_tok, in
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const unsigned short *xr[MT], *wr[NJ];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xr[m] = a.x + (int64_t)order[min(blk.begin + 16 * m + n, blk.end - 1)] * a.ldx;
+    for (int m = 0; m < MT; ++m) xr[m] = a.x + (int64_t)token_of(order, min(blk.begin + 16 * m + n, blk.end - 1), n_tok) * a.ldx;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
         wr[j] = a.W + ((int64_t)blk.group * max_rank + min(16 * j + n, max_rank - 1)) * a.dim;
@@ -333,7 +340,9 @@ __global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, in
                                                    const int4 *__restrict__ tiles, ShrinkArg a0, ShrinkArg a1) {
     constexpr int R = 16 * NJ, NT = grad_terms<E>();
     const ShrinkArg &a = blockIdx.y ? a1 : a0;
-    const int4 tile = tiles[blockIdx.x];
+    int4 tile = tiles[blockIdx.x];
+    tile.y = min(max(tile.y, 0), n_tok);
+    tile.z = min(min(tile.z, tile.y + LR_TILE), n_tok);
     if ((unsigned)tile.x >= (unsigned)n_adapters || tile.y >= tile.z) return;
     if (rank_of(ranks, tile.x, max_rank) == 0) return;
     const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
@@ -430,7 +439,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tok[m][i] = order[min(blk.begin + 16 * m + 4 * q + i, blk.end - 1)];
+        for (int i = 0; i < 4; ++i) tok[m][i] = token_of(order, min(blk.begin + 16 * m + 4 * q + i, blk.end - 1), n_tok);
     if (y_in) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -603,7 +612,7 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
     int tok[8];
     auto load_tok = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tok[i] = order[min(t + 8 * q + i, t1 - 1)];
+        for (int i = 0; i < 8; ++i) tok[i] = token_of(order, min(t + 8 * q + i, t1 - 1), n_tok);
     };
     auto load_rows = [&](u32x4(&r)[8]) {
 #pragma unroll

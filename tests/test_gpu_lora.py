@@ -294,6 +294,26 @@ def test_two_streams_at_once():
     assert all(torch.equal(y, want) for y, _ in outs)
 
 
+def test_a_plan_that_was_never_built_reads_and_writes_inside():
+    """Any contents of the plan arrays: rows outside x and y are not touched."""
+    T, K, N, n, r = 40, 64, 96, 3, 8
+    s = _make(T, K, N, n, r, "f16", seed=2, ranks="full")
+    p = S.RoutePlan(T, 1, n)
+    rng = np.random.default_rng(4)
+    for arr in (p.order, p.offsets, p.tiles):
+        bad = rng.choice([-2 ** 31, -7, 0, 5, 39, 40, 1000, 2 ** 31 - 1], arr.numel()).astype(np.int32)
+        arr.copy_(torch.from_numpy(bad).cuda().view(arr.shape))
+    yb = torch.full((T + 2, N), -3.0, device="cuda")
+    for fn in (lambda: S.lora_apply(s["ranks_t"], s["scale"], s["A"], s["B"], p.order, p.offsets, p.tiles, s["x"], None,
+                                    yb[1:T + 1], s["ws"]),
+               lambda: S.lora_grad(s["ranks_t"], s["scale"], s["A"], s["B"], p.order, p.offsets, p.tiles, s["x"],
+                                   torch.zeros(T, N, device="cuda").half(), torch.empty(n, r, K, device="cuda"),
+                                   torch.empty(n, r, N, device="cuda"), s["ws"])):
+        fn()
+        torch.cuda.synchronize()
+        assert (yb[0] == -3).all() and (yb[T + 1] == -3).all()
+
+
 def test_refusals_of_shapes():
     s = _make(8, 64, 64, 2, 8, "f16", seed=1)
     y = torch.zeros(8, 64, device="cuda")
