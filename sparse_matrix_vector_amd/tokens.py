@@ -24,6 +24,7 @@ _WORD = (torch.uint32, torch.int32)                     # packed code words
 _BYTE = (torch.int8, torch.uint8)
 _CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _FUNCS = {}
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _func(name):
@@ -49,11 +50,11 @@ def _launch(device, stream, name, *args):
     current, since kernels and streams belong to a device."""
     index = device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        status = _func(name)(*args, stream)
+    if _current_device() == index:
+        status = (_FUNCS.get(name) or _func(name))(*args, stream)
     else:
         with torch.cuda.device(device):
             status = _func(name)(*args, stream)
@@ -121,11 +122,16 @@ def _rows(t, dtype, name, n, width, device):
 
 
 def _matrix(t, name):
-    """(device, rows, width) of a 2-D CUDA tensor."""
+    """(device, rows, width, device pointer, row stride) of a 2-D CUDA tensor
+    whose rows are contiguous."""
     d = _device(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    return d, t.shape[0], t.shape[1]
+    n, width = t.shape
+    ld, one = t.stride()
+    if n > 1 and ld < width or one != 1 and width > 1:
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return d, n, width, t.data_ptr(), ld if n > 1 else width
 
 
 def _code(t, name):
@@ -166,9 +172,10 @@ def macko_spmm_workspace_size(n_groups, n_rows, n_cols, n_tok) -> int:
 
 
 def _spmm(name, n_rows, n_cols, bdelta, mrow_ptr, codes, vals, plan, alpha, x, beta, y, workspace, tok_offsets, stream):
-    d, n, _ = _matrix(x, "x")
+    d, n, width, xp, ldx = _matrix(x, "x")
+    if width != n_cols or x.dtype not in _HALF:
+        _rows(x, _HALF, "x", n, n_cols, d)                    # says which
     n_groups = 1 if tok_offsets is None else tok_offsets.numel() - 1
-    xp, ldx = _rows(x, _HALF, "x", n, n_cols, d)
     yp, ldy = _rows(y, (torch.float16, _F32), "y", n, n_rows, d)
     pp, pb = _ws(plan, d)
     if pb < 4 * n_groups * n_rows * ((n_cols + 255) // 256 + 1):
@@ -261,8 +268,7 @@ def _top_k(pos, n_tok):
 def route_gather(x, pos, xs, weights=None, stream=None):
     """xs[pos[t, c]] = weights[t, c] * x[t]; pos: [tokens, top_k]."""
     k = _top_k(pos, x.shape[0])
-    d, n, dim = _matrix(x, "x")
-    xp, ldx = _rows(x, x.dtype, "x", n, dim, d)
+    d, n, dim, xp, ldx = _matrix(x, "x")
     sp, lds = _rows(xs, x.dtype, "xs", n * k, dim, d)
     _launch(d, stream, "route_gather", n, k, dim, _code(x, "x"), _ptr(pos, _I32, "pos", n * k, d),
             _opt(weights, _F32, "weights", n * k, d), xp, ldx, sp, lds)
@@ -272,9 +278,8 @@ def route_gather(x, pos, xs, weights=None, stream=None):
 def route_combine(ys, pos, y, weights=None, stream=None):
     """y[t] = sum_c weights[t, c] * ys[pos[t, c]]; pos: [tokens, top_k]."""
     k = _top_k(pos, y.shape[0])
-    d, n, dim = _matrix(y, "y")
+    d, n, dim, yp, ldy = _matrix(y, "y")
     sp, lds = _rows(ys, y.dtype, "ys", n * k, dim, d)
-    yp, ldy = _rows(y, y.dtype, "y", n, dim, d)
     _launch(d, stream, "route_combine", n, k, dim, _code(y, "y"), _ptr(pos, _I32, "pos", n * k, d),
             _opt(weights, _F32, "weights", n * k, d), sp, lds, yp, ldy)
     return y
@@ -283,8 +288,7 @@ def route_combine(ys, pos, y, weights=None, stream=None):
 def route_combine_grad(dy, ys, pos, weights, dys, dw, stream=None):
     """dys[pos[t, c]] = weights[t, c] * dy[t]; dw[t, c] = <ys[pos[t, c]], dy[t]>."""
     k = _top_k(pos, dy.shape[0])
-    d, n, dim = _matrix(dy, "dy")
-    gp, ldg = _rows(dy, dy.dtype, "dy", n, dim, d)
+    d, n, dim, gp, ldg = _matrix(dy, "dy")
     sp, lds = _rows(ys, dy.dtype, "ys", n * k, dim, d)
     op, ldo = _rows(dys, dy.dtype, "dys", n * k, dim, d)
     _launch(d, stream, "route_combine_grad", n, k, dim, _code(dy, "dy"), gp, ldg, sp, lds, _ptr(pos, _I32, "pos", n * k, d),
@@ -330,7 +334,7 @@ def lora_workspace_size(n_tok, max_rank) -> int:
 
 
 def _lora_args(ranks, scale, A, B, order, offsets, tiles, x):
-    d, n, n_in = _matrix(x, "x")
+    d, n, n_in, xp, ldx = _matrix(x, "x")
     dt = x.dtype
     if dt is not torch.float16 and dt is not torch.bfloat16:
         raise TypeError(f"x must be float16 or bfloat16, got {dt}")
@@ -338,9 +342,10 @@ def _lora_args(ranks, scale, A, B, order, offsets, tiles, x):
         raise ValueError(f"A and B must be [adapters, rank, width], got {tuple(A.shape)} and {tuple(B.shape)}")
     n_ad, r, width = A.shape
     n_out = B.shape[2]
+    if width != n_in:
+        raise ValueError(f"x must have {width} columns like A, got {n_in}")
     if offsets.numel() != n_ad + 1 or order.numel() != n:
         raise ValueError("the plan is not one of x's tokens and A's adapters")
-    xp, ldx = _rows(x, dt, "x", n, width, d)
     return d, (n, n_in, n_out, n_ad, r, _opt(ranks, _I32, "ranks", n_ad, d), _opt(scale, _F32, "scale", n_ad, d),
                _ptr(A, dt, "A", 0, d), _ptr(B, dt, "B", 0, d), _CODE[dt], _ptr(order, _I32, "order", n, d),
                _ptr(offsets, _I32, "offsets", n_ad + 1, d), _ptr(tiles, _I32, "tiles", 0, d), tiles.numel() // 4, xp, ldx)
