@@ -369,8 +369,10 @@ __global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, in
     for (int j = 0; j < NJ; ++j) store_terms<E, NT, R>(a.terms, n_tok, row0, tile.z, 16 * j + n, v[j], e);
 }
 
-// Eight neighbouring results of one token.  VEC (n >= 8): near the end the
-// row's last 8; a lane whose columns overlap its neighbour's stores its own only.
+// Eight neighbouring results of one token, read and written once (non-temporal:
+// 4093 tokens of 12288 bf16 results, inputs from HBM, 75.6 against 81.8 us).
+// VEC (n >= 8): near the end the row's last 8; a lane whose columns overlap its
+// neighbour's stores its own only.
 template <typename Y>
 struct RowPiece {
     typename Y::T v[8];
@@ -381,7 +383,7 @@ __device__ __forceinline__ void load_piece(RowPiece<Y> &r, const typename Y::T *
         constexpr int PER = 16 / (int)sizeof(typename Y::T);
 #pragma unroll
         for (int i = 0; i < 8; i += PER) {
-            const Vec<Y, PER> t = load_any<Y, PER>(p + min(c, n - 8) + i);
+            const Vec<Y, PER> t = load_once<Y, PER>(p + min(c, n - 8) + i);
 #pragma unroll
             for (int k = 0; k < PER; ++k) r.v[i + k] = t.v[k];
         }
@@ -399,7 +401,7 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
             Vec<Y, PER> r;
 #pragma unroll
             for (int k = 0; k < PER; ++k) r.v[k] = (typename Y::T)v[i + k];
-            store_any<Y, PER>(p + c + i, r);
+            store_once<Y, PER>(p + c + i, r);
         }
     } else {
         const int at = VEC ? n - 8 : c;
