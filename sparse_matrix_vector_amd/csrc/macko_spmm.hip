@@ -744,13 +744,23 @@ Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok) {
     c.tiles = (int)ceil_div(t16, c.nt);
     c.width = n_groups > 1 ? c.nt : (int)ceil_div(t16, c.tiles);
     c.split = 1;
-    // parts of the columns: fewest rounds of slabs over the resident
-    // workgroups, each further part costing the traffic of its sums
-    const int64_t wgs = n_groups * ceil_div(n_rows, BlockShape<4>::ROWS) * c.tiles;
+    // Parts of the columns, by an estimate of the time in us: a slab takes
+    // longer the more workgroups share a CU (`alone` + `each` per resident one,
+    // rough figures of this kernel's own times), starting a workgroup is counted
+    // as two slabs, joining as a launch and the traffic of the parts' sums at
+    // 4 TB/s.  Against counting rounds of slabs only: 4096 x 4096, 10 % kept, 64
+    // tokens 26.3 -> 16.3 us (16 parts were too many); 12288 x 12288, 30 % kept,
+    // 64 tokens 68.7 -> 63.0, 128 tokens 116.8 -> 105.6; 513 tokens the same.
+    const int fit = c.nt < 8 ? 4 : 2;                       // workgroups per CU
+    const double alone = c.nt == 2 ? 0.8 : c.nt == 4 ? 1.0 : c.nt == 8 ? 1.2 : 1.9;
+    const double each = c.nt == 2 ? 0.95 : c.nt == 4 ? 1.0 : c.nt == 8 ? 1.5 : 2.2;
     double best = 1e30;
     for (int s = 1; s <= 16 && s <= slabs; ++s) {
-        const double cost = (double)ceil_div(wgs * s, 256 * (c.nt < 8 ? 4 : 2)) * (double)ceil_div(slabs, s) +
-                            (s > 1 ? 1.0 + s * (double)n_tok * (double)n_rows * 4e-7 : 0.0);
+        const int64_t wgs = n_groups * ceil_div(n_rows, BlockShape<4>::ROWS) * c.tiles * s, full = wgs / (256 * fit);
+        const int64_t rest = ceil_div(wgs - full * 256 * fit, 256);
+        const double slab = (double)full * (alone + each * fit) + (rest ? alone + each * (double)rest : 0.0);
+        const double cost = slab * (double)(ceil_div(slabs, s) + 2) +
+                            (s > 1 ? 4.0 + s * (double)n_tok * (double)n_rows * 2e-6 : 0.0);
         if (cost < best) best = cost, c.split = s;
     }
     return c;
