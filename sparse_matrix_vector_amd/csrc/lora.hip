@@ -413,7 +413,7 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
 
 // One workgroup: a block of tokens and 512 columns, 128 per wave; the columns
 // of a block are neighbours in the launch and together move whole rows of y.
-template <typename E, typename Y, int NJ, int NT, int MT, bool VEC>
+template <typename E, typename Y, int NJ, int NT, bool VEC>
 __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, int max_rank, int split,
                                                      const int *__restrict__ ranks,
                                                      const float *__restrict__ scale,
@@ -424,10 +424,10 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
                                                      typename Y::T *y, int64_t ldy) {
     typedef typename Frag<E>::V V;
     constexpr int R = 16 * NJ, LD = R + 8;
-    __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE * MT][LD];
-    __shared__ float unscale[LR_TILE * MT];
+    __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE][LD];
+    __shared__ float unscale[LR_TILE];
     const int id = blockIdx.x / pieces, piece = blockIdx.x - id * pieces;
-    const Block blk = block_of<MT>(tiles, n_tiles, id, offsets, n_tok, n_adapters);
+    const Block blk = block_of<1>(tiles, n_tiles, id, offsets, n_tok, n_adapters);
     if (blk.begin >= blk.end) return;
     const int rank = blk.group >= 0 ? rank_of(ranks, blk.group, max_rank) : 0;
     if (rank == 0 && y_in == y) return;
@@ -436,30 +436,22 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
     const int c0 = piece * (4 * LR_WAVE_COLS) + wv * LR_WAVE_COLS + 8 * n;
 
     // y_in of the lane's rows is in flight over everything else
-    int64_t tok[MT][4];
-    RowPiece<Y> base[MT][4];
+    int64_t tok[4];
+    RowPiece<Y> base[4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tok[m][i] = token_of(order, min(blk.begin + 16 * m + 4 * q + i, blk.end - 1), n_tok);
+    for (int i = 0; i < 4; ++i) tok[i] = token_of(order, min(blk.begin + 4 * q + i, blk.end - 1), n_tok);
     if (y_in) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) load_piece<Y, VEC>(base[m][i], y_in + tok[m][i] * ldyin, c0, dim);
+        for (int i = 0; i < 4; ++i) load_piece<Y, VEC>(base[i], y_in + tok[i] * ldyin, c0, dim);
     } else {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) base[m][i].v[c] = (typename Y::T)0.0f;
+            for (int c = 0; c < 8; ++c) base[i].v[c] = (typename Y::T)0.0f;
     }
-    f32x4 acc[MT][8];
+    f32x4 acc[8];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < 8; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (rank > 0) {
         const unsigned short *Br = B + (int64_t)blk.group * max_rank * dim;
         u32x4 r[8];
@@ -470,33 +462,30 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
         load_b(NJ == 1 ? 8 * (q & 1) : 8 * q);
         // 16 lanes per token: the partial sums of h in order, the token's
         // largest |h|, and the scaled terms
+        const int t = (threadIdx.x >> 4), l = threadIdx.x & 15;
+        const int64_t row = min(blk.begin + t, blk.end - 1);
+        float v[NJ], top = 0.0f;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int t = 16 * m + (threadIdx.x >> 4), l = threadIdx.x & 15;
-            const int64_t row = min(blk.begin + t, blk.end - 1);
-            float v[NJ], top = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) v[j] = 0.0f;
-            const float *hr = h + row * R + l;
+        for (int j = 0; j < NJ; ++j) v[j] = 0.0f;
+        const float *hr = h + row * R + l;
 #pragma unroll 4
-            for (int s = 0; s < split; ++s)
+        for (int s = 0; s < split; ++s)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    if (16 * j < rank) v[j] += hr[(int64_t)s * n_tok * R + 16 * j];
+            for (int j = 0; j < NJ; ++j)
+                if (16 * j < rank) v[j] += hr[(int64_t)s * n_tok * R + 16 * j];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) top = fmaxf(top, fabsf(v[j]));
+        for (int j = 0; j < NJ; ++j) top = fmaxf(top, fabsf(v[j]));
 #pragma unroll
-            for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-            const int e = E::CODE == SPMV_F16 ? scale_exponent(top) : 0;
+        for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        const int e = E::CODE == SPMV_F16 ? scale_exponent(top) : 0;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                unsigned short terms[NT];
-                split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(v[j], e) : v[j], terms);
+        for (int j = 0; j < NJ; ++j) {
+            unsigned short terms[NT];
+            split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(v[j], e) : v[j], terms);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) hs[i][t][16 * j + l] = terms[i];
-            }
-            if (l == 0) unscale[t] = ldexpf(scale ? scale[blk.group] : 1.0f, -e);
+            for (int i = 0; i < NT; ++i) hs[i][t][16 * j + l] = terms[i];
         }
+        if (l == 0) unscale[t] = ldexpf(scale ? scale[blk.group] : 1.0f, -e);
         __syncthreads();
         if constexpr (NJ == 1) {
             // up to 16 ranks: the terms share the contraction, eight ranks
@@ -512,18 +501,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int term = 2 * s + (q >> 1);
-                u32x4 a[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    a[m] = u32x4{0u, 0u, 0u, 0u};
-                    if (term < NT)
-                        a[m] = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][16 * m + n][8 * (q & 1)]);
-                }
+                u32x4 a = {0u, 0u, 0u, 0u};
+                if (term < NT)
+                    a = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][n][8 * (q & 1)]);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const V b = __builtin_bit_cast(V, column_of(r, c));
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) acc[m][c] = Frag<E>::mma(__builtin_bit_cast(V, a[m]), b, acc[m][c]);
+                    acc[c] = Frag<E>::mma(__builtin_bit_cast(V, a), b, acc[c]);
                 }
             }
         } else {
@@ -536,40 +520,33 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
 #pragma unroll
                         for (int d = 0; d < 4; ++d) r[i][d] = jb + i < rank ? r[i][d] : 0u;
                 }
-                V a[MT][NT];
+                V a[NT];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        a[m][i] = __builtin_bit_cast(V, *reinterpret_cast<const u32x4 *>(&hs[i][16 * m + n][jb]));
+                for (int i = 0; i < NT; ++i)
+                    a[i] = __builtin_bit_cast(V, *reinterpret_cast<const u32x4 *>(&hs[i][n][jb]));
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const V b = __builtin_bit_cast(V, column_of(r, c));
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) acc[m][c] = Frag<E>::mma(a[m][i], b, acc[m][c]);
+                    for (int i = 0; i < NT; ++i) acc[c] = Frag<E>::mma(a[i], b, acc[c]);
                 }
             }
         }
     }
     if (c0 >= dim) return;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * q + i;
+        if (blk.begin + t >= blk.end) break;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 16 * m + 4 * q + i;
-            if (blk.begin + t >= blk.end) break;
-            float v[8];
+        for (int c = 0; c < 8; ++c) v[c] = (float)base[i].v[c];
+        if (rank > 0) {
+            const float f = unscale[t];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = (float)base[m][i].v[c];
-            if (rank > 0) {
-                const float f = unscale[t];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] = fmaf(f, acc[m][c][i], v[c]);
-            }
-            store_row8<Y, VEC>(y + tok[m][i] * ldy, c0, dim, v);
+            for (int c = 0; c < 8; ++c) v[c] = fmaf(f, acc[c][i], v[c]);
         }
+        store_row8<Y, VEC>(y + tok[i] * ldy, c0, dim, v);
     }
 }
 
@@ -715,9 +692,17 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
 // ---------------------------------------------------------------------------
 int rank_tiles(int max_rank) { return max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : max_rank <= 64 ? 4 : 8; }
 
-// Blocks of 4 tiles where adapters have 64 tokens or more on average: an
-// operand of A or B then serves 4 tiles.
-bool wide_blocks(int64_t n_tok, int64_t n_adapters, int max_rank) { return max_rank <= 32 && n_tok >= 64 * n_adapters && n_tok >= 512; }
+constexpr int LR_WIDE = 4;
+
+// lora_grad's products take blocks of LR_WIDE tiles, an operand of A or B serving all
+// four, where that still fills the card and adapters have 64 tokens or more on
+// average.  Rank 32, 4096 x 4096, 8 adapters: 16384 tokens 149 us (181 in single
+// tiles), 8192 tokens 101 (109), 4096 tokens 87 (73).  Rank 16: 16384 tokens 122
+// (128), 8192 tokens 92 (75).  At rank 64 the registers do not allow it.
+// lora_apply is better off with single tiles (8192 tokens 69 us, 82 in blocks).
+bool wide_blocks(int64_t n_tok, int64_t n_adapters, int max_rank) {
+    return max_rank <= 32 && n_tok >= 64 * n_adapters && n_tok >= (max_rank <= 16 ? 16384 : 8192);
+}
 
 // Workgroups that share a block's contraction.  Whoever reads h adds the parts,
 // once per 512 columns of the result, so there are only as many as it takes to
@@ -765,8 +750,6 @@ spmv_status check_common(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_a
     if (!aligned16(workspace)) return fail(SPMV_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
     return SPMV_OK;
 }
-
-constexpr int shrink_tiles(int nj) { return nj == 8 ? 2 : 4; }   // the waves' sums in LDS: 3 KB per tile and 16 ranks
 
 template <typename F>
 spmv_status by_rank(int max_rank, F f) {
@@ -816,8 +799,7 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
     if (n_tok == 0) return SPMV_OK;
     if (!x || !y) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
     hipStream_t s = as_stream(stream);
-    const bool wide = wide_blocks(n_tok, n_adapters, max_rank);
-    const int split = split_of(n_tok, n_tiles / (wide ? 4 : 1), n_in);
+    const int split = split_of(n_tok, n_tiles, n_in);
     const int4 *tl = reinterpret_cast<const int4 *>(tiles);
     const ShrinkArg sa = {static_cast<const unsigned short *>(x), static_cast<const unsigned short *>(A), ldx, n_in,
                           static_cast<float *>(workspace), nullptr, nullptr};
@@ -826,13 +808,8 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
             return by_bool(n_in >= 8, [&](auto vec) {
                 constexpr int NJ = decltype(nj)::value;
                 constexpr bool VEC = decltype(vec)::value;
-                const int grid = (n_tiles + 3) / 4 * 4 * split;
-                if (wide)
-                    k_lora_shrink<decltype(e), NJ, shrink_tiles(NJ), VEC>
-                        <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 1, sa, sa);
-                else
-                    k_lora_shrink<decltype(e), NJ, 1, VEC>
-                        <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 1, sa, sa);
+                k_lora_shrink<decltype(e), NJ, 1, VEC><<<n_tiles * split, 64 * SHRINK_WAVES, 0, s>>>(
+                    n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 1, sa, sa);
                 SPMV_LAUNCHED("k_lora_shrink");
                 return SPMV_OK;
             });
@@ -850,14 +827,11 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
                 constexpr bool VEC = decltype(vec)::value;
                 auto go = [&](auto yt, auto nt) {
                     typedef decltype(yt) Y;
-                    auto run = [&](auto mt) {
-                        k_lora_expand<E, Y, NJ, decltype(nt)::value, decltype(mt)::value, VEC><<<grid, 256, 0, s>>>(
-                            n_tok, n_adapters, max_rank, split, ranks, scale, order, offsets, tl, n_tiles,
-                            static_cast<const float *>(workspace), static_cast<const unsigned short *>(B), n_out,
-                            (int)pieces,
-                            static_cast<const typename Y::T *>(y_in), ldyin, static_cast<typename Y::T *>(y), ldy);
-                    };
-                    run(std::integral_constant<int, 1>{});
+                    k_lora_expand<E, Y, NJ, decltype(nt)::value, VEC><<<grid, 256, 0, s>>>(
+                        n_tok, n_adapters, max_rank, split, ranks, scale, order, offsets, tl, n_tiles,
+                        static_cast<const float *>(workspace), static_cast<const unsigned short *>(B), n_out,
+                        (int)pieces,
+                        static_cast<const typename Y::T *>(y_in), ldyin, static_cast<typename Y::T *>(y), ldy);
                 };
                 if (y_dtype == SPMV_F32)
                     go(F32{}, std::integral_constant<int, E::CODE == SPMV_BF16 ? 3 : 2>{});
@@ -882,7 +856,7 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
     if (!dA || !dB || (n_tok > 0 && (!x || !dy))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
     hipStream_t s = as_stream(stream);
     const bool wide = wide_blocks(n_tok, n_adapters, max_rank);
-    const int split = split_of(n_tok, 2 * n_tiles / (wide ? 4 : 1), std::min(n_in, n_out));
+    const int split = split_of(n_tok, 2 * n_tiles, std::min(n_in, n_out));   // 1 in wide blocks: n_tok alone sees to it
     const size_t hb = h_bytes(n_tok, max_rank), tb = terms_bytes(n_tok, max_rank);
     char *w = static_cast<char *>(workspace);
     const auto *xs = static_cast<const unsigned short *>(x), *dys = static_cast<const unsigned short *>(dy);
@@ -908,13 +882,14 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
                 if (n_tok > 0) {
                     ShrinkArg s0 = hx, s1 = gy;
                     if (split > 1) s0.terms = s1.terms = nullptr;
-                    const int grid = (n_tiles + 3) / 4 * 4 * split * 2;
-                    if (wide)
-                        k_lora_shrink<E, NJ, shrink_tiles(NJ), VEC>
-                            <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 2, s0, s1);
-                    else
-                        k_lora_shrink<E, NJ, 1, VEC>
-                            <<<grid, 64 * SHRINK_WAVES, 0, s>>>(n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 2, s0, s1);
+                    if (NJ <= 2 && wide) {
+                        constexpr int MT = NJ <= 2 ? LR_WIDE : 1;
+                        k_lora_shrink<E, NJ, MT, VEC><<<(n_tiles + MT - 1) / MT * MT * split * 2, 64 * SHRINK_WAVES, 0, s>>>(
+                            n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 2, s0, s1);
+                    } else {
+                        k_lora_shrink<E, NJ, 1, VEC><<<n_tiles * split * 2, 64 * SHRINK_WAVES, 0, s>>>(
+                            n_tok, n_adapters, max_rank, ranks, order, offsets, tl, n_tiles, split, 2, s0, s1);
+                    }
                     SPMV_LAUNCHED("k_lora_shrink");
                     if (split > 1) {
                         k_lora_terms<E, NJ><<<dim3(n_tiles, 2), 64, 0, s>>>(n_tok, n_adapters, max_rank, split, ranks, tl, hx,
@@ -922,7 +897,10 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
                         SPMV_LAUNCHED("k_lora_terms");
                     }
                 }
-                // few column blocks (one adapter): fewer rank tiles each, x read again from the caches
+                // Two rank tiles per workgroup share a reading of x; with few column
+                // blocks one each fills the card better.  Rank 32: 8192 tokens, 2048
+                // columns, 4 adapters (128 blocks) 58 us one each, 72 in twos; 2048
+                // tokens, 4096 columns, 32 adapters (2048 blocks) 109 and 98.
                 constexpr int JB = NJ < 2 ? NJ : 2;
                 const int64_t blocks = (int64_t)(oa.blocks + ob.blocks) * n_adapters;
                 if (blocks < 192)

@@ -166,7 +166,8 @@ def test_bad_token_stays_alone():
 @pytest.mark.parametrize("shape", [(1, 64, 64, 1, 1), (300, 1000, 1504, 3, 8), (500, 136, 520, 4, 24), (77, 33, 70, 2, 5),
                                    (260, 512, 128, 1, 64), (90, 128, 264, 3, 128), (600, 64, 64, 20, 16),
                                    (2100, 1040, 1096, 2, 32), (1500, 72, 64, 3, 48), (700, 2560, 2056, 1, 16), (200, 1031, 515, 2, 16), (80, 9, 7, 2, 4),
-                                   (600, 517, 135, 2, 32)])
+                                   (600, 517, 135, 2, 32), (8200, 136, 72, 5, 32),
+                                   (8199, 7, 265, 3, 20), (16390, 72, 40, 9, 12)])
 def test_grad(shape, dt):
     T, K, N, n, r = shape
     s = _make(T, K, N, n, r, dt, seed=T)
