@@ -1,8 +1,9 @@
 /*
  * spmv.h -- C ABI of the MI355X (gfx950) sparse matrix-vector library.
  *
- * Every entry point computes (a step of) y = alpha * A * x + beta * y, the
- * operation all four source pages turn on:
+ * Every entry point computes (a step of) y = alpha * A * x + beta * y, for one
+ * vector or, in the operators of many tokens at the end, for many; the
+ * operation is the one all four source pages turn on:
  *   - "Why SpMV needs CUDA optimisation" (codechina.net): CSR scalar and
  *     warp-per-row kernels (sections 2.1, 4.1), ELL and the CV-based format
  *     rule (sections 2.1-2.2);

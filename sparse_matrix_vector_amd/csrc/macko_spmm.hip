@@ -3,11 +3,11 @@
 //
 // With one token the product is a gather (macko.hip).  With more, every
 // decoded entry serves all tokens, so a piece of W is decoded into a dense
-// fp16 tile in LDS and multiplied with the matrix cores.  A wave owns 16 rows
-// and walks slabs of 256 columns: it clears its own 16 x 256 tile, decodes
-// into it, and runs eight 16x16x32 products per 16 tokens on it, so waves
-// never wait for each other; the waves of a workgroup take turns over the
-// slabs of the same rows and add their sums at the end, in order.
+// fp16 tile in LDS, a slab of 256 columns at a time, and multiplied with the
+// matrix cores (16x16x32, sums in fp32).  Two kernels: for few tokens a wave
+// owns 16 rows and its tile, and waves never wait for each other
+// (k_macko_spmm); for more, four waves share a tile of 64 rows and split the
+// tokens (k_macko_spmm_block).  Sums are added in a fixed order everywhere.
 //
 // A row's columns are known only after everything before them is decoded, so
 // a plan built once per weight (macko_spmm_plan) keeps, for each row and slab,
@@ -135,7 +135,8 @@ __device__ __forceinline__ int last8(int v) {
     return __builtin_amdgcn_update_dpp(quad, quad, DPP_ROW_SHL4, 0xf, 0x5, false);
 }
 
-// Plan: one wave per row walks the row's units 64 at a time.
+// Plan: one wave per row walks the row's units 64 at a time.  Built once per
+// weight; it reads the codes: 15 to 25 us for 12288 x 12288, half kept.
 template <int BD>
 __global__ __launch_bounds__(256) void k_macko_spmm_plan(int n_rows, int n_slabs, const int *__restrict__ mrp,
                                                          const unsigned int *__restrict__ codes,
@@ -252,7 +253,9 @@ __device__ __forceinline__ RowPair load_rows(const SpmmArg &a, int64_t row0, int
 
 // The units of one slab in registers: SM_STEPS of 8 lanes cover a slab of a
 // half pruned row, further ones are loaded while decoding.  No load hides
-// behind a branch, so they stay in flight over other work.
+// behind a branch, so they stay in flight over other work.  (Two steps: 12288 x
+// 12288 times 2 to 128, 30 % kept, 2 to 7 % faster; half kept times 513, 445
+// against 422 us.)
 constexpr int SM_STEPS = 3;
 template <int BD, bool I8>
 struct Stage {
@@ -406,8 +409,12 @@ __device__ __forceinline__ void wave_lds_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Workgroup: rows 16 blockIdx.y .. of group blockIdx.z, tokens 16 NT blockIdx.x ..
-// of that group, slabs wave, wave + WAVES, ...
+// Few tokens.  Workgroup: rows 16 blockIdx.y .. of group blockIdx.z, tokens
+// 16 NT blockIdx.x .. of that group, slabs wave, wave + WAVES, ...; the waves add
+// their sums at the end.  Bound by the latency of a slab's chain (plan word,
+// codes, scan, LDS, product), so small calls want many waves.  5.7 us for
+// 2048 x 2048 (half kept) times 5, of which about 3 are the launch; 38 us
+// for 12288 x 12288 (30 % kept) times 2, 116 MB at 3.0 TB/s.
 template <int BD, bool I8, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
     extern __shared__ __attribute__((aligned(16))) unsigned short lds[];
@@ -509,6 +516,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
 // from memory straight to the registers of the one wave that uses it, and a W
 // operand read from LDS serves all of the wave's tokens.  With fewer than four
 // token tiles the waves of one tile share out its columns instead.
+//
+// Per slab a workgroup clears 33 KB of LDS, scatters its entries two bytes at a
+// time and reads the tile once per wave; with decoding's integer work these
+// take turns between two barriers, hidden only by the CU's other workgroups.
+// 12288 x 12288, 30 % kept: 46 us times 32 (116 MB at 2.5 TB/s).  Half kept,
+// int8: 420 us times 513 (369 TFLOP/s counting every position): x comes from
+// L2 once per 64 rows, 2.4 GB.  Measured and not kept: x through LDS (580),
+// 128 rows per workgroup (495), two W tiles in turn (432 + join).
 // ---------------------------------------------------------------------------
 template <int NT>
 struct BlockShape {
@@ -667,7 +682,8 @@ __global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) vo
     }
 }
 
-// Adds the parts of k_macko_spmm_block in order.
+// Adds the parts of k_macko_spmm_block in order; bound by their traffic (513
+// tokens of 12288 rows: 20 us).
 template <bool I8>
 __global__ __launch_bounds__(256) void k_macko_spmm_join(SpmmArg a, int n_groups, int split,
                                                          const float *__restrict__ partial, int ldp) {

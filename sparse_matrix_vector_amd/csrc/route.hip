@@ -41,7 +41,8 @@ __device__ __forceinline__ int bin_of(int key, int n_groups) {
     return (unsigned)key < (unsigned)n_groups ? key : n_groups;
 }
 
-// Slots per bin of each chunk of the keys (several workgroups).
+// Slots per bin of each chunk of the keys (several workgroups): 4.7 us for 65528
+// slots, and 7.7 us for the sort after it; both are short chains of LDS steps.
 __global__ __launch_bounds__(1024) void k_route_count(int n_slots, int n_groups, int chunk,
                                                       const int *__restrict__ keys, int *__restrict__ counts) {
     extern __shared__ int hist[];
@@ -165,9 +166,8 @@ template <typename E, int VEC>
 constexpr int piece_accesses() { return VEC > 1 ? 4 : 8; }
 
 // xs[pos[t, c]] = w[t, c] * x[t]: a wave reads a piece of a token's row once and
-// writes it to every choice's place.  (By sorted rows each x row is read k
-// times, from beyond L2: 73 us for 8191 tokens of 2048 bf16 with k = 8, 268 MB
-// written.)
+// writes it to every choice's place: 54 us for 8191 tokens of 2048 bf16 with
+// k = 8 (302 MB, 5.6 TB/s).  By sorted rows, each x row read k times, 73 us.
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void k_route_gather(int n_tok, int n_slots, int k, int dim, int pieces,
                                                       const int *__restrict__ pos, const float *__restrict__ w,
@@ -205,7 +205,8 @@ __global__ __launch_bounds__(256) void k_route_gather(int n_tok, int n_slots, in
     }
 }
 
-// y[t] = sum over choices c (ascending) of w[t, c] * ys[pos[t, c]], rounded once.
+// y[t] = sum over choices c (ascending) of w[t, c] * ys[pos[t, c]], rounded once:
+// 54 us at the same sizes (302 MB, 5.6 TB/s).
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void k_route_combine(int n_tok, int n_slots, int k, int dim, int pieces,
                                                        const int *__restrict__ pos, const float *__restrict__ w,
@@ -263,7 +264,8 @@ __global__ __launch_bounds__(256) void k_route_combine(int n_tok, int n_slots, i
 }
 
 // dys[pos[t, c]] = w[t, c] * dy[t] and dw[t, c] = <ys[pos[t, c]], dy[t]>: one
-// workgroup per token, so each row of dy is read once per 8 choices.
+// workgroup per token, so each row of dy is read once per 8 choices: 106 us at
+// the same sizes (570 MB, 5.4 TB/s).
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void k_route_combine_grad(int n_slots, int k, int dim,
                                                             const typename E::T *__restrict__ dy, int64_t lddy,
