@@ -584,7 +584,7 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
     typedef typename Frag<E>::V V;
     constexpr int NT = grad_terms<E>();
     constexpr bool F = E::CODE == SPMV_F16;
-    __shared__ f32x4 sum[8][64];
+    __shared__ f32x4 sum[8][8][64];
     const int r0 = blockIdx.z * 16 * NJ;   // first rank of this workgroup
     const bool second = (int)blockIdx.x >= a0.blocks;
     const OuterArg &a = second ? a1 : a0;
@@ -670,17 +670,18 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
             if (t + 256 < t1) step(t + 256, rb, ra);
         }
     }
-    // waves add their sums one after the other, so the order is fixed
+    // the waves' sums, in wave order: wave w adds those of the products w
     const float f = scale ? scale[ad] : 1.0f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        for (int w = 0; w < 8; ++w) {
-            if (wv == w) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) sum[c][lane] = w == 0 ? acc[j][c] : sum[c][lane] + acc[j][c];
-            }
-            __syncthreads();
-        }
+        for (int c = 0; c < 8; ++c) sum[wv][c][lane] = acc[j][c];
+        __syncthreads();
+        f32x4 all = sum[0][wv][lane];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) all += sum[w][wv][lane];
+        sum[0][wv][lane] = all;
+        __syncthreads();
         // all 8 waves write: wave w the rows 4 q + (w & 3) of half the lanes' groups
         const int i = wv & 3;
         const int row = r0 + 16 * j + 4 * q + i;
@@ -688,7 +689,7 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
             float v[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                const f32x4 s4 = sum[c][lane];
+                const f32x4 s4 = sum[0][c][lane];
                 const float s1 = i == 0 ? s4[0] : i == 1 ? s4[1] : i == 2 ? s4[2] : s4[3];
                 v[c] = row < rank ? f * s1 : 0.0f;
             }
