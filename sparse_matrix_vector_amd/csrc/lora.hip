@@ -566,17 +566,19 @@ struct OuterArg {
     float *out;                // [n_adapters, max_rank, dim]
 };
 
-// Bound by the latency of the rows of x and dy, which few workgroups walk (one
-// adapter's 128 columns each): 8192 tokens of 4096 + 4096 bf16, rank 32,
-// 4 adapters 41 us (134 MB, 3.3 TB/s); 300 tokens at rank 8 7 us.  More workgroups would
-// have to add partial gradients.
+// Bound by the latency of the rows of x and dy, which few waves walk (a
+// workgroup has one adapter's 128 columns): 8192 tokens of 4096 + 4096 bf16,
+// rank 32, 4 adapters 39 us (134 MB, 3.4 TB/s); 300 tokens at rank 8 5.3 us.
+// More workgroups would have to add partial gradients; the terms loaded a step
+// ahead as well was 3 to 8 % slower (registers).
 // One workgroup: 128 columns of adapter blockIdx.y's gradient; blockIdx.x
 // counts the column blocks of the first product, then of the second, and
-// blockIdx.z blocks of NJ rank tiles out of the R / 16 of h.  The 8 waves take
+// blockIdx.z blocks of NJ rank tiles out of the R / 16 of h.  The waves take
 // turns over 32-token steps (two plan tiles), the next step's rows loading
-// over the current one's products, and their sums are added in order.
-template <typename E, int NJ, int R, bool VEC>
-__global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
+// over the current one's products, and their sums are added in order, each wave
+// those of its own columns.
+template <typename E, int NJ, int R, int WAVES, bool VEC>
+__global__ __launch_bounds__(64 * WAVES) void k_lora_outer(int n_tok, int max_rank,
                                                     const int *__restrict__ ranks,
                                                     const float *__restrict__ scale,
                                                     const int *__restrict__ order,
@@ -584,7 +586,7 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
     typedef typename Frag<E>::V V;
     constexpr int NT = grad_terms<E>();
     constexpr bool F = E::CODE == SPMV_F16;
-    __shared__ f32x4 sum[8][8][64];
+    __shared__ f32x4 sum[WAVES][8][64];
     const int r0 = blockIdx.z * 16 * NJ;   // first rank of this workgroup
     const bool second = (int)blockIdx.x >= a0.blocks;
     const OuterArg &a = second ? a1 : a0;
@@ -612,7 +614,7 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
         // the next step's rows, and the tokens of the one after (past the end
         // the last ones again)
         load_rows(next);
-        load_tok(t + 512);
+        load_tok(t + 64 * WAVES);
         __builtin_amdgcn_sched_barrier(0);
         const int at = min(t + 8 * q, t1 - 1), valid = t1 - (t + 8 * q);   // tokens of this lane
         u32x4 op[NJ][NT];
@@ -664,28 +666,31 @@ __global__ __launch_bounds__(512) void k_lora_outer(int n_tok, int max_rank,
         u32x4 ra[8], rb[8];
         load_tok(t);
         load_rows(ra);
-        load_tok(t + 256);
-        for (; t < t1; t += 512) {
+        load_tok(t + 32 * WAVES);
+        for (; t < t1; t += 64 * WAVES) {
             step(t, ra, rb);
-            if (t + 256 < t1) step(t + 256, rb, ra);
+            if (t + 32 * WAVES < t1) step(t + 32 * WAVES, rb, ra);
         }
     }
-    // the waves' sums, in wave order: wave w adds those of the products w
+    // the waves' sums, in wave order, shared out over the waves by product
     const float f = scale ? scale[ad] : 1.0f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) sum[wv][c][lane] = acc[j][c];
         __syncthreads();
-        f32x4 all = sum[0][wv][lane];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) all += sum[w][wv][lane];
-        sum[0][wv][lane] = all;
+        for (int c = wv; c < 8; c += WAVES) {
+            f32x4 all = sum[0][c][lane];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) all += sum[w][c][lane];
+            sum[0][c][lane] = all;
+        }
         __syncthreads();
-        // all 8 waves write: wave w the rows 4 q + (w & 3) of half the lanes' groups
+        // wave w writes the rows 4 q + (w & 3), of 8 waves those of half the lanes' groups
         const int i = wv & 3;
         const int row = r0 + 16 * j + 4 * q + i;
-        if ((q & 1) == (wv >> 2) && row < max_rank && c0 < a.dim) {
+        if ((WAVES == 4 || (q & 1) == (wv >> 2)) && row < max_rank && c0 < a.dim) {
             float v[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -706,12 +711,13 @@ int rank_tiles(int max_rank) { return max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : 
 
 constexpr int LR_WIDE = 4;
 
-// lora_grad's products take blocks of LR_WIDE tiles, an operand of A or B serving all
-// four, where that still fills the card and adapters have 64 tokens or more on
-// average.  Rank 32, 4096 x 4096, 8 adapters: 16384 tokens 149 us (181 in single
-// tiles), 8192 tokens 101 (109), 4096 tokens 87 (73).  Rank 16: 16384 tokens 122
-// (128), 8192 tokens 92 (75).  At rank 64 the registers do not allow it.
-// lora_apply is better off with single tiles (8192 tokens 69 us, 82 in blocks).
+// lora_grad's products take blocks of LR_WIDE tiles, an operand of A or B serving
+// all of them, where that still fills the card and adapters have 64 tokens or
+// more on average.  Gradient at 4096 x 4096, 8 adapters, rank 32: 16384 tokens
+// 156 us (185 in single tiles), 8192 tokens 92 (100), 4096 tokens 53 and 87 in
+// two batches (62 and 73); rank 16: 16384 tokens 121 (126), 8192 tokens 90 (70).
+// At rank 64 the registers do not allow it.  lora_apply is better off with single
+// tiles (8192 tokens 69 us, 82 in blocks).
 bool wide_blocks(int64_t n_tok, int64_t n_adapters, int max_rank) {
     return max_rank <= 32 && n_tok >= 64 * n_adapters && n_tok >= (max_rank <= 16 ? 16384 : 8192);
 }
@@ -909,17 +915,20 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
                         SPMV_LAUNCHED("k_lora_terms");
                     }
                 }
-                // Two rank tiles per workgroup share a reading of x; with few column
-                // blocks one each fills the card better.  Rank 32: 8192 tokens, 2048
-                // columns, 4 adapters (128 blocks) 58 us one each, 72 in twos; 2048
-                // tokens, 4096 columns, 32 adapters (2048 blocks) 109 and 98.
+                // With few column blocks, 8 waves and one rank tile per workgroup fill
+                // the card better; with more, 4 waves, so that two workgroups share a
+                // CU, and two rank tiles that share a reading of x.  Rank 32, gradient in
+                // us: 8192 tokens, 2048 columns, 1 adapter (32 blocks) 67, with 4 waves
+                // 79, with two rank tiles 88; 8192 tokens, 4096 columns, 8 adapters (512
+                // blocks) 92 with 4 waves and 8, 103 with one rank tile; 64 adapters 114,
+                // with 8 waves 145.
                 constexpr int JB = NJ < 2 ? NJ : 2;
                 const int64_t blocks = (int64_t)(oa.blocks + ob.blocks) * n_adapters;
                 if (blocks < 192)
-                    k_lora_outer<E, 1, 16 * NJ, VEC><<<dim3(oa.blocks + ob.blocks, n_adapters, NJ), 512, 0, s>>>(
+                    k_lora_outer<E, 1, 16 * NJ, 8, VEC><<<dim3(oa.blocks + ob.blocks, n_adapters, NJ), 64 * 8, 0, s>>>(
                         n_tok, max_rank, ranks, scale, order, offsets, oa, ob);
                 else
-                    k_lora_outer<E, JB, 16 * NJ, VEC><<<dim3(oa.blocks + ob.blocks, n_adapters, NJ / JB), 512, 0, s>>>(
+                    k_lora_outer<E, JB, 16 * NJ, 4, VEC><<<dim3(oa.blocks + ob.blocks, n_adapters, NJ / JB), 64 * 4, 0, s>>>(
                         n_tok, max_rank, ranks, scale, order, offsets, oa, ob);
                 SPMV_LAUNCHED("k_lora_outer");
                 return SPMV_OK;

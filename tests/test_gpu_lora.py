@@ -167,7 +167,8 @@ def test_bad_token_stays_alone():
                                    (260, 512, 128, 1, 64), (90, 128, 264, 3, 128), (600, 64, 64, 20, 16),
                                    (2100, 1040, 1096, 2, 32), (1500, 72, 64, 3, 48), (700, 2560, 2056, 1, 16), (200, 1031, 515, 2, 16), (80, 9, 7, 2, 4),
                                    (600, 517, 135, 2, 32), (8200, 136, 72, 5, 32),
-                                   (8199, 7, 265, 3, 20), (16390, 72, 40, 9, 12)])
+                                   (8199, 7, 265, 3, 20), (16390, 72, 40, 9, 12), (300, 33, 135, 70, 24),
+                                   (600, 1032, 520, 20, 48), (130, 5, 9, 100, 100), (513, 264, 136, 50, 16)])
 def test_grad(shape, dt):
     T, K, N, n, r = shape
     s = _make(T, K, N, n, r, dt, seed=T)
