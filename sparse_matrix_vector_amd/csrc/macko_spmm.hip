@@ -755,6 +755,8 @@ Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok) {
         return c;
     }
     // a group's share of the tokens is not known here: room for twice the mean
+    // (8 groups of 4096 x 2048, 30 % kept, in random shares: 400 tokens 33 us, 47 with
+    // room for the mean; 1000 tokens 54 and 77; 600 tokens 43 and 38)
     const int64_t room = n_groups > 1 ? std::min(t16, ceil_div(2 * n_tok, 16 * n_groups)) : t16;
     c.nt = room > 8 ? 16 : room > 4 ? 8 : room > 2 ? 4 : 2;
     c.tiles = (int)ceil_div(t16, c.nt);
