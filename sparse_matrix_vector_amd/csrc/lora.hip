@@ -20,11 +20,11 @@
 //           neighbouring columns of the result;
 //   outer   dA or dB: the contraction is the tokens, x (dy) is read the same
 //           way as B.
-// h stays fp32 in memory.  As an operand it is split into a sum of two 16-bit
-// numbers (fp16, after scaling by a power of two so that neither part
-// overflows or vanishes: 22 bits) or three (bf16 with an fp32 result: 24 bits;
-// two, 16 bits, when the result is rounded to bf16 anyway), so the rank
-// vector loses nothing that the result could show.
+// h stays fp32 in memory.  As an operand it is split into a sum of 16-bit numbers.
+// expand: two (fp16, after scaling by a power of two so that neither part
+// overflows or vanishes: 22 bits of the token's largest entry) or three (bf16
+// with an fp32 result: 24 bits; two, 16 bits, when the result is rounded to bf16
+// anyway).  outer: three bf16 numbers, all 24 bits of every entry.
 #include "elem.hpp"
 
 #include <algorithm>
@@ -89,7 +89,6 @@ struct ShrinkArg {
     int dim;
     float *h;                      // [split][n_tok][16 NJ], rows in sorted order
     unsigned short *terms;         // the weight gradients' operand (below), or NULL
-    int *exps;
 };
 
 __device__ __forceinline__ int rank_of(const int *ranks, int a, int max_rank) {
@@ -148,28 +147,27 @@ __device__ __forceinline__ int scale_exponent(float m) {
     return e == 0 || e == 255 ? 0 : 127 - e;
 }
 
-// Operands of the weight gradients: h as NT terms, transposed to
-// [term][rank][n_tok + LR_PAD] so that 8 tokens of a rank are one load; fp16
-// terms scaled by a power of two per tile, whose exponent is kept at the
-// tile's first row.
+// Operands of the weight gradients: h as three bf16 terms, 24 bits over fp32's
+// whole range whatever its neighbours hold (the tokens are the contraction there,
+// so a scale would have to be shared by tokens and tiles, and fp16 terms lose
+// what is small beside a neighbour), transposed to [term][rank][n_tok + LR_PAD]
+// so that 8 tokens of a rank are one load.
 constexpr int LR_PAD = 8;
-template <typename E, int NT, int R>
+constexpr int LR_GRAD_TERMS = 3;
+template <int R>
 __device__ __forceinline__ void store_terms(unsigned short *__restrict__ terms, int n_tok, int row, int end, int rank,
-                                            const float (&v)[4], int e) {
-    unsigned short t[4][NT];
+                                            const float (&v)[4]) {
+    unsigned short t[4][LR_GRAD_TERMS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(v[i], e) : v[i], t[i]);
+    for (int i = 0; i < 4; ++i) split_terms<BF16, LR_GRAD_TERMS>(v[i], t[i]);
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
+    for (int k = 0; k < LR_GRAD_TERMS; ++k) {
         unsigned short *p = terms + ((int64_t)k * R + rank) * (n_tok + LR_PAD) + row;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (row + i < end) p[i] = t[i][k];
     }
 }
-
-template <typename E>
-constexpr int grad_terms() { return E::CODE == SPMV_BF16 ? 3 : 2; }
 
 // The 64-wide steps lo .. hi - 1 of MT token tiles and the first N rank tiles.
 // Two register sets take turns, so a step's loads are in flight over the
@@ -250,7 +248,7 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(int n_tok, in
                                                      const int *__restrict__ order, const int *__restrict__ offsets,
                                                      const int4 *__restrict__ tiles, int n_tiles, int split, int products,
                                                      ShrinkArg a0, ShrinkArg a1) {
-    constexpr int NT = grad_terms<E>(), WAVES = SHRINK_WAVES;
+    constexpr int WAVES = SHRINK_WAVES;
     __shared__ f32x4 part[WAVES - 1][MT][NJ][64];
     const int id = blockIdx.x / split, spl = blockIdx.x - id * split;
     const int tile = products > 1 ? id >> 1 : id;
@@ -301,16 +299,13 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(int n_tok, in
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int row0 = blk.begin + 16 * m + 4 * q;    // D: row 4 q + i, column n
-        float top = 0.0f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
 #pragma unroll
             for (int w = 0; w < WAVES - 1; ++w) acc[m][j] += part[w][m][j][lane];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i)
                 if (16 * j + n >= rank || row0 + i >= blk.end) acc[m][j][i] = 0.0f;
-                top = fmaxf(top, fabsf(acc[m][j][i]));
-            }
         }
         if (!a.terms) {
 #pragma unroll
@@ -320,28 +315,21 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void k_lora_shrink(int n_tok, in
                     if (row0 + i < blk.end) h[(int64_t)(row0 + i) * (16 * NJ) + 16 * j + n] = acc[m][j][i];
             continue;
         }
-        int e = 0;
-        if (E::CODE == SPMV_F16) {
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-            e = scale_exponent(top);
-            if (lane == 0 && blk.begin + 16 * m < blk.end) a.exps[blk.begin + 16 * m] = e;
-        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const float v[4] = {acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]};
-            store_terms<E, NT, 16 * NJ>(a.terms, n_tok, row0, blk.end, 16 * j + n, v, e);
+            store_terms<16 * NJ>(a.terms, n_tok, row0, blk.end, 16 * j + n, v);
         }
     }
 }
 
 // Adds a split shrink's parts in order and writes the gradients' operands:
 // one wave per tile and product.
-template <typename E, int NJ>
+template <int NJ>
 __global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, int max_rank, int split,
                                                    const int *__restrict__ ranks,
                                                    const int4 *__restrict__ tiles, ShrinkArg a0, ShrinkArg a1) {
-    constexpr int R = 16 * NJ, NT = grad_terms<E>();
+    constexpr int R = 16 * NJ;
     const ShrinkArg &a = blockIdx.y ? a1 : a0;
     int4 tile = tiles[blockIdx.x];
     tile.y = min(max(tile.y, 0), n_tok);
@@ -350,7 +338,7 @@ __global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, in
     if (rank_of(ranks, tile.x, max_rank) == 0) return;
     const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
     const int row0 = tile.y + 4 * q;
-    float v[NJ][4], top = 0.0f;
+    float v[NJ][4];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -359,17 +347,9 @@ __global__ __launch_bounds__(64) void k_lora_terms(int n_tok, int n_adapters, in
             float t = 0.0f;
             for (int s = 0; s < split; ++s) t += a.h[((int64_t)s * n_tok + row) * R + 16 * j + n];
             v[j][i] = row0 + i < tile.z ? t : 0.0f;
-            top = fmaxf(top, fabsf(v[j][i]));
         }
-    int e = 0;
-    if (E::CODE == SPMV_F16) {
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        e = scale_exponent(top);
-        if (lane == 0) a.exps[tile.y] = e;
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) store_terms<E, NT, R>(a.terms, n_tok, row0, tile.z, 16 * j + n, v[j], e);
+    for (int j = 0; j < NJ; ++j) store_terms<R>(a.terms, n_tok, row0, tile.z, 16 * j + n, v[j]);
 }
 
 // Eight neighbouring results of one token, read and written once (non-temporal:
@@ -557,12 +537,41 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
     }
 }
 
+// Eight elements as an exact sum of N operands in bf16: fp16's 11 bits are one
+// number of 8 and one of 3, and bf16 holds all of its exponents.  For fp16 this
+// conversion, on the vector unit and once per reading of x, costs 2 to 10 us: 8192
+// tokens, 4096 + 4096 columns, rank 32, 4 adapters 69 us a gradient against 62 with
+// h as scaled fp16 numbers, which dropped entries 2^25 below their neighbours;
+// 2048 + 2048 columns, 1 adapter, 85 against 60.  Without the smallest of the six
+// products 2 % less.
+template <typename E>
+struct Exact;
+template <>
+struct Exact<BF16> {
+    static constexpr int N = 1;
+    b8 v[N];
+    __device__ __forceinline__ explicit Exact(u32x4 r) { v[0] = __builtin_bit_cast(b8, r); }
+};
+template <>
+struct Exact<F16> {
+    static constexpr int N = 2;
+    b8 v[N];
+    __device__ __forceinline__ explicit Exact(u32x4 r) {
+        const h8 h = __builtin_bit_cast(h8, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = (float)h[i];
+            v[0][i] = (__bf16)f;
+            v[1][i] = (__bf16)(f - (float)v[0][i]);
+        }
+    }
+};
+
 struct OuterArg {
     const unsigned short *x;   // x or dy
     int64_t ldx;
     int dim, blocks;           // columns, and their 128-column blocks
     const unsigned short *terms;
-    const int *exps;
     float *out;                // [n_adapters, max_rank, dim]
 };
 
@@ -583,9 +592,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_lora_outer(int n_tok, int max_ra
                                                     const float *__restrict__ scale,
                                                     const int *__restrict__ order,
                                                     const int *__restrict__ offsets, OuterArg a0, OuterArg a1) {
-    typedef typename Frag<E>::V V;
-    constexpr int NT = grad_terms<E>();
-    constexpr bool F = E::CODE == SPMV_F16;
+    constexpr int NT = LR_GRAD_TERMS;
     __shared__ f32x4 sum[WAVES][8][64];
     const int r0 = blockIdx.z * 16 * NJ;   // first rank of this workgroup
     const bool second = (int)blockIdx.x >= a0.blocks;
@@ -623,18 +630,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_lora_outer(int n_tok, int max_ra
 #pragma unroll
             for (int k = 0; k < NT; ++k)
                 __builtin_memcpy(&op[j][k], a.terms + ((int64_t)k * R + r0 + 16 * j + n) * (n_tok + LR_PAD) + at, 16);
-        float back = 1.0f;
-        if (F) {
-            // the two tiles' terms on the scale of the larger: its exponent is the smaller
-            const int e = a.exps[min(t + 16 * (q >> 1), t0 + (t1 - 1 - t0) / 16 * 16)];
-            const int both = min(e, __shfl_xor(e, 32));
-            const _Float16 f = (_Float16)ldexpf(1.0f, max(both - e, -40));   // 0 below 2^-25
-            back = ldexpf(1.0f, -both);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int k = 0; k < NT; ++k) op[j][k] = __builtin_bit_cast(u32x4, __builtin_bit_cast(h8, op[j][k]) * f);
-        }
         if (t + 32 > t1) {                 // uniform: tokens past the end count nothing
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
@@ -646,19 +641,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_lora_outer(int n_tok, int max_ra
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const V b = __builtin_bit_cast(V, column_of(r, c));
+            const Exact<E> b(column_of(r, c));
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                f32x4 d = F ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j][c];
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                for (int k = 0; k < NT; ++k) d = Frag<E>::mma(__builtin_bit_cast(V, op[j][k]), b, d);
-                if (F) {
+                for (int k = 0; k < NT; ++k) {
+                    const b8 g = __builtin_bit_cast(b8, op[j][k]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][c][i] = fmaf(back, d[i], acc[j][c][i]);
-                } else {
-                    acc[j][c] = d;
+                    for (int i = 0; i < Exact<E>::N; ++i) acc[j][c] = Frag<BF16>::mma(g, b.v[i], acc[j][c]);
                 }
-            }
         }
     };
     int t = t0 + 32 * wv;
@@ -738,11 +729,11 @@ int split_of(int64_t n_tok, int64_t blocks, int64_t dim) {
 size_t h_bytes(int64_t n_tok, int max_rank) {
     return ((size_t)max_split(n_tok) * (size_t)n_tok * (size_t)(16 * rank_tiles(max_rank)) * 4 + 255) & ~size_t(255);
 }
-// terms of one product (three at most), and the tiles' exponents behind them
+// terms of one product
 size_t terms_bytes(int64_t n_tok, int max_rank) {
-    return (((size_t)3 * (size_t)(16 * rank_tiles(max_rank)) * (size_t)(n_tok + LR_PAD) * 2 + 255) & ~size_t(255)) +
-           (((size_t)n_tok + 63) & ~size_t(63)) * 4;
+    return ((size_t)LR_GRAD_TERMS * (size_t)(16 * rank_tiles(max_rank)) * (size_t)(n_tok + LR_PAD) * 2 + 255) & ~size_t(255);
 }
+
 spmv_status check_common(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adapters, int32_t max_rank,
                          int32_t dtype, const void *A, const void *B, const int32_t *order, const int32_t *offsets,
                          const int32_t *tiles, int32_t n_tiles, const void *workspace, size_t workspace_bytes) {
@@ -820,7 +811,7 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
     const int split = split_of(n_tok, n_tiles, n_in);
     const int4 *tl = reinterpret_cast<const int4 *>(tiles);
     const ShrinkArg sa = {static_cast<const unsigned short *>(x), static_cast<const unsigned short *>(A), ldx, n_in,
-                          static_cast<float *>(workspace), nullptr, nullptr};
+                          static_cast<float *>(workspace), nullptr};
     st = by_half(dtype, [&](auto e) {
         return by_rank(max_rank, [&](auto nj) {
             return by_bool(n_in >= 8, [&](auto vec) {
@@ -881,16 +872,11 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
     const bool vec = n_in >= 8 && n_out >= 8;
     const int4 *tl = reinterpret_cast<const int4 *>(tiles);
     unsigned short *terms[2];
-    int *exps[2];
-    for (int i = 0; i < 2; ++i) {
-        terms[i] = reinterpret_cast<unsigned short *>(w + 2 * hb + i * tb);
-        exps[i] = reinterpret_cast<int *>(w + 2 * hb + (i + 1) * tb) - ((n_tok + 63) & ~63);
-    }
-    ShrinkArg hx = {xs, static_cast<const unsigned short *>(A), ldx, n_in, reinterpret_cast<float *>(w), terms[0], exps[0]};
-    ShrinkArg gy = {dys, static_cast<const unsigned short *>(B), lddy, n_out, reinterpret_cast<float *>(w + hb), terms[1],
-                    exps[1]};
-    const OuterArg oa = {xs, ldx, n_in, (int)ceil_div(n_in, LR_WAVE_COLS), terms[1], exps[1], dA};
-    const OuterArg ob = {dys, lddy, n_out, (int)ceil_div(n_out, LR_WAVE_COLS), terms[0], exps[0], dB};
+    for (int i = 0; i < 2; ++i) terms[i] = reinterpret_cast<unsigned short *>(w + 2 * hb + i * tb);
+    ShrinkArg hx = {xs, static_cast<const unsigned short *>(A), ldx, n_in, reinterpret_cast<float *>(w), terms[0]};
+    ShrinkArg gy = {dys, static_cast<const unsigned short *>(B), lddy, n_out, reinterpret_cast<float *>(w + hb), terms[1]};
+    const OuterArg oa = {xs, ldx, n_in, (int)ceil_div(n_in, LR_WAVE_COLS), terms[1], dA};
+    const OuterArg ob = {dys, lddy, n_out, (int)ceil_div(n_out, LR_WAVE_COLS), terms[0], dB};
     return by_half(dtype, [&](auto e) {
         typedef decltype(e) E;
         return by_rank(max_rank, [&](auto nj) {
@@ -910,7 +896,7 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
                     }
                     SPMV_LAUNCHED("k_lora_shrink");
                     if (split > 1) {
-                        k_lora_terms<E, NJ><<<dim3(n_tiles, 2), 64, 0, s>>>(n_tok, n_adapters, max_rank, split, ranks, tl, hx,
+                        k_lora_terms<NJ><<<dim3(n_tiles, 2), 64, 0, s>>>(n_tok, n_adapters, max_rank, split, ranks, tl, hx,
                                                                            gy);
                         SPMV_LAUNCHED("k_lora_terms");
                     }

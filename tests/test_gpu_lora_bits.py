@@ -1,0 +1,120 @@
+"""How many bits of the rank vectors the adapters' kernels keep: tokens, ranks
+and tiles of very different size beside each other, against 64 bits.  Each
+entry of a rank vector counts with its own size in the bounds, never with
+that of a larger neighbour."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+S = pytest.importorskip("sparse_matrix_vector_amd")
+
+import op_refs as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+F = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+NAN = float("nan")
+
+
+def _plan(keys, n):
+    return S.RoutePlan(len(keys), 1, n).build(torch.from_numpy(np.asarray(keys, np.int32)).cuda())
+
+
+def _randn(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return lambda *sh: torch.randn(*sh, device="cuda", generator=g)
+
+
+# ---------------------------------------------------------------------------
+# Weight gradients
+# ---------------------------------------------------------------------------
+def _grad(A, B, x, dy, keys=None):
+    n, r, _ = A.shape
+    p = _plan(np.zeros(x.shape[0]) if keys is None else keys, n)
+    dA, dB = (torch.full(t.shape, NAN, device="cuda") for t in (A, B))
+    ws = torch.full((S.lora_workspace_size(x.shape[0], r),), 255, dtype=torch.uint8, device="cuda")
+    S.lora_grad(None, None, A, B, p.order, p.offsets, p.tiles, x, dy, dA, dB, ws)
+    torch.cuda.synchronize()
+    return dA, dB
+
+
+def _check_grad(A, B, x, dy, keys=None, what=""):
+    """dA[a, j, k] = sum_t g_tj x_tk with g = dy B^T, and dB the same with x and
+    dy, A and B exchanged.  g: chains of at most K / 32 + 32 additions and 40
+    partial sums; as an operand 2^-23 of each entry's own size.  The sum over
+    tokens: at most 6 instructions per 32 tokens, each adding up 32 products
+    (counted as 32 additions once and one per instruction), 16 partial sums."""
+    dA, dB = _grad(A, B, x, dy, keys)
+    keys = np.zeros(x.shape[0]) if keys is None else np.asarray(keys)
+    for got, W, u, v, name in ((dA, B, dy, x, "dA"), (dB, A, x, dy, "dB")):
+        W, u, v = R.f64(W), R.f64(u), R.f64(v)
+        for a in range(W.shape[0]):
+            at = torch.from_numpy(np.flatnonzero(keys == a))
+            g = u[at] @ W[a].t()
+            dg = (u[at].abs() @ W[a].abs().t()) * ((u.shape[1] / 32 + 72) * R.ADD) + g.abs() * 2.0 ** -23
+            mag = (g.abs() + dg).t() @ v[at].abs()
+            bound = dg.t() @ v[at].abs() + mag * ((32 + 6 * (len(at) / 32 + 1) + 16) * R.ADD)
+            R.check(got[a], g.t() @ v[at], bound, f"{what} {name} of adapter {a}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,K,N,r", [(20, 128, 72, 8), (700, 264, 136, 8), (300, 1040, 520, 16), (8200, 64, 72, 16)])
+def test_grad_with_ranks_of_different_size(T, K, N, r, dt):
+    """The rows of A and B each 8 times smaller than the one before."""
+    randn = _randn(T)
+    fall = torch.tensor([8.0 ** -(j % 8) for j in range(r)], device="cuda")[None, :, None]
+    _check_grad(((randn(1, r, K) * fall)).to(F[dt]), (randn(1, r, N) * fall).to(F[dt]), randn(T, K).to(F[dt]),
+                randn(T, N).to(F[dt]))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("big", [0, 17, 299])
+def test_grad_with_one_large_token(big, dt):
+    """One token's rows 2^18 above the others', with columns that only the others use."""
+    T, K, N, r = 300, 136, 264, 8
+    randn = _randn(big)
+    size = torch.full((T, 1), 2.0 ** -12, device="cuda")
+    size[big] = 2.0 ** 6
+    x, dy = randn(T, K), randn(T, N)
+    for large, other in ((dy, x), (x, dy)):
+        a, b = large * size, other.clone()
+        b[big, ::2] = 0
+        xx, dd = (b, a) if large is dy else (a, b)
+        _check_grad(randn(1, r, K).to(F[dt]), randn(1, r, N).to(F[dt]), xx.to(F[dt]), dd.to(F[dt]))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("K,N,r", [(64, 72, 8), (520, 264, 40), (7, 135, 20)])
+def test_grad_of_tiles_far_apart(K, N, r, dt):
+    """Tiles of 16 tokens 2^26 apart, in both orders, and columns that only the small ones use."""
+    randn = _randn(K)
+    for order in (0, 1):
+        x, dy = randn(64, K), randn(64, N)
+        for t in range(0, 64, 16):
+            small = (t // 16 + order) % 2 == 0
+            dy[t:t + 16] *= 2.0 ** -14 if small else 2.0 ** 12
+            if not small:
+                x[t:t + 16, ::2] = 0
+        A, B = randn(2, r, K).to(F[dt]), randn(2, r, N).to(F[dt])
+        keys = np.r_[np.zeros(40), np.ones(24)]
+        _check_grad(A, B, x.to(F[dt]), dy.to(F[dt]), keys)
+        _check_grad(B, A, dy.to(F[dt]), x.to(F[dt]), keys)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_grad_of_exact_rank_vectors(dt):
+    """Columns with one entry in A and B: rank vectors are single products, so
+    only the operand's rounding and the sum over tokens are left.  Token t's
+    rank vector is 2^(t mod 20) times another's; x gives them all one size."""
+    T, r = 160, 8
+    randn = _randn(3)
+    up = torch.tensor([2.0 ** (t % 20 - 10) for t in range(T)], device="cuda")[:, None]
+    A = torch.zeros(1, r, r, device="cuda")
+    B = torch.zeros(1, r, r, device="cuda")
+    for j in range(r):
+        A[0, j, j], B[0, j, j] = 1 + j / 8, 2.0 ** -j * (1 + j / 16)
+    A, B, x, dy = (t.to(F[dt]) for t in (A, B, randn(T, r) / up, randn(T, r) * up))
+    dA, dB = _grad(A, B, x, dy)
+    for got, W, u, v in ((dA, B, dy, x), (dB, A, x, dy)):
+        g, v = R.f64(u) @ R.f64(W)[0].t(), R.f64(v)
+        R.check(got[0], g.t() @ v, (g.abs().t() @ v.abs()) * (2.0 ** -23 + (32 + 6 * (T / 32 + 1) + 16) * R.ADD))
