@@ -21,10 +21,11 @@
 //   outer   dA or dB: the contraction is the tokens, x (dy) is read the same
 //           way as B.
 // h stays fp32 in memory.  As an operand it is split into a sum of 16-bit numbers.
-// expand: two (fp16, after scaling by a power of two so that neither part
-// overflows or vanishes: 22 bits of the token's largest entry) or three (bf16
-// with an fp32 result: 24 bits; two, 16 bits, when the result is rounded to bf16
-// anyway).  outer: three bf16 numbers, all 24 bits of every entry.
+// expand: two fp16 numbers, 22 bits of every entry, scaled by a power of two per
+// token; entries too far below the token's largest for that scale take another
+// pass of the product at their own.  With bf16 three numbers (an fp32 result: 24
+// bits) or two (16 bits, when the result is rounded to bf16 anyway).
+// outer: three bf16 numbers, all 24 bits of every entry.
 #include "elem.hpp"
 
 #include <algorithm>
@@ -141,11 +142,17 @@ __device__ __forceinline__ void split_terms(float v, unsigned short (&t)[NT]) {
     }
 }
 
-// The power of two that brings max |v| = m into [1, 2) (1 for 0, infinities and NaN).
+// The power of two that brings max |v| = m into [2^14, 2^15), half of fp16's range
+// (1 for 0, infinities and NaN), or to more than 2^-2 at least: products of fp16
+// numbers are multiples of 2^-48, and the largest power leaves room to bring
+// sums of the largest fp16 numbers to a smaller one's scale (2^27 columns, fp32).
 __device__ __forceinline__ int scale_exponent(float m) {
     const int e = (__float_as_int(m) >> 23) & 255;
-    return e == 0 || e == 255 ? 0 : 127 - e;
+    return e == 0 || e == 255 ? 0 : min(127 + 14 - e, 46);
 }
+// Entries down to 2^-LR_SPREAD of the largest keep 22 bits in two terms at that
+// scale: 2^-2 is then the smallest, and fp16's last bit is 2^-24.
+constexpr int LR_SPREAD = 16;
 
 // Operands of the weight gradients: h as three bf16 terms, 24 bits over fp32's
 // whole range whatever its neighbours hold (the tokens are the contraction there,
@@ -400,8 +407,10 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
 // of a tile are neighbours in the launch and together move whole rows of y.
 // Two or four tiles per workgroup, sharing B, were slower (79 and 114 us against
 // 67 then): fewer rows in flight.
+// fp16's passes by size cost up to 6 % where every tile takes one (3000 tokens of
+// 2048 columns, rank 128, 8192 fp16 results: 63.8 us, 60.2 with small entries lost).
 template <typename E, typename Y, int NJ, int NT, bool VEC>
-__global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, int max_rank, int split,
+__global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int n_adapters, int max_rank, int split,
                                                      const int *__restrict__ ranks,
                                                      const float *__restrict__ scale,
                                                      const int *__restrict__ order, const int *__restrict__ offsets,
@@ -411,8 +420,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
                                                      typename Y::T *y, int64_t ldy) {
     typedef typename Frag<E>::V V;
     constexpr int R = 16 * NJ, LD = R + 8;
+    constexpr bool F = E::CODE == SPMV_F16;
     __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE][LD];
-    __shared__ float unscale[LR_TILE];
+    __shared__ int exps[LR_TILE], again[4];
     const int id = blockIdx.x / pieces, piece = blockIdx.x - id * pieces;
     const Block blk = block_of<1>(tiles, n_tiles, id, offsets, n_tok, n_adapters);
     if (blk.begin >= blk.end) return;
@@ -439,6 +449,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
     f32x4 acc[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    int e[4] = {0, 0, 0, 0};
     if (rank > 0) {
         const unsigned short *Br = B + (int64_t)blk.group * max_rank * dim;
         u32x4 r[8];
@@ -447,11 +458,10 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
             for (int i = 0; i < 8; ++i) r[i] = load8<VEC>(Br + (int64_t)min(jb + i, max_rank - 1) * dim, c0, dim);
         };
         load_b(NJ == 1 ? 8 * (q & 1) : 8 * q);
-        // 16 lanes per token: the partial sums of h in order, the token's
-        // largest |h|, and the scaled terms
+        // 16 lanes per token: the partial sums of h in order
         const int t = (threadIdx.x >> 4), l = threadIdx.x & 15;
         const int64_t row = min(blk.begin + t, blk.end - 1);
-        float v[NJ], top = 0.0f;
+        float v[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) v[j] = 0.0f;
         const float *hr = h + row * R + l;
@@ -460,67 +470,114 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
                 if (16 * j < rank) v[j] += hr[(int64_t)s * n_tok * R + 16 * j];
+        // The terms of v.  fp16: of the entries that are not far below the token's
+        // largest, at the scale of that; the others stay in v for another pass.
+        auto next_terms = [&]() {
+            int e = 0;
+            float least = 0.0f;
+            if (F) {
+                float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) top = fmaxf(top, fabsf(v[j]));
+                for (int j = 0; j < NJ; ++j) top = fmaxf(top, fabsf(v[j]));
 #pragma unroll
-        for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        const int e = E::CODE == SPMV_F16 ? scale_exponent(top) : 0;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            unsigned short terms[NT];
-            split_terms<E, NT>(E::CODE == SPMV_F16 ? ldexpf(v[j], e) : v[j], terms);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) hs[i][t][16 * j + l] = terms[i];
-        }
-        if (l == 0) unscale[t] = ldexpf(scale ? scale[blk.group] : 1.0f, -e);
-        __syncthreads();
-        if constexpr (NJ == 1) {
-            // up to 16 ranks: the terms share the contraction, eight ranks
-            // of one term per lane group and step
-            constexpr int STEPS = (2 * NT + 3) / 4;
-            const int live = rank - 8 * (q & 1);
-            if (rank < 16) {                                // rows past the rank may hold anything
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) r[i][d] = i < live ? r[i][d] : 0u;
+                for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+                e = scale_exponent(top);
+                least = ldexpf(top, -LR_SPREAD);
             }
+            bool left = false;
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int term = 2 * s + (q >> 1);
-                u32x4 a = {0u, 0u, 0u, 0u};
-                if (term < NT)
-                    a = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][n][8 * (q & 1)]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const V b = __builtin_bit_cast(V, column_of(r, c));
-                    acc[c] = Frag<E>::mma(__builtin_bit_cast(V, a), b, acc[c]);
+            for (int j = 0; j < NJ; ++j) {
+                float now = v[j];
+                if (F) {
+                    const bool later = fabsf(now) < least;
+                    left |= later && now != 0.0f;
+                    v[j] = later ? now : 0.0f;
+                    now = later ? 0.0f : ldexpf(now, e);
                 }
+                unsigned short terms[NT];
+                split_terms<E, NT>(now, terms);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) hs[i][t][16 * j + l] = terms[i];
             }
-        } else {
-            for (int j0 = 0; j0 < rank; j0 += 32) {
-                const int jb = j0 + 8 * q;
-                if (j0 > 0) load_b(jb);
-                if (j0 + 32 > rank) {
+            if (F) {
+                if (l == 0) exps[t] = e;
+                const int any = __any(left);
+                if (lane == 0) again[wv] = any;
+            }
+            __syncthreads();
+        };
+        // acc += the terms times B; loaded: r holds B's first rows
+        auto multiply = [&](bool loaded) {
+            if constexpr (NJ == 1) {
+                // up to 16 ranks: the terms share the contraction, eight ranks
+                // of one term per lane group and step
+                constexpr int STEPS = (2 * NT + 3) / 4;
+                const int live = rank - 8 * (q & 1);
+                if (!loaded) load_b(8 * (q & 1));
+                if (rank < 16) {                            // rows past the rank may hold anything
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
 #pragma unroll
-                        for (int d = 0; d < 4; ++d) r[i][d] = jb + i < rank ? r[i][d] : 0u;
+                        for (int w = 0; w < 4; ++w) r[i][w] = i < live ? r[i][w] : 0u;
                 }
-                V a[NT];
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    a[i] = __builtin_bit_cast(V, *reinterpret_cast<const u32x4 *>(&hs[i][n][jb]));
+                for (int s = 0; s < STEPS; ++s) {
+                    const int term = 2 * s + (q >> 1);
+                    u32x4 a = {0u, 0u, 0u, 0u};
+                    if (term < NT)
+                        a = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][n][8 * (q & 1)]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const V b = __builtin_bit_cast(V, column_of(r, c));
+                    for (int c = 0; c < 8; ++c) {
+                        const V b = __builtin_bit_cast(V, column_of(r, c));
+                        acc[c] = Frag<E>::mma(__builtin_bit_cast(V, a), b, acc[c]);
+                    }
+                }
+            } else {
+                for (int j0 = 0; j0 < rank; j0 += 32) {
+                    const int jb = j0 + 8 * q;
+                    if (j0 > 0 || !loaded) load_b(jb);
+                    if (j0 + 32 > rank) {
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) acc[c] = Frag<E>::mma(a[i], b, acc[c]);
+                        for (int i = 0; i < 8; ++i)
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) r[i][w] = jb + i < rank ? r[i][w] : 0u;
+                    }
+                    V a[NT];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        a[i] = __builtin_bit_cast(V, *reinterpret_cast<const u32x4 *>(&hs[i][n][jb]));
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const V b = __builtin_bit_cast(V, column_of(r, c));
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) acc[c] = Frag<E>::mma(a[i], b, acc[c]);
+                    }
                 }
             }
+        };
+        for (bool first = true;; first = false) {
+            next_terms();
+            if (F) {
+                // the sums so far to this pass's scale
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int to = exps[4 * q + i];
+                    if (!first) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) acc[c][i] = ldexpf(acc[c][i], to - e[i]);
+                    }
+                    e[i] = to;
+                }
+            }
+            multiply(first);
+            // uniform; rare for entries of ordinary spread, and 7 passes at most for sums
+            // of fp16 products, as each takes every token's entries of 16 powers of two
+            if (!F || !(again[0] | again[1] | again[2] | again[3])) break;
+            __syncthreads();
         }
     }
     if (c0 >= dim) return;
+    const float f = rank > 0 && scale ? scale[blk.group] : 1.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = 4 * q + i;
@@ -529,9 +586,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(int n_tok, int n_adapters, 
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] = (float)base[i].v[c];
         if (rank > 0) {
-            const float f = unscale[t];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = fmaf(f, acc[c][i], v[c]);
+            for (int c = 0; c < 8; ++c) v[c] = fmaf(f, F ? ldexpf(acc[c][i], -e[i]) : acc[c][i], v[c]);
         }
         store_row8<Y, VEC>(y + tok[i] * ldy, c0, dim, v);
     }

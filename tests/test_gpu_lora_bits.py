@@ -118,3 +118,72 @@ def test_grad_of_exact_rank_vectors(dt):
     for got, W, u, v in ((dA, B, dy, x), (dB, A, x, dy)):
         g, v = R.f64(u) @ R.f64(W)[0].t(), R.f64(v)
         R.check(got[0], g.t() @ v, (g.abs().t() @ v.abs()) * (2.0 ** -23 + (32 + 6 * (T / 32 + 1) + 16) * R.ADD))
+
+
+# ---------------------------------------------------------------------------
+# The adapters' product
+# ---------------------------------------------------------------------------
+def _check_apply(A, B, x, y_in, ydt, bits, what=""):
+    """y = y_in + B^T (A x).  h = A x: chains of at most K / 32 + 32 additions and
+    40 partial sums; as an operand 2^-(bits + 1) of each entry's own size; then at
+    most three terms of r products, and 24 more sums and products."""
+    n, r, K = A.shape
+    T, N = x.shape[0], B.shape[2]
+    keys = (np.arange(T) + 1) % (n + 1) - 1
+    p = _plan(keys, n)
+    ws = torch.full((S.lora_workspace_size(T, r),), 255, dtype=torch.uint8, device="cuda")
+    y = torch.full((T, N), NAN, device="cuda", dtype=ydt)
+    base = None if y_in is None else y_in.to(ydt)
+    S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, base, y, ws)
+    torch.cuda.synchronize()
+    ref = torch.zeros(T, N, dtype=torch.float64) if base is None else R.f64(base).clone()
+    bound = torch.zeros(T, N, dtype=torch.float64)
+    A, B, x = R.f64(A), R.f64(B), R.f64(x)
+    for a in range(n):
+        at = torch.from_numpy(np.flatnonzero(keys == a))
+        h = x[at] @ A[a].t()
+        dh = (x[at].abs() @ A[a].abs().t()) * ((K / 32 + 72) * R.ADD) + h.abs() * 2.0 ** -(bits + 1)
+        mag = (h.abs() + dh) @ B[a].abs()
+        ref[at] += h @ B[a]
+        bound[at] = dh @ B[a].abs() + mag * ((3 * r + 24) * R.ADD) + ref[at].abs() * 2 * R.ADD
+    R.check(y, ref, bound + R.rounded(ref.abs() + bound, ydt), what)
+
+
+def _spread(T, K, N, r, lo, hi, seed):
+    """Adapters whose rank vectors hold entries of very different size, in another
+    order for every token, beside columns of B that take one rank each: rank j
+    reads the columns of x with k mod r = j, whose size is 2^s."""
+    rng = np.random.default_rng(seed)
+    randn = _randn(seed)
+    s = torch.from_numpy(rng.uniform(lo, hi, (T, r))).cuda()
+    col = torch.arange(K, device="cuda") % r
+    x = randn(T, K) * torch.exp2(torch.round(s))[:, col]
+    A = randn(2, r, K) * (col[None, None, :] == torch.arange(r, device="cuda")[None, :, None])
+    B = randn(2, r, N) * (torch.arange(N, device="cuda")[None, None, :] % r == torch.arange(r, device="cuda")[None, :, None])
+    return A, B, x
+
+
+@pytest.mark.parametrize("y", ["x", "f32"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,K,N,r", [(1, 128, 72, 8), (37, 264, 1032, 8), (20, 520, 130, 24), (300, 136, 264, 40), (33, 200, 515, 100)])
+def test_apply_with_ranks_of_different_size(T, K, N, r, dt, y):
+    """The rows of A each 8 times smaller than the one before, those of B larger."""
+    randn = _randn(T)
+    step = torch.tensor([8.0 ** (j % 8) for j in range(r)], device="cuda")[None, :, None]
+    ydt = F[dt] if y == "x" else torch.float32
+    A, B = (randn(2, r, K) / step).to(F[dt]), (randn(2, r, N) * step / 1024).to(F[dt])
+    _check_apply(A, B, randn(T, K).to(F[dt]), randn(T, N), ydt, 22 if dt == "f16" else 24 if y == "f32" else 16)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,K,N,r", [(1, 64, 64, 4), (18, 8, 8, 8), (50, 264, 515, 16), (35, 260, 1032, 20), (300, 200, 264, 33), (40, 512, 200, 128),
+                                     (20, 7, 5, 3)])
+def test_apply_with_entries_far_apart(T, K, N, r, dt):
+    """Rank vectors with entries up to 2^60 apart."""
+    A, B, x = _spread(T, K, N, r, -13, 14, seed=T + r)
+    up = torch.exp2(torch.round(torch.linspace(-12, 14, r, device="cuda")))[None, :, None]
+    bits = 22 if dt == "f16" else 24
+    _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), None, torch.float32, bits, "far")
+    _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), torch.float32, bits, "far, added")
+    A, B, x = _spread(T, K, N, r, -3, 14, seed=T + r)
+    _check_apply((A / 256).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), F[dt], bits if dt == "f16" else 16, "rounded")
