@@ -23,9 +23,9 @@
 // h stays fp32 in memory.  As an operand it is split into a sum of 16-bit numbers.
 // expand: two fp16 numbers, 22 bits of every entry, scaled by a power of two per
 // token; entries too far below the token's largest for that scale take another
-// pass of the product at their own.  With bf16 three numbers (an fp32 result: 24
-// bits) or two (16 bits, when the result is rounded to bf16 anyway).
-// outer: three bf16 numbers, all 24 bits of every entry.
+// pass of the product at their own.  With bf16, and in outer with both types, three
+// bf16 numbers, all 24 bits of every entry (two, 16 bits, show in a rounded result
+// too where ranks cancel).
 #include "elem.hpp"
 
 #include <algorithm>
@@ -409,7 +409,7 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
 // 67 then): fewer rows in flight.
 // fp16's passes by size cost up to 6 % where every tile takes one (3000 tokens of
 // 2048 columns, rank 128, 8192 fp16 results: 63.8 us, 60.2 with small entries lost).
-template <typename E, typename Y, int NJ, int NT, bool VEC>
+template <typename E, typename Y, int NJ, bool VEC>
 __global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int n_adapters, int max_rank, int split,
                                                      const int *__restrict__ ranks,
                                                      const float *__restrict__ scale,
@@ -421,6 +421,7 @@ __global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int
     typedef typename Frag<E>::V V;
     constexpr int R = 16 * NJ, LD = R + 8;
     constexpr bool F = E::CODE == SPMV_F16;
+    constexpr int NT = F ? 2 : 3;
     __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE][LD];
     __shared__ int exps[LR_TILE], again[4];
     const int id = blockIdx.x / pieces, piece = blockIdx.x - id * pieces;
@@ -890,18 +891,18 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
             return by_bool(n_out >= 8, [&](auto vec) {
                 constexpr int NJ = decltype(nj)::value;
                 constexpr bool VEC = decltype(vec)::value;
-                auto go = [&](auto yt, auto nt) {
+                auto go = [&](auto yt) {
                     typedef decltype(yt) Y;
-                    k_lora_expand<E, Y, NJ, decltype(nt)::value, VEC><<<grid, 256, 0, s>>>(
+                    k_lora_expand<E, Y, NJ, VEC><<<grid, 256, 0, s>>>(
                         n_tok, n_adapters, max_rank, split, ranks, scale, order, offsets, tl, n_tiles,
                         static_cast<const float *>(workspace), static_cast<const unsigned short *>(B), n_out,
                         (int)pieces,
                         static_cast<const typename Y::T *>(y_in), ldyin, static_cast<typename Y::T *>(y), ldy);
                 };
                 if (y_dtype == SPMV_F32)
-                    go(F32{}, std::integral_constant<int, E::CODE == SPMV_BF16 ? 3 : 2>{});
+                    go(F32{});
                 else
-                    go(E{}, std::integral_constant<int, 2>{});
+                    go(E{});
                 SPMV_LAUNCHED("k_lora_expand");
                 return SPMV_OK;
             });

@@ -187,3 +187,31 @@ def test_apply_with_entries_far_apart(T, K, N, r, dt):
     _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), torch.float32, bits, "far, added")
     A, B, x = _spread(T, K, N, r, -3, 14, seed=T + r)
     _check_apply((A / 256).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), F[dt], bits if dt == "f16" else 16, "rounded")
+
+
+@pytest.mark.parametrize("y", ["x", "f32"])
+@pytest.mark.parametrize("r", [2, 40])
+def test_apply_where_ranks_cancel(r, y):
+    """bf16 rank vectors of 24 bits, exact in fp32 (two products each), whose
+    neighbours differ by 2^-15 and meet rows of B of opposite sign: what is left
+    shows every bit of the operand."""
+    T, N = 64, 136
+    rng = np.random.default_rng(r)
+    A = torch.zeros(1, r, 2, device="cuda")
+    one = 1 + torch.from_numpy(rng.integers(0, 128, (r // 2, 2)) / 128).float()
+    A[0, 0::2] = A[0, 1::2] = one.cuda()
+    A[0, 1::2, 1] += torch.where(A[0, 1::2, 1] < 1.9, 2.0 ** -7, -2.0 ** -7)
+    B = _randn(5)(1, r, N)
+    B[0, 1::2] = -B[0, 0::2]
+    x = 1 + torch.from_numpy(rng.integers(0, 128, (T, 2)) / 128).float().cuda()
+    x[:, 1] *= 2.0 ** -8
+    A, B, x = A.bfloat16(), B.bfloat16(), x.bfloat16()
+    h = R.f64(x) @ R.f64(A)[0].t()
+    assert torch.equal(h, h.float().double())
+    p = _plan(np.zeros(T), 1)
+    out = torch.full((T, N), NAN, device="cuda", dtype=F["bf16"] if y == "x" else torch.float32)
+    S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, out,
+                 torch.empty(S.lora_workspace_size(T, r), dtype=torch.uint8, device="cuda"))
+    ref = h @ R.f64(B)[0]
+    bound = (h.abs() @ R.f64(B)[0].abs()) * ((3 * r + 6) * R.ADD)
+    R.check(out, ref, bound + R.rounded(ref.abs() + bound, out.dtype), "cancelled")
