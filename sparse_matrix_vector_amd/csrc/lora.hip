@@ -21,11 +21,11 @@
 //   outer   dA or dB: the contraction is the tokens, x (dy) is read the same
 //           way as B.
 // h stays fp32 in memory.  As an operand it is split into a sum of 16-bit numbers.
-// expand: two fp16 numbers, 22 bits of every entry, scaled by a power of two per
+// Three hold all 24 bits of every entry (two show where ranks cancel, bf16's 16
+// bits in a rounded result too).  expand with fp16: scaled by a power of two per
 // token; entries too far below the token's largest for that scale take another
-// pass of the product at their own.  With bf16, and in outer with both types, three
-// bf16 numbers, all 24 bits of every entry (two, 16 bits, show in a rounded result
-// too where ranks cancel).
+// pass of the product at their own.  Otherwise, and in outer with both types:
+// bf16 numbers, which need no scale.
 #include "elem.hpp"
 
 #include <algorithm>
@@ -150,9 +150,9 @@ __device__ __forceinline__ int scale_exponent(float m) {
     const int e = (__float_as_int(m) >> 23) & 255;
     return e == 0 || e == 255 ? 0 : min(127 + 14 - e, 46);
 }
-// Entries down to 2^-LR_SPREAD of the largest keep 22 bits in two terms at that
-// scale: 2^-2 is then the smallest, and fp16's last bit is 2^-24.
-constexpr int LR_SPREAD = 16;
+// Entries down to 2^-LR_SPREAD of the largest keep all 24 bits in three terms at that
+// scale: the smallest is then 2^-1, whose last bit is fp16's, 2^-24.
+constexpr int LR_SPREAD = 15;
 
 // Operands of the weight gradients: h as three bf16 terms, 24 bits over fp32's
 // whole range whatever its neighbours hold (the tokens are the contraction there,
@@ -407,8 +407,10 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
 // of a tile are neighbours in the launch and together move whole rows of y.
 // Two or four tiles per workgroup, sharing B, were slower (79 and 114 us against
 // 67 then): fewer rows in flight.
-// fp16's passes by size cost up to 6 % where every tile takes one (3000 tokens of
-// 2048 columns, rank 128, 8192 fp16 results: 63.8 us, 60.2 with small entries lost).
+// fp16's third term and its passes by size (normal entries: a second one in 6e-5 of
+// them, so 1 tile in 8 at rank 128) cost 4 to 5 %, 12 at rank 128 (3000 tokens of
+// 2048 columns, 8192 fp16 results: 66.5 us; 59.4 with small entries lost).  Such
+// tiles in fp32 on the vector unit instead: 91.6.
 template <typename E, typename Y, int NJ, bool VEC>
 __global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int n_adapters, int max_rank, int split,
                                                      const int *__restrict__ ranks,
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int
     typedef typename Frag<E>::V V;
     constexpr int R = 16 * NJ, LD = R + 8;
     constexpr bool F = E::CODE == SPMV_F16;
-    constexpr int NT = F ? 2 : 3;
+    constexpr int NT = 3;
     __shared__ __attribute__((aligned(16))) unsigned short hs[NT][LR_TILE][LD];
     __shared__ int exps[LR_TILE], again[4];
     const int id = blockIdx.x / pieces, piece = blockIdx.x - id * pieces;
@@ -521,17 +523,20 @@ __global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int
 #pragma unroll
                         for (int w = 0; w < 4; ++w) r[i][w] = i < live ? r[i][w] : 0u;
                 }
+                V a[STEPS];
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
                     const int term = 2 * s + (q >> 1);
-                    u32x4 a = {0u, 0u, 0u, 0u};
+                    u32x4 w = {0u, 0u, 0u, 0u};
                     if (term < NT)
-                        a = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][n][8 * (q & 1)]);
+                        w = *reinterpret_cast<const u32x4 *>(&hs[term < NT ? term : 0][n][8 * (q & 1)]);
+                    a[s] = __builtin_bit_cast(V, w);
+                }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const V b = __builtin_bit_cast(V, column_of(r, c));
-                        acc[c] = Frag<E>::mma(__builtin_bit_cast(V, a), b, acc[c]);
-                    }
+                for (int c = 0; c < 8; ++c) {
+                    const V b = __builtin_bit_cast(V, column_of(r, c));
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) acc[c] = Frag<E>::mma(a[s], b, acc[c]);
                 }
             } else {
                 for (int j0 = 0; j0 < rank; j0 += 32) {
@@ -571,8 +576,8 @@ __global__ __launch_bounds__(256, VEC ? 3 : 1) void k_lora_expand(int n_tok, int
                 }
             }
             multiply(first);
-            // uniform; rare for entries of ordinary spread, and 7 passes at most for sums
-            // of fp16 products, as each takes every token's entries of 16 powers of two
+            // uniform; rare for entries of ordinary spread, and 8 passes at most for sums
+            // of fp16 products, as each takes every token's entries of 15 powers of two
             if (!F || !(again[0] | again[1] | again[2] | again[3])) break;
             __syncthreads();
         }

@@ -215,3 +215,25 @@ def test_apply_where_ranks_cancel(r, y):
     ref = h @ R.f64(B)[0]
     bound = (h.abs() @ R.f64(B)[0].abs()) * ((3 * r + 6) * R.ADD)
     R.check(out, ref, bound + R.rounded(ref.abs() + bound, out.dtype), "cancelled")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("r", [1, 20, 100])
+def test_rows_of_one_give_the_rank_vector_itself(r, dt):
+    """B holds the unit rows, so y is A x: sums of two products that fill fp32's
+    24 bits come back exactly."""
+    T = 50
+    rng = np.random.default_rng(r)
+    step = 1024 if dt == "f16" else 128                  # a type's last bit of 1.xx
+    mant = lambda *sh: torch.from_numpy(1 + rng.integers(0, step * 2 // 5, sh) / step).cuda()  # noqa: E731
+    A, x = mant(1, r, 2), mant(T, 2)
+    x[:, 1] *= 2.0 ** (-2 if dt == "f16" else -8)
+    x *= torch.exp2(torch.arange(T, device="cuda") % 21 - 10.0)[:, None]
+    A, x, B = A.to(F[dt]), x.to(F[dt]), torch.eye(r, device="cuda")[None].to(F[dt])
+    h = R.f64(x) @ R.f64(A)[0].t()
+    assert torch.equal(h, h.float().double())
+    p = _plan(np.zeros(T), 1)
+    y = torch.full((T, r), NAN, device="cuda")
+    S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, y,
+                 torch.empty(S.lora_workspace_size(T, r), dtype=torch.uint8, device="cuda"))
+    assert torch.equal(R.f64(y), h)
