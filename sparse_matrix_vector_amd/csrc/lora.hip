@@ -131,14 +131,19 @@ __device__ __forceinline__ Block block_of(const int4 *__restrict__ tiles, int n_
     return b;
 }
 
-// v as a sum of NT numbers of type E.
+// v as a sum of NT numbers of type E.  bf16's first is cut off, not rounded, so that
+// fp32's largest numbers stay finite (the next two still hold the 16 bits left);
+// infinities and NaN are the first term alone.
 template <typename E, int NT>
 __device__ __forceinline__ void split_terms(float v, unsigned short (&t)[NT]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const typename E::T p = (typename E::T)v;
-        t[i] = __builtin_bit_cast(unsigned short, p);
-        v -= (float)p;
+        if (E::CODE == SPMV_BF16 && i == 0)
+            t[i] = (unsigned short)(__float_as_uint(v) >> 16);
+        else
+            t[i] = __builtin_bit_cast(unsigned short, (typename E::T)v);
+        const float p = (float)__builtin_bit_cast(typename E::T, t[i]);
+        v = i == 0 && !(fabsf(p) < INFINITY) ? 0.0f : v - p;
     }
 }
 

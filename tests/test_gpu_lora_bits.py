@@ -237,3 +237,79 @@ def test_rows_of_one_give_the_rank_vector_itself(r, dt):
     S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, y,
                  torch.empty(S.lora_workspace_size(T, r), dtype=torch.uint8, device="cuda"))
     assert torch.equal(R.f64(y), h)
+
+
+# ---------------------------------------------------------------------------
+# Infinities
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("N,r", [(64, 1), (265, 8), (72, 24), (136, 90), (7, 3)])
+def test_apply_of_infinities(N, r, dt):
+    """A token with an infinity gets infinities of the definition's signs, and NaN
+    where it has NaN: where they meet zeros or each other."""
+    T, K = 20, 72
+    randn = _randn(N)
+    A, B, x = randn(1, r, K).abs() + 0.25, randn(1, r, N), randn(T, K)
+    B[0, :, ::3] = B[0, :, ::3].abs() + 0.25
+    B[0, :, 1::9] = 0
+    x[3, 5], x[7, 71], x[8, 0] = float("inf"), -float("inf"), NAN
+    x[9, 1], x[9, 2] = float("inf"), -float("inf")
+    A, B, x = A.to(F[dt]), B.to(F[dt]), x.to(F[dt])
+    base = randn(T, N)
+    p = _plan(np.zeros(T), 1)
+    y = torch.empty(T, N, device="cuda")
+    S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, base, y,
+                 torch.empty(S.lora_workspace_size(T, r), dtype=torch.uint8, device="cuda"))
+    h = (R.f64(x)[:, None, :] * R.f64(A)[0]).sum(2)
+    ref = R.f64(base) + (h[:, :, None] * R.f64(B)[0]).sum(1)
+    got = R.f64(y)
+    for t in (3, 7, 8, 9):
+        assert torch.equal(torch.isnan(got[t]), torch.isnan(ref[t])), t
+        ok = ~torch.isnan(ref[t])
+        assert torch.equal(got[t][ok], ref[t][ok]) and not torch.isfinite(ref[t]).any(), t
+    rest = [t for t in range(T) if t not in (3, 7, 8, 9)]
+    assert torch.isfinite(got[rest]).all()
+
+
+def test_rank_vector_past_fp32_beside_a_finite_one():
+    """bf16: one entry of A x overflows to an infinity, its neighbour is close to
+    fp32's largest number and stays finite."""
+    A = torch.zeros(1, 2, 8, device="cuda").bfloat16()
+    A[0, 0, 0], A[0, 1, 1], A[0, 1, 2] = 2.0 ** 100, 2.0 ** 100, 2.0 ** 92
+    x = torch.zeros(3, 8, device="cuda").bfloat16()
+    x[0, 0] = 2.0 ** 100
+    x[1, 1], x[1, 2] = 2.0 ** 28 - 2.0 ** 20, 2.0 ** 28 - 2.0 ** 20        # 2^128 - 2^112: rounds past bf16's largest
+    x[2, 1] = 1.0
+    B = torch.zeros(1, 2, 16, device="cuda").bfloat16()
+    B[0, 0, :8], B[0, 1, 8:] = 2.0, 2.0 ** -20
+    p = _plan(np.zeros(3), 1)
+    y = torch.empty(3, 16, device="cuda")
+    S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, y,
+                 torch.empty(S.lora_workspace_size(3, 2), dtype=torch.uint8, device="cuda"))
+    h = (R.f64(x)[:, None, :] * R.f64(A)[0]).sum(2)
+    assert h[1, 1] < 2.0 ** 128 and float(h[1, 1].float()) == float(h[1, 1])
+    assert (y[0, :8] == float("inf")).all() and torch.isnan(y[0, 8:]).all()      # an infinity times zero
+    assert (R.f64(y[1, 8:]) == h[1, 1] * 2.0 ** -20).all() and (y[1, :8] == 0).all()
+    assert (y[2, 8:] == 2.0 ** 80).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_grad_of_infinities(dt):
+    """What a bad element takes part in is not finite, the rest is as without it."""
+    T, K, N, n, r = 100, 72, 136, 3, 20
+    randn = _randn(9)
+    A, B, x, dy = (t.to(F[dt]) for t in (randn(n, r, K), randn(n, r, N), randn(T, K), randn(T, N)))
+    keys = np.arange(T) % n
+    dA0, dB0 = _grad(A, B, x, dy, keys)
+    for bad in (float("inf"), NAN):
+        xb, db = x.clone(), dy.clone()
+        xb[7, 5] = bad                     # adapter 1
+        db[11, 130] = bad                  # adapter 2
+        dA, dB = _grad(A, B, xb, db, keys)
+        assert torch.equal(dA[0], dA0[0]) and torch.equal(dB[0], dB0[0])
+        keep = [k for k in range(K) if k != 5]
+        assert torch.equal(dA[1][:, keep], dA0[1][:, keep]) and not torch.isfinite(dA[1][:, 5]).any()
+        assert not torch.isfinite(dB[1]).any()
+        keep = [k for k in range(N) if k != 130]
+        assert torch.equal(dB[2][:, keep], dB0[2][:, keep]) and not torch.isfinite(dB[2][:, 130]).any()
+        assert not torch.isfinite(dA[2]).any()
