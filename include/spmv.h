@@ -730,8 +730,8 @@ spmv_status route_combine_grad(int32_t n_tok, int32_t top_k, int32_t dim, int32_
 /* that one takes part in is infinite or NaN.  A and B are finite.              */
 /* ------------------------------------------------------------------------ */
 
-/* Bytes of the workspace of the two calls below.  Host only.  Ranks above 128
- * are SPMV_ERR_UNSUPPORTED. */
+/* Bytes of the workspace of the two calls below (a call without tokens takes NULL).
+ * Host only.  Ranks above 128 are SPMV_ERR_UNSUPPORTED. */
 spmv_status lora_workspace_size(int32_t n_tok, int32_t max_rank, size_t *bytes);
 
 /* dtype: SPMV_F16 or SPMV_BF16, of x, A and B; y_dtype: the same, or SPMV_F32.

@@ -819,7 +819,7 @@ spmv_status check_common(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_a
     if (!A || !B || !offsets || (n_tok > 0 && (!order || !tiles))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
     if (!aligned16(tiles)) return fail(SPMV_ERR_UNSUPPORTED, "tiles must be 16-byte aligned");
     size_t need = 0;
-    lora_workspace_size(n_tok, max_rank, &need);
+    if (n_tok > 0) lora_workspace_size(n_tok, max_rank, &need);
     if (n_tok > 0 && !workspace) return fail(SPMV_ERR_INVALID_VALUE, "workspace is NULL (lora_workspace_size gives its size)");
     if (workspace_bytes < need)
         return fail(SPMV_ERR_INVALID_VALUE, "workspace of %zu bytes is smaller than %zu", workspace_bytes, need);

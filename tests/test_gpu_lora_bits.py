@@ -313,3 +313,13 @@ def test_grad_of_infinities(dt):
         keep = [k for k in range(N) if k != 130]
         assert torch.equal(dB[2][:, keep], dB0[2][:, keep]) and not torch.isfinite(dB[2][:, 130]).any()
         assert not torch.isfinite(dA[2]).any()
+
+
+def test_grad_without_tokens_or_workspace():
+    A, B = torch.ones(3, 8, 64, device="cuda").half(), torch.ones(3, 8, 72, device="cuda").half()
+    p = _plan([], 3)
+    dA, dB = torch.full(A.shape, NAN, device="cuda"), torch.full(B.shape, NAN, device="cuda")
+    x, dy = A[0, :0], B[0, :0]
+    S.lora_grad(None, None, A, B, p.order, p.offsets, p.tiles, x, dy, dA, dB, None)
+    assert (dA == 0).all() and (dB == 0).all()
+    assert S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, dy, None) is dy
