@@ -640,8 +640,10 @@ spmv_status macko_spmm_plan(int32_t n_rows, int32_t n_cols, int32_t bdelta, cons
 /* Bytes of the workspace of macko_spmm at this shape: room for x where it cannot
  * be read 16 bytes at a time (n_cols or ldx not a multiple of 8, or x not
  * 16-byte aligned: it is copied there first), and for partial sums where the
- * columns are split over workgroups.  A call that needs neither also takes
- * NULL.  Not monotone in n_tok.  Host only. */
+ * columns are best split over workgroups.  A workspace of this size for the
+ * largest batch serves every smaller one: the columns are split as far as it has
+ * room (which the bits of the sums depend on), with less or NULL as far as none.
+ * Only x that has to be copied must fit.  Not monotone in n_tok.  Host only. */
 spmv_status macko_spmm_workspace_size(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t n_tok,
                                       size_t *bytes);
 

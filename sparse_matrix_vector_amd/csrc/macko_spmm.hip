@@ -735,7 +735,7 @@ struct Cut {
     int split;        // workgroups over the columns
 };
 
-Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok) {
+Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok, int64_t max_split = 16) {
     Cut c = {};
     const int64_t t16 = std::max<int64_t>(1, ceil_div(n_tok, 16));
     // Up to 32 tokens, as long as the traffic of x (every 16 rows read all of it)
@@ -773,7 +773,7 @@ Cut cut_of(int64_t n_groups, int64_t n_rows, int64_t n_cols, int64_t n_tok) {
     const double alone = c.nt == 2 ? 0.8 : c.nt == 4 ? 1.0 : c.nt == 8 ? 1.2 : 1.9;
     const double each = c.nt == 2 ? 0.95 : c.nt == 4 ? 1.0 : c.nt == 8 ? 1.5 : 2.2;
     double best = 1e30;
-    for (int s = 1; s <= 16 && s <= slabs; ++s) {
+    for (int s = 1; s <= 16 && s <= slabs && (s == 1 || s <= max_split); ++s) {
         const int64_t wgs = n_groups * ceil_div(n_rows, BlockShape<4>::ROWS) * c.tiles * s, full = wgs / (256 * fit);
         const int64_t rest = ceil_div(wgs - full * 256 * fit, 256);
         const double slab = (double)full * (alone + each * fit) + (rest ? alone + each * (double)rest : 0.0);
@@ -789,6 +789,9 @@ int64_t partial_ld(int64_t n_rows) { return ceil_div(n_rows, 4) * 4; }
 size_t packed_bytes(int64_t n_tok, int64_t n_cols) {
     return ((size_t)n_tok * (size_t)(ceil_div(n_cols, 8) * 8) * 2 + 15) & ~size_t(15);
 }
+
+// the sums of one part of the columns
+size_t part_bytes(int64_t n_tok, int64_t n_rows) { return (size_t)n_tok * (size_t)partial_ld(n_rows) * 4; }
 
 template <int BD, bool I8, int NT>
 spmv_status launch_block(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
@@ -877,15 +880,17 @@ spmv_status spmm_apply(int32_t n_groups, int32_t n_rows, int32_t n_cols, int32_t
             return macko_spmv(n_rows, n_cols, bdelta, mrow_ptr, codes, static_cast<const uint16_t *>(vals), alpha, x, beta,
                               static_cast<float *>(y), stream);
     }
-    const Cut cut = cut_of(n_groups, n_rows, n_cols, n_tok);
+    // the workspace: x packed where that is needed, then as many parts as fit
+    // (the best cut of a smaller batch may want more than a larger one's)
     const bool pack = !aligned16(x) || ldx % 8 != 0 || n_cols % 8 != 0;
-    if (pack || cut.split > 1) {
-        size_t need = 0;
-        macko_spmm_workspace_size(n_groups, n_rows, n_cols, n_tok, &need);
-        if (!workspace || workspace_bytes < need || !aligned16(workspace))
-            return fail(SPMV_ERR_INVALID_VALUE, "this product needs a 16-byte aligned workspace of %zu bytes", need);
-    }
-    float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + packed_bytes(n_tok, n_cols));
+    const size_t packed = pack ? packed_bytes(n_tok, n_cols) : 0;
+    if (pack && (!workspace || workspace_bytes < packed))
+        return fail(SPMV_ERR_INVALID_VALUE, "x of this shape and alignment needs a workspace of %zu bytes", packed);
+    const size_t room = workspace && workspace_bytes > packed ? workspace_bytes - packed : 0;
+    const Cut cut = cut_of(n_groups, n_rows, n_cols, n_tok, (int64_t)std::min<size_t>(16, room / part_bytes(n_tok, n_rows)));
+    if ((pack || cut.split > 1) && !aligned16(workspace))
+        return fail(SPMV_ERR_INVALID_VALUE, "workspace must be 16-byte aligned");
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + packed);
     if (pack) {
         const int ldp = (int)(ceil_div(n_cols, 8) * 8);
         k_macko_spmm_pack<<<dim3((unsigned)ceil_div(ldp, 256), (unsigned)std::min(n_tok, 65535)), 256, 0, s>>>(
@@ -950,7 +955,7 @@ extern "C" spmv_status macko_spmm_workspace_size(int32_t n_groups, int32_t n_row
     if (st != SPMV_OK) return st;
     const Cut c = cut_of(n_groups, n_rows, n_cols, n_tok);
     *bytes = packed_bytes(n_tok, n_cols) +
-             (c.split > 1 ? (size_t)c.split * (size_t)n_tok * (size_t)partial_ld(n_rows) * 4 : 0);
+             (c.split > 1 ? (size_t)c.split * part_bytes(n_tok, n_rows) : 0);
     return SPMV_OK;
 }
 

@@ -191,7 +191,8 @@ def macko_spmm(n_rows, n_cols, mrow_ptr, codes, mvals, plan, alpha, x, beta, y, 
                stream=None, bdelta=4):
     """y = alpha * x W^T + beta * y for x [tokens, n_cols] fp16 and y [tokens,
     n_rows] fp32 or fp16; tok_offsets (int32 [groups + 1]): one stacked weight
-    per group of tokens.  workspace: macko_spmm_workspace_size bytes."""
+    per group of tokens.  workspace: macko_spmm_workspace_size bytes, or those of
+    a larger batch."""
     return _spmm("macko_spmm", int(n_rows), int(n_cols), int(bdelta), mrow_ptr, codes,
                  lambda d, g: (_ptr(mvals, _HALF, "mvals", 0, d),), plan, alpha, x, beta, y, workspace, tok_offsets, stream)
 
