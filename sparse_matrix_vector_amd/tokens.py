@@ -206,15 +206,18 @@ def macko_spmm_i8(n_rows, n_cols, mrow_ptr, codes, q, row_scale, plan, alpha, x,
 
 class MackoMatrix:
     """One MACKO weight (or n_groups stacked ones) with its many-token plan.
-    row_scale: the int8 values' scales, or None for fp16 values."""
+    row_scale: the int8 values' scales, or None for fp16 values.  The plan is
+    made on `stream`: other streams wait for it before they use the matrix, and
+    it is kept until their calls are done."""
 
     def __init__(self, n_rows, n_cols, mrow_ptr, codes, vals, row_scale=None, n_groups=1, bdelta=4, stream=None):
         self.n_rows, self.n_cols, self.n_groups, self.bdelta = int(n_rows), int(n_cols), int(n_groups), int(bdelta)
         self.mrow_ptr, self.codes, self.vals, self.row_scale = mrow_ptr, codes, vals, row_scale
         if mrow_ptr.numel() != self.n_groups * self.n_rows + 1:
             raise ValueError(f"mrow_ptr must have {self.n_groups * self.n_rows + 1} elements")
-        self.plan = torch.empty(max(macko_spmm_plan_size(self.n_groups * self.n_rows, n_cols), 4), dtype=torch.uint8,
-                                device=mrow_ptr.device)
+        with _stream_scope(stream, mrow_ptr.device):
+            self.plan = torch.empty(max(macko_spmm_plan_size(self.n_groups * self.n_rows, n_cols), 4), dtype=torch.uint8,
+                                    device=mrow_ptr.device)
         macko_spmm_plan(self.n_groups * self.n_rows, n_cols, mrow_ptr, codes, self.plan, stream, bdelta)
 
     def workspace(self, n_tok):
@@ -300,7 +303,9 @@ def route_combine_grad(dy, ys, pos, weights, dys, dw, stream=None):
 class RoutePlan:
     """The plan of a batch of n_tok tokens with top_k choices of n_groups
     groups each: build() sorts, gather() and combine() move rows there and
-    back.  One plan serves every layer that shares the batch's keys."""
+    back.  One plan serves every layer that shares the batch's keys.  Its arrays
+    are allocated on the current stream: another one that build() is to run on
+    waits for it first."""
 
     def __init__(self, n_tok, top_k, n_groups, device="cuda"):
         self.n_tok, self.top_k, self.n_groups = int(n_tok), int(top_k), int(n_groups)

@@ -46,3 +46,22 @@ def test_a_larger_batchs_workspace_serves_smaller_ones(shape, i8):
                 outs.append(y)
             assert torch.equal(outs[0], m.apply(x, torch.empty_like(y), tok_offsets=dev_off))
         assert (buf[size:] == 77).all()
+
+
+def test_plan_of_a_side_stream_has_memory_of_that_stream():
+    rows, cols = 40, 300
+    w = _weight(rows, cols, "0.5", 4, 3)
+    m = _matrix(w, rows, cols, 4)
+    size = m.plan.numel()
+    x = _x(9, cols, 1)
+    want = m.apply(x, torch.empty(9, rows, device="cuda"))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        freed = torch.empty(size, dtype=torch.uint8, device="cuda")
+        block = freed.data_ptr()
+        del freed
+        other = S.MackoMatrix(rows, cols, m.mrow_ptr, m.codes, m.vals, stream=stream)
+        assert other.plan.data_ptr() != block
+        side.synchronize()
+        assert torch.equal(other.apply(x, torch.empty(9, rows, device="cuda")), want)
