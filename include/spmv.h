@@ -607,7 +607,8 @@ spmv_status spgemm_destroy(spgemm_t h);
 /* projection for a batch of tokens (or for experts' groups of tokens), tokens */
 /* sorted by group and back, and low-rank adapters of many requests.          */
 /* Matrices of activations are row-major [tokens, width] with a row stride    */
-/* (ld*) in elements, at least the width.                                     */
+/* (ld*) in elements, at least the width.  A call whose launch would need 2^32  */
+/* threads or more is SPMV_ERR_OVERFLOW.                                       */
 /* ======================================================================== */
 typedef enum { SPMV_F16 = 0, SPMV_BF16 = 1, SPMV_F32 = 2 } spmv_dtype;
 

@@ -24,6 +24,12 @@ struct F32 {
 };
 
 inline bool dtype_ok(int32_t d) { return d == SPMV_F16 || d == SPMV_BF16 || d == SPMV_F32; }
+// A grid holds fewer than 2^32 threads.
+inline spmv_status check_grid(int64_t blocks, int threads = 256) {
+    if (blocks > (int64_t)(UINT32_MAX / (unsigned)threads))
+        return fail(SPMV_ERR_OVERFLOW, "the launch would need 2^32 threads or more");
+    return SPMV_OK;
+}
 inline size_t dtype_size(int32_t d) { return d == SPMV_F32 ? 4 : 2; }
 
 // N elements of type E, loaded and stored with one aligned access.

@@ -874,6 +874,10 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
     if (y_in == y && y_in && ldyin != ldy) return fail(SPMV_ERR_INVALID_VALUE, "y_in is y, but their row strides differ");
     if (n_tok == 0) return SPMV_OK;
     if (!x || !y) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
+    const int64_t pieces = ceil_div(n_out, 4 * LR_WAVE_COLS);
+    st = check_grid(n_tiles * pieces);
+    if (st != SPMV_OK) return st;
+    const int grid = (int)(n_tiles * pieces);
     hipStream_t s = as_stream(stream);
     const int split = split_of(n_tok, n_tiles, n_in);
     const int4 *tl = reinterpret_cast<const int4 *>(tiles);
@@ -892,9 +896,6 @@ extern "C" spmv_status lora_apply(int32_t n_tok, int32_t n_in, int32_t n_out, in
         });
     });
     if (st != SPMV_OK) return st;
-    const int64_t pieces = ceil_div(n_out, 4 * LR_WAVE_COLS);
-    if (n_tiles * pieces > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "the launch does not fit int32");
-    const int grid = (int)(n_tiles * pieces);
     return by_half(dtype, [&](auto e) {
         typedef decltype(e) E;
         return by_rank(max_rank, [&](auto nj) {

@@ -797,7 +797,8 @@ template <int BD, bool I8, int NT>
 spmv_status launch_block(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
     const int row_blocks = (int)ceil_div(a.n_rows, BlockShape<NT>::ROWS);
     const int64_t grid = (int64_t)row_blocks * c.tiles * c.split * n_groups;
-    if (grid > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "the launch does not fit int32");
+    const spmv_status fits = check_grid(grid, 64 * BlockShape<NT>::WAVES);
+    if (fits != SPMV_OK) return fits;
     k_macko_spmm_block<BD, I8, NT><<<(unsigned)grid, 64 * BlockShape<NT>::WAVES, BlockShape<NT>::LDS, st>>>(
         a, n_groups, row_blocks, c.tiles, c.width, c.split, partial, (int)partial_ld(a.n_rows));
     SPMV_LAUNCHED("k_macko_spmm_block");

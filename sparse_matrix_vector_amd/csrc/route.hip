@@ -348,11 +348,6 @@ spmv_status check_rows(int32_t n_tok, int32_t top_k, int32_t dim, int32_t dtype)
 // whether a row holds at least one 16-byte access
 bool wide_rows(int32_t dim, int32_t dtype) { return (size_t)dim * dtype_size(dtype) >= 16; }
 
-spmv_status check_grid(int64_t blocks) {
-    if (blocks > INT32_MAX) return fail(SPMV_ERR_OVERFLOW, "the launch does not fit int32");
-    return SPMV_OK;
-}
-
 template <typename F>
 spmv_status by_type(int32_t dtype, bool vec, F f) {
     if (dtype == SPMV_F16) return vec ? f(F16{}, std::integral_constant<int, 8>{}) : f(F16{}, std::integral_constant<int, 1>{});
@@ -476,6 +471,8 @@ extern "C" spmv_status route_combine_grad(int32_t n_tok, int32_t top_k, int32_t 
     if (lddy < dim || ldys < dim || lddys < dim) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
     if (n_tok == 0) return SPMV_OK;
     if (!pos || !dw || (dim > 0 && (!dy || !ys || !dys))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
+    st = check_grid(n_tok);
+    if (st != SPMV_OK) return st;
     return by_type(dtype, wide_rows(dim, dtype), [&](auto e, auto vec) {
         typedef decltype(e) E;
         typedef typename E::T T;

@@ -42,3 +42,19 @@ def test_macko_plan_is_allocated_on_the_stream_that_fills_it(monkeypatch):
     seen.clear()
     S.MackoMatrix(3, 64, torch.zeros(4, dtype=torch.int32), None, None)
     assert seen == [("alloc", [None]), ("fill", None)]          # the current stream
+
+
+def test_launches_of_2_to_the_32_threads_are_refused():
+    """A grid holds fewer than 2^32 threads: 2^24 workgroups of 256 do not fit."""
+    L = S.lib()
+    # 4 tokens' pieces per workgroup: 2^22 tokens of 16 (combine) or 2^23 of 8 (gather) pieces
+    assert L.route_combine(1 << 22, 1, 8192, 0, P, None, P, 8192, P, 8192, None) == OVERFLOW
+    assert L.route_gather(1 << 23, 1, 16384, 1, P, None, P, 16384, P, 16384, None) == OVERFLOW
+    assert L.route_combine_grad(1 << 24, 1, 8, 2, P, 8, P, 8, P, None, P, 8, P, None) == OVERFLOW
+    # 262145 tiles of 64 pieces of 512 columns
+    n, n_out = 1 << 22, 32768
+    tiles = S.route_tile_count(n, 1)
+    assert L.lora_apply(n, 8, n_out, 1, 8, None, None, P, P, 0, P, P, P, tiles, P, 8, None, 0, P, 2, n_out, P,
+                        S.lora_workspace_size(n, 8), None) == OVERFLOW
+    # 512 groups of 64 row blocks and 512 token tiles
+    assert L.macko_spmm(512, 4096, 256, 4, P, P, P, P, P, 131072, 1.0, P, 256, 0.0, P, 2, 4096, None, 0, None) == OVERFLOW
