@@ -409,28 +409,28 @@ __device__ __forceinline__ void wave_lds_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Few tokens.  Workgroup: rows 16 blockIdx.y .. of group blockIdx.z, tokens
-// 16 NT blockIdx.x .. of that group, slabs wave, wave + WAVES, ...; the waves add
-// their sums at the end.  Bound by the latency of a slab's chain (plan word,
+// Few tokens, 32 at most.  Workgroup: rows 16 blockIdx.x .. of group blockIdx.y and
+// that group's tokens, slabs wave, wave + WAVES, ...; the waves add their sums at
+// the end.  Bound by the latency of a slab's chain (plan word,
 // codes, scan, LDS, product), so small calls want many waves.  5.7 us for
 // 2048 x 2048 (half kept) times 5, of which about 3 are the launch; 38 us
 // for 12288 x 12288 (30 % kept) times 2, 116 MB at 3.0 TB/s.
 template <int BD, bool I8, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
+    static_assert(NT <= 2, "x is held in registers for a whole slab");
     extern __shared__ __attribute__((aligned(16))) unsigned short lds[];
     const int lane = __lane_id(), q = lane >> 4, n = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     int t0 = 0, t1 = a.n_tok;
     if (a.tok_offsets) {
-        t0 = min(max(a.tok_offsets[blockIdx.z], 0), a.n_tok);
-        t1 = min(max(a.tok_offsets[blockIdx.z + 1], t0), a.n_tok);
+        t0 = min(max(a.tok_offsets[blockIdx.y], 0), a.n_tok);
+        t1 = min(max(a.tok_offsets[blockIdx.y + 1], t0), a.n_tok);
     }
-    t0 += blockIdx.x * 16 * NT;
     if (t0 >= t1) return;
     const int live = min(NT, (t1 - t0 + 15) / 16);      // token tiles in use
-    const int r0 = blockIdx.y * SM_ROWS;
+    const int r0 = blockIdx.x * SM_ROWS;
     const int rows = min(SM_ROWS, a.n_rows - r0);
-    const int64_t row0 = (int64_t)blockIdx.z * a.n_rows + r0;
+    const int64_t row0 = (int64_t)blockIdx.y * a.n_rows + r0;
     unsigned short *tile = lds + SM_FRONT + wv * SM_ROWS * SM_LDW;
     const unsigned short *xr[NT];
 #pragma unroll
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const Streams str = streams_of<BD, I8>(a.codes, a.vals, a.mrp[(int64_t)gridDim.z * a.n_rows] / 8);
+    const Streams str = streams_of<BD, I8>(a.codes, a.vals, a.mrp[(int64_t)gridDim.y * a.n_rows] / 8);
     const RowPair rp = load_rows(a, row0, rows, lane);
     // one slab: its units are in st; next gets those of slab k + WAVES, whose
     // plan words are in pw, and pw those of the slab after that
@@ -450,14 +450,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
         // first goes first, and the next slab's units last
         // columns past the last are read as the row's last ones: W is zero there
         const int c0 = k * SM_SLAB + 8 * q, cm = a.n_cols - 8;
-        u32x4 x[NT < 4 ? NT : 1][8];
-        if constexpr (NT < 4) {
+        u32x4 x[NT][8];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    x[i][s] = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 32 * s, cm));
-        }
+            for (int s = 0; s < 8; ++s)
+                x[i][s] = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 32 * s, cm));
         const PlanWords after = load_plan(rp, min(k + 2 * WAVES, top));
         __builtin_amdgcn_sched_barrier(0);
         load_stage<BD, I8>(next, str, rp, pw, lane & 7);
@@ -472,14 +470,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_macko_spmm(SpmmArg a) {
             const h8 w = __builtin_bit_cast(
                 h8, *reinterpret_cast<const u32x4 *>(tile + n * SM_LDW + 32 * s + 8 * q));
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if constexpr (NT < 4) {
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, x[i][s]), acc[i], 0, 0, 0);
-                } else if (i < live) {                   // uniform
-                    const u32x4 xv = *reinterpret_cast<const u32x4 *>(xr[i] + min(c0 + 32 * s, cm));
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, xv), acc[i], 0, 0, 0);
-                }
-            }
+            for (int i = 0; i < NT; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(h8, x[i][s]), acc[i], 0, 0, 0);
         }
         wave_lds_order();
     };
@@ -589,63 +581,62 @@ __global__ __launch_bounds__(64 * BlockShape<NT>::WAVES, BlockShape<NT>::OCC) vo
 #pragma unroll
     for (int t = 0; t < B::TW; ++t)
         xr[t] = a.x + (int64_t)min(t0 + 16 * (tw0 + B::GROUPS * t) + n, t1 - 1) * a.ldx;
+    // at least one slab: split is at most their number
     const int lo = (int)((int64_t)a.n_slabs * part / split), hi = (int)((int64_t)a.n_slabs * (part + 1) / split);
     const int cm = a.n_cols - 8;
-    if (lo < hi) {
-        const int col = kp * 32 * B::STEPS + 8 * q;         // the lane's first column in a slab
-        u32x4 x[B::AHEAD][B::TW];
-        // columns past the last are read as the row's last ones: W is zero there
-        auto load_x = [&](int k, int s, int slot) {
+    const int col = kp * 32 * B::STEPS + 8 * q;         // the lane's first column in a slab
+    u32x4 x[B::AHEAD][B::TW];
+    // columns past the last are read as the row's last ones: W is zero there
+    auto load_x = [&](int k, int s, int slot) {
 #pragma unroll
-            for (int t = 0; t < B::TW; ++t)
-                x[slot][t] = *reinterpret_cast<const u32x4 *>(xr[t] + min(k * SM_SLAB + col + 32 * s, cm));
-        };
-        Stage<BD, I8> st;
-        const PlanWords first = load_plan(rp, lo);
-        PlanWords pw = load_plan(rp, min(lo + 1, hi - 1));
-        __builtin_amdgcn_sched_barrier(0);
-        load_stage<BD, I8>(st, str, rp, first, lane & 7);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < B::TW; ++t)
+            x[slot][t] = *reinterpret_cast<const u32x4 *>(xr[t] + min(k * SM_SLAB + col + 32 * s, cm));
+    };
+    Stage<BD, I8> st;
+    const PlanWords first = load_plan(rp, lo);
+    PlanWords pw = load_plan(rp, min(lo + 1, hi - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    load_stage<BD, I8>(st, str, rp, first, lane & 7);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < B::AHEAD; ++s) load_x(lo, s, s);
-        for (int k = lo; k < hi; ++k) {
-            clear_tile(tile, lane);
-            wave_lds_order();
-            // half by half, the next slab's units are loaded as soon as their
-            // registers are free; the next x is in flight over the decoding
-            const PlanWords after = load_plan(rp, min(k + 2, hi - 1));
+    for (int s = 0; s < B::AHEAD; ++s) load_x(lo, s, s);
+    for (int k = lo; k < hi; ++k) {
+        clear_tile(tile, lane);
+        wave_lds_order();
+        // half by half, the next slab's units are loaded as soon as their
+        // registers are free; the next x is in flight over the decoding
+        const PlanWords after = load_plan(rp, min(k + 2, hi - 1));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                decode_half<BD, I8>(st, str, rp, lane, lds_offset(tile), h);
-                __builtin_amdgcn_sched_barrier(0);
-                load_half<BD, I8>(st, str, rp, pw, lane & 7, h);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            pw = after;
-            lds_barrier();
-#pragma unroll
-            for (int s = 0; s < B::STEPS; ++s) {
-                h8 w[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    w[r] = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4 *>(lds + SM_FRONT + (16 * r + n) * SM_LDW +
-                                                                                   (kp * B::STEPS + s) * 32 + 8 * q));
-#pragma unroll
-                for (int t = 0; t < B::TW; ++t) {
-                    if (t < mine) {                         // uniform
-                        const h8 xv = __builtin_bit_cast(h8, x[s % B::AHEAD][t]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[r], xv, acc[r][t], 0, 0, 0);
-                    }
-                }
-                if (s + B::AHEAD < B::STEPS)
-                    load_x(k, s + B::AHEAD, s % B::AHEAD);
-                else
-                    load_x(min(k + 1, hi - 1), (s + B::AHEAD) % B::STEPS, s % B::AHEAD);
-            }
-            lds_barrier();
+        for (int h = 0; h < 2; ++h) {
+            decode_half<BD, I8>(st, str, rp, lane, lds_offset(tile), h);
+            __builtin_amdgcn_sched_barrier(0);
+            load_half<BD, I8>(st, str, rp, pw, lane & 7, h);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        pw = after;
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < B::STEPS; ++s) {
+            h8 w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                w[r] = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4 *>(lds + SM_FRONT + (16 * r + n) * SM_LDW +
+                                                                               (kp * B::STEPS + s) * 32 + 8 * q));
+#pragma unroll
+            for (int t = 0; t < B::TW; ++t) {
+                if (t < mine) {                         // uniform
+                    const h8 xv = __builtin_bit_cast(h8, x[s % B::AHEAD][t]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[r], xv, acc[r][t], 0, 0, 0);
+                }
+            }
+            if (s + B::AHEAD < B::STEPS)
+                load_x(k, s + B::AHEAD, s % B::AHEAD);
+            else
+                load_x(min(k + 1, hi - 1), (s + B::AHEAD) % B::STEPS, s % B::AHEAD);
+        }
+        lds_barrier();
     }
     if (B::KW > 1) {                                        // the column parts, in order
         f32x4 *sums = reinterpret_cast<f32x4 *>(lds) + tw0 * (4 * B::TW * 64) + lane;   // [KW - 1][GROUPS][TW][4][64]
@@ -816,7 +807,7 @@ void launch_waves(const SpmmArg &a, const Cut &c, dim3 grid, hipStream_t st) {
 template <int BD, bool I8>
 spmv_status launch_shape(const SpmmArg &a, const Cut &c, int n_groups, float *partial, hipStream_t st) {
     if (!c.block) {
-        const dim3 grid(c.tiles, (unsigned)ceil_div(a.n_rows, SM_ROWS), n_groups);
+        const dim3 grid((unsigned)ceil_div(a.n_rows, SM_ROWS), n_groups);
         if (c.nt == 1)
             launch_waves<BD, I8, 1>(a, c, grid, st);
         else
