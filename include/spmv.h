@@ -687,7 +687,10 @@ spmv_status route_tile_count(int32_t n_slots, int32_t n_groups, int32_t *n_tiles
 /* Bytes of route_plan's workspace (0 where it needs none).  Host only. */
 spmv_status route_workspace_size(int32_t n_slots, int32_t n_groups, size_t *bytes);
 
-/* Builds the plan.  keys int32[n_slots]; all pointers device.  Asynchronous. */
+/* Builds the plan.  keys int32[n_slots]; all pointers device.  Asynchronous.
+ * Above 8192 slots the work grows with their square times n_groups (every part of
+ * the sort adds up all parts' counts): 2^16 slots of 64 groups take 24 us, 2^22 of
+ * 64 87 us, but 2^20 of 2048 groups 5.6 ms and 2^22 of 2048 68 ms. */
 spmv_status route_plan(int32_t n_slots, int32_t n_groups, const int32_t *keys, int32_t *offsets,
                        int32_t *order, int32_t *pos, int32_t *tiles, void *workspace,
                        size_t workspace_bytes, void *stream);

@@ -406,8 +406,9 @@ __device__ __forceinline__ void store_row8(typename Y::T *p, int c, int n, const
     }
 }
 
-// Bound by the traffic of y: 4093 tokens of 12288 bf16 results at rank 64, read
-// and written, 201 MB in 51 us (3.9 TB/s).
+// Bound by the traffic of y and B: 4093 tokens of 12288 bf16 results at rank 64, read
+// and written, 201 MB in 51 us (3.9 TB/s), and 412 MB of B from L2, which every tile
+// of tokens reads for itself.
 // One workgroup: a tile of tokens and 512 columns, 128 per wave; the columns
 // of a tile are neighbours in the launch and together move whole rows of y.
 // Two or four tiles per workgroup, sharing B, were slower (79 and 114 us against
@@ -644,7 +645,7 @@ struct OuterArg {
 
 // Bound by the latency of the rows of x and dy, which few waves walk (a
 // workgroup has one adapter's 128 columns): 8192 tokens of 4096 + 4096 bf16,
-// rank 32, 4 adapters 39 us (134 MB, 3.4 TB/s); 300 tokens at rank 8 5.3 us.
+// rank 32, 4 adapters 38 us (134 MB, 3.5 TB/s); 300 fp16 tokens at rank 8 6.2 us.
 // More workgroups would have to add partial gradients; the terms loaded a step
 // ahead as well was 3 to 8 % slower (registers).
 // One workgroup: 128 columns of adapter blockIdx.y's gradient; blockIdx.x
@@ -771,9 +772,13 @@ constexpr int LR_WIDE = 4;
 
 // lora_grad's products take blocks of LR_WIDE tiles, an operand of A or B serving
 // all of them, where that still fills the card and adapters have 64 tokens or
-// more on average.  Gradient at 4096 x 4096, 8 adapters, rank 32: 16384 tokens
-// 156 us (185 in single tiles), 8192 tokens 92 (100), 4096 tokens 53 and 87 in
-// two batches (62 and 73); rank 16: 16384 tokens 121 (126), 8192 tokens 90 (70).
+// more on average.  Gradient in us with (and without), bf16; fp16 the same way:
+//   tokens                          4096         6000         8192        16384
+//   4 adapters, 4096^2, rank 32  46.2 (44.7)  79.1 (63.3)  60.8 (81.1)  116 (154)
+//   1 adapter,  2048^2, rank 32  43.1 (41.3)  53.8 (57.6)  63.9 (73.3)  131 (152)
+//   4 adapters, 4096^2, rank 16  40.2 (35.5)  66.9 (49.7)  56.0 (65.1)  106 (123)
+//   8 adapters, 4096^2, rank 16                            90   (70)    121 (126)
+// Up to rank 16 and below 16384 tokens it depends on the number of adapters.
 // At rank 64 the registers do not allow it.  lora_apply is better off with single
 // tiles (8192 tokens 69 us, 82 in blocks).
 bool wide_blocks(int64_t n_tok, int64_t n_adapters, int max_rank) {
@@ -971,11 +976,14 @@ extern "C" spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int
                 }
                 // With few column blocks, 8 waves and one rank tile per workgroup fill
                 // the card better; with more, 4 waves, so that two workgroups share a
-                // CU, and two rank tiles that share a reading of x.  Rank 32, gradient in
-                // us: 8192 tokens, 2048 columns, 1 adapter (32 blocks) 67, with 4 waves
-                // 79, with two rank tiles 88; 8192 tokens, 4096 columns, 8 adapters (512
-                // blocks) 92 with 4 waves and 8, 103 with one rank tile; 64 adapters 114,
-                // with 8 waves 145.
+                // CU, and two rank tiles that share a reading of x.  Gradient in us with 8
+                // waves and one rank tile (with 4 and, above rank 16, two), bf16; fp16 alike:
+                //   blocks     32          64          128         192         256
+                //   rank 16 65.6 (81.4) 19.8 (20.5) 23.0 (24.5) 27.8 (27.6) 34.0 (35.9)
+                //   rank 32 64.1 (88.5) 23.1 (26.6) 28.4 (31.4) 42.1 (40.0) 53.9 (44.5)
+                //   rank 64 91.4 (115)  29.4 (32.8) 46.4 (41.2) 66.2 (59.6) 92.8 (68.7)
+                // (32 blocks: 8192 tokens, otherwise 4096).  Above rank 32 the two meet
+                // nearer 100 blocks.
                 constexpr int JB = NJ < 2 ? NJ : 2;
                 const int64_t blocks = (int64_t)(oa.blocks + ob.blocks) * n_adapters;
                 if (blocks < 192)
