@@ -731,7 +731,7 @@ spmv_status route_combine_grad(int32_t n_tok, int32_t top_k, int32_t dim, int32_
 /* (one choice per token) and n_adapters groups; tokens whose key is dropped    */
 /* have no adapter: y[t] = y_in[t].  n_tiles: route_tile_count's value.         */
 /* Sums over n_in, n_out and tokens are fp32, and the rank vector A x keeps     */
-/* fp32's 24 bits.  Results are the same bits on every call.  An infinity or   */
+/* fp32's 24 bits (down to 2^-133).  Results are the same bits on every call.  An infinity or   */
 /* NaN in x gives its token what the definition says; in lora_grad every entry */
 /* that one takes part in is infinite or NaN.  A and B are finite.              */
 /* ------------------------------------------------------------------------ */

@@ -323,3 +323,26 @@ def test_grad_without_tokens_or_workspace():
     S.lora_grad(None, None, A, B, p.order, p.offsets, p.tiles, x, dy, dA, dB, None)
     assert (dA == 0).all() and (dB == 0).all()
     assert S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, dy, None) is dy
+
+
+@pytest.mark.parametrize("low", [-60, -104, -118, -124])
+def test_rank_vectors_near_the_smallest_numbers(low):
+    """bf16: entries of A x of 2^low come back through unit rows of B, and through the
+    gradients, to 24 bits or to multiples of bf16's smallest number, 2^-133."""
+    T, r = 40, 8
+    rng = np.random.default_rng(-low)
+    mant = lambda *sh: torch.from_numpy(1 + rng.integers(0, 51, sh) / 128).cuda()  # noqa: E731
+    A, x = mant(1, r, 2) * 2.0 ** (low // 2), mant(T, 2) * 2.0 ** (low - low // 2)
+    x[:, 1] *= 2.0 ** -8
+    A, x, B = A.bfloat16(), x.bfloat16(), torch.eye(r, device="cuda")[None].bfloat16()
+    h = R.f64(x) @ R.f64(A)[0].t()
+    p = _plan(np.zeros(T), 1)
+    y = torch.full((T, r), NAN, device="cuda")
+    S.lora_apply(None, None, A, B, p.order, p.offsets, p.tiles, x, None, y,
+                 torch.empty(S.lora_workspace_size(T, r), dtype=torch.uint8, device="cuda"))
+    # the products' own last bits in fp32, and the operand's
+    R.check(y, h, h.abs() * 2.0 ** -24 + 2.0 ** -149 + 2.0 ** -134, "apply")
+    dy = torch.zeros(T, r, device="cuda").bfloat16()
+    dy[3, 2] = 1.0
+    dA, dB = _grad(A, B, x, dy)
+    R.check(dB[0, :, 2], h[3], h[3].abs() * 2.0 ** -24 + 2.0 ** -149 + 2.0 ** -134, "dB")
