@@ -160,10 +160,10 @@ __device__ __forceinline__ int scale_exponent(float m) {
 constexpr int LR_SPREAD = 15;
 
 // Operands of the weight gradients: h as three bf16 terms, 24 bits (down to bf16's
-// smallest number, 2^-133) whatever its neighbours hold (the tokens are the contraction there,
-// so a scale would have to be shared by tokens and tiles, and fp16 terms lose
-// what is small beside a neighbour), transposed to [term][rank][n_tok + LR_PAD]
-// so that 8 tokens of a rank are one load.
+// smallest number, 2^-133) whatever its neighbours hold.  (The tokens are the
+// contraction there, so a scale would have to be shared by tokens and tiles, and
+// scaled fp16 terms lose what is small beside a neighbour.)  Transposed to
+// [term][rank][n_tok + LR_PAD], so that 8 tokens of a rank are one load.
 constexpr int LR_PAD = 8;
 constexpr int LR_GRAD_TERMS = 3;
 template <int R>
