@@ -123,10 +123,10 @@ def test_grad_of_exact_rank_vectors(dt):
 # ---------------------------------------------------------------------------
 # The adapters' product
 # ---------------------------------------------------------------------------
-def _check_apply(A, B, x, y_in, ydt, bits, what=""):
+def _check_apply(A, B, x, y_in, ydt, what=""):
     """y = y_in + B^T (A x).  h = A x: chains of at most K / 32 + 32 additions and
-    40 partial sums; as an operand 2^-(bits + 1) of each entry's own size; then at
-    most three terms of r products, and 24 more sums and products."""
+    40 partial sums; as an operand all 24 bits (2^-25 of each entry's own size); then
+    at most three terms of r products, and 24 more sums and products."""
     n, r, K = A.shape
     T, N = x.shape[0], B.shape[2]
     keys = (np.arange(T) + 1) % (n + 1) - 1
@@ -142,7 +142,7 @@ def _check_apply(A, B, x, y_in, ydt, bits, what=""):
     for a in range(n):
         at = torch.from_numpy(np.flatnonzero(keys == a))
         h = x[at] @ A[a].t()
-        dh = (x[at].abs() @ A[a].abs().t()) * ((K / 32 + 72) * R.ADD) + h.abs() * 2.0 ** -(bits + 1)
+        dh = (x[at].abs() @ A[a].abs().t()) * ((K / 32 + 72) * R.ADD) + h.abs() * 2.0 ** -25
         mag = (h.abs() + dh) @ B[a].abs()
         ref[at] += h @ B[a]
         bound[at] = dh @ B[a].abs() + mag * ((3 * r + 24) * R.ADD) + ref[at].abs() * 2 * R.ADD
@@ -172,7 +172,7 @@ def test_apply_with_ranks_of_different_size(T, K, N, r, dt, y):
     step = torch.tensor([8.0 ** (j % 8) for j in range(r)], device="cuda")[None, :, None]
     ydt = F[dt] if y == "x" else torch.float32
     A, B = (randn(2, r, K) / step).to(F[dt]), (randn(2, r, N) * step / 1024).to(F[dt])
-    _check_apply(A, B, randn(T, K).to(F[dt]), randn(T, N), ydt, 22 if dt == "f16" else 24 if y == "f32" else 16)
+    _check_apply(A, B, randn(T, K).to(F[dt]), randn(T, N), ydt)
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -182,11 +182,10 @@ def test_apply_with_entries_far_apart(T, K, N, r, dt):
     """Rank vectors with entries up to 2^60 apart."""
     A, B, x = _spread(T, K, N, r, -13, 14, seed=T + r)
     up = torch.exp2(torch.round(torch.linspace(-12, 14, r, device="cuda")))[None, :, None]
-    bits = 22 if dt == "f16" else 24
-    _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), None, torch.float32, bits, "far")
-    _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), torch.float32, bits, "far, added")
+    _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), None, torch.float32, "far")
+    _check_apply((A * up).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), torch.float32, "far, added")
     A, B, x = _spread(T, K, N, r, -3, 14, seed=T + r)
-    _check_apply((A / 256).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), F[dt], bits if dt == "f16" else 16, "rounded")
+    _check_apply((A / 256).to(F[dt]), B.to(F[dt]), x.to(F[dt]), _randn(2)(T, N), F[dt], "rounded")
 
 
 @pytest.mark.parametrize("y", ["x", "f32"])
