@@ -766,6 +766,99 @@ spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adap
                       size_t workspace_bytes, void *stream);
 
 /* ======================================================================== */
+/* Dense weights of 4 bits, for one token or many: the product, and a whole     */
+/* layer of gated experts for the few tokens of a decoding step.               */
+/* Layout of a weight [n_rows, n_cols]: a row is ceil(n_cols / 128) blocks of    */
+/* 128 columns (the last one filled up with any codes), 16 words each; word      */
+/* 4 j + m of a block (j, m = 0 .. 3) holds the block's columns 32 m + 8 j + e,   */
+/* e = 0 .. 7, column e in bits 4 i .. 4 i + 3 with i = e / 2 + 4 (e % 2).       */
+/* group (32, 64 or 128) columns share a scale (fp16 or bf16) and, where zeros   */
+/* is not NULL, a zero point (uint8, its low four bits); both are arrays         */
+/* [n_rows, ceil(n_cols / 128) * 128 / group].  The weight is                    */
+/*   W[i, j] = scale * (code - zero), zero = 8 where zeros is NULL.              */
+/* ======================================================================== */
+
+/* Codes, scales and (unless zeros is NULL) zero points of w [n_rows, n_cols] of
+ * type w_dtype, with scales of type dtype (SPMV_F16 or SPMV_BF16).  Symmetric
+ * (zeros NULL): scale = max |w| / 7 of the group, code = w / scale + 8.  With zero
+ * points: scale = max(w, 0) / 15 - min(w, 0) / 15, zero = -min(w, 0) / scale,
+ * code = w / scale + zero.  fp32 throughout: the scale is rounded to its type (at
+ * most its largest number) before it divides, quotients are rounded to nearest with
+ * ties to even, codes and zero points kept in 0 .. 15; where the scale is 0 the
+ * codes are the zero point (8; 0 with zero points).  w is finite.  All pointers
+ * device.  Asynchronous. */
+spmv_status q4_quantize(int32_t n_rows, int32_t n_cols, int32_t group, const void *w, int32_t w_dtype,
+                        int64_t ldw, int32_t dtype, uint32_t *codes, void *scales, uint8_t *zeros,
+                        void *stream);
+
+/* Bytes of the workspace of q4_matmul for up to n_tok tokens (it serves fewer as
+ * well; 0 where none is needed).  Host only. */
+spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes);
+
+/* y[t, i] = alpha * sum_j W[i, j] x[t, j] + beta * y[t, i] for x [n_tok, n_cols] of
+ * type dtype (the scales' type) and y [n_tok, n_rows] of the same type or fp32,
+ * rounded once.  A group's products with code - zero are exact and summed in fp32,
+ * and so are the groups' sums times their scales.  Row strides ldx, ldy in elements.
+ * codes: 16-byte aligned; workspace: 16-byte aligned, not shared by calls that may
+ * overlap.  x and y must not overlap.  The same bits on every call; an infinity or
+ * NaN reaches its own token's row only.  All pointers device.  Asynchronous. */
+spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, const uint32_t *codes,
+                      const void *scales, const uint8_t *zeros, int32_t dtype, int32_t n_tok,
+                      float alpha, const void *x, int64_t ldx, float beta, void *y, int32_t y_dtype,
+                      int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of the workspace of moe_apply.  Host only.  At most 256 tokens and 4096
+ * choices n_tok * top_k (SPMV_ERR_UNSUPPORTED). */
+spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t inter, size_t *bytes);
+
+/* A layer of gated experts for a few tokens, in two launches:
+ *   y[t] = sum_c weights[t, c] * Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])), e = keys[t, c]
+ * with silu(v) = v / (1 + exp(-v)).  Weights in the layout above, the experts
+ * stacked: up_* of [n_experts * 2 * inter, dim], an expert's inter gate rows before
+ * its inter up rows, and down_* of [n_experts * dim, inter]; one group size, and
+ * zero points in both or in neither.  keys int32 [n_tok * top_k]: a choice
+ * outside [0, n_experts) is dropped; an expert chosen twice by a token counts with
+ * both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A token without an
+ * expert gets zeros.  x [n_tok, dim] of type dtype (the scales' type), y [n_tok, dim]
+ * of the same type or fp32, rounded once; the products between are kept with fp32's
+ * 24 bits.  Only the weights of chosen experts are read.  At most 1024 experts
+ * (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
+ * overlap; x and y must not overlap.  The same bits on every call.  All pointers
+ * device.  Asynchronous. */
+spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,
+                      int32_t group, const int32_t *keys, const float *weights,
+                      const uint32_t *up_codes, const void *up_scales, const uint8_t *up_zeros,
+                      const uint32_t *down_codes, const void *down_scales, const uint8_t *down_zeros,
+                      int32_t dtype, const void *x, int64_t ldx, void *y, int32_t y_dtype, int64_t ldy,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* ======================================================================== */
+/* Rows of a table by token id, and the table's gradient: the products of the   */
+/* 0/1 matrix of the ids with the table, and of its transpose with dy.          */
+/* ======================================================================== */
+
+/* y[t] = scale * table[ids[t]], zeros for an id outside [0, n_vocab).  table
+ * [n_vocab, dim] of type dtype, y [n_tok, dim] of the same type or fp32 (the product
+ * in fp32, rounded once); ids int32.  All pointers device.  Asynchronous. */
+spmv_status embed_lookup(int32_t n_tok, int32_t n_vocab, int32_t dim, int32_t dtype, const int32_t *ids,
+                         const void *table, int64_t ldt, float scale, void *y, int32_t y_dtype,
+                         int64_t ldy, void *stream);
+
+/* Bytes of the workspace of embed_grad.  Host only.  At most 2^22 tokens
+ * (SPMV_ERR_UNSUPPORTED). */
+spmv_status embed_grad_workspace_size(int32_t n_tok, int32_t n_vocab, int32_t dim, size_t *bytes);
+
+/* dtable[v] = scale * (sum of dy[t] over the tokens t with ids[t] = v), fp32, every row
+ * written; with accumulate != 0 added to dtable instead, and only rows with a token
+ * are touched.  dy [n_tok, dim] of type dtype, of which rows with an id outside
+ * [0, n_vocab) are not read; dtable [n_vocab, dim].  fp32 sums in an order fixed by
+ * the ids, so the same bits on every call.  workspace: 16-byte aligned, not shared
+ * by calls that may overlap.  All pointers device.  Asynchronous. */
+spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, int32_t dtype, const int32_t *ids,
+                       const void *dy, int64_t lddy, float scale, int32_t accumulate, float *dtable,
+                       int64_t lddt, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ======================================================================== */
 /* Reference streams: the measured bandwidth a plain kernel reaches, beside  */
 /* the HBM peak, as the second denominator of the roofline figures.          */
 /* ======================================================================== */

@@ -10,7 +10,7 @@ the library's message.
 
 ``CSRMatrix`` is a small convenience wrapper that owns the plan workspace and
 the handle of ``spmv_csr_create``; ``MackoMatrix`` and ``RoutePlan`` own the plans of
-the many-token operators.  Those check shapes, strides and devices here, since
+the many-token operators, ``Q4Matrix`` holds a weight of 4 bits.  Those check shapes, strides and devices here, since
 their tensors carry what the C interface takes as sizes.
 """
 from __future__ import annotations
@@ -39,9 +39,12 @@ __all__ = [
     "F16", "BF16", "F32", "macko_spmm_plan_size", "macko_spmm_plan", "macko_spmm_workspace_size", "macko_spmm",
     "macko_spmm_i8", "MackoMatrix", "route_tile_count", "route_workspace_size", "route_plan", "route_gather",
     "route_combine", "route_combine_grad", "RoutePlan", "lora_workspace_size", "lora_apply", "lora_grad",
+    "q4_quantize", "q4_workspace_size", "q4_matmul", "Q4Matrix", "moe_workspace_size", "moe_apply",
+    "embed_lookup", "embed_grad_workspace_size", "embed_grad",
 ]
 
-_TOKENS = frozenset(__all__[__all__.index("macko_spmm_plan_size"):])
+_TOKENS = frozenset(__all__[__all__.index("macko_spmm_plan_size"):__all__.index("q4_quantize")])
+_QUANT = frozenset(__all__[__all__.index("q4_quantize"):])
 
 STATUS = {0: "SPMV_OK", 1: "SPMV_ERR_INVALID_VALUE", 2: "SPMV_ERR_INVALID_MATRIX",
           3: "SPMV_ERR_UNSORTED", 4: "SPMV_ERR_OVERFLOW", 5: "SPMV_ERR_UNSUPPORTED", 6: "SPMV_ERR_HIP"}
@@ -802,10 +805,14 @@ def fem_assemble_csr(n_elem, n_dof, edof, rho, penalty, Ke, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# Operators of many tokens (tokens.py, which imports torch: loaded on first use)
+# Operators of many tokens (tokens.py), 4-bit weights and embeddings (quant.py):
+# both import torch and are loaded on first use
 # ---------------------------------------------------------------------------
 def __getattr__(name):
     if name in _TOKENS:
         from . import tokens
         return getattr(tokens, name)
+    if name in _QUANT:
+        from . import quant
+        return getattr(quant, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,277 @@
+// Products with 4-bit weights on gfx950: y[t, :] = alpha * W x[t, :] + beta * y[t, :].
+//
+// Up to 16 tokens (k_q4_few) a wave owns 16 or 32 rows and every waves-th piece
+// of the columns, and a workgroup's waves add their sums through LDS: the codes
+// are read once and straight to registers, and the bound is HBM.  The
+// matrix cores serve one token as well as 16: the product of a fragment costs
+// the same, and decoding is what the vector unit does.
+#include "q4.hpp"
+
+#include <algorithm>
+
+namespace spmv {
+namespace {
+
+constexpr int QF_UNROLL = 4;         // blocks of a piece: 512 columns
+constexpr int QF_MAX_WAVES = 16;
+constexpr int QF_TOKENS = 16;
+
+template <class E>
+__device__ __forceinline__ void q4_store(void *y, bool f32, int64_t at, float v, float beta) {
+    if (f32) {
+        float *p = static_cast<float *>(y) + at;
+        *p = beta != 0.0f ? fmaf(beta, *p, v) : v;
+    } else {
+        typename E::T *p = static_cast<typename E::T *>(y) + at;
+        *p = (typename E::T)(beta != 0.0f ? fmaf(beta, (float)*p, v) : v);
+    }
+}
+
+// The products of U blocks with one token tile, for RT row tiles.
+template <class E, bool ZP, int G, int U, int RT>
+__device__ __forceinline__ void q4_products(const Q4Piece<E, ZP, G, U> (&w)[RT], const u32x4 (&x)[U][4], f32x4 (&acc)[RT]) {
+    constexpr int GB = Q4_BLOCK / G, PG = G / 32;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int g = 0; g < GB; ++g) {
+                const typename Q4Op<E>::Zero nz = Q4Op<E>::zero(w[r].zero(u, g));
+                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int m = g * PG; m < (g + 1) * PG; ++m)
+                    sum = Q4Op<E>::mfma(x[u][m], Q4Op<E>::decode(w[r].c[u][m], nz), sum);
+                const float s = w[r].scale(u, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(s, sum[i], acc[r][i]);
+            }
+}
+
+template <class E, bool ZP, int G, int RT>
+__global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_cols, int n_blk,
+                                                              const u32x4 *__restrict__ codes,
+                                                              const typename E::T *__restrict__ scales,
+                                                              const unsigned char *__restrict__ zeros, int n_tok,
+                                                              float alpha, const typename E::T *__restrict__ x,
+                                                              int64_t ldx, float beta, void *__restrict__ y, bool f32,
+                                                              int64_t ldy) {
+    constexpr int GB = Q4_BLOCK / G, U = QF_UNROLL;
+    extern __shared__ __attribute__((aligned(16))) f32x4 part[];      // [waves][RT][64]
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    const int quarter = lane / 16;
+    const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
+    const u32x4 *c[RT];
+    const typename E::T *s[RT];
+    const unsigned char *z[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int64_t row = min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1);     // rows past the end: not stored
+        c[r] = codes + row * n_blk * 4 + quarter;
+        s[r] = scales + row * n_blk * GB;
+        z[r] = ZP ? zeros + row * n_blk * GB : nullptr;
+    }
+    // tokens past the end take the last one's row: their sums are not stored
+    const typename E::T *xr = x + (int64_t)min(lane & 15, n_tok - 1) * ldx;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int whole = n_cols / (Q4_BLOCK * U);                  // pieces without an end in them
+    for (int p = wv; p < whole; p += waves) {
+        const int b = p * U;
+        Q4Piece<E, ZP, G, U> w[RT];
+        u32x4 xv[U][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[r].load(c[r] + (int64_t)b * 4, s[r] + (int64_t)b * GB, z[r] + (int64_t)b * GB);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                xv[u][m] = *reinterpret_cast<const u32x4_any *>(xr + (int64_t)(b + u) * Q4_BLOCK + 32 * m + 8 * quarter);
+        q4_products<E, ZP, G, U, RT>(w, xv, acc);
+    }
+    for (int b = whole * U + wv; b < n_blk; b += waves) {
+        Q4Piece<E, ZP, G, 1> w[RT];
+        u32x4 xv[1][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[r].load(c[r] + (int64_t)b * 4, s[r] + (int64_t)b * GB, z[r] + (int64_t)b * GB);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            xv[0][m] = q4_token_piece(xr, (int64_t)b * Q4_BLOCK + 32 * m + 8 * quarter, n_cols);
+        q4_products<E, ZP, G, 1, RT>(w, xv, acc);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) part[(wv * RT + r) * 64 + lane] = acc[r];
+    __syncthreads();
+    const float *sums = reinterpret_cast<const float *>(part);
+    for (int o = threadIdx.x; o < RT * 16 * n_tok; o += blockDim.x) {
+        const int row = o % (16 * RT), t = o / (16 * RT);
+        const int at = ((row / 16) * 64 + (t / 4) * 16 + row % 16) * 4 + t % 4;
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w) v += sums[w * RT * 256 + at];
+        if (row0 + row < n_rows) q4_store<E>(y, f32, t * ldy + row0 + row, alpha * v, beta);
+    }
+}
+
+// y = beta * y where W has no columns.
+template <class E>
+__global__ __launch_bounds__(256) void k_q4_scale(int n_rows, int64_t n, float beta, void *__restrict__ y, bool f32,
+                                                  int64_t ldy) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        q4_store<E>(y, f32, i / n_rows * ldy + i % n_rows, 0.0f, beta);
+}
+
+// Codes of a dense weight, one thread per group.  Symmetric: s = max |w| / 7,
+// q = w / s rounded to even + 8.  With zero points: s = (max(w, 0) - min(w, 0)) / 15,
+// z = -min(w, 0) / s and q = w / s + z, each rounded to even and kept in 0 .. 15.
+// s is rounded to its type (at most its largest number) before it divides.
+template <class S, class W>
+__global__ __launch_bounds__(256) void k_q4_quantize(int64_t n_groups, int n_cols, int gpr, int group,
+                                                     const typename W::T *__restrict__ w, int64_t ldw,
+                                                     unsigned *__restrict__ codes, typename S::T *__restrict__ scales,
+                                                     unsigned char *__restrict__ zeros) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= n_groups) return;
+    const int64_t row = id / gpr;
+    const int64_t c0 = (id - row * gpr) * group, c1 = min(c0 + group, (int64_t)n_cols);
+    const typename W::T *src = w + row * ldw;
+    float lo = 0.0f, hi = 0.0f;
+    for (int64_t c = c0; c < c1; ++c) {
+        const float v = (float)src[c];
+        lo = fminf(lo, v);
+        hi = fmaxf(hi, v);
+    }
+    const float largest = std::is_same<S, F16>::value ? 65504.0f : 3.3895314e38f;
+    // the difference of two large numbers may pass fp32's range; a fifteenth of each does not
+    const float want = zeros ? hi / 15.0f - lo / 15.0f : fmaxf(hi, -lo) / 7.0f;
+    const typename S::T st = (typename S::T)fminf(want, largest);
+    const float s = (float)st;
+    const float z = zeros ? (s > 0.0f ? fminf(rintf(-lo / s), 15.0f) : 0.0f) : 8.0f;
+    scales[id] = st;
+    if (zeros) zeros[id] = (unsigned char)z;
+    unsigned *dst = codes + (row * (gpr * (int64_t)group / Q4_BLOCK)) * Q4_WORDS;
+    for (int i = 0; i < group / 8; ++i) {
+        const int64_t c = c0 + 8 * i;
+        unsigned word = 0;
+        for (int e = 0; e < 8; ++e) {
+            const float v = c + e < n_cols ? (float)src[c + e] : 0.0f;
+            const float q = s > 0.0f ? fminf(fmaxf(rintf(v / s) + z, 0.0f), 15.0f) : z;
+            word |= (unsigned)q << (4 * q4_place(e));
+        }
+        const int in = (int)(c % Q4_BLOCK);
+        dst[c / Q4_BLOCK * Q4_WORDS + 4 * (in % 32 / 8) + in / 32] = word;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+spmv_status check_weight(int32_t n_rows, int32_t n_cols, int32_t group, int32_t dtype) {
+    if (n_rows < 0 || n_cols < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
+    if (!q4_group_ok(group)) return fail(SPMV_ERR_INVALID_VALUE, "group must be 32, 64 or 128, not %d", group);
+    if (!dtype_ok(dtype)) return fail(SPMV_ERR_INVALID_VALUE, "element type %d is not a spmv_dtype", dtype);
+    if (dtype == SPMV_F32) return fail(SPMV_ERR_UNSUPPORTED, "scales and x are fp16 or bf16");
+    return SPMV_OK;
+}
+
+template <class F>
+spmv_status by_weight(int32_t dtype, bool zp, int32_t group, F f) {
+    auto g = [&](auto e, auto z) {
+        if (group == 32) return f(e, z, std::integral_constant<int, 32>{});
+        if (group == 64) return f(e, z, std::integral_constant<int, 64>{});
+        return f(e, z, std::integral_constant<int, 128>{});
+    };
+    if (dtype == SPMV_F16) return zp ? g(F16{}, std::true_type{}) : g(F16{}, std::false_type{});
+    return zp ? g(BF16{}, std::true_type{}) : g(BF16{}, std::false_type{});
+}
+
+}  // namespace
+}  // namespace spmv
+
+using namespace spmv;
+
+extern "C" spmv_status q4_quantize(int32_t n_rows, int32_t n_cols, int32_t group, const void *w, int32_t w_dtype,
+                                   int64_t ldw, int32_t dtype, uint32_t *codes, void *scales, uint8_t *zeros,
+                                   void *stream) {
+    spmv_status st = check_weight(n_rows, n_cols, group, dtype);
+    if (st != SPMV_OK) return st;
+    if (!dtype_ok(w_dtype)) return fail(SPMV_ERR_INVALID_VALUE, "element type %d is not a spmv_dtype", w_dtype);
+    if (ldw < n_cols) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
+    if (n_rows == 0 || n_cols == 0) return SPMV_OK;
+    if (!w || !codes || !scales) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
+    const int64_t gpr = q4_blocks(n_cols) * (Q4_BLOCK / group), n = gpr * n_rows;
+    st = check_grid(ceil_div(n, 256));
+    if (st != SPMV_OK) return st;
+    auto run = [&](auto s, auto e) {
+        typedef decltype(s) S;
+        typedef decltype(e) W;
+        k_q4_quantize<S, W><<<(int)ceil_div(n, 256), 256, 0, as_stream(stream)>>>(
+            n, n_cols, (int)gpr, group, static_cast<const typename W::T *>(w), ldw, codes,
+            static_cast<typename S::T *>(scales), zeros);
+    };
+    auto by_w = [&](auto s) {
+        if (w_dtype == SPMV_F16)
+            run(s, F16{});
+        else if (w_dtype == SPMV_BF16)
+            run(s, BF16{});
+        else
+            run(s, F32{});
+    };
+    if (dtype == SPMV_F16)
+        by_w(F16{});
+    else
+        by_w(BF16{});
+    SPMV_LAUNCHED("k_q4_quantize");
+    return SPMV_OK;
+}
+
+extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes) {
+    if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
+    if (n_rows < 0 || n_cols < 0 || n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
+    *bytes = 0;
+    return SPMV_OK;
+}
+
+extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, const uint32_t *codes,
+                                 const void *scales, const uint8_t *zeros, int32_t dtype, int32_t n_tok, float alpha,
+                                 const void *x, int64_t ldx, float beta, void *y, int32_t y_dtype, int64_t ldy,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    spmv_status st = check_weight(n_rows, n_cols, group, dtype);
+    if (st != SPMV_OK) return st;
+    if (n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
+    if (!dtype_ok(y_dtype)) return fail(SPMV_ERR_INVALID_VALUE, "element type %d is not a spmv_dtype", y_dtype);
+    if (y_dtype != SPMV_F32 && y_dtype != dtype) return fail(SPMV_ERR_UNSUPPORTED, "y must be fp32 or have x's type");
+    if (ldx < n_cols || ldy < n_rows) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
+    if (n_rows == 0 || n_tok == 0) return SPMV_OK;
+    if (!y || (n_cols > 0 && (!codes || !scales || !x))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
+    if (!aligned16(codes)) return fail(SPMV_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
+    hipStream_t s = as_stream(stream);
+    const bool f32 = y_dtype == SPMV_F32;
+    const size_t ysize = dtype_size(y_dtype);
+    if (n_cols == 0) {
+        const int64_t n = (int64_t)n_rows * n_tok;
+        const int grid = (int)std::min<int64_t>(ceil_div(n, 256), 65536);
+        if (dtype == SPMV_F16)
+            k_q4_scale<F16><<<grid, 256, 0, s>>>(n_rows, n, beta, y, f32, ldy);
+        else
+            k_q4_scale<BF16><<<grid, 256, 0, s>>>(n_rows, n, beta, y, f32, ldy);
+        SPMV_LAUNCHED("k_q4_scale");
+        return SPMV_OK;
+    }
+    const int n_blk = (int)q4_blocks(n_cols);
+    return by_weight(dtype, zeros != nullptr, group, [&](auto e, auto zp, auto g) -> spmv_status {
+        typedef decltype(e) E;
+        typedef typename E::T T;
+        constexpr bool ZP = decltype(zp)::value;
+        constexpr int G = decltype(g)::value, RT = 2;
+        const int waves = (int)std::min<int64_t>(8, ceil_div(n_blk, QF_UNROLL));
+        for (int32_t t = 0; t < n_tok; t += QF_TOKENS) {
+            const int n = std::min(QF_TOKENS, n_tok - t);
+            k_q4_few<E, ZP, G, RT><<<(int)ceil_div(n_rows, 16 * RT), 64 * waves, (size_t)waves * RT * 1024, s>>>(
+                n_rows, n_cols, n_blk, reinterpret_cast<const u32x4 *>(codes), static_cast<const T *>(scales), zeros, n,
+                alpha, static_cast<const T *>(x) + t * ldx, ldx, beta, static_cast<char *>(y) + t * ldy * ysize, f32, ldy);
+            SPMV_LAUNCHED("k_q4_few");
+        }
+        return SPMV_OK;
+    });
+}

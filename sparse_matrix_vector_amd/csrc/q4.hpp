@@ -1,0 +1,145 @@
+// Weights of 4 bits with group scales on gfx950: the layout, the decoding into
+// matrix-core operands, and a wave's pass over a piece of 16 rows.
+//
+// A row is cut into blocks of 128 columns (64 bytes of codes).  Word 4 j + m of
+// a block holds columns 32 m + 8 j .. + 7, so that the 16 bytes that lane
+// quarter j loads are its operands of the block's four 16x16x32 products: the
+// product m covers the columns 32 m .. 32 m + 31 whole, and a group of 32, 64
+// or 128 columns is one, two or four products.  The weight's fragment is the
+// second operand (D's columns are rows of W), the tokens' the first: a lane
+// then decodes the row whose scale it multiplies with.
+//
+// Codes become exact 16-bit numbers q - z (fp16: (q - z) 2^-9; a code masked out
+// of a word is the fp16 subnormal q 2^-24 or 16 q 2^-24, and one fused
+// multiply-add brings it to q - z).  The products of a group are summed in fp32
+// and multiplied with the group's scale in fp32: no weight is rounded.
+#pragma once
+
+#include "elem.hpp"
+
+#include <type_traits>
+
+namespace spmv {
+
+typedef _Float16 q4_h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 q4_h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 q4_b2 __attribute__((ext_vector_type(2)));
+typedef __bf16 q4_b8 __attribute__((ext_vector_type(8)));
+
+constexpr int Q4_BLOCK = 128;      // columns of a block
+constexpr int Q4_WORDS = 16;       // its words
+constexpr int Q4_ROWS = 16;        // rows of a matrix-core operand
+
+inline bool q4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
+inline int64_t q4_blocks(int64_t n_cols) { return ceil_div(n_cols, Q4_BLOCK); }
+
+// nibble of column e of a word's eight
+__host__ __device__ constexpr int q4_place(int e) { return (e >> 1) + 4 * (e & 1); }
+
+template <class E>
+struct Q4Op;
+
+template <>
+struct Q4Op<F16> {
+    typedef q4_h2 Zero;
+    static constexpr float UNIT = 512.0f;      // what the group's sum is short of
+    static __device__ __forceinline__ Zero zero(int z) {
+        // z as the fp16 subnormal z 2^-24, times -2^15
+        const q4_h2 s = __builtin_bit_cast(q4_h2, (unsigned)z * 0x00010001u);
+        return s * q4_h2{(_Float16)-32768.0f, (_Float16)-32768.0f};
+    }
+    static __device__ __forceinline__ u32x4 decode(unsigned w, Zero nz) {
+        const q4_h2 k0 = {(_Float16)32768.0f, (_Float16)32768.0f}, k1 = {(_Float16)2048.0f, (_Float16)2048.0f};
+        const unsigned v = w >> 8;
+        u32x4 o;
+        o[0] = __builtin_bit_cast(unsigned, __builtin_elementwise_fma(__builtin_bit_cast(q4_h2, w & 0x000F000Fu), k0, nz));
+        o[1] = __builtin_bit_cast(unsigned, __builtin_elementwise_fma(__builtin_bit_cast(q4_h2, w & 0x00F000F0u), k1, nz));
+        o[2] = __builtin_bit_cast(unsigned, __builtin_elementwise_fma(__builtin_bit_cast(q4_h2, v & 0x000F000Fu), k0, nz));
+        o[3] = __builtin_bit_cast(unsigned, __builtin_elementwise_fma(__builtin_bit_cast(q4_h2, v & 0x00F000F0u), k1, nz));
+        return o;
+    }
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(q4_h8, a), __builtin_bit_cast(q4_h8, b), c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Q4Op<BF16> {
+    typedef float Zero;
+    static constexpr float UNIT = 1.0f;
+    static __device__ __forceinline__ Zero zero(int z) { return -(float)z; }
+    static __device__ __forceinline__ unsigned pair(unsigned bits, float k, Zero nz) {
+        const q4_h2 h = __builtin_bit_cast(q4_h2, bits);
+        q4_b2 r;
+        r[0] = (__bf16)__builtin_fmaf((float)h[0], k, nz);
+        r[1] = (__bf16)__builtin_fmaf((float)h[1], k, nz);
+        return __builtin_bit_cast(unsigned, r);
+    }
+    static __device__ __forceinline__ u32x4 decode(unsigned w, Zero nz) {
+        const unsigned v = w >> 8;
+        u32x4 o;
+        o[0] = pair(w & 0x000F000Fu, 16777216.0f, nz);
+        o[1] = pair(w & 0x00F000F0u, 1048576.0f, nz);
+        o[2] = pair(v & 0x000F000Fu, 16777216.0f, nz);
+        o[3] = pair(v & 0x00F000F0u, 1048576.0f, nz);
+        return o;
+    }
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(q4_b8, a), __builtin_bit_cast(q4_b8, b), c, 0, 0, 0);
+    }
+};
+
+// N bytes at any address.
+template <int N>
+struct Bytes {
+    unsigned char b[N];
+};
+template <int N>
+__device__ __forceinline__ Bytes<N> load_bytes(const void *p) {
+    Bytes<N> r;
+    __builtin_memcpy(&r, p, N);
+    return r;
+}
+
+// U blocks of one row as a lane holds them: its quarter's codes, and the scales
+// and zero points of all their groups.
+template <class E, bool ZP, int G, int U>
+struct Q4Piece {
+    static constexpr int GB = Q4_BLOCK / G;        // groups of a block
+    typedef typename E::T T;
+    u32x4 c[U];
+    Vec<E, U * GB> s;
+    Bytes<ZP ? U * GB : 1> z;
+
+    // codes: the row's blocks from this one on, quarter's 16 bytes; scales, zeros: of its groups
+    __device__ __forceinline__ void load(const u32x4 *codes, const T *scales, const unsigned char *zeros) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) c[u] = __builtin_nontemporal_load(codes + 4 * u);
+        __builtin_memcpy(&s, __builtin_assume_aligned(scales, 2), sizeof s);
+        if constexpr (ZP) z = load_bytes<U * GB>(zeros);
+    }
+    __device__ __forceinline__ float scale(int u, int g) const { return (float)s.v[u * GB + g]; }
+    __device__ __forceinline__ int zero(int u, int g) const {
+        if constexpr (ZP)
+            return z.b[u * GB + g] & 15;
+        else
+            return 8;
+    }
+};
+
+// 8 consecutive elements of a token's row from column c on, zeros past n_cols.
+template <class T>
+__device__ __forceinline__ u32x4 q4_token_piece(const T *row, int64_t c, int64_t n_cols) {
+    if (c + 8 <= n_cols) return *reinterpret_cast<const u32x4_any *>(row + c);
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < n_cols) {
+            unsigned short h;
+            __builtin_memcpy(&h, row + c + i, 2);
+            v[i / 2] |= (unsigned)h << (16 * (i & 1));
+        }
+    return v;
+}
+
+}  // namespace spmv
