@@ -113,6 +113,140 @@ __global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_
     }
 }
 
+// More tokens: a workgroup's four waves own 16 RT rows each and share a tile of
+// 16 TT tokens, a block of 128 columns at a time, through LDS (16-byte pieces
+// exchanged within a row by the token's number, so that 16 tokens' pieces lie in
+// different banks).  Every fragment of W is decoded once and used TT times; its
+// codes go straight to registers, a block ahead.  With few tiles the columns are
+// split over workgroups, whose sums k_q4_join adds.
+template <class E, bool ZP, int G, int RT, int TT>
+__global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int n_blk, int row_tiles, int tok_tiles,
+                                                    int split, const u32x4 *__restrict__ codes,
+                                                    const typename E::T *__restrict__ scales,
+                                                    const unsigned char *__restrict__ zeros, int n_tok, float alpha,
+                                                    const typename E::T *__restrict__ x, int64_t ldx, float beta,
+                                                    void *__restrict__ y, bool f32, int64_t ldy,
+                                                    float *__restrict__ parts) {
+    constexpr int GB = Q4_BLOCK / G, PG = G / 32, TN = 16 * TT;
+    __shared__ u32x4 xt[2][TN * 16];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
+    // neighbouring workgroups run on different XCDs; every 8th one shares a row tile, whose codes one L2 then holds
+    const int id = blockIdx.x, group = id / (8 * tok_tiles), in = id % (8 * tok_tiles);
+    const int wide = min(8, row_tiles - group * 8);
+    const int row_tile = group * 8 + in % wide, tok_tile = in / wide;
+    const int64_t row0 = ((int64_t)row_tile * 4 + wv) * (16 * RT);
+    const int t0 = tok_tile * TN;
+    const int b0 = (int)((int64_t)n_blk * blockIdx.y / split), b1 = (int)((int64_t)n_blk * (blockIdx.y + 1) / split);
+    const u32x4 *c[RT];
+    const typename E::T *s[RT];
+    const unsigned char *z[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int64_t row = min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1);
+        c[r] = codes + row * n_blk * 4 + quarter;
+        s[r] = scales + row * n_blk * GB;
+        z[r] = ZP ? zeros + row * n_blk * GB : nullptr;
+    }
+    const typename E::T *xr[TT];
+    int slot[TT];
+#pragma unroll
+    for (int q = 0; q < TT; ++q) {
+        const int t = (threadIdx.x + 256 * q) / 16, piece = threadIdx.x % 16;
+        xr[q] = x + (int64_t)min(t0 + t, n_tok - 1) * ldx + piece * 8;
+        slot[q] = t * 16 + (piece ^ (t & 15));
+    }
+    auto load_x = [&](int b, u32x4 (&v)[TT]) {
+        const int64_t at = (int64_t)b * Q4_BLOCK;
+        if (at + Q4_BLOCK <= n_cols) {
+#pragma unroll
+            for (int q = 0; q < TT; ++q) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at);
+        } else {
+            const int piece = (threadIdx.x % 16) * 8;
+#pragma unroll
+            for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q] - piece, at + piece, n_cols);
+        }
+    };
+    Q4Piece<E, ZP, G, 1> w[RT];
+    u32x4 v[TT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) w[r].load(c[r] + (int64_t)b0 * 4, s[r] + (int64_t)b0 * GB, z[r] + (int64_t)b0 * GB);
+    load_x(b0, v);
+#pragma unroll
+    for (int q = 0; q < TT; ++q) xt[0][slot[q]] = v[q];
+    f32x4 acc[RT][TT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    for (int b = b0; b < b1; ++b) {
+        const u32x4 *now = xt[(b - b0) & 1];
+        const int next = min(b + 1, b1 - 1);
+        Q4Piece<E, ZP, G, 1> wn[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            wn[r].load(c[r] + (int64_t)next * 4, s[r] + (int64_t)next * GB, z[r] + (int64_t)next * GB);
+        load_x(next, v);
+#pragma unroll
+        for (int g = 0; g < GB; ++g) {
+            f32x4 sum[RT][TT];
+#pragma unroll
+            for (int m = g * PG; m < (g + 1) * PG; ++m) {
+                u32x4 xv[TT];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) xv[t] = now[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const u32x4 f = Q4Op<E>::decode(w[r].c[0][m], Q4Op<E>::zero(w[r].zero(0, g)));
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+                        sum[r][t] = Q4Op<E>::mfma(xv[t], f, m == g * PG ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float sc = w[r].scale(0, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < TT; ++q) xt[(b - b0 + 1) & 1][slot[q]] = v[q];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[r] = wn[r];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int64_t row = row0 + 16 * r + (lane & 15);
+        if (row >= n_rows) continue;
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = t0 + 16 * t + 4 * quarter + i;
+                if (tok >= n_tok) continue;
+                if (split > 1)
+                    parts[((int64_t)blockIdx.y * n_tok + tok) * n_rows + row] = acc[r][t][i];
+                else
+                    q4_store<E>(y, f32, (int64_t)tok * ldy + row, alpha * acc[r][t][i], beta);
+            }
+    }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int split, float alpha, float beta,
+                                                 const float *__restrict__ parts, void *__restrict__ y, bool f32,
+                                                 int64_t ldy) {
+    const int64_t n = (int64_t)n_rows * n_tok, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float v = 0.0f;
+    for (int k = 0; k < split; ++k) v += parts[k * n + i];
+    q4_store<E>(y, f32, i / n_rows * ldy + i % n_rows, alpha * v, beta);
+}
+
 // y = beta * y where W has no columns.
 template <class E>
 __global__ __launch_bounds__(256) void k_q4_scale(int n_rows, int64_t n, float beta, void *__restrict__ y, bool f32,
@@ -185,6 +319,28 @@ spmv_status by_weight(int32_t dtype, bool zp, int32_t group, F f) {
     return zp ? g(BF16{}, std::true_type{}) : g(BF16{}, std::false_type{});
 }
 
+// How a product of more than QF_TOKENS tokens is cut: rows of a wave, tokens of a tile, parts of the columns.
+struct Tiling {
+    int rt, tt, row_tiles, tok_tiles, split;
+};
+constexpr int QT_GROUPS = 512;       // workgroups wanted: two on each CU
+constexpr int QT_MIN_BLOCKS = 4;     // blocks of columns of a part at least
+Tiling tiling(int64_t n_rows, int64_t n_cols, int64_t n_tok) {
+    Tiling t;
+    t.tt = n_tok <= 32 ? 2 : 4;
+    t.rt = n_tok <= 64 ? 2 : 4;
+    t.row_tiles = (int)ceil_div(n_rows, 64 * t.rt);
+    t.tok_tiles = (int)ceil_div(n_tok, 16 * t.tt);
+    const int64_t tiles = (int64_t)t.row_tiles * t.tok_tiles;
+    t.split = (int)std::max<int64_t>(1, std::min(QT_GROUPS / tiles, q4_blocks(n_cols) / QT_MIN_BLOCKS));
+    return t;
+}
+size_t split_bytes(int64_t n_rows, int64_t n_cols, int64_t n_tok) {
+    if (n_tok <= QF_TOKENS || n_rows == 0 || n_cols == 0) return 0;
+    const Tiling t = tiling(n_rows, n_cols, n_tok);
+    return t.split > 1 ? (size_t)t.split * n_tok * n_rows * 4 : 0;
+}
+
 }  // namespace
 }  // namespace spmv
 
@@ -228,7 +384,14 @@ extern "C" spmv_status q4_quantize(int32_t n_rows, int32_t n_cols, int32_t group
 extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes) {
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
     if (n_rows < 0 || n_cols < 0 || n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
-    *bytes = 0;
+    // the most that any batch of up to n_tok tokens needs: full tiles of 32, then of 64 tokens, while there is a split
+    size_t most = split_bytes(n_rows, n_cols, n_tok);
+    for (int64_t t = 32; t < n_tok; t += t < 64 ? 32 : 64) {
+        const size_t b = split_bytes(n_rows, n_cols, t);
+        if (b == 0) break;
+        most = std::max(most, b);
+    }
+    *bytes = most;
     return SPMV_OK;
 }
 
@@ -247,7 +410,6 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
     if (!aligned16(codes)) return fail(SPMV_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
     hipStream_t s = as_stream(stream);
     const bool f32 = y_dtype == SPMV_F32;
-    const size_t ysize = dtype_size(y_dtype);
     if (n_cols == 0) {
         const int64_t n = (int64_t)n_rows * n_tok;
         const int grid = (int)std::min<int64_t>(ceil_div(n, 256), 65536);
@@ -259,19 +421,58 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         return SPMV_OK;
     }
     const int n_blk = (int)q4_blocks(n_cols);
-    return by_weight(dtype, zeros != nullptr, group, [&](auto e, auto zp, auto g) -> spmv_status {
+    if (n_tok <= QF_TOKENS)
+        return by_weight(dtype, zeros != nullptr, group, [&](auto e, auto zp, auto g) -> spmv_status {
+            typedef decltype(e) E;
+            typedef typename E::T T;
+            constexpr bool ZP = decltype(zp)::value;
+            constexpr int G = decltype(g)::value, RT = 2;
+            const int waves = (int)std::min<int64_t>(8, ceil_div(n_blk, QF_UNROLL));
+            k_q4_few<E, ZP, G, RT><<<(int)ceil_div(n_rows, 16 * RT), 64 * waves, (size_t)waves * RT * 1024, s>>>(
+                n_rows, n_cols, n_blk, reinterpret_cast<const u32x4 *>(codes), static_cast<const T *>(scales), zeros,
+                n_tok, alpha, static_cast<const T *>(x), ldx, beta, y, f32, ldy);
+            SPMV_LAUNCHED("k_q4_few");
+            return SPMV_OK;
+        });
+    const Tiling t = tiling(n_rows, n_cols, n_tok);
+    const size_t need = split_bytes(n_rows, n_cols, n_tok);
+    if (need && !workspace) return fail(SPMV_ERR_INVALID_VALUE, "workspace is NULL (q4_workspace_size gives its size)");
+    if (workspace_bytes < need)
+        return fail(SPMV_ERR_INVALID_VALUE, "workspace of %zu bytes is smaller than %zu", workspace_bytes, need);
+    if (!aligned16(workspace)) return fail(SPMV_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+    st = check_grid((int64_t)t.row_tiles * t.tok_tiles);
+    if (st != SPMV_OK) return st;
+    st = by_weight(dtype, zeros != nullptr, group, [&](auto e, auto zp, auto g) -> spmv_status {
         typedef decltype(e) E;
         typedef typename E::T T;
         constexpr bool ZP = decltype(zp)::value;
-        constexpr int G = decltype(g)::value, RT = 2;
-        const int waves = (int)std::min<int64_t>(8, ceil_div(n_blk, QF_UNROLL));
-        for (int32_t t = 0; t < n_tok; t += QF_TOKENS) {
-            const int n = std::min(QF_TOKENS, n_tok - t);
-            k_q4_few<E, ZP, G, RT><<<(int)ceil_div(n_rows, 16 * RT), 64 * waves, (size_t)waves * RT * 1024, s>>>(
-                n_rows, n_cols, n_blk, reinterpret_cast<const u32x4 *>(codes), static_cast<const T *>(scales), zeros, n,
-                alpha, static_cast<const T *>(x) + t * ldx, ldx, beta, static_cast<char *>(y) + t * ldy * ysize, f32, ldy);
-            SPMV_LAUNCHED("k_q4_few");
-        }
+        constexpr int G = decltype(g)::value;
+        auto run = [&](auto rt, auto tt) {
+            k_q4_tile<E, ZP, G, decltype(rt)::value, decltype(tt)::value>
+                <<<dim3((unsigned)(t.row_tiles * t.tok_tiles), (unsigned)t.split), 256, 0, s>>>(
+                    n_rows, n_cols, n_blk, t.row_tiles, t.tok_tiles, t.split, reinterpret_cast<const u32x4 *>(codes),
+                    static_cast<const T *>(scales), zeros, n_tok, alpha, static_cast<const T *>(x), ldx, beta, y, f32,
+                    ldy, static_cast<float *>(workspace));
+        };
+        const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 4> four;
+        if (t.rt == 4)
+            run(four, four);
+        else if (t.tt == 4)
+            run(two, four);
+        else
+            run(two, two);
+        SPMV_LAUNCHED("k_q4_tile");
         return SPMV_OK;
     });
+    if (st != SPMV_OK || t.split == 1) return st;
+    const int grid = (int)ceil_div((int64_t)n_rows * n_tok, 256);
+    if (dtype == SPMV_F16)
+        k_q4_join<F16><<<grid, 256, 0, s>>>(n_rows, n_tok, t.split, alpha, beta, static_cast<const float *>(workspace), y,
+                                            f32, ldy);
+    else
+        k_q4_join<BF16><<<grid, 256, 0, s>>>(n_rows, n_tok, t.split, alpha, beta, static_cast<const float *>(workspace), y,
+                                             f32, ldy);
+    SPMV_LAUNCHED("k_q4_join");
+    return SPMV_OK;
 }
