@@ -791,21 +791,35 @@ spmv_status q4_quantize(int32_t n_rows, int32_t n_cols, int32_t group, const voi
                         int64_t ldw, int32_t dtype, uint32_t *codes, void *scales, uint8_t *zeros,
                         void *stream);
 
+/* The arrangement that the products read: for every 16 rows and block of 128
+ * columns one record of 64 x 16 bytes of codes (quarter j of row r of the tile, words
+ * 4 j .. 4 j + 3 of its block, at 16 (16 j + r)), the 16 rows' scales of the block's
+ * groups and their zero points; the record of tile i and block b is the
+ * (i ceil(n_cols / 128) + b)-th.  Made once per weight; codes, scales and zeros may
+ * be freed afterwards.  Stacked weights are arranged together, n_rows counting the
+ * rows of all.  q4_tiles_size: bytes, host only.  q4_tiles: all pointers device;
+ * codes and tiles 16-byte aligned; scales fp16 or bf16.  Asynchronous. */
+spmv_status q4_tiles_size(int32_t n_rows, int32_t n_cols, int32_t group, int32_t with_zeros, size_t *bytes);
+spmv_status q4_tiles(int32_t n_rows, int32_t n_cols, int32_t group, const uint32_t *codes,
+                     const void *scales, const uint8_t *zeros, void *tiles, size_t tiles_bytes,
+                     void *stream);
+
 /* Bytes of the workspace of q4_matmul for up to n_tok tokens (it serves fewer as
  * well; 0 where none is needed).  Host only. */
 spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes);
 
 /* y[t, i] = alpha * sum_j W[i, j] x[t, j] + beta * y[t, i] for x [n_tok, n_cols] of
  * type dtype (the scales' type) and y [n_tok, n_rows] of the same type or fp32,
- * rounded once.  A group's products with code - zero are exact and summed in fp32,
- * and so are the groups' sums times their scales.  Row strides ldx, ldy in elements.
- * codes: 16-byte aligned; workspace: 16-byte aligned, not shared by calls that may
- * overlap.  x and y must not overlap.  The same bits on every call; an infinity or
- * NaN reaches its own token's row only.  All pointers device.  Asynchronous. */
-spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, const uint32_t *codes,
-                      const void *scales, const uint8_t *zeros, int32_t dtype, int32_t n_tok,
-                      float alpha, const void *x, int64_t ldx, float beta, void *y, int32_t y_dtype,
-                      int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+ * rounded once; tiles as q4_tiles wrote them, with zero points if with_zeros != 0.
+ * A group's products with code - zero are exact and summed in fp32, and so are the
+ * groups' sums times their scales.  Row strides ldx, ldy in elements.  tiles and
+ * workspace: 16-byte aligned; the workspace is not shared by calls that may overlap.
+ * x and y must not overlap.  The same bits on every call; an infinity or NaN
+ * reaches its own token's row only.  All pointers device.  Asynchronous. */
+spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, int32_t with_zeros, const void *tiles,
+                      int32_t dtype, int32_t n_tok, float alpha, const void *x, int64_t ldx, float beta,
+                      void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t workspace_bytes,
+                      void *stream);
 
 /* Bytes of the workspace of moe_apply.  Host only.  At most 256 tokens and 4096
  * choices n_tok * top_k (SPMV_ERR_UNSUPPORTED). */
@@ -813,10 +827,10 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t inter, size
 
 /* A layer of gated experts for a few tokens, in two launches:
  *   y[t] = sum_c weights[t, c] * Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])), e = keys[t, c]
- * with silu(v) = v / (1 + exp(-v)).  Weights in the layout above, the experts
- * stacked: up_* of [n_experts * 2 * inter, dim], an expert's inter gate rows before
- * its inter up rows, and down_* of [n_experts * dim, inter]; one group size, and
- * zero points in both or in neither.  keys int32 [n_tok * top_k]: a choice
+ * with silu(v) = v / (1 + exp(-v)).  Weights as q4_tiles arranges them, the experts
+ * stacked: up_tiles of [n_experts * 2 * inter, dim], an expert's inter gate rows
+ * before its inter up rows, and down_tiles of [n_experts * dim, inter]; one group
+ * size, and zero points in both (with_zeros != 0) or in neither.  keys int32 [n_tok * top_k]: a choice
  * outside [0, n_experts) is dropped; an expert chosen twice by a token counts with
  * both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A token without an
  * expert gets zeros.  x [n_tok, dim] of type dtype (the scales' type), y [n_tok, dim]
@@ -826,11 +840,9 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t inter, size
  * overlap; x and y must not overlap.  The same bits on every call.  All pointers
  * device.  Asynchronous. */
 spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,
-                      int32_t group, const int32_t *keys, const float *weights,
-                      const uint32_t *up_codes, const void *up_scales, const uint8_t *up_zeros,
-                      const uint32_t *down_codes, const void *down_scales, const uint8_t *down_zeros,
-                      int32_t dtype, const void *x, int64_t ldx, void *y, int32_t y_dtype, int64_t ldy,
-                      void *workspace, size_t workspace_bytes, void *stream);
+                      int32_t group, int32_t with_zeros, const int32_t *keys, const float *weights,
+                      const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x,
+                      int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ======================================================================== */
 /* Rows of a table by token id, and the table's gradient: the products of the   */

@@ -39,7 +39,7 @@ __all__ = [
     "F16", "BF16", "F32", "macko_spmm_plan_size", "macko_spmm_plan", "macko_spmm_workspace_size", "macko_spmm",
     "macko_spmm_i8", "MackoMatrix", "route_tile_count", "route_workspace_size", "route_plan", "route_gather",
     "route_combine", "route_combine_grad", "RoutePlan", "lora_workspace_size", "lora_apply", "lora_grad",
-    "q4_quantize", "q4_workspace_size", "q4_matmul", "Q4Matrix", "moe_workspace_size", "moe_apply",
+    "q4_quantize", "q4_tiles_size", "q4_tiles", "q4_workspace_size", "q4_matmul", "Q4Matrix", "moe_workspace_size", "moe_apply",
     "embed_lookup", "embed_grad_workspace_size", "embed_grad",
 ]
 

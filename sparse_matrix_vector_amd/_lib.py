@@ -99,10 +99,12 @@ SIGNATURES = {
                   vp, vp, vp, c_sz, vp],
     "q4_quantize": [c_i32, c_i32, c_i32, vp, c_i32, c_i64, c_i32, vp, vp, vp, vp],
     "q4_workspace_size": [c_i32, c_i32, c_i32, P_sz],
-    "q4_matmul": [c_i32, c_i32, c_i32, vp, vp, vp, c_i32, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32, c_i64, vp, c_sz, vp],
+    "q4_tiles_size": [c_i32, c_i32, c_i32, c_i32, P_sz],
+    "q4_tiles": [c_i32, c_i32, c_i32, vp, vp, vp, vp, c_sz, vp],
+    "q4_matmul": [c_i32, c_i32, c_i32, c_i32, vp, c_i32, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32, c_i64, vp, c_sz, vp],
     "moe_workspace_size": [c_i32, c_i32, c_i32, P_sz],
-    "moe_apply": [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp, vp, vp, vp, c_i32, vp, c_i64, vp, c_i32,
-                  c_i64, vp, c_sz, vp],
+    "moe_apply": [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, c_i32, vp, c_i64, vp, c_i32, c_i64, vp,
+                  c_sz, vp],
     "embed_lookup": [c_i32, c_i32, c_i32, c_i32, vp, vp, c_i64, c_f32, vp, c_i32, c_i64, vp],
     "embed_grad_workspace_size": [c_i32, c_i32, c_i32, P_sz],
     "embed_grad": [c_i32, c_i32, c_i32, c_i32, vp, vp, c_i64, c_f32, c_i32, vp, c_i64, vp, c_sz, vp],

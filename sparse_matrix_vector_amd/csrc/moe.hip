@@ -70,11 +70,9 @@ __device__ __forceinline__ void up_products(const Q4Piece<E, ZP, G, U> (&w)[RT],
 template <class E, bool ZP, int G>
 __global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_experts, int dim, int inter, int n_blk,
                                                 bool by_slot, const int *__restrict__ keys,
-                                                const u32x4 *__restrict__ codes,
-                                                const typename E::T *__restrict__ scales,
-                                                const unsigned char *__restrict__ zeros,
+                                                const char *__restrict__ tiles,
                                                 const typename E::T *__restrict__ x, int64_t ldx, Hidden h) {
-    constexpr int GB = Q4_BLOCK / G, U = ME_UNROLL;
+    constexpr int U = ME_UNROLL;
     extern __shared__ __attribute__((aligned(16))) f32x4 part[];       // [waves][2][64]
     __shared__ unsigned short list[ME_MAX_TOK];                        // slots of the expert, one per token
     __shared__ int n_list;
@@ -103,16 +101,10 @@ __global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_expe
     __syncthreads();
     const int n = n_list;
     const int row0 = blockIdx.x * 16, quarter = lane / 16;
-    const u32x4 *c[2];
-    const typename E::T *s[2];
-    const unsigned char *z[2];
+    Q4Row<ZP, G> rows[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t row = ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1);
-        c[r] = codes + row * n_blk * 4 + quarter;
-        s[r] = scales + row * n_blk * GB;
-        z[r] = ZP ? zeros + row * n_blk * GB : nullptr;
-    }
+    for (int r = 0; r < 2; ++r)
+        rows[r] = Q4Row<ZP, G>(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk, quarter);
     const int whole = dim / (Q4_BLOCK * U);
     for (int first = 0; first < n; first += 16) {
         const typename E::T *xr = x + (int64_t)(list[min(first + (lane & 15), n - 1)] / top_k) * ldx;
@@ -122,7 +114,7 @@ __global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_expe
             Q4Piece<E, ZP, G, U> w[2];
             u32x4 xv[U][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[r].load(c[r] + (int64_t)b * 4, s[r] + (int64_t)b * GB, z[r] + (int64_t)b * GB);
+            for (int r = 0; r < 2; ++r) w[r].load(rows[r], b);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -134,7 +126,7 @@ __global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_expe
             Q4Piece<E, ZP, G, 1> w[2];
             u32x4 xv[1][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[r].load(c[r] + (int64_t)b * 4, s[r] + (int64_t)b * GB, z[r] + (int64_t)b * GB);
+            for (int r = 0; r < 2; ++r) w[r].load(rows[r], b);
 #pragma unroll
             for (int m = 0; m < 4; ++m)
                 xv[0][m] = q4_token_piece(xr, (int64_t)b * Q4_BLOCK + 32 * m + 8 * quarter, dim);
@@ -164,9 +156,7 @@ __global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_expe
 template <class E, bool ZP, int G>
 __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_experts, int dim, int n_blk,
                                                    const int *__restrict__ keys, const float *__restrict__ weights,
-                                                   const u32x4 *__restrict__ codes,
-                                                   const typename E::T *__restrict__ scales,
-                                                   const unsigned char *__restrict__ zeros, Hidden h,
+                                                   const char *__restrict__ tiles, Hidden h,
                                                    void *__restrict__ y, bool f32, int64_t ldy) {
     constexpr int GB = Q4_BLOCK / G, PG = G / 32, U = ME_UNROLL;
     typedef Q4Op<BF16> Op;
@@ -229,10 +219,7 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
             n += __popcll(has);
         }
         __builtin_amdgcn_wave_barrier();
-        const int64_t row = (int64_t)e * dim + min(row0 + (lane & 15), dim - 1);
-        const u32x4 *c = codes + row * n_blk * 4 + quarter;
-        const typename E::T *s = scales + row * n_blk * GB;
-        const unsigned char *z = ZP ? zeros + row * n_blk * GB : nullptr;
+        const Q4Row<ZP, G> row(tiles, (int64_t)e * dim + min(row0 + (lane & 15), dim - 1), n_blk, quarter);
         for (int first = 0; first < n; first += 16) {
             const unsigned short *hr = h.p + (int64_t)list[min(first + (lane & 15), n - 1)] * h.ld + 8 * quarter;
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -262,13 +249,13 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
                 const int b0 = p * U;
                 if (b0 + U <= n_blk) {
                     Q4Piece<E, ZP, G, U> w;
-                    w.load(c + (int64_t)b0 * 4, s + (int64_t)b0 * GB, z + (int64_t)b0 * GB);
+                    w.load(row, b0);
 #pragma unroll
                     for (int u = 0; u < U; ++u) block(w, u, b0 + u);
                 } else {
                     for (int b = b0; b < n_blk; ++b) {
                         Q4Piece<E, ZP, G, 1> w;
-                        w.load(c + (int64_t)b * 4, s + (int64_t)b * GB, z + (int64_t)b * GB);
+                        w.load(row, b);
                         block(w, 0, b);
                     }
                 }
@@ -331,10 +318,8 @@ extern "C" spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t 
 }
 
 extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,
-                                 int32_t group, const int32_t *keys, const float *weights, const uint32_t *up_codes,
-                                 const void *up_scales, const uint8_t *up_zeros, const uint32_t *down_codes,
-                                 const void *down_scales, const uint8_t *down_zeros, int32_t dtype, const void *x,
-                                 int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace,
+                                 int32_t group, int32_t with_zeros, const int32_t *keys, const float *weights,
+                                 const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x, int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, void *stream) {
     size_t need = 0;
     spmv_status st = moe_workspace_size(n_tok, top_k, inter, &need);
@@ -347,11 +332,9 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     if (y_dtype != SPMV_F32 && y_dtype != dtype) return fail(SPMV_ERR_UNSUPPORTED, "y must be fp32 or have x's type");
     if (ldx < dim || ldy < dim) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
     if (n_tok == 0) return SPMV_OK;
-    if (!keys || !up_codes || !up_scales || !down_codes || !down_scales || !x || !y)
+    if (!keys || !up_tiles || !down_tiles || !x || !y)
         return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
-    if ((up_zeros == nullptr) != (down_zeros == nullptr))
-        return fail(SPMV_ERR_INVALID_VALUE, "both weights have zero points, or neither");
-    if (!aligned16(up_codes) || !aligned16(down_codes)) return fail(SPMV_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
+    if (!aligned16(up_tiles) || !aligned16(down_tiles)) return fail(SPMV_ERR_UNSUPPORTED, "tiles must be 16-byte aligned");
     if (!workspace) return fail(SPMV_ERR_INVALID_VALUE, "workspace is NULL (moe_workspace_size gives its size)");
     if (workspace_bytes < need)
         return fail(SPMV_ERR_INVALID_VALUE, "workspace of %zu bytes is smaller than %zu", workspace_bytes, need);
@@ -374,14 +357,14 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         const int up_waves = (int)std::min<int64_t>(8, ceil_div(up_blk, ME_UNROLL));
         k_moe_up<E, ZP, G><<<dim3((unsigned)(ld / 16), by_slot ? slots : n_experts), 64 * up_waves,
                              (size_t)up_waves * 2048, s>>>(
-            n_tok, top_k, n_experts, dim, inter, up_blk, by_slot, keys, reinterpret_cast<const u32x4 *>(up_codes),
-            static_cast<const T *>(up_scales), up_zeros, static_cast<const T *>(x), ldx, h);
+            n_tok, top_k, n_experts, dim, inter, up_blk, by_slot, keys, static_cast<const char *>(up_tiles),
+            static_cast<const T *>(x), ldx, h);
         SPMV_LAUNCHED("k_moe_up");
         // a wave's sums take 64 bytes per token: 16 waves up to 64 tokens, 8 up to 256
         const int waves = n_tok <= 64 ? 16 : 8;
         k_moe_down<E, ZP, G><<<(int)ceil_div(dim, 16), 64 * waves, down_lds(waves, n_tok, top_k, n_experts), s>>>(
-            n_tok, top_k, n_experts, dim, down_blk, keys, weights, reinterpret_cast<const u32x4 *>(down_codes),
-            static_cast<const T *>(down_scales), down_zeros, h, y, y_dtype == SPMV_F32, ldy);
+            n_tok, top_k, n_experts, dim, down_blk, keys, weights, static_cast<const char *>(down_tiles), h, y,
+            y_dtype == SPMV_F32, ldy);
         SPMV_LAUNCHED("k_moe_down");
         return SPMV_OK;
     };
@@ -390,6 +373,6 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         if (group == 64) return launch(e, z, std::integral_constant<int, 64>{});
         return launch(e, z, std::integral_constant<int, 128>{});
     };
-    if (dtype == SPMV_F16) return up_zeros ? by_group(F16{}, std::true_type{}) : by_group(F16{}, std::false_type{});
-    return up_zeros ? by_group(BF16{}, std::true_type{}) : by_group(BF16{}, std::false_type{});
+    if (dtype == SPMV_F16) return with_zeros ? by_group(F16{}, std::true_type{}) : by_group(F16{}, std::false_type{});
+    return with_zeros ? by_group(BF16{}, std::true_type{}) : by_group(BF16{}, std::false_type{});
 }

@@ -50,27 +50,19 @@ __device__ __forceinline__ void q4_products(const Q4Piece<E, ZP, G, U> (&w)[RT],
 
 template <class E, bool ZP, int G, int RT>
 __global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_cols, int n_blk,
-                                                              const u32x4 *__restrict__ codes,
-                                                              const typename E::T *__restrict__ scales,
-                                                              const unsigned char *__restrict__ zeros, int n_tok,
+                                                              const char *__restrict__ tiles, int n_tok,
                                                               float alpha, const typename E::T *__restrict__ x,
                                                               int64_t ldx, float beta, void *__restrict__ y, bool f32,
                                                               int64_t ldy) {
-    constexpr int GB = Q4_BLOCK / G, U = QF_UNROLL;
+    constexpr int U = QF_UNROLL;
     extern __shared__ __attribute__((aligned(16))) f32x4 part[];      // [waves][RT][64]
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
     const int quarter = lane / 16;
     const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
-    const u32x4 *c[RT];
-    const typename E::T *s[RT];
-    const unsigned char *z[RT];
+    Q4Row<ZP, G> rows[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int64_t row = min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1);     // rows past the end: not stored
-        c[r] = codes + row * n_blk * 4 + quarter;
-        s[r] = scales + row * n_blk * GB;
-        z[r] = ZP ? zeros + row * n_blk * GB : nullptr;
-    }
+    for (int r = 0; r < RT; ++r)                                 // rows past the end: not stored
+        rows[r] = Q4Row<ZP, G>(tiles, min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1), n_blk, quarter);
     // tokens past the end take the last one's row: their sums are not stored
     const typename E::T *xr = x + (int64_t)min(lane & 15, n_tok - 1) * ldx;
     f32x4 acc[RT];
@@ -82,7 +74,7 @@ __global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_
         Q4Piece<E, ZP, G, U> w[RT];
         u32x4 xv[U][4];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) w[r].load(c[r] + (int64_t)b * 4, s[r] + (int64_t)b * GB, z[r] + (int64_t)b * GB);
+        for (int r = 0; r < RT; ++r) w[r].load(rows[r], b);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -94,7 +86,7 @@ __global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_
         Q4Piece<E, ZP, G, 1> w[RT];
         u32x4 xv[1][4];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) w[r].load(c[r] + (int64_t)b * 4, s[r] + (int64_t)b * GB, z[r] + (int64_t)b * GB);
+        for (int r = 0; r < RT; ++r) w[r].load(rows[r], b);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
             xv[0][m] = q4_token_piece(xr, (int64_t)b * Q4_BLOCK + 32 * m + 8 * quarter, n_cols);
@@ -121,9 +113,7 @@ __global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_
 // split over workgroups, whose sums k_q4_join adds.
 template <class E, bool ZP, int G, int RT, int TT>
 __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int n_blk, int row_tiles, int tok_tiles,
-                                                    int split, const u32x4 *__restrict__ codes,
-                                                    const typename E::T *__restrict__ scales,
-                                                    const unsigned char *__restrict__ zeros, int n_tok, float alpha,
+                                                    int split, const char *__restrict__ tiles, int n_tok, float alpha,
                                                     const typename E::T *__restrict__ x, int64_t ldx, float beta,
                                                     void *__restrict__ y, bool f32, int64_t ldy,
                                                     float *__restrict__ parts) {
@@ -137,16 +127,10 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     const int64_t row0 = ((int64_t)row_tile * 4 + wv) * (16 * RT);
     const int t0 = tok_tile * TN;
     const int b0 = (int)((int64_t)n_blk * blockIdx.y / split), b1 = (int)((int64_t)n_blk * (blockIdx.y + 1) / split);
-    const u32x4 *c[RT];
-    const typename E::T *s[RT];
-    const unsigned char *z[RT];
+    Q4Row<ZP, G> rows[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int64_t row = min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1);
-        c[r] = codes + row * n_blk * 4 + quarter;
-        s[r] = scales + row * n_blk * GB;
-        z[r] = ZP ? zeros + row * n_blk * GB : nullptr;
-    }
+    for (int r = 0; r < RT; ++r)
+        rows[r] = Q4Row<ZP, G>(tiles, min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1), n_blk, quarter);
     const typename E::T *xr[TT];
     int slot[TT];
 #pragma unroll
@@ -169,7 +153,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     Q4Piece<E, ZP, G, 1> w[RT];
     u32x4 v[TT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) w[r].load(c[r] + (int64_t)b0 * 4, s[r] + (int64_t)b0 * GB, z[r] + (int64_t)b0 * GB);
+    for (int r = 0; r < RT; ++r) w[r].load(rows[r], b0);
     load_x(b0, v);
 #pragma unroll
     for (int q = 0; q < TT; ++q) xt[0][slot[q]] = v[q];
@@ -184,8 +168,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
         const int next = min(b + 1, b1 - 1);
         Q4Piece<E, ZP, G, 1> wn[RT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-            wn[r].load(c[r] + (int64_t)next * 4, s[r] + (int64_t)next * GB, z[r] + (int64_t)next * GB);
+        for (int r = 0; r < RT; ++r) wn[r].load(rows[r], next);
         load_x(next, v);
 #pragma unroll
         for (int g = 0; g < GB; ++g) {
@@ -253,6 +236,27 @@ __global__ __launch_bounds__(256) void k_q4_scale(int n_rows, int64_t n, float b
                                                   int64_t ldy) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
         q4_store<E>(y, f32, i / n_rows * ldy + i % n_rows, 0.0f, beta);
+}
+
+// The records from the rows: a workgroup writes the records of four blocks, a wave
+// each; words and groups past the last row are zeros.
+__global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_blk, int gb, int64_t n_rec, int rec_bytes,
+                                                  const u32x4 *__restrict__ codes,
+                                                  const unsigned short *__restrict__ scales,
+                                                  const unsigned char *__restrict__ zeros, char *__restrict__ tiles) {
+    const int lane = __lane_id();
+    const int64_t rec = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (rec >= n_rec) return;
+    const int64_t tile = rec / n_blk, row = tile * 16 + (lane & 15);
+    const int b = (int)(rec - tile * n_blk);
+    char *out = tiles + rec * rec_bytes;
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    reinterpret_cast<u32x4 *>(out)[lane] = row < n_rows ? codes[(row * n_blk + b) * 4 + lane / 16] : none;
+    for (int i = lane; i < 16 * gb; i += 64) {
+        const int64_t r = tile * 16 + i / gb, at = (r * n_blk + b) * gb + i % gb;
+        reinterpret_cast<unsigned short *>(out + Q4_SCALES)[i] = r < n_rows ? scales[at] : (unsigned short)0;
+        if (zeros) reinterpret_cast<unsigned char *>(out + Q4_SCALES + 32 * gb)[i] = r < n_rows ? zeros[at] : (unsigned char)0;
+    }
 }
 
 // Codes of a dense weight, one thread per group.  Symmetric: s = max |w| / 7,
@@ -381,6 +385,35 @@ extern "C" spmv_status q4_quantize(int32_t n_rows, int32_t n_cols, int32_t group
     return SPMV_OK;
 }
 
+extern "C" spmv_status q4_tiles_size(int32_t n_rows, int32_t n_cols, int32_t group, int32_t with_zeros, size_t *bytes) {
+    if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
+    const spmv_status st = check_weight(n_rows, n_cols, group, SPMV_F16);
+    if (st != SPMV_OK) return st;
+    *bytes = (size_t)ceil_div(n_rows, 16) * (size_t)q4_blocks(n_cols) * q4_record(group, with_zeros != 0);
+    return SPMV_OK;
+}
+
+extern "C" spmv_status q4_tiles(int32_t n_rows, int32_t n_cols, int32_t group, const uint32_t *codes,
+                                const void *scales, const uint8_t *zeros, void *tiles, size_t tiles_bytes, void *stream) {
+    size_t need = 0;
+    spmv_status st = q4_tiles_size(n_rows, n_cols, group, zeros != nullptr, &need);
+    if (st != SPMV_OK) return st;
+    if (need == 0) return SPMV_OK;
+    if (!codes || !scales || !tiles) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
+    if (tiles_bytes < need)
+        return fail(SPMV_ERR_INVALID_VALUE, "tiles of %zu bytes are smaller than %zu", tiles_bytes, need);
+    if (!aligned16(codes) || !aligned16(tiles)) return fail(SPMV_ERR_UNSUPPORTED, "codes and tiles must be 16-byte aligned");
+    const int64_t n_blk = q4_blocks(n_cols), n_rec = ceil_div(n_rows, 16) * n_blk;
+    st = check_grid(ceil_div(n_rec, 4));
+    if (st != SPMV_OK) return st;
+    k_q4_tiles<<<(int)ceil_div(n_rec, 4), 256, 0, as_stream(stream)>>>(
+        n_rows, (int)n_blk, Q4_BLOCK / group, n_rec, (int)q4_record(group, zeros != nullptr),
+        reinterpret_cast<const u32x4 *>(codes), static_cast<const unsigned short *>(scales), zeros,
+        static_cast<char *>(tiles));
+    SPMV_LAUNCHED("k_q4_tiles");
+    return SPMV_OK;
+}
+
 extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes) {
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
     if (n_rows < 0 || n_cols < 0 || n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
@@ -395,9 +428,8 @@ extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t
     return SPMV_OK;
 }
 
-extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, const uint32_t *codes,
-                                 const void *scales, const uint8_t *zeros, int32_t dtype, int32_t n_tok, float alpha,
-                                 const void *x, int64_t ldx, float beta, void *y, int32_t y_dtype, int64_t ldy,
+extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, int32_t with_zeros, const void *tiles,
+                                 int32_t dtype, int32_t n_tok, float alpha, const void *x, int64_t ldx, float beta, void *y, int32_t y_dtype, int64_t ldy,
                                  void *workspace, size_t workspace_bytes, void *stream) {
     spmv_status st = check_weight(n_rows, n_cols, group, dtype);
     if (st != SPMV_OK) return st;
@@ -406,8 +438,8 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
     if (y_dtype != SPMV_F32 && y_dtype != dtype) return fail(SPMV_ERR_UNSUPPORTED, "y must be fp32 or have x's type");
     if (ldx < n_cols || ldy < n_rows) return fail(SPMV_ERR_INVALID_VALUE, "a row stride is shorter than the row");
     if (n_rows == 0 || n_tok == 0) return SPMV_OK;
-    if (!y || (n_cols > 0 && (!codes || !scales || !x))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
-    if (!aligned16(codes)) return fail(SPMV_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
+    if (!y || (n_cols > 0 && (!tiles || !x))) return fail(SPMV_ERR_INVALID_VALUE, "NULL pointer");
+    if (!aligned16(tiles)) return fail(SPMV_ERR_UNSUPPORTED, "tiles must be 16-byte aligned");
     hipStream_t s = as_stream(stream);
     const bool f32 = y_dtype == SPMV_F32;
     if (n_cols == 0) {
@@ -422,15 +454,14 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
     }
     const int n_blk = (int)q4_blocks(n_cols);
     if (n_tok <= QF_TOKENS)
-        return by_weight(dtype, zeros != nullptr, group, [&](auto e, auto zp, auto g) -> spmv_status {
+        return by_weight(dtype, with_zeros != 0, group, [&](auto e, auto zp, auto g) -> spmv_status {
             typedef decltype(e) E;
             typedef typename E::T T;
             constexpr bool ZP = decltype(zp)::value;
             constexpr int G = decltype(g)::value, RT = 2;
             const int waves = (int)std::min<int64_t>(8, ceil_div(n_blk, QF_UNROLL));
             k_q4_few<E, ZP, G, RT><<<(int)ceil_div(n_rows, 16 * RT), 64 * waves, (size_t)waves * RT * 1024, s>>>(
-                n_rows, n_cols, n_blk, reinterpret_cast<const u32x4 *>(codes), static_cast<const T *>(scales), zeros,
-                n_tok, alpha, static_cast<const T *>(x), ldx, beta, y, f32, ldy);
+                n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n_tok, alpha, static_cast<const T *>(x), ldx, beta, y, f32, ldy);
             SPMV_LAUNCHED("k_q4_few");
             return SPMV_OK;
         });
@@ -442,7 +473,7 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
     if (!aligned16(workspace)) return fail(SPMV_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
     st = check_grid((int64_t)t.row_tiles * t.tok_tiles);
     if (st != SPMV_OK) return st;
-    st = by_weight(dtype, zeros != nullptr, group, [&](auto e, auto zp, auto g) -> spmv_status {
+    st = by_weight(dtype, with_zeros != 0, group, [&](auto e, auto zp, auto g) -> spmv_status {
         typedef decltype(e) E;
         typedef typename E::T T;
         constexpr bool ZP = decltype(zp)::value;
@@ -450,9 +481,8 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         auto run = [&](auto rt, auto tt) {
             k_q4_tile<E, ZP, G, decltype(rt)::value, decltype(tt)::value>
                 <<<dim3((unsigned)(t.row_tiles * t.tok_tiles), (unsigned)t.split), 256, 0, s>>>(
-                    n_rows, n_cols, n_blk, t.row_tiles, t.tok_tiles, t.split, reinterpret_cast<const u32x4 *>(codes),
-                    static_cast<const T *>(scales), zeros, n_tok, alpha, static_cast<const T *>(x), ldx, beta, y, f32,
-                    ldy, static_cast<float *>(workspace));
+                    n_rows, n_cols, n_blk, t.row_tiles, t.tok_tiles, t.split, static_cast<const char *>(tiles), n_tok,
+                    alpha, static_cast<const T *>(x), ldx, beta, y, f32, ldy, static_cast<float *>(workspace));
         };
         const std::integral_constant<int, 2> two;
         const std::integral_constant<int, 4> four;

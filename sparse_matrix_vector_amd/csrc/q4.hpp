@@ -1,13 +1,18 @@
-// Weights of 4 bits with group scales on gfx950: the layout, the decoding into
-// matrix-core operands, and a wave's pass over a piece of 16 rows.
+// Weights of 4 bits with group scales on gfx950: the layout that the kernels
+// read, the decoding into matrix-core operands, and a lane's piece of a row.
 //
-// A row is cut into blocks of 128 columns (64 bytes of codes).  Word 4 j + m of
-// a block holds columns 32 m + 8 j .. + 7, so that the 16 bytes that lane
-// quarter j loads are its operands of the block's four 16x16x32 products: the
-// product m covers the columns 32 m .. 32 m + 31 whole, and a group of 32, 64
-// or 128 columns is one, two or four products.  The weight's fragment is the
-// second operand (D's columns are rows of W), the tokens' the first: a lane
-// then decodes the row whose scale it multiplies with.
+// Rows are taken 16 at a time (a matrix-core operand) and columns in blocks of
+// 128.  The tile of 16 rows and a block is one record, in the order of the lanes
+// that read it: 64 times 16 bytes of codes, lane l's those of row l % 16 and
+// quarter l / 16, then 16 x groups scales and 16 x groups zero points.  (Row by
+// row, as the weights come, the 16 lanes of a quarter touch 16 cache lines for 16
+// bytes each: 8.3 M cache accesses for 12288 x 12288 and 28 us.)  A lane's 16
+// bytes are its operands of the block's four 16x16x32 products: its word m holds
+// columns 32 m + 8 (l / 16) .. + 7, so that product m covers the columns 32 m ..
+// 32 m + 31 whole, and a group of 32, 64 or 128 columns is one, two or four
+// products.  The weight's fragment is the second operand (D's columns are rows of
+// W), the tokens' the first: a lane then decodes the row whose scale it multiplies
+// with.
 //
 // Codes become exact 16-bit numbers q - z (fp16: (q - z) 2^-9; a code masked out
 // of a word is the fp16 subnormal q 2^-24 or 16 q 2^-24, and one fused
@@ -32,6 +37,7 @@ constexpr int Q4_ROWS = 16;        // rows of a matrix-core operand
 
 inline bool q4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 inline int64_t q4_blocks(int64_t n_cols) { return ceil_div(n_cols, Q4_BLOCK); }
+inline size_t q4_record(int32_t group, bool zeros) { return 1024 + (size_t)(Q4_BLOCK / group) * (zeros ? 48 : 32); }
 
 // nibble of column e of a word's eight
 __host__ __device__ constexpr int q4_place(int e) { return (e >> 1) + 4 * (e & 1); }
@@ -101,27 +107,53 @@ __device__ __forceinline__ Bytes<N> load_bytes(const void *p) {
     return r;
 }
 
+// Bytes of a record, and where its scales and zero points begin.
+constexpr int Q4_SCALES = 1024;
+template <bool ZP, int G>
+struct Q4Rec {
+    static constexpr int GB = Q4_BLOCK / G;        // groups of a block
+    static constexpr int ZEROS = Q4_SCALES + 32 * GB;
+    static constexpr int SIZE = ZEROS + (ZP ? 16 * GB : 0);
+};
+
+// A lane's place in the records of one row.
+template <bool ZP, int G>
+struct Q4Row {
+    const char *codes, *scales, *zeros;
+    __device__ __forceinline__ Q4Row() {}
+    __device__ __forceinline__ Q4Row(const char *tiles, int64_t row, int n_blk, int quarter) {
+        const int r = (int)(row & 15);
+        const char *rec = tiles + (row >> 4) * n_blk * Q4Rec<ZP, G>::SIZE;
+        codes = rec + (quarter * 16 + r) * 16;
+        scales = rec + Q4_SCALES + r * 2 * Q4Rec<ZP, G>::GB;
+        zeros = rec + Q4Rec<ZP, G>::ZEROS + r * Q4Rec<ZP, G>::GB;
+    }
+};
+
 // U blocks of one row as a lane holds them: its quarter's codes, and the scales
 // and zero points of all their groups.
 template <class E, bool ZP, int G, int U>
 struct Q4Piece {
-    static constexpr int GB = Q4_BLOCK / G;        // groups of a block
+    static constexpr int GB = Q4_BLOCK / G;
     typedef typename E::T T;
     u32x4 c[U];
-    Vec<E, U * GB> s;
-    Bytes<ZP ? U * GB : 1> z;
+    Vec<E, GB> s[U];
+    Bytes<ZP ? GB : 1> z[U];
 
-    // codes: the row's blocks from this one on, quarter's 16 bytes; scales, zeros: of its groups
-    __device__ __forceinline__ void load(const u32x4 *codes, const T *scales, const unsigned char *zeros) {
+    __device__ __forceinline__ void load(const Q4Row<ZP, G> &row, int b) {
+        constexpr int SIZE = Q4Rec<ZP, G>::SIZE;
+        const int64_t at = (int64_t)b * SIZE;
 #pragma unroll
-        for (int u = 0; u < U; ++u) c[u] = __builtin_nontemporal_load(codes + 4 * u);
-        __builtin_memcpy(&s, __builtin_assume_aligned(scales, 2), sizeof s);
-        if constexpr (ZP) z = load_bytes<U * GB>(zeros);
+        for (int u = 0; u < U; ++u) {
+            c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row.codes + at + u * SIZE));
+            s[u] = load_vec<E, GB>(reinterpret_cast<const T *>(row.scales + at + u * SIZE));
+            if constexpr (ZP) z[u] = load_bytes<GB>(row.zeros + at + u * SIZE);
+        }
     }
-    __device__ __forceinline__ float scale(int u, int g) const { return (float)s.v[u * GB + g]; }
+    __device__ __forceinline__ float scale(int u, int g) const { return (float)s[u].v[g]; }
     __device__ __forceinline__ int zero(int u, int g) const {
         if constexpr (ZP)
-            return z.b[u * GB + g] & 15;
+            return z[u].b[g] & 15;
         else
             return 8;
     }

@@ -45,16 +45,32 @@ def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
     return codes, scales, zeros
 
 
+def q4_tiles_size(n_rows, n_cols, group=128, with_zeros=False) -> int:
+    return _size("q4_tiles_size", ctypes.c_size_t, n_rows, n_cols, group, with_zeros)
+
+
+def q4_tiles(n_rows, n_cols, codes, scales, zeros, tiles, group=128, stream=None):
+    """Fills tiles (uint8, q4_tiles_size bytes), what the products read, from the
+    rows' codes, scales and zero points (or None)."""
+    n_rows, n_cols = int(n_rows), int(n_cols)
+    d, per = _device(codes, "codes"), n_rows * _groups(n_cols, _group(group))
+    if not isinstance(scales, torch.Tensor) or scales.dtype not in _HALF_TYPES:
+        raise TypeError("scales must be a float16 or bfloat16 tensor")
+    tp, tb = _ws(tiles, d)
+    _launch(d, stream, "q4_tiles", n_rows, n_cols, group,
+            _ptr(codes, _WORD, "codes", n_rows * ((n_cols + 127) // 128) * 16, d),
+            _ptr(scales, scales.dtype, "scales", per, d), _opt(zeros, torch.uint8, "zeros", per, d), tp, tb)
+    return tiles
+
+
 def q4_workspace_size(n_rows, n_cols, n_tok) -> int:
     return _size("q4_workspace_size", ctypes.c_size_t, n_rows, n_cols, n_tok)
 
 
-def q4_matmul(n_rows, n_cols, codes, scales, zeros, alpha, x, beta, y, workspace=None, group=128, stream=None):
+def q4_matmul(n_rows, n_cols, tiles, alpha, x, beta, y, workspace=None, group=128, with_zeros=False, stream=None):
     """y = alpha * x W^T + beta * y for x [tokens, n_cols] of the scales' type and y
     [tokens, n_rows] of the same type or fp32.  workspace: q4_workspace_size bytes for
     these tokens or more."""
-    n_rows, n_cols = int(n_rows), int(n_cols)
-    per = _groups(n_cols, _group(group))
     d, n, width, xp, ldx = _matrix(x, "x")
     dt = x.dtype
     if dt not in _HALF_TYPES:
@@ -63,26 +79,29 @@ def q4_matmul(n_rows, n_cols, codes, scales, zeros, alpha, x, beta, y, workspace
         raise ValueError(f"x must have {n_cols} columns, got {width}")
     yp, ldy = _rows(y, (dt, _F32), "y", n, n_rows, d)
     wp, wb = _ws(workspace, d)
-    _launch(d, stream, "q4_matmul", n_rows, n_cols, group,
-            _ptr(codes, _WORD, "codes", n_rows * ((n_cols + 127) // 128) * 16, d),
-            _ptr(scales, dt, "scales", n_rows * per, d), _opt(zeros, torch.uint8, "zeros", n_rows * per, d), _CODE[dt], n,
-            alpha, xp, ldx, beta, yp, _CODE[y.dtype], ldy, wp, wb)
+    tp, tb = _ws(tiles, d)
+    if tb < (n_rows + 15) // 16 * ((n_cols + 127) // 128) * (1024 + 128 // _group(group) * (48 if with_zeros else 32)):
+        raise ValueError("tiles are smaller than q4_tiles_size")
+    _launch(d, stream, "q4_matmul", n_rows, n_cols, group, with_zeros, tp, _CODE[dt], n, alpha, xp, ldx, beta, yp,
+            _CODE[y.dtype], ldy, wp, wb)
     return y
 
 
 class Q4Matrix:
-    """One 4-bit weight, or n_groups stacked ones (the experts of moe_apply): codes,
-    scales and zero points (or None) in the layout of include/spmv.h."""
+    """One 4-bit weight, or n_groups stacked ones (the experts of moe_apply), arranged
+    for the products from codes, scales and zero points (or None) in the layout of
+    include/spmv.h, which may be freed afterwards.  It is made on `stream`: other
+    streams wait for it before they use the matrix, and it is kept until their calls
+    are done."""
 
-    def __init__(self, n_rows, n_cols, codes, scales, zeros=None, group=128, n_groups=1):
+    def __init__(self, n_rows, n_cols, codes, scales, zeros=None, group=128, n_groups=1, stream=None):
         self.n_rows, self.n_cols, self.n_groups, self.group = int(n_rows), int(n_cols), int(n_groups), _group(group)
-        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.with_zeros = int(zeros is not None)
         d, total = _device(codes, "codes"), self.n_rows * self.n_groups
-        _ptr(codes, _WORD, "codes", total * ((self.n_cols + 127) // 128) * 16, d)
-        if scales.dtype not in _HALF_TYPES:
-            raise TypeError(f"scales must be float16 or bfloat16, got {scales.dtype}")
-        _ptr(scales, scales.dtype, "scales", total * _groups(self.n_cols, group), d)
-        _opt(zeros, torch.uint8, "zeros", total * _groups(self.n_cols, group), d)
+        with _stream_scope(stream, d):
+            self.tiles = torch.empty(q4_tiles_size(total, n_cols, group, self.with_zeros), dtype=torch.uint8, device=d)
+        q4_tiles(total, n_cols, codes, scales, zeros, self.tiles, group, stream)
+        self.dtype = scales.dtype
 
     @classmethod
     def quantize(cls, w, group=128, dtype=None, zeros=False, stream=None):
@@ -100,23 +119,25 @@ class Q4Matrix:
             scales = torch.empty(shape, dtype=dtype, device=w.device)
             zp = torch.empty(shape, dtype=torch.uint8, device=w.device) if zeros else None
         q4_quantize(w, codes, scales, zp, group, stream)
-        return cls(rows, cols, codes, scales, zp, group, n_groups)
+        return cls(rows, cols, codes, scales, zp, group, n_groups, stream)
 
     def workspace(self, n_tok):
         """A workspace for calls of up to n_tok tokens."""
         return torch.empty(q4_workspace_size(self.n_rows, self.n_cols, n_tok), dtype=torch.uint8,
-                           device=self.codes.device)
+                           device=self.tiles.device)
 
     def apply(self, x, y, alpha=1.0, beta=0.0, workspace=None, stream=None):
         """y = alpha * x W^T + beta * y (of a single weight).  Without a workspace one
         is allocated for the call, in the order of the stream it runs on."""
         if self.n_groups != 1:
             raise ValueError("apply takes a single weight; stacked ones are moe_apply's")
+        if x.dtype is not self.dtype:
+            raise TypeError(f"x must be {self.dtype} like the scales, got {x.dtype}")
         if workspace is None and x.dim() == 2:
-            with _stream_scope(stream, self.codes.device):
+            with _stream_scope(stream, self.tiles.device):
                 workspace = self.workspace(x.shape[0])
-        return q4_matmul(self.n_rows, self.n_cols, self.codes, self.scales, self.zeros, alpha, x, beta, y, workspace,
-                         self.group, stream)
+        return q4_matmul(self.n_rows, self.n_cols, self.tiles, alpha, x, beta, y, workspace, self.group, self.with_zeros,
+                         stream)
 
 
 # ---------------------------------------------------------------------------
@@ -141,17 +162,15 @@ def moe_apply(keys, weights, gate_up, down, x, y, workspace, stream=None):
     if gate_up.n_cols != dim or gate_up.n_rows != 2 * inter or down.n_rows != dim or down.n_groups != e:
         raise ValueError(f"{e} x {gate_up.n_rows} x {gate_up.n_cols} and {down.n_groups} x {down.n_rows} x {down.n_cols} "
                          f"are not the weights of a layer of width {dim}")
-    if gate_up.group != down.group:
-        raise ValueError("the two weights must have the same group size")
-    if dt not in _HALF_TYPES or gate_up.scales.dtype != dt or down.scales.dtype != dt:
-        raise TypeError(f"x must be float16 or bfloat16 and the scales of its type, got {dt}, {gate_up.scales.dtype} "
-                        f"and {down.scales.dtype}")
+    if gate_up.group != down.group or gate_up.with_zeros != down.with_zeros:
+        raise ValueError("the two weights must have the same group size, and both zero points or neither")
+    if gate_up.dtype is not dt or down.dtype is not dt:
+        raise TypeError(f"x must be of the scales' type, got {dt}, {gate_up.dtype} and {down.dtype}")
     yp, ldy = _rows(y, (dt, _F32), "y", n, dim, d)
     wp, wb = _ws(workspace, d)
-    w = [p for m in (gate_up, down) for p in (_ptr(m.codes, _WORD, "codes", 0, d), _ptr(m.scales, dt, "scales", 0, d),
-                                              _opt(m.zeros, torch.uint8, "zeros", 0, d))]
-    _launch(d, stream, "moe_apply", n, k, e, dim, inter, down.group, _ptr(keys, _I32, "keys", n * k, d),
-            _opt(weights, _F32, "weights", n * k, d), *w, _CODE[dt], xp, ldx, yp, _CODE[y.dtype], ldy, wp, wb)
+    (up, _), (dn, _) = _ws(gate_up.tiles, d), _ws(down.tiles, d)
+    _launch(d, stream, "moe_apply", n, k, e, dim, inter, down.group, down.with_zeros, _ptr(keys, _I32, "keys", n * k, d),
+            _opt(weights, _F32, "weights", n * k, d), up, dn, _CODE[dt], xp, ldx, yp, _CODE[y.dtype], ldy, wp, wb)
     return y
 
 

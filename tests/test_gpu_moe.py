@@ -95,19 +95,20 @@ def test_without_weights_and_strided():
 
 def test_small_and_cancelling_hidden_values():
     """Down weights that cancel the large part of h leave what 16 bits of it would not hold."""
-    dim, inter, dt = 128, 128, "f16"
-    m = Layer(1, dim, inter, 128, dt, False, seed=11)
+    dim, inter = 128, 128
+    m = Layer(1, dim, inter, 128, "f16", False, seed=11)
     q = np.full((dim, inter), 8)
     q[:, 0], q[:, 1] = 15, 1                                 # y = 7 s (h0 - h1)
-    m.dn = S.Q4Matrix(dim, inter, Q.pack(q).cuda(), m.dn.scales, None, group=128)
-    m.dn64 = Q.dense(m.dn.codes, m.dn.scales, None, 128, inter).view(1, dim, inter)
-    u = Q.unpack(m.gu.codes)
+    s = torch.full((dim, 1), 0.25).half()
+    m.dn = S.Q4Matrix(dim, inter, Q.pack(q).cuda(), s.cuda(), None, group=128)
+    m.dn64 = Q.dense(Q.pack(q), s, None, 128, inter).view(1, dim, inter)
+    w, s, _ = Q.weight(2 * inter, dim, 128, torch.float16, False, 12, scale=0.04)
+    u = Q.unpack(w)
     u[1], u[inter + 1] = u[0], u[inter]
-    m.gu = S.Q4Matrix(2 * inter, dim, Q.pack(u).cuda(), m.gu.scales, None, group=128)
-    s = m.gu.scales
     s[1], s[inter + 1] = s[0], s[inter] * 1.001              # h1 is h0 but for a thousandth
-    m.up64 = Q.dense(m.gu.codes, s, None, 128, dim).view(1, 2 * inter, dim)
-    keys, w, x = _batch(8, 1, 1, dim, dt, 2, "one")
+    m.gu = S.Q4Matrix(2 * inter, dim, Q.pack(u).cuda(), s.cuda(), None, group=128)
+    m.up64 = Q.dense(Q.pack(u), s, None, 128, dim).view(1, 2 * inter, dim)
+    keys, w, x = _batch(8, 1, 1, dim, "f16", 2, "one")
     m.check(keys, w, x, m(keys, w, x))
 
 

@@ -147,8 +147,11 @@ def test_quantize(src, dt, group, zeros):
     t = torch.from_numpy(w).to(F[src])
     wide = torch.full((rows, cols + 5), float("nan")).to(F[src])
     wide[:, 2:2 + cols] = t
-    m = S.Q4Matrix.quantize(wide.cuda()[:, 2:2 + cols], group=group, dtype=F[dt], zeros=zeros)
     n = Q.blocks(cols) * 128
+    codes = torch.empty(rows, n // 8, dtype=torch.int32, device="cuda")
+    scales = torch.empty(rows, n // group, dtype=F[dt], device="cuda")
+    points = torch.empty(rows, n // group, dtype=torch.uint8, device="cuda") if zeros else None
+    S.q4_quantize(wide.cuda()[:, 2:2 + cols], codes, scales, points, group)
     full = np.zeros((rows, n), np.float32)
     full[:, :cols] = t.float().numpy()
     g = full.reshape(rows, n // group, group)
@@ -156,24 +159,47 @@ def test_quantize(src, dt, group, zeros):
     f = np.float32
     want = hi / f(15) - lo / f(15) if zeros else np.maximum(hi, -lo) / f(7)
     s = torch.from_numpy(np.minimum(want, f(torch.finfo(F[dt]).max))).to(F[dt])
-    assert torch.equal(m.scales.cpu(), s)
+    assert torch.equal(scales.cpu(), s)
     sf = s.float().numpy()
     safe = np.where(sf > 0, sf, f(1))
     z = np.where(sf > 0, np.minimum(np.rint(-lo / safe), f(15)), f(0)) if zeros else np.full_like(sf, 8)
     if zeros:
-        assert np.array_equal(m.zeros.cpu().numpy(), z.astype(np.uint8))
+        assert np.array_equal(points.cpu().numpy(), z.astype(np.uint8))
     q = np.where(sf[:, :, None] > 0, np.clip(np.rint(g / safe[:, :, None]) + z[:, :, None], 0, 15), z[:, :, None])
-    assert np.array_equal(Q.unpack(m.codes), q.reshape(rows, n).astype(np.int64))
+    assert np.array_equal(Q.unpack(codes), q.reshape(rows, n).astype(np.int64))
 
 
 def test_quantized_weight_is_near_the_weight():
     """Half a step of the scale per weight (symmetric: the scale is at most max / 7 rounded)."""
-    w = torch.randn(3, 64, 500, device="cuda")
+    w = torch.randn(64, 500, device="cuda")
     m = S.Q4Matrix.quantize(w, group=32, dtype=torch.float16)
-    assert m.n_groups == 3 and m.n_rows == 64
-    d = Q.dense(m.codes, m.scales, None, 32, 500)
-    step = torch.repeat_interleave(R.f64(m.scales), 32, 1)[:, :500]
-    assert ((d - R.f64(w).reshape(-1, 500)).abs() <= step * (0.5 + 8 * 2.0 ** -11)).all()
+    x = torch.eye(500, device="cuda").half()                 # the weight's columns
+    d = R.f64(m.apply(x, torch.empty(500, 64, device="cuda"))).t()
+    top = R.f64(w).abs()
+    top = torch.nn.functional.pad(top, (0, 12)).view(64, 16, 32).amax(2)
+    step = torch.repeat_interleave(top / 7, 32, 1)[:, :500]
+    assert ((d - R.f64(w)).abs() <= step * (0.5 + 8 * 2.0 ** -11)).all()
+    assert S.Q4Matrix.quantize(torch.randn(3, 20, 40, device="cuda").bfloat16(), zeros=True).n_groups == 3
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("rows,cols,group", [(1, 1, 128), (16, 128, 64), (35, 300, 32), (48, 129, 128)])
+def test_tiles(rows, cols, group, zeros):
+    """The records word for word."""
+    w, s, z = Q.weight(rows, cols, group, torch.float16, zeros, rows)
+    m = S.Q4Matrix(rows, cols, w.cuda(), s.cuda(), None if z is None else z.cuda(), group=group)
+    nb, gb = Q.blocks(cols), 128 // group
+    rec = m.tiles.cpu().numpy().reshape(-1, 1024 + gb * (48 if zeros else 32))
+    pad = lambda t: np.pad(t.numpy(), ((0, -rows % 16), (0, 0)))  # noqa: E731
+    for i in range((rows + 15) // 16):
+        for b in range(nb):
+            r = rec[i * nb + b]
+            codes = pad(w)[16 * i:16 * i + 16, 16 * b:16 * b + 16].reshape(16, 4, 4).transpose(1, 0, 2)
+            assert np.array_equal(r[:1024].view(np.int32).reshape(4, 16, 4), codes)
+            sc = pad(s)[16 * i:16 * i + 16, gb * b:gb * b + gb]
+            assert np.array_equal(r[1024:1024 + 32 * gb].view(np.float16).reshape(16, gb), sc)
+            if zeros:
+                assert np.array_equal(r[1024 + 32 * gb:].reshape(16, gb), pad(z)[16 * i:16 * i + 16, gb * b:gb * b + gb])
 
 
 @pytest.mark.parametrize("tok", [1, 12, 40, 300])

@@ -29,9 +29,31 @@ def test_quantize_refusals():
     assert _quantize(rows=0, w=None) == OK and _quantize(cols=0, ldw=0, w=None) == OK
 
 
-def _matmul(rows=40, cols=100, group=64, codes=P, scales=P, zeros=None, dt=F16, n=4, x=P, ldx=100, beta=0.0, y=P, ydt=F32,
-            ldy=40, ws=None, wsb=0):
-    return S.lib().q4_matmul(rows, cols, group, codes, scales, zeros, dt, n, 1.0, x, ldx, beta, y, ydt, ldy, ws, wsb, None)
+def _tiles(rows=20, cols=300, group=64, codes=P, scales=P, zeros=None, tiles=P, tb=1 << 20):
+    return S.lib().q4_tiles(rows, cols, group, codes, scales, zeros, tiles, tb, None)
+
+
+def test_tiles_sizes_and_refusals():
+    assert S.q4_tiles_size(20, 300, 64) == 2 * 3 * (1024 + 2 * 32)
+    assert S.q4_tiles_size(16, 128, 32, True) == 1024 + 4 * 48 and S.q4_tiles_size(1, 1, 128) == 1056
+    assert S.q4_tiles_size(0, 300) == 0 and S.q4_tiles_size(20, 0) == 0
+    z = ctypes.c_size_t()
+    L = S.lib()
+    assert L.q4_tiles_size(-1, 4, 32, 0, ctypes.byref(z)) == VALUE and L.q4_tiles_size(4, -1, 32, 0, ctypes.byref(z)) == VALUE
+    assert L.q4_tiles_size(4, 4, 31, 0, ctypes.byref(z)) == VALUE and L.q4_tiles_size(4, 4, 32, 0, None) == VALUE
+    assert _tiles(rows=-1) == VALUE and _tiles(group=16) == VALUE
+    for k in ("codes", "scales", "tiles"):
+        assert _tiles(**{k: None}) == VALUE, k
+    assert _tiles(tb=S.q4_tiles_size(20, 300, 64) - 1) == VALUE
+    assert _tiles(zeros=P, tb=S.q4_tiles_size(20, 300, 64)) == VALUE
+    assert _tiles(codes=P + 8) == UNSUPPORTED and _tiles(tiles=P + 8) == UNSUPPORTED
+    assert _tiles(rows=2 ** 31 - 1, cols=2 ** 20, tb=2 ** 62) == OVERFLOW
+    assert _tiles(rows=0, codes=None) == OK and _tiles(cols=0, tiles=None) == OK
+
+
+def _matmul(rows=40, cols=100, group=64, zp=0, tiles=P, dt=F16, n=4, x=P, ldx=100, beta=0.0, y=P, ydt=F32, ldy=40, ws=None,
+            wsb=0):
+    return S.lib().q4_matmul(rows, cols, group, zp, tiles, dt, n, 1.0, x, ldx, beta, y, ydt, ldy, ws, wsb, None)
 
 
 def test_matmul_refusals():
@@ -39,9 +61,14 @@ def test_matmul_refusals():
     assert _matmul(group=48) == VALUE and _matmul(dt=5) == VALUE and _matmul(ydt=5) == VALUE
     assert _matmul(dt=F32) == UNSUPPORTED and _matmul(dt=F16, ydt=BF16) == UNSUPPORTED
     assert _matmul(ldx=99) == VALUE and _matmul(ldy=39) == VALUE
-    for k in ("codes", "scales", "x", "y"):
+    for k in ("tiles", "x", "y"):
         assert _matmul(**{k: None}) == VALUE, k
-    assert _matmul(codes=P + 4) == UNSUPPORTED
+    assert _matmul(tiles=P + 8) == UNSUPPORTED
+    need = S.q4_workspace_size(64, 12288, 48)
+    assert need > 0
+    big = dict(rows=64, cols=12288, ldx=12288, ldy=64, n=48)
+    assert _matmul(**big) == VALUE and b"workspace" in S.lib().spmv_last_error()
+    assert _matmul(ws=P, wsb=need - 1, **big) == VALUE and _matmul(ws=P + 8, wsb=need, **big) == UNSUPPORTED
     assert _matmul(rows=0, y=None) == OK and _matmul(n=0, x=None, y=None) == OK
     assert S.lib().q4_workspace_size(4, 4, 4, None) == VALUE
     z = ctypes.c_size_t()
@@ -55,13 +82,13 @@ def test_matmul_workspace_serves_fewer_tokens():
         assert sizes == sorted(sizes) and sizes[0] == 0
 
 
-def _moe(n=4, k=2, e=8, dim=64, inter=96, group=32, keys=P, w=None, uc=P, us=P, uz=None, dc=P, ds=P, dz=None, dt=F16, x=P,
-         ldx=64, y=P, ydt=F16, ldy=64, ws=P, wsb=None):
+def _moe(n=4, k=2, e=8, dim=64, inter=96, group=32, zp=0, keys=P, w=None, up=P, dn=P, dt=F16, x=P, ldx=64, y=P, ydt=F16,
+         ldy=64, ws=P, wsb=None):
     if wsb is None:
         z = ctypes.c_size_t()
-        wsb = z.value if S.lib().moe_workspace_size(n, k, inter, ctypes.byref(z)) == OK else 0
+        S.lib().moe_workspace_size(n, k, inter, ctypes.byref(z))
         wsb = z.value
-    return S.lib().moe_apply(n, k, e, dim, inter, group, keys, w, uc, us, uz, dc, ds, dz, dt, x, ldx, y, ydt, ldy, ws, wsb, None)
+    return S.lib().moe_apply(n, k, e, dim, inter, group, zp, keys, w, up, dn, dt, x, ldx, y, ydt, ldy, ws, wsb, None)
 
 
 def test_moe_refusals():
@@ -70,10 +97,9 @@ def test_moe_refusals():
     assert _moe(n=257) == UNSUPPORTED and _moe(n=256, k=17) == UNSUPPORTED and _moe(e=1025) == UNSUPPORTED
     assert _moe(dt=F32) == UNSUPPORTED and _moe(dt=9) == VALUE and _moe(ydt=9) == VALUE and _moe(ydt=BF16) == UNSUPPORTED
     assert _moe(ldx=63) == VALUE and _moe(ldy=63) == VALUE
-    for p in ("keys", "uc", "us", "dc", "ds", "x", "y", "ws"):
+    for p in ("keys", "up", "dn", "x", "y", "ws"):
         assert _moe(**{p: None}) == VALUE, p
-    assert _moe(uz=P) == VALUE and _moe(dz=P) == VALUE
-    assert _moe(uc=P + 8) == UNSUPPORTED and _moe(dc=P + 8) == UNSUPPORTED and _moe(ws=P + 8) == UNSUPPORTED
+    assert _moe(up=P + 8) == UNSUPPORTED and _moe(dn=P + 8) == UNSUPPORTED and _moe(ws=P + 8) == UNSUPPORTED
     assert _moe(wsb=S.moe_workspace_size(4, 2, 96) - 1) == VALUE
     assert b"workspace" in S.lib().spmv_last_error()
     assert _moe(dim=2 ** 31 - 1, ldx=2 ** 31, ldy=2 ** 31) == OVERFLOW
@@ -127,7 +153,7 @@ def test_binding_refuses_cpu_tensors_and_shapes():
     with pytest.raises(ValueError):
         S.Q4Matrix(4, 100, c, s, group=100)
     with pytest.raises(TypeError):
-        S.q4_matmul(4, 100, c, s, None, 1.0, x, 0.0, torch.zeros(2, 4))
+        S.q4_matmul(4, 100, c, 1.0, x, 0.0, torch.zeros(2, 4))
     with pytest.raises(TypeError):
         S.q4_quantize(torch.zeros(4, 100), c, s)
     with pytest.raises(TypeError):
