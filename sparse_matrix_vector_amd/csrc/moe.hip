@@ -101,10 +101,10 @@ __global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_expe
     __syncthreads();
     const int n = n_list;
     const int row0 = blockIdx.x * 16, quarter = lane / 16;
-    Q4Row<ZP, G> rows[2];
+    Q4Rows<ZP, G> rows[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
-        rows[r] = Q4Row<ZP, G>(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk, quarter);
+        rows[r] = Q4Rows<ZP, G>::any(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk);
     const int whole = dim / (Q4_BLOCK * U);
     for (int first = 0; first < n; first += 16) {
         const typename E::T *xr = x + (int64_t)(list[min(first + (lane & 15), n - 1)] / top_k) * ldx;
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
             n += __popcll(has);
         }
         __builtin_amdgcn_wave_barrier();
-        const Q4Row<ZP, G> row(tiles, (int64_t)e * dim + min(row0 + (lane & 15), dim - 1), n_blk, quarter);
+        const Q4Rows<ZP, G> row = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + (lane & 15), dim - 1), n_blk);
         for (int first = 0; first < n; first += 16) {
             const unsigned short *hr = h.p + (int64_t)list[min(first + (lane & 15), n - 1)] * h.ld + 8 * quarter;
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -1,10 +1,10 @@
 // Products with 4-bit weights on gfx950: y[t, :] = alpha * W x[t, :] + beta * y[t, :].
 //
-// Up to 16 tokens (k_q4_few) a wave owns 16 or 32 rows and every waves-th piece
-// of the columns, and a workgroup's waves add their sums through LDS: the codes
-// are read once and straight to registers, and the bound is HBM.  The
-// matrix cores serve one token as well as 16: the product of a fragment costs
-// the same, and decoding is what the vector unit does.
+// The codes go from memory straight to the registers that decode them, and the
+// matrix cores serve one token as well as 16: the product of a fragment costs the
+// same, and decoding is what the vector unit does.  Up to 4 tokens (k_q4_few) the
+// waves of a workgroup split the columns of 16 rows and the bound is HBM; more
+// (k_q4_tile) share tiles of x through LDS.
 #include "q4.hpp"
 
 #include <algorithm>
@@ -12,9 +12,11 @@
 namespace spmv {
 namespace {
 
-constexpr int QF_UNROLL = 4;         // blocks of a piece: 512 columns
-constexpr int QF_MAX_WAVES = 16;
-constexpr int QF_TOKENS = 16;
+constexpr int QF_UNROLL = 2;         // blocks of a wave's turn
+constexpr int QF_AHEAD = 1;          // turns whose codes are on their way
+constexpr int QF_WAVES = 8;
+constexpr int QF_TOKENS = 4;
+constexpr int QF_LDS = 65536;        // bytes of x at most
 
 template <class E>
 __device__ __forceinline__ void q4_store(void *y, bool f32, int64_t at, float v, float beta) {
@@ -27,81 +29,153 @@ __device__ __forceinline__ void q4_store(void *y, bool f32, int64_t at, float v,
     }
 }
 
-// The products of U blocks with one token tile, for RT row tiles.
-template <class E, bool ZP, int G, int U, int RT>
-__device__ __forceinline__ void q4_products(const Q4Piece<E, ZP, G, U> (&w)[RT], const u32x4 (&x)[U][4], f32x4 (&acc)[RT]) {
-    constexpr int GB = Q4_BLOCK / G, PG = G / 32;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int g = 0; g < GB; ++g) {
-                const typename Q4Op<E>::Zero nz = Q4Op<E>::zero(w[r].zero(u, g));
-                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int m = g * PG; m < (g + 1) * PG; ++m)
-                    sum = Q4Op<E>::mfma(x[u][m], Q4Op<E>::decode(w[r].c[u][m], nz), sum);
-                const float s = w[r].scale(u, g) * Q4Op<E>::UNIT;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(s, sum[i], acc[r][i]);
-            }
-}
-
-template <class E, bool ZP, int G, int RT>
-__global__ __launch_bounds__(64 * QF_MAX_WAVES) void k_q4_few(int n_rows, int n_cols, int n_blk,
-                                                              const char *__restrict__ tiles, int n_tok,
-                                                              float alpha, const typename E::T *__restrict__ x,
-                                                              int64_t ldx, float beta, void *__restrict__ y, bool f32,
-                                                              int64_t ldy) {
-    constexpr int U = QF_UNROLL;
-    extern __shared__ __attribute__((aligned(16))) f32x4 part[];      // [waves][RT][64]
+// Up to TP tokens: a workgroup owns 16 rows and keeps x whole in LDS (padded with
+// zeros to whole blocks); its waves take QF_UNROLL blocks in turn, whose codes are
+// loaded QF_AHEAD turns before they are used.
+template <class E, bool ZP, int G, int TP>
+__global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols, int n_blk,
+                                                              const char *__restrict__ tiles, int n_tok, float alpha,
+                                                              const typename E::T *__restrict__ x, int64_t ldx,
+                                                              float beta, void *__restrict__ y, bool f32, int64_t ldy) {
+    constexpr int U = QF_UNROLL, A = QF_AHEAD, GB = Q4_BLOCK / G, PG = G / 32;
+    extern __shared__ __attribute__((aligned(16))) u32x4 lds[];       // x [n_tok][ld], then the waves' sums
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
     const int quarter = lane / 16;
-    const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
-    Q4Row<ZP, G> rows[RT];
+    const int64_t row0 = (int64_t)blockIdx.x * 16;
+    const int ld = n_blk * 16 + 1;                  // 16-byte pieces of a token: the odd one spreads tokens over the banks
+    const Q4Rows<ZP, G> row(tiles, blockIdx.x, n_blk);
+    Q4Piece<E, ZP, G, 1> w[A + 1][U];
+    const int step = waves * U;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)                                 // rows past the end: not stored
-        rows[r] = Q4Row<ZP, G>(tiles, min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1), n_blk, quarter);
-    // tokens past the end take the last one's row: their sums are not stored
-    const typename E::T *xr = x + (int64_t)min(lane & 15, n_tok - 1) * ldx;
-    f32x4 acc[RT];
+    for (int a = 0; a < A; ++a)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int whole = n_cols / (Q4_BLOCK * U);                  // pieces without an end in them
-    for (int p = wv; p < whole; p += waves) {
-        const int b = p * U;
-        Q4Piece<E, ZP, G, U> w[RT];
-        u32x4 xv[U][4];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) w[r].load(rows[r], b);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                xv[u][m] = *reinterpret_cast<const u32x4_any *>(xr + (int64_t)(b + u) * Q4_BLOCK + 32 * m + 8 * quarter);
-        q4_products<E, ZP, G, U, RT>(w, xv, acc);
+        for (int u = 0; u < U; ++u) w[a][u].load(row, min(wv * U + a * step + u, n_blk - 1));
+    for (int i = threadIdx.x; i < n_tok * n_blk * 16; i += blockDim.x) {
+        const int t = TP == 1 ? 0 : i / (n_blk * 16), p = i - t * n_blk * 16;
+        lds[t * ld + p] = q4_token_piece(x + t * ldx, (int64_t)p * 8, n_cols);
     }
-    for (int b = whole * U + wv; b < n_blk; b += waves) {
-        Q4Piece<E, ZP, G, 1> w[RT];
-        u32x4 xv[1][4];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) w[r].load(rows[r], b);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-            xv[0][m] = q4_token_piece(xr, (int64_t)b * Q4_BLOCK + 32 * m + 8 * quarter, n_cols);
-        q4_products<E, ZP, G, 1, RT>(w, xv, acc);
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) part[(wv * RT + r) * 64 + lane] = acc[r];
     __syncthreads();
-    const float *sums = reinterpret_cast<const float *>(part);
-    for (int o = threadIdx.x; o < RT * 16 * n_tok; o += blockDim.x) {
-        const int row = o % (16 * RT), t = o / (16 * RT);
-        const int at = ((row / 16) * 64 + (t / 4) * 16 + row % 16) * 4 + t % 4;
+    // tokens past the end take the last one's row: their sums are not stored
+    const u32x4 *xr = lds + (TP == 1 ? 0 : min(lane & 15, n_tok - 1) * ld) + quarter;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b0 = wv * U; b0 < n_blk; b0 += (A + 1) * step) {
+#pragma unroll
+        for (int a = 0; a <= A; ++a) {
+            const int b = b0 + a * step;
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[(a + A) % (A + 1)][u].load(row, min(b + A * step + u, n_blk - 1));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (b + u >= n_blk) break;
+#pragma unroll
+                for (int g = 0; g < GB; ++g) {
+                    const typename Q4Op<E>::Zero nz = Q4Op<E>::zero(w[a][u].zero(0, g));
+                    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int m = g * PG; m < (g + 1) * PG; ++m)
+                        sum = Q4Op<E>::mfma(xr[(b + u) * 16 + 4 * m], Q4Op<E>::decode(w[a][u].c[0][m], nz), sum);
+                    const float s = w[a][u].scale(0, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, sum[i], acc[i]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds);
+    part[wv * 64 + lane] = acc;
+    __syncthreads();
+    const float *sums = reinterpret_cast<const float *>(lds);
+    for (int o = threadIdx.x; o < 16 * n_tok; o += blockDim.x) {
+        const int r = o % 16, t = o / 16, at = ((t / 4) * 16 + r) * 4 + t % 4;
         float v = 0.0f;
-        for (int w = 0; w < waves; ++w) v += sums[w * RT * 256 + at];
-        if (row0 + row < n_rows) q4_store<E>(y, f32, t * ldy + row0 + row, alpha * v, beta);
+        for (int k = 0; k < waves; ++k) v += sums[k * 256 + at];
+        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * v, beta);
+    }
+}
+
+// Up to 64 tokens of smaller weights: as above, for 16 TT tokens, but a wave brings x
+// block by block into LDS of its own (16-byte pieces exchanged within a row by the
+// token's number, so that 16 tokens' pieces lie in different banks): no waiting for
+// other waves before the sums at the end.
+template <class E, bool ZP, int G, int TT>
+__global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols, int n_blk,
+                                                          const char *__restrict__ tiles, int n_tok, float alpha,
+                                                          const typename E::T *__restrict__ x, int64_t ldx, float beta,
+                                                          void *__restrict__ y, bool f32, int64_t ldy) {
+    constexpr int PG = G / 32, TN = 16 * TT;
+    extern __shared__ __attribute__((aligned(16))) u32x4 lds[];       // [waves][TN][16], then the waves' sums
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    const int quarter = lane / 16;
+    const int64_t row0 = (int64_t)blockIdx.x * 16;
+    const Q4Rows<ZP, G> row(tiles, blockIdx.x, n_blk);
+    u32x4 *mine = lds + wv * TN * 16;
+    const int piece = lane % 16;
+    const typename E::T *xr[4 * TT];                 // tokens past the end take the last one's row
+#pragma unroll
+    for (int q = 0; q < 4 * TT; ++q) xr[q] = x + (int64_t)min(4 * q + quarter, n_tok - 1) * ldx;
+    auto load_x = [&](int b, u32x4 (&v)[4 * TT]) {
+        const int64_t at = (int64_t)b * Q4_BLOCK;
+        if (at + Q4_BLOCK <= n_cols) {
+#pragma unroll
+            for (int q = 0; q < 4 * TT; ++q) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at + piece * 8);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_piece(xr[q], at + piece * 8, n_cols);
+        }
+    };
+    f32x4 acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Q4Piece<E, ZP, G, 1> w[2];
+    u32x4 v[4 * TT];
+    load_x(min(wv, n_blk - 1), v);
+    w[0].load(row, min(wv, n_blk - 1));
+    for (int bb = wv; bb < n_blk; bb += 2 * waves) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int b = bb + a * waves;
+            if (b >= n_blk) break;
+#pragma unroll
+            for (int q = 0; q < 4 * TT; ++q) {
+                const int t = 4 * q + quarter;
+                mine[t * 16 + (piece ^ (t & 15))] = v[q];
+            }
+            load_x(min(b + waves, n_blk - 1), v);
+            w[1 - a].load(row, min(b + waves, n_blk - 1));
+            f32x4 sum[TT];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int g = m / PG;
+                u32x4 xv[TT];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) xv[t] = mine[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
+                const u32x4 f = Q4Op<E>::decode(w[a].c[0][m], Q4Op<E>::zero(w[a].zero(0, g)));
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    sum[t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[t]);
+                if ((m + 1) % PG == 0) {
+                    const float sc = w[a].scale(0, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(sc, sum[t][i], acc[t][i]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) part[(wv * TT + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    const float *sums = reinterpret_cast<const float *>(lds);
+    for (int o = threadIdx.x; o < 16 * n_tok; o += blockDim.x) {
+        const int r = o % 16, t = o / 16;
+        const int at = (t / 16 * 64 + (t % 16 / 4) * 16 + r) * 4 + t % 4;
+        float s = 0.0f;
+        for (int k = 0; k < waves; ++k) s += sums[k * TT * 256 + at];
+        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * s, beta);
     }
 }
 
@@ -117,7 +191,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                                                     const typename E::T *__restrict__ x, int64_t ldx, float beta,
                                                     void *__restrict__ y, bool f32, int64_t ldy,
                                                     float *__restrict__ parts) {
-    constexpr int GB = Q4_BLOCK / G, PG = G / 32, TN = 16 * TT;
+    constexpr int PG = G / 32, TN = 16 * TT, A = RT == 4 || (G == 32 && TT == 4) ? 1 : 2;
     __shared__ u32x4 xt[2][TN * 16];
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
     // neighbouring workgroups run on different XCDs; every 8th one shares a row tile, whose codes one L2 then holds
@@ -127,10 +201,10 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     const int64_t row0 = ((int64_t)row_tile * 4 + wv) * (16 * RT);
     const int t0 = tok_tile * TN;
     const int b0 = (int)((int64_t)n_blk * blockIdx.y / split), b1 = (int)((int64_t)n_blk * (blockIdx.y + 1) / split);
-    Q4Row<ZP, G> rows[RT];
+    Q4Rows<ZP, G> rows[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-        rows[r] = Q4Row<ZP, G>(tiles, min(row0 + 16 * r + (lane & 15), (int64_t)n_rows - 1), n_blk, quarter);
+    for (int r = 0; r < RT; ++r)                     // tiles past the end: not stored
+        rows[r] = Q4Rows<ZP, G>(tiles, min(row0 / 16 + r, (int64_t)(n_rows - 1) / 16), n_blk);
     const typename E::T *xr[TT];
     int slot[TT];
 #pragma unroll
@@ -150,11 +224,13 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
             for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q] - piece, at + piece, n_cols);
         }
     };
-    Q4Piece<E, ZP, G, 1> w[RT];
+    Q4Piece<E, ZP, G, 1> w[A + 1][RT];
     u32x4 v[TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) w[r].load(rows[r], b0);
     load_x(b0, v);
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[a][r].load(rows[r], min(b0 + a, b1 - 1));
 #pragma unroll
     for (int q = 0; q < TT; ++q) xt[0][slot[q]] = v[q];
     f32x4 acc[RT][TT];
@@ -163,43 +239,48 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    for (int b = b0; b < b1; ++b) {
-        const u32x4 *now = xt[(b - b0) & 1];
-        const int next = min(b + 1, b1 - 1);
-        Q4Piece<E, ZP, G, 1> wn[RT];
+    for (int bb = b0; bb < b1; bb += A + 1) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) wn[r].load(rows[r], next);
-        load_x(next, v);
+        for (int a = 0; a <= A; ++a) {
+            const int b = bb + a;
+            if (b >= b1) break;
+            const u32x4 *now = xt[(b - b0) & 1];
+            // x first: what waits for it does not wait for the codes behind it
+            load_x(min(b + 1, b1 - 1), v);
 #pragma unroll
-        for (int g = 0; g < GB; ++g) {
+            for (int r = 0; r < RT; ++r) w[(a + A) % (A + 1)][r].load(rows[r], min(b + A, b1 - 1));
+            __builtin_amdgcn_sched_barrier(0);
             f32x4 sum[RT][TT];
 #pragma unroll
-            for (int m = g * PG; m < (g + 1) * PG; ++m) {
+            for (int m = 0; m < 4; ++m) {
+                const int g = m / PG;
                 u32x4 xv[TT];
 #pragma unroll
                 for (int t = 0; t < TT; ++t) xv[t] = now[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const u32x4 f = Q4Op<E>::decode(w[r].c[0][m], Q4Op<E>::zero(w[r].zero(0, g)));
+                    const u32x4 f = Q4Op<E>::decode(w[a][r].c[0][m], Q4Op<E>::zero(w[a][r].zero(0, g)));
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
-                        sum[r][t] = Q4Op<E>::mfma(xv[t], f, m == g * PG ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
+                        sum[r][t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
                 }
+                if ((m + 1) % PG == 0) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const float sc = w[a][r].scale(0, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+                    }
+                }
+                // keeps the fragments of one product in registers at a time
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const float sc = w[r].scale(0, g) * Q4Op<E>::UNIT;
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
-            }
+            for (int q = 0; q < TT; ++q) xt[(b - b0 + 1) & 1][slot[q]] = v[q];
+            __syncthreads();
         }
-#pragma unroll
-        for (int q = 0; q < TT; ++q) xt[(b - b0 + 1) & 1][slot[q]] = v[q];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) w[r] = wn[r];
-        __syncthreads();
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -327,22 +408,45 @@ spmv_status by_weight(int32_t dtype, bool zp, int32_t group, F f) {
 struct Tiling {
     int rt, tt, row_tiles, tok_tiles, split;
 };
-constexpr int QT_GROUPS = 512;       // workgroups wanted: two on each CU
 constexpr int QT_MIN_BLOCKS = 4;     // blocks of columns of a part at least
-Tiling tiling(int64_t n_rows, int64_t n_cols, int64_t n_tok) {
+Tiling tiling(int64_t n_rows, int64_t n_cols, int64_t n_tok, bool wide) {
     Tiling t;
-    t.tt = n_tok <= 32 ? 2 : 4;
-    t.rt = n_tok <= 64 ? 2 : 4;
+    t.tt = (int)std::min<int64_t>(4, ceil_div(n_tok, 16));
+    // 64 rows of a wave share a fragment of x, where their sums fit the registers: 513
+    // tokens of 12288 x 12288 206 us against 230 with 32 rows (groups of 128); 1300
+    // against 295 with groups of 32 and zero points, whose code needs more registers
+    t.rt = n_tok > 64 && wide ? 4 : 2;
     t.row_tiles = (int)ceil_div(n_rows, 64 * t.rt);
     t.tok_tiles = (int)ceil_div(n_tok, 16 * t.tt);
-    const int64_t tiles = (int64_t)t.row_tiles * t.tok_tiles;
-    t.split = (int)std::max<int64_t>(1, std::min(QT_GROUPS / tiles, q4_blocks(n_cols) / QT_MIN_BLOCKS));
+    // as many workgroups as run at once: 48 tokens of 12288 x 12288 40 us with 768 (3 per CU), 47 with 512, 48 with 1024
+    const int64_t tiles = (int64_t)t.row_tiles * t.tok_tiles, groups = t.rt == 4 || t.tt == 4 ? 512 : 768;
+    t.split = (int)std::max<int64_t>(1, std::min(groups / tiles, q4_blocks(n_cols) / QT_MIN_BLOCKS));
     return t;
 }
+// bytes of LDS of k_q4_few
+size_t few_lds(int64_t n_cols, int64_t n_tok, int waves) {
+    return std::max<size_t>((size_t)n_tok * (q4_blocks(n_cols) * 16 + 1) * 16, (size_t)waves * 1024);
+}
+bool few(int64_t n_cols, int64_t n_tok) {
+    return n_tok <= QF_TOKENS && few_lds(n_cols, n_tok, 0) <= QF_LDS;
+}
+// Whether k_q4_mid takes the product: every 16 rows read x again, which costs less
+// than a second launch up to about 160 MB (f16, groups of 128: 4096 x 4096, 16
+// tokens, 34 MB, 6.3 us against 10.1 by tiles; 48 tokens, 134 MB, 11.5 against 14.9;
+// 12288 x 12288, 16 tokens, 302 MB, 31 against 24).
+constexpr int64_t QM_BYTES = 160000000;
+bool mid(int64_t n_rows, int64_t n_cols, int64_t n_tok) {
+    return n_tok <= 64 && ceil_div(n_rows, 16) * (ceil_div(n_tok, 16) * 16) * n_cols * 2 <= QM_BYTES;
+}
 size_t split_bytes(int64_t n_rows, int64_t n_cols, int64_t n_tok) {
-    if (n_tok <= QF_TOKENS || n_rows == 0 || n_cols == 0) return 0;
-    const Tiling t = tiling(n_rows, n_cols, n_tok);
-    return t.split > 1 ? (size_t)t.split * n_tok * n_rows * 4 : 0;
+    if (n_rows == 0 || n_cols == 0 || few(n_cols, n_tok) || mid(n_rows, n_cols, n_tok)) return 0;
+    // the larger of both tilings: the size does not depend on the group
+    size_t most = 0;
+    for (const bool wide : {false, true}) {
+        const Tiling t = tiling(n_rows, n_cols, n_tok, wide);
+        if (t.split > 1) most = std::max(most, (size_t)t.split * n_tok * n_rows * 4);
+    }
+    return most;
 }
 
 }  // namespace
@@ -417,11 +521,11 @@ extern "C" spmv_status q4_tiles(int32_t n_rows, int32_t n_cols, int32_t group, c
 extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes) {
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
     if (n_rows < 0 || n_cols < 0 || n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
-    // the most that any batch of up to n_tok tokens needs: full tiles of 32, then of 64 tokens, while there is a split
+    // the most that any batch of up to n_tok tokens needs: full tiles of tokens, as long as there is a split
     size_t most = split_bytes(n_rows, n_cols, n_tok);
-    for (int64_t t = 32; t < n_tok; t += t < 64 ? 32 : 64) {
+    for (int64_t t = QF_TOKENS; t < n_tok; t = t < 16 ? 16 : t < 64 ? t + 16 : t + 64) {
         const size_t b = split_bytes(n_rows, n_cols, t);
-        if (b == 0) break;
+        if (b == 0 && t > 64) break;
         most = std::max(most, b);
     }
     *bytes = most;
@@ -453,19 +557,51 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         return SPMV_OK;
     }
     const int n_blk = (int)q4_blocks(n_cols);
-    if (n_tok <= QF_TOKENS)
+    if (few(n_cols, n_tok))
         return by_weight(dtype, with_zeros != 0, group, [&](auto e, auto zp, auto g) -> spmv_status {
             typedef decltype(e) E;
             typedef typename E::T T;
             constexpr bool ZP = decltype(zp)::value;
-            constexpr int G = decltype(g)::value, RT = 2;
-            const int waves = (int)std::min<int64_t>(8, ceil_div(n_blk, QF_UNROLL));
-            k_q4_few<E, ZP, G, RT><<<(int)ceil_div(n_rows, 16 * RT), 64 * waves, (size_t)waves * RT * 1024, s>>>(
-                n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n_tok, alpha, static_cast<const T *>(x), ldx, beta, y, f32, ldy);
+            constexpr int G = decltype(g)::value;
+            const int waves = (int)std::min<int64_t>(QF_WAVES, ceil_div(n_blk, QF_UNROLL));
+            auto run = [&](auto tp) {
+                k_q4_few<E, ZP, G, decltype(tp)::value>
+                    <<<(int)ceil_div(n_rows, 16), 64 * waves, few_lds(n_cols, n_tok, waves), s>>>(
+                        n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n_tok, alpha, static_cast<const T *>(x),
+                        ldx, beta, y, f32, ldy);
+            };
+            if (n_tok == 1)
+                run(std::integral_constant<int, 1>{});
+            else
+                run(std::integral_constant<int, QF_TOKENS>{});
             SPMV_LAUNCHED("k_q4_few");
             return SPMV_OK;
         });
-    const Tiling t = tiling(n_rows, n_cols, n_tok);
+    if (mid(n_rows, n_cols, n_tok))
+        return by_weight(dtype, with_zeros != 0, group, [&](auto e, auto zp, auto g) -> spmv_status {
+            typedef decltype(e) E;
+            typedef typename E::T T;
+            constexpr bool ZP = decltype(zp)::value;
+            constexpr int G = decltype(g)::value;
+            const int waves = (int)std::min<int64_t>(QF_WAVES, n_blk);
+            auto run = [&](auto tt) {
+                constexpr int TT = decltype(tt)::value;
+                k_q4_mid<E, ZP, G, TT><<<(int)ceil_div(n_rows, 16), 64 * waves, (size_t)waves * TT * 4096, s>>>(
+                    n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n_tok, alpha, static_cast<const T *>(x), ldx,
+                    beta, y, f32, ldy);
+            };
+            if (n_tok <= 16)
+                run(std::integral_constant<int, 1>{});
+            else if (n_tok <= 32)
+                run(std::integral_constant<int, 2>{});
+            else if (n_tok <= 48)
+                run(std::integral_constant<int, 3>{});
+            else
+                run(std::integral_constant<int, 4>{});
+            SPMV_LAUNCHED("k_q4_mid");
+            return SPMV_OK;
+        });
+    const Tiling t = tiling(n_rows, n_cols, n_tok, group == 128 && !with_zeros);
     const size_t need = split_bytes(n_rows, n_cols, n_tok);
     if (need && !workspace) return fail(SPMV_ERR_INVALID_VALUE, "workspace is NULL (q4_workspace_size gives its size)");
     if (workspace_bytes < need)
@@ -486,12 +622,16 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         };
         const std::integral_constant<int, 2> two;
         const std::integral_constant<int, 4> four;
-        if (t.rt == 4)
-            run(four, four);
-        else if (t.tt == 4)
+        if (t.rt == 4) {
+            if constexpr (G == 128 && !ZP) run(four, four);
+        } else if (t.tt == 4)
             run(two, four);
-        else
+        else if (t.tt == 3)
+            run(two, std::integral_constant<int, 3>{});
+        else if (t.tt == 2)
             run(two, two);
+        else
+            run(two, std::integral_constant<int, 1>{});
         SPMV_LAUNCHED("k_q4_tile");
         return SPMV_OK;
     });

@@ -116,17 +116,20 @@ struct Q4Rec {
     static constexpr int SIZE = ZEROS + (ZP ? 16 * GB : 0);
 };
 
-// A lane's place in the records of one row.
+// A lane's place in the records of a row: of the 16 rows of a tile (the same base
+// for all lanes, kept in scalar registers) or, tile by tile, of any row.
 template <bool ZP, int G>
-struct Q4Row {
-    const char *codes, *scales, *zeros;
-    __device__ __forceinline__ Q4Row() {}
-    __device__ __forceinline__ Q4Row(const char *tiles, int64_t row, int n_blk, int quarter) {
-        const int r = (int)(row & 15);
-        const char *rec = tiles + (row >> 4) * n_blk * Q4Rec<ZP, G>::SIZE;
-        codes = rec + (quarter * 16 + r) * 16;
-        scales = rec + Q4_SCALES + r * 2 * Q4Rec<ZP, G>::GB;
-        zeros = rec + Q4Rec<ZP, G>::ZEROS + r * Q4Rec<ZP, G>::GB;
+struct Q4Rows {
+    const char *base;
+    int lane, row;
+    __device__ __forceinline__ Q4Rows() {}
+    __device__ __forceinline__ Q4Rows(const char *tiles, int64_t tile, int n_blk)
+        : base(tiles + tile * n_blk * Q4Rec<ZP, G>::SIZE), lane(__lane_id()), row(__lane_id() & 15) {}
+    static __device__ __forceinline__ Q4Rows any(const char *tiles, int64_t r, int n_blk) {
+        Q4Rows q(tiles, r >> 4, n_blk);
+        q.row = (int)(r & 15);
+        q.lane = (__lane_id() & 48) + q.row;
+        return q;
     }
 };
 
@@ -140,14 +143,14 @@ struct Q4Piece {
     Vec<E, GB> s[U];
     Bytes<ZP ? GB : 1> z[U];
 
-    __device__ __forceinline__ void load(const Q4Row<ZP, G> &row, int b) {
-        constexpr int SIZE = Q4Rec<ZP, G>::SIZE;
-        const int64_t at = (int64_t)b * SIZE;
+    __device__ __forceinline__ void load(const Q4Rows<ZP, G> &rows, int b) {
+        typedef Q4Rec<ZP, G> Rec;
+        const char *rec = rows.base + (int64_t)b * Rec::SIZE;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row.codes + at + u * SIZE));
-            s[u] = load_vec<E, GB>(reinterpret_cast<const T *>(row.scales + at + u * SIZE));
-            if constexpr (ZP) z[u] = load_bytes<GB>(row.zeros + at + u * SIZE);
+            c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(rec + u * Rec::SIZE) + rows.lane);
+            s[u] = *(reinterpret_cast<const Vec<E, GB> *>(rec + u * Rec::SIZE + Q4_SCALES) + rows.row);
+            if constexpr (ZP) z[u] = load_bytes<GB>(rec + u * Rec::SIZE + Rec::ZEROS + rows.row * GB);
         }
     }
     __device__ __forceinline__ float scale(int u, int g) const { return (float)s[u].v[g]; }

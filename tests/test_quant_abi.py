@@ -64,9 +64,9 @@ def test_matmul_refusals():
     for k in ("tiles", "x", "y"):
         assert _matmul(**{k: None}) == VALUE, k
     assert _matmul(tiles=P + 8) == UNSUPPORTED
-    need = S.q4_workspace_size(64, 12288, 48)
+    need = S.q4_workspace_size(2048, 12288, 64)
     assert need > 0
-    big = dict(rows=64, cols=12288, ldx=12288, ldy=64, n=48)
+    big = dict(rows=2048, cols=12288, ldx=12288, ldy=2048, n=64)
     assert _matmul(**big) == VALUE and b"workspace" in S.lib().spmv_last_error()
     assert _matmul(ws=P, wsb=need - 1, **big) == VALUE and _matmul(ws=P + 8, wsb=need, **big) == UNSUPPORTED
     assert _matmul(rows=0, y=None) == OK and _matmul(n=0, x=None, y=None) == OK
@@ -77,7 +77,7 @@ def test_matmul_refusals():
 
 
 def test_matmul_workspace_serves_fewer_tokens():
-    for rows, cols in ((64, 12288), (256, 4096), (4096, 4096), (12288, 128)):
+    for rows, cols in ((64, 12288), (2048, 12288), (256, 4096), (4096, 4096), (12288, 128)):
         sizes = [S.q4_workspace_size(rows, cols, n) for n in range(0, 700)]
         assert sizes == sorted(sizes) and sizes[0] == 0
 
