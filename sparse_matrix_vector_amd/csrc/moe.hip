@@ -4,19 +4,23 @@
 // with the weights of token t's c-th expert.  The bound is reading each used
 // expert's weights once.
 //
-// Up (k_moe_up): a workgroup owns 16 gate rows and the same 16 up rows of one
-// expert and finds the expert's tokens among the keys itself: no sort comes
-// before it.  Where there are fewer slots than experts the grid counts slots,
-// and the first slot of an expert does its work.
-// Down (k_moe_down): a workgroup owns 16 rows of y for all experts; its waves
-// take an expert (or a part of its columns) each, add the weighted results to
-// sums of their own in LDS, and these are added in order at the end: no
-// atomics, the same bits on every call.
+// Up (k_moe_up): a wave owns 16 gate rows and the same 16 up rows of one expert, or
+// a part of their columns, and the workgroup finds the expert's tokens among the
+// keys itself: no sort comes before it.  Where there are fewer slots than experts
+// the grid counts slots, and the first slot of an expert does its work.
+// Down (k_moe_down): a workgroup owns 16 (or 8) rows of y for all experts; its waves
+// take an expert, or a part of its columns, each, add the weighted results to sums
+// of their own in LDS, and these are added in order at the end: no atomics on
+// results, the same bits on every call.
 //
 // h is kept as three bf16 numbers whose sum has all of fp32's 24 bits (cut, not
 // rounded, so that the largest numbers stay finite): the down product is
 // three products of the same fragment, and it is the decoding and the weights'
-// bytes that cost.
+// bytes that cost.  It lies in the order in which the down product reads it: an
+// expert's tokens (its entries) behind those of smaller experts, 16 at a time, and in
+// such a tile of n entries [block][part][8 columns][entry], so that a fragment is
+// one run of 64 n bytes.  (With a row per slot, 16 lanes touch 16 cache lines: 125 M
+// accesses and 294 us for 200 tokens and 24 experts of 4096 x 1500.)
 #include "q4.hpp"
 
 #include <algorithm>
@@ -27,13 +31,15 @@ namespace {
 constexpr int ME_MAX_TOK = 256;
 constexpr int ME_MAX_SLOTS = 4096;
 constexpr int ME_MAX_EXPERTS = 1024;
-constexpr int ME_UNROLL = 4;
+constexpr size_t ME_LDS = 160 * 1024 - 64;
+constexpr int ME_UP_WAVES = 4;
+constexpr int ME_UNROLL = 2;         // blocks whose codes a wave of the down product loads at once
+constexpr int ME_UNITS = 2;          // units of a wave of the down product, about
 
-// h as three bf16 planes [slot][h_ld]
-struct Hidden {
-    unsigned short *p;
-    int64_t ld, plane;
-};
+// Where the tile of entries first .. first + n - 1 of all entries begins, and a
+// piece of 8 columns in it (in 16-bit numbers).
+__device__ __forceinline__ int64_t hidden_tile(int first, int n_blk) { return (int64_t)first * n_blk * (Q4_BLOCK * 3); }
+__device__ __forceinline__ int hidden_piece(int b, int part, int piece, int n) { return ((b * 3 + part) * 16 + piece) * n * 8; }
 
 // v = a + b + c with 8 bits each; an infinity or NaN is whole in the first.
 __device__ __forceinline__ void split3(float v, unsigned short (&o)[3]) {
@@ -47,181 +53,246 @@ __device__ __forceinline__ void split3(float v, unsigned short (&o)[3]) {
     o[2] = (unsigned short)(__float_as_uint(r - __uint_as_float(b)) >> 16);
 }
 
-template <class E, bool ZP, int G, int U, int RT>
-__device__ __forceinline__ void up_products(const Q4Piece<E, ZP, G, U> (&w)[RT], const u32x4 (&x)[U][4], f32x4 (&acc)[RT]) {
-    constexpr int GB = Q4_BLOCK / G, PG = G / 32;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int g = 0; g < GB; ++g) {
-                const typename Q4Op<E>::Zero nz = Q4Op<E>::zero(w[r].zero(u, g));
-                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int m = g * PG; m < (g + 1) * PG; ++m)
-                    sum = Q4Op<E>::mfma(x[u][m], Q4Op<E>::decode(w[r].c[u][m], nz), sum);
-                const float s = w[r].scale(u, g) * Q4Op<E>::UNIT;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(s, sum[i], acc[r][i]);
-            }
-}
-
-template <class E, bool ZP, int G>
-__global__ __launch_bounds__(512) void k_moe_up(int n_tok, int top_k, int n_experts, int dim, int inter, int n_blk,
-                                                bool by_slot, const int *__restrict__ keys,
-                                                const char *__restrict__ tiles,
-                                                const typename E::T *__restrict__ x, int64_t ldx, Hidden h) {
-    constexpr int U = ME_UNROLL;
-    extern __shared__ __attribute__((aligned(16))) f32x4 part[];       // [waves][2][64]
-    __shared__ unsigned short list[ME_MAX_TOK];                        // slots of the expert, one per token
-    __shared__ int n_list;
-    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+template <class E, bool ZP, int G, int TT>
+__global__ __launch_bounds__(64 * ME_UP_WAVES) void k_moe_up(int n_tok, int top_k, int n_experts, int dim, int inter,
+                                                             int n_blk, int h_blk, int parts, bool by_slot,
+                                                             const int *__restrict__ keys,
+                                                             const char *__restrict__ tiles,
+                                                             const typename E::T *__restrict__ x, int64_t ldx,
+                                                             unsigned short *__restrict__ h) {
+    constexpr int PG = G / 32, TN = 16 * TT, W = ME_UP_WAVES;
+    __shared__ u32x4 xt[W][TN * 16];                                   // a wave's block of x, then its sums
+    __shared__ unsigned short list[ME_MAX_TOK];                        // tokens of the expert
+    __shared__ int n_list, below[W], equal[W];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
+    const int slots = n_tok * top_k;
     int e = blockIdx.y;
     if (by_slot) {
         const int s = blockIdx.y;
         e = keys[s];
         int before = 0;
-        for (int i = threadIdx.x; i < s; i += blockDim.x) before |= keys[i] == e;
+        for (int i = threadIdx.x; i < s; i += 64 * W) before |= keys[i] == e;
         if (__syncthreads_or(before) || (unsigned)e >= (unsigned)n_experts) return;
     }
+    int lo = 0, eq = 0;                                                // choices of smaller experts, and of this one
+    for (int i0 = wv * 64; i0 < slots; i0 += 64 * W) {
+        const int k = i0 + lane < slots ? keys[i0 + lane] : -1;
+        lo += __popcll(__ballot(k >= 0 && k < e));
+        eq += __popcll(__ballot(k == e));
+    }
+    if (lane == 0) below[wv] = lo, equal[wv] = eq;
     if (wv == 0) {
         int n = 0;
         for (int t0 = 0; t0 < n_tok; t0 += 64) {
             const int t = t0 + lane;
-            int c = top_k;
+            bool mine = false;
             if (t < n_tok)
-                for (c = 0; c < top_k && keys[t * top_k + c] != e; ++c) {}
-            const unsigned long long has = __ballot(t < n_tok && c < top_k);
-            if (t < n_tok && c < top_k) list[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)(t * top_k + c);
+                for (int c = 0; c < top_k; ++c) mine |= keys[t * top_k + c] == e;
+            const unsigned long long has = __ballot(mine);
+            if (mine) list[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)t;
             n += __popcll(has);
         }
         if (lane == 0) n_list = n;
     }
     __syncthreads();
-    const int n = n_list;
-    const int row0 = blockIdx.x * 16, quarter = lane / 16;
+    const int n = __builtin_amdgcn_readfirstlane(n_list);
+    if (n == 0) return;
+    int base = 0, room = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) base += below[w], room += equal[w];
+
+    const int part = wv % parts, row0 = ((int)blockIdx.x * (W / parts) + wv / parts) * 16;
     Q4Rows<ZP, G> rows[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
         rows[r] = Q4Rows<ZP, G>::any(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk);
-    const int whole = dim / (Q4_BLOCK * U);
-    for (int first = 0; first < n; first += 16) {
-        const typename E::T *xr = x + (int64_t)(list[min(first + (lane & 15), n - 1)] / top_k) * ldx;
-        f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        for (int p = wv; p < whole; p += waves) {
-            const int b = p * U;
-            Q4Piece<E, ZP, G, U> w[2];
-            u32x4 xv[U][4];
+    u32x4 *mine = xt[wv];
+    const int piece = lane % 16;
+    for (int first = 0; first < n; first += TN) {
+        const int here = min(TN, n - first);                           // entries of this turn
+        const typename E::T *xr[4 * TT];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[r].load(rows[r], b);
+        for (int q = 0; q < 4 * TT; ++q) xr[q] = x + (int64_t)list[min(first + 4 * q + quarter, n - 1)] * ldx;
+        // only entries that there are; the others' sums are not stored
+        auto load_x = [&](int b, u32x4 (&v)[4 * TT]) {
+            const int64_t at = (int64_t)b * Q4_BLOCK;
+            if (at + Q4_BLOCK <= dim) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int q = 0; q < 4 * TT; ++q)
+                    if (4 * q < here) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at + piece * 8);
+            } else {
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    xv[u][m] = *reinterpret_cast<const u32x4_any *>(xr + (int64_t)(b + u) * Q4_BLOCK + 32 * m + 8 * quarter);
-            up_products<E, ZP, G, U, 2>(w, xv, acc);
-        }
-        for (int b = whole * U + wv; b < n_blk; b += waves) {
-            Q4Piece<E, ZP, G, 1> w[2];
-            u32x4 xv[1][4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) w[r].load(rows[r], b);
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                xv[0][m] = q4_token_piece(xr, (int64_t)b * Q4_BLOCK + 32 * m + 8 * quarter, dim);
-            up_products<E, ZP, G, 1, 2>(w, xv, acc);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) part[(wv * 2 + r) * 64 + lane] = acc[r];
-        __syncthreads();
-        const float *sums = reinterpret_cast<const float *>(part);
-        for (int o = threadIdx.x; o < 16 * min(16, n - first); o += blockDim.x) {
-            const int row = o % 16, t = o / 16;
-            const int at = ((t / 4) * 16 + row) * 4 + t % 4;
-            float gate = 0.0f, up = 0.0f;
-            for (int w = 0; w < waves; ++w) {
-                gate += sums[w * 512 + at];
-                up += sums[w * 512 + 256 + at];
+                for (int q = 0; q < 4 * TT; ++q)
+                    if (4 * q < here) v[q] = q4_token_piece(xr[q], at + piece * 8, dim);
             }
-            unsigned short v[3] = {0, 0, 0};                            // columns past inter are zeros
-            if (row0 + row < inter) split3(gate / (1.0f + expf(-gate)) * up, v);
+        };
+        f32x4 acc[2][TT];
 #pragma unroll
-            for (int i = 0; i < 3; ++i) h.p[i * h.plane + list[first + t] * h.ld + row0 + row] = v[i];
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        Q4Piece<E, ZP, G, 1> w[2][2];
+        u32x4 v[4 * TT];
+#pragma unroll
+        for (int q = 0; q < 4 * TT; ++q) v[q] = u32x4{0u, 0u, 0u, 0u};
+        load_x(min(part, n_blk - 1), v);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], min(part, n_blk - 1));
+        for (int bb = part; bb < n_blk; bb += 2 * parts) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int b = bb + a * parts;
+                if (b >= n_blk) break;
+#pragma unroll
+                for (int q = 0; q < 4 * TT; ++q) {
+                    const int t = 4 * q + quarter;
+                    if (4 * q < here) mine[t * 16 + (piece ^ (t & 15))] = v[q];
+                }
+                load_x(min(b + parts, n_blk - 1), v);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + parts, n_blk - 1));
+                f32x4 sum[2][TT];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int g = m / PG;
+                    u32x4 xv[TT];
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) xv[t] = mine[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const u32x4 f = Q4Op<E>::decode(w[a][r].c[0][m], Q4Op<E>::zero(w[a][r].zero(0, g)));
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+                            sum[r][t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
+                    }
+                    if ((m + 1) % PG == 0) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float sc = w[a][r].scale(0, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+                        }
+                    }
+                }
+            }
+        }
+        f32x4 *sums = reinterpret_cast<f32x4 *>(mine);                 // [2][TT][64] of the wave's 4 TT KB
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) sums[(r * TT + t) * 64 + lane] = acc[r][t];
+        __syncthreads();
+        if (part == 0) {                                               // the wave of the first columns adds the others'
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                f32x4 gate = acc[0][t], up = acc[1][t];
+                for (int p = 1; p < parts; ++p) {
+                    const f32x4 *other = reinterpret_cast<const f32x4 *>(xt[wv + p]);
+                    gate += other[t * 64 + lane];
+                    up += other[(TT + t) * 64 + lane];
+                }
+                const int row = row0 + (lane & 15);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 16 * t + 4 * quarter + i;
+                    if (at >= here || row >= h_blk * Q4_BLOCK) continue;
+                    unsigned short o[3] = {0, 0, 0};                    // columns past inter are zeros
+                    if (row < inter) split3(gate[i] / (1.0f + expf(-gate[i])) * up[i], o);
+                    const int tile = (first + at) / 16 * 16, in = min(16, room - tile);
+                    unsigned short *d = h + hidden_tile(base + tile, h_blk) + (first + at - tile) * 8 + row % 8;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        d[hidden_piece(row / Q4_BLOCK, k, row % Q4_BLOCK / 8, in)] = o[k];
+                }
+            }
         }
         __syncthreads();
     }
 }
 
 template <class E, bool ZP, int G>
-__global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_experts, int dim, int n_blk,
+__global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_experts, int dim, int rows, int n_blk,
                                                    const int *__restrict__ keys, const float *__restrict__ weights,
-                                                   const char *__restrict__ tiles, Hidden h,
-                                                   void *__restrict__ y, bool f32, int64_t ldy) {
+                                                   const char *__restrict__ tiles,
+                                                   const unsigned short *__restrict__ h, void *__restrict__ y, bool f32,
+                                                   int64_t ldy) {
     constexpr int GB = Q4_BLOCK / G, PG = G / 32, U = ME_UNROLL;
     typedef Q4Op<BF16> Op;
     extern __shared__ __attribute__((aligned(16))) float sums[];        // [waves][n_tok][16], then what follows
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
     const int quarter = lane / 16, slots = n_tok * top_k;
     float *mine = sums + (size_t)wv * n_tok * 16;
-    int *mark = reinterpret_cast<int *>(sums + (size_t)waves * n_tok * 16);     // first slot of each expert
-    float *share = reinterpret_cast<float *>(mark + n_experts) + wv * n_tok;   // the wave's list: weight ..
-    short *key = reinterpret_cast<short *>(reinterpret_cast<float *>(mark + n_experts) + waves * n_tok);
-    unsigned short *list = reinterpret_cast<unsigned short *>(key + slots) + wv * n_tok;   // .. and slot
-    unsigned short *active = reinterpret_cast<unsigned short *>(key + slots) + waves * n_tok;
+    float *share = sums + (size_t)waves * n_tok * 16;                   // an entry's weight [slots] ..
+    int *first_of = reinterpret_cast<int *>(share + slots);             // entries of smaller experts [n_experts + 1]
+    short *key = reinterpret_cast<short *>(first_of + n_experts + 1);   // [slots]
+    unsigned short *list = reinterpret_cast<unsigned short *>(key + slots);   // .. and its token [slots]
+    unsigned short *active = list + slots, *count = active + min(slots, n_experts);
     __shared__ int n_active;
-    for (int i = threadIdx.x; i < n_experts; i += blockDim.x) mark[i] = slots;
+    for (int i = threadIdx.x; i <= n_experts; i += blockDim.x) first_of[i] = 0;
     for (int i = threadIdx.x; i < waves * n_tok * 16; i += blockDim.x) sums[i] = 0.0f;
     __syncthreads();
     for (int i = threadIdx.x; i < slots; i += blockDim.x) {
         const int e = keys[i];
         const bool in = (unsigned)e < (unsigned)n_experts;
         key[i] = (short)(in ? e : -1);
-        if (in) atomicMin(&mark[e], i);
+        if (in) atomicAdd(&first_of[e], 1);
     }
     __syncthreads();
-    if (wv == 0) {                                                      // the experts in the order of their first slots
-        int n = 0;
-        for (int s0 = 0; s0 < slots; s0 += 64) {
-            const int s = s0 + lane, e = s < slots ? key[s] : -1;
-            const bool first = e >= 0 && mark[e] == s;
-            const unsigned long long has = __ballot(first);
-            if (first) active[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)e;
+    if (wv == 0) {
+        int n = 0, before = 0;
+        for (int e0 = 0; e0 < n_experts; e0 += 64) {
+            const int e = e0 + lane, c = e < n_experts ? first_of[e] : 0;
+            const unsigned long long has = __ballot(c > 0);
+            if (c > 0) active[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)e;
             n += __popcll(has);
+            const int incl = wave_inclusive_scan(c);
+            if (e < n_experts) first_of[e] = before + incl - c;
+            before += __builtin_amdgcn_readlane(incl, 63);
         }
-        if (lane == 0) n_active = n;
+        if (lane == 0) first_of[n_experts] = before, n_active = n;
     }
     __syncthreads();
     const int na = n_active;
-    // with fewer experts than waves, several waves share an expert's columns
-    const int pieces = (n_blk + U - 1) / U;
-    const int split = na > 0 ? min(pieces, max(1, (waves + na - 1) / na)) : 1;
-    const int row0 = blockIdx.x * 16;
-    for (int unit = wv; unit < na * split; unit += waves) {
-        const int e = __builtin_amdgcn_readfirstlane(active[unit / split]), k0 = unit % split;
+    for (int a = wv; a < na; a += waves) {
+        const int e = active[a], at0 = first_of[e];
         int n = 0;
         for (int t0 = 0; t0 < n_tok; t0 += 64) {
             const int t = t0 + lane;
-            int slot = -1;
+            bool has = false;
             float w = 0.0f;
             if (t < n_tok)
-                for (int c = top_k - 1; c >= 0; --c)                    // an expert chosen twice counts with both weights
+                for (int c = 0; c < top_k; ++c)                         // an expert chosen twice counts with both weights
                     if (key[t * top_k + c] == e) {
-                        slot = t * top_k + c;
-                        w += weights ? weights[slot] : 1.0f;
+                        has = true;
+                        w += weights ? weights[t * top_k + c] : 1.0f;
                     }
-            const unsigned long long has = __ballot(slot >= 0);
-            if (slot >= 0) {
-                const int at = n + __popcll(has & ((1ull << lane) - 1));
-                list[at] = (unsigned short)slot;
+            const unsigned long long all = __ballot(has);
+            if (has) {
+                const int at = at0 + n + __popcll(all & ((1ull << lane) - 1));
+                list[at] = (unsigned short)t;
                 share[at] = w;
             }
-            n += __popcll(has);
+            n += __popcll(all);
         }
-        __builtin_amdgcn_wave_barrier();
-        const Q4Rows<ZP, G> row = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + (lane & 15), dim - 1), n_blk);
+        if (lane == 0) count[a] = (unsigned short)n;
+    }
+    __syncthreads();
+    // several units for each wave, so that waves end together: parts of an expert's columns
+    const int pieces = (n_blk + U - 1) / U;
+    const int split = na > 0 ? min(pieces, max(1, (ME_UNITS * waves + na - 1) / na)) : 1;
+    const int row0 = blockIdx.x * rows, r = lane & (rows - 1);
+    for (int unit = wv; unit < na * split; unit += waves) {
+        const int a = unit / split, k0 = unit - a * split;
+        const int e = __builtin_amdgcn_readfirstlane(active[a]), n = __builtin_amdgcn_readfirstlane(count[a]);
+        const int at0 = __builtin_amdgcn_readfirstlane(first_of[e]);
+        const int room = __builtin_amdgcn_readfirstlane(first_of[e + 1]) - at0;
+        const Q4Rows<ZP, G> row = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + r, dim - 1), n_blk);
         for (int first = 0; first < n; first += 16) {
-            const unsigned short *hr = h.p + (int64_t)list[min(first + (lane & 15), n - 1)] * h.ld + 8 * quarter;
+            const int in = min(16, room - first);
+            const unsigned short *hr = h + hidden_tile(at0 + first, n_blk) + (quarter * in + min(lane & 15, in - 1)) * 8;
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
             auto block = [&](const auto &w, int u, int b) {
                 u32x4 v[3][4];
@@ -229,7 +300,7 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
                 for (int i = 0; i < 3; ++i)
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-                        v[i][m] = *reinterpret_cast<const u32x4 *>(hr + i * h.plane + (int64_t)b * Q4_BLOCK + 32 * m);
+                        v[i][m] = *reinterpret_cast<const u32x4 *>(hr + hidden_piece(b, i, 4 * m, in));
 #pragma unroll
                 for (int g = 0; g < GB; ++g) {
                     const Op::Zero nz = Op::zero(w.zero(u, g));
@@ -263,21 +334,20 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = first + quarter * 4 + i;
-                if (at < n) {                                           // a token is once in the list: no two lanes meet
-                    float *d = mine + (list[at] / top_k) * 16 + (lane & 15);
-                    *d = fmaf(share[at], acc[i], *d);
+                if (at < n && (lane & 15) < rows) {                     // a token is once in the list: no two lanes meet
+                    float *d = mine + list[at0 + at] * 16 + r;
+                    *d = fmaf(share[at0 + at], acc[i], *d);
                 }
             }
         }
-        __builtin_amdgcn_wave_barrier();
     }
     __syncthreads();
-    for (int o = threadIdx.x; o < n_tok * 16; o += blockDim.x) {
-        const int row = row0 + o % 16;
+    for (int o = threadIdx.x; o < n_tok * rows; o += blockDim.x) {
+        const int in = o % rows, t = o / rows, row = row0 + in;
         float v = 0.0f;
-        for (int w = 0; w < waves; ++w) v += sums[(size_t)w * n_tok * 16 + o];
+        for (int w = 0; w < waves; ++w) v += sums[((size_t)w * n_tok + t) * 16 + in];
         if (row < dim) {
-            const int64_t at = (int64_t)(o / 16) * ldy + row;
+            const int64_t at = (int64_t)t * ldy + row;
             if (f32)
                 static_cast<float *>(y)[at] = v;
             else
@@ -300,8 +370,7 @@ int64_t hidden_ld(int32_t inter) { return q4_blocks(inter) * Q4_BLOCK; }
 
 size_t down_lds(int waves, int n_tok, int top_k, int n_experts) {
     const size_t slots = (size_t)n_tok * top_k;
-    return (size_t)waves * n_tok * (16 * 4 + 4 + 2) + (size_t)n_experts * 4 + slots * 2 +
-           std::min<size_t>(slots, n_experts) * 2;
+    return (size_t)waves * n_tok * 64 + slots * 8 + ((size_t)n_experts + 1) * 4 + std::min<size_t>(slots, n_experts) * 4;
 }
 
 }  // namespace
@@ -341,29 +410,43 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     if (!aligned16(workspace)) return fail(SPMV_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
     const int slots = n_tok * top_k;
     const int64_t ld = hidden_ld(inter);
-    const Hidden h = {static_cast<unsigned short *>(workspace), ld, ld * slots};
     const bool by_slot = slots <= n_experts;
     const int up_blk = (int)q4_blocks(dim), down_blk = (int)q4_blocks(inter);
-    st = check_grid(ld / 16 * (by_slot ? slots : n_experts), 512);
+    // parts of the columns in the up product: enough waves for the card
+    const int64_t groups = by_slot ? slots : n_experts, up_tiles_n = ld / 16 * groups;
+    int parts = 1;
+    while (parts < ME_UP_WAVES && parts < up_blk && up_tiles_n * parts < 4096) parts *= 2;
+    const int64_t up_grid = ceil_div(ld / 16, ME_UP_WAVES / parts);
+    st = check_grid(up_grid * groups, 64 * ME_UP_WAVES);
     if (st != SPMV_OK) return st;
-    st = check_grid(ceil_div(dim, 16), 1024);
+    // 8 rows for a workgroup of the down product where 16 would leave compute units without one
+    const int rows = ceil_div(dim, 16) < 256 ? 8 : 16;
+    st = check_grid(ceil_div(dim, rows), 1024);
     if (st != SPMV_OK) return st;
+    // a wave's sums take 64 bytes per token
+    const int waves = n_tok <= 64 ? 16 : n_tok <= 128 || down_lds(8, n_tok, top_k, n_experts) <= ME_LDS ? 8 : 4;
     hipStream_t s = as_stream(stream);
+    unsigned short *h = static_cast<unsigned short *>(workspace);
     auto launch = [&](auto e, auto zp, auto g) -> spmv_status {
         typedef decltype(e) E;
         typedef typename E::T T;
         constexpr bool ZP = decltype(zp)::value;
         constexpr int G = decltype(g)::value;
-        const int up_waves = (int)std::min<int64_t>(8, ceil_div(up_blk, ME_UNROLL));
-        k_moe_up<E, ZP, G><<<dim3((unsigned)(ld / 16), by_slot ? slots : n_experts), 64 * up_waves,
-                             (size_t)up_waves * 2048, s>>>(
-            n_tok, top_k, n_experts, dim, inter, up_blk, by_slot, keys, static_cast<const char *>(up_tiles),
-            static_cast<const T *>(x), ldx, h);
+        auto up = [&](auto tt) {
+            k_moe_up<E, ZP, G, decltype(tt)::value><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
+                n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, parts, by_slot, keys,
+                static_cast<const char *>(up_tiles), static_cast<const T *>(x), ldx, h);
+        };
+        // tokens of an expert at a time, by their number if the choices are even
+        if (slots <= 12 * groups)
+            up(std::integral_constant<int, 1>{});
+        else if (slots <= 24 * groups)
+            up(std::integral_constant<int, 2>{});
+        else
+            up(std::integral_constant<int, 4>{});
         SPMV_LAUNCHED("k_moe_up");
-        // a wave's sums take 64 bytes per token: 16 waves up to 64 tokens, 8 up to 256
-        const int waves = n_tok <= 64 ? 16 : 8;
-        k_moe_down<E, ZP, G><<<(int)ceil_div(dim, 16), 64 * waves, down_lds(waves, n_tok, top_k, n_experts), s>>>(
-            n_tok, top_k, n_experts, dim, down_blk, keys, weights, static_cast<const char *>(down_tiles), h, y,
+        k_moe_down<E, ZP, G><<<(int)ceil_div(dim, rows), 64 * waves, down_lds(waves, n_tok, top_k, n_experts), s>>>(
+            n_tok, top_k, n_experts, dim, rows, down_blk, keys, weights, static_cast<const char *>(down_tiles), h, y,
             y_dtype == SPMV_F32, ldy);
         SPMV_LAUNCHED("k_moe_down");
         return SPMV_OK;
