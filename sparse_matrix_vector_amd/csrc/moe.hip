@@ -53,34 +53,34 @@ __device__ __forceinline__ void split3(float v, unsigned short (&o)[3]) {
     o[2] = (unsigned short)(__float_as_uint(r - __uint_as_float(b)) >> 16);
 }
 
-template <class E, bool ZP, int G, int TT>
-__global__ __launch_bounds__(64 * ME_UP_WAVES) void k_moe_up(int n_tok, int top_k, int n_experts, int dim, int inter,
-                                                             int n_blk, int h_blk, int parts, bool by_slot,
-                                                             const int *__restrict__ keys,
-                                                             const char *__restrict__ tiles,
-                                                             const typename E::T *__restrict__ x, int64_t ldx,
-                                                             unsigned short *__restrict__ h) {
-    constexpr int PG = G / 32, TN = 16 * TT, W = ME_UP_WAVES;
-    __shared__ u32x4 xt[W][TN * 16];                                   // a wave's block of x, then its sums
-    __shared__ unsigned short list[ME_MAX_TOK];                        // tokens of the expert
-    __shared__ int n_list, below[W], equal[W];
-    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
+// An expert's tokens, found by a workgroup of the up product: list[0 .. n) (each
+// token once, ascending), where its entries begin among all, and the room there is
+// for them (its choices).
+struct Entries {
+    int n, base, room;
+};
+struct EntryLds {
+    unsigned short list[ME_MAX_TOK];
+    int n, below[ME_UP_WAVES], equal[ME_UP_WAVES];
+};
+// The expert of this workgroup, or -1 if another one does its work.
+__device__ __forceinline__ int expert_of(int n_experts, bool by_slot, const int *__restrict__ keys) {
+    if (!by_slot) return blockIdx.y;
+    const int s = blockIdx.y, e = keys[s];
+    int before = 0;
+    for (int i = threadIdx.x; i < s; i += 64 * ME_UP_WAVES) before |= keys[i] == e;
+    return __syncthreads_or(before) || (unsigned)e >= (unsigned)n_experts ? -1 : e;
+}
+__device__ __forceinline__ Entries find_entries(int n_tok, int top_k, int e, const int *__restrict__ keys, EntryLds &l) {
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int slots = n_tok * top_k;
-    int e = blockIdx.y;
-    if (by_slot) {
-        const int s = blockIdx.y;
-        e = keys[s];
-        int before = 0;
-        for (int i = threadIdx.x; i < s; i += 64 * W) before |= keys[i] == e;
-        if (__syncthreads_or(before) || (unsigned)e >= (unsigned)n_experts) return;
-    }
-    int lo = 0, eq = 0;                                                // choices of smaller experts, and of this one
-    for (int i0 = wv * 64; i0 < slots; i0 += 64 * W) {
+    int lo = 0, eq = 0;
+    for (int i0 = wv * 64; i0 < slots; i0 += 64 * ME_UP_WAVES) {
         const int k = i0 + lane < slots ? keys[i0 + lane] : -1;
         lo += __popcll(__ballot(k >= 0 && k < e));
         eq += __popcll(__ballot(k == e));
     }
-    if (lane == 0) below[wv] = lo, equal[wv] = eq;
+    if (lane == 0) l.below[wv] = lo, l.equal[wv] = eq;
     if (wv == 0) {
         int n = 0;
         for (int t0 = 0; t0 < n_tok; t0 += 64) {
@@ -89,42 +89,193 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES) void k_moe_up(int n_tok, int top_
             if (t < n_tok)
                 for (int c = 0; c < top_k; ++c) mine |= keys[t * top_k + c] == e;
             const unsigned long long has = __ballot(mine);
-            if (mine) list[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)t;
+            if (mine) l.list[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)t;
             n += __popcll(has);
         }
-        if (lane == 0) n_list = n;
+        if (lane == 0) l.n = n;
     }
     __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(n_list);
-    if (n == 0) return;
-    int base = 0, room = 0;
+    Entries r = {__builtin_amdgcn_readfirstlane(l.n), 0, 0};
 #pragma unroll
-    for (int w = 0; w < W; ++w) base += below[w], room += equal[w];
+    for (int w = 0; w < ME_UP_WAVES; ++w) r.base += l.below[w], r.room += l.equal[w];
+    r.base = __builtin_amdgcn_readfirstlane(r.base);
+    r.room = __builtin_amdgcn_readfirstlane(r.room);
+    return r;
+}
 
-    const int part = wv % parts, row0 = ((int)blockIdx.x * (W / parts) + wv / parts) * 16;
+// One block's products of gate and up rows with TT tiles of x, as they lie in LDS.
+template <class E, bool ZP, int G, int TT>
+__device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G, 1> (&w)[2], const u32x4 *xt, f32x4 (&acc)[2][TT]) {
+    constexpr int PG = G / 32;
+    const int lane = __lane_id(), quarter = lane / 16;
+    f32x4 sum[2][TT];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int g = m / PG;
+        u32x4 xv[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) xv[t] = xt[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const u32x4 f = Q4Op<E>::decode(w[r].c[0][m], Q4Op<E>::zero(w[r].zero(0, g)));
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+                sum[r][t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
+        }
+        if ((m + 1) % PG == 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float sc = w[r].scale(0, g) * Q4Op<E>::UNIT;
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+            }
+        }
+    }
+}
+
+// h of the 16 columns from row0 on and the 16 entries from `first` on, of which `here` are there.
+__device__ __forceinline__ void store_hidden(const f32x4 &gate, const f32x4 &up, const Entries &en, int first, int here,
+                                             int row0, int inter, int h_blk, unsigned short *__restrict__ h) {
+    const int lane = __lane_id(), row = row0 + (lane & 15), in = min(16, en.room - first);
+    if (row >= h_blk * Q4_BLOCK) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = 4 * (lane / 16) + i;
+        if (at >= here) continue;
+        unsigned short o[3] = {0, 0, 0};                                // columns past inter are zeros
+        if (row < inter) split3(gate[i] / (1.0f + expf(-gate[i])) * up[i], o);
+        unsigned short *d = h + hidden_tile(en.base + first, h_blk) + at * 8 + row % 8;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) d[hidden_piece(row / Q4_BLOCK, k, row % Q4_BLOCK / 8, in)] = o[k];
+    }
+}
+
+// Few tokens of an expert: a wave brings its block of x into LDS of its own and
+// takes every parts-th block of its rows.
+template <class E, bool ZP, int G>
+__global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int top_k, int n_experts, int dim, int inter,
+                                                                int n_blk, int h_blk, int parts, bool by_slot,
+                                                                const int *__restrict__ keys,
+                                                                const char *__restrict__ tiles,
+                                                                const typename E::T *__restrict__ x, int64_t ldx,
+                                                                unsigned short *__restrict__ h) {
+    __shared__ u32x4 xt[ME_UP_WAVES][16 * 16];                         // a wave's block of x, then its sums
+    __shared__ EntryLds el;
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
+    const int e = __builtin_amdgcn_readfirstlane(expert_of(n_experts, by_slot, keys));
+    if (e < 0) return;
+    const int part = wv % parts, row0 = ((int)blockIdx.x * (ME_UP_WAVES / parts) + wv / parts) * 16;
+    Q4Rows<ZP, G> rows[2];
+    Q4Piece<E, ZP, G, 1> w[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        rows[r] = Q4Rows<ZP, G>::any(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk);
+        w[0][r].load(rows[r], min(part, n_blk - 1));                    // on its way while the tokens are found
+    }
+    const Entries en = find_entries(n_tok, top_k, e, keys, el);
+    if (en.n == 0) return;
+    u32x4 *mine = xt[wv];
+    const int piece = lane % 16;
+    for (int first = 0; first < en.n; first += 16) {
+        const int here = min(16, en.n - first);
+        const typename E::T *xr[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) xr[q] = x + (int64_t)el.list[min(first + 4 * q + quarter, en.n - 1)] * ldx + piece * 8;
+        // only entries that there are; the others' sums are not stored
+        auto load_x = [&](int b, u32x4 (&v)[4]) {
+            const int64_t at = (int64_t)b * Q4_BLOCK;
+            if (at + Q4_BLOCK <= dim) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (4 * q < here) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (4 * q < here) v[q] = q4_token_piece(xr[q] - piece * 8, at + piece * 8, dim);
+            }
+        };
+        f32x4 acc[2][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
+        u32x4 v[4];
+        load_x(min(part, n_blk - 1), v);
+        if (first > 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], min(part, n_blk - 1));
+        }
+        for (int bb = part; bb < n_blk; bb += 2 * parts) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int b = bb + a * parts;
+                if (b >= n_blk) break;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int t = 4 * q + quarter;
+                    if (4 * q < here) mine[t * 16 + (piece ^ t)] = v[q];
+                }
+                load_x(min(b + parts, n_blk - 1), v);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + parts, n_blk - 1));
+                up_block<E, ZP, G, 1>(w[a], mine, acc);
+            }
+        }
+        f32x4 *sums = reinterpret_cast<f32x4 *>(mine);                 // [2][64] of the wave's 4 KB
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sums[r * 64 + lane] = acc[r][0];
+        __syncthreads();
+        if (part == 0) {                                               // the wave of the first columns adds the others'
+            f32x4 gate = acc[0][0], up = acc[1][0];
+            for (int p = 1; p < parts; ++p) {
+                const f32x4 *other = reinterpret_cast<const f32x4 *>(xt[wv + p]);
+                gate += other[lane];
+                up += other[64 + lane];
+            }
+            store_hidden(gate, up, en, first, here, row0, inter, h_blk, h);
+        }
+        __syncthreads();
+    }
+}
+
+// More: the waves of a workgroup share the block of x of 16 TT tokens.
+template <class E, bool ZP, int G, int TT>
+__global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, int top_k, int n_experts, int dim,
+                                                                     int inter, int n_blk, int h_blk,
+                                                                     const int *__restrict__ keys,
+                                                                     const char *__restrict__ tiles,
+                                                                     const typename E::T *__restrict__ x, int64_t ldx,
+                                                                     unsigned short *__restrict__ h) {
+    constexpr int TN = 16 * TT;
+    __shared__ u32x4 xt[2][TN * 16];
+    __shared__ EntryLds el;
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int e = blockIdx.y, row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 16;
+    const Entries en = find_entries(n_tok, top_k, e, keys, el);
     Q4Rows<ZP, G> rows[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
         rows[r] = Q4Rows<ZP, G>::any(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk);
-    u32x4 *mine = xt[wv];
-    const int piece = lane % 16;
-    for (int first = 0; first < n; first += TN) {
-        const int here = min(TN, n - first);                           // entries of this turn
-        const typename E::T *xr[4 * TT];
+    const int piece = threadIdx.x % 16, mine = threadIdx.x / 16;       // this thread's pieces: of entries mine + 16 q
+    for (int first = 0; first < en.n; first += TN) {
+        const int here = min(TN, en.n - first);
+        const typename E::T *xr[TT];
 #pragma unroll
-        for (int q = 0; q < 4 * TT; ++q) xr[q] = x + (int64_t)list[min(first + 4 * q + quarter, n - 1)] * ldx;
-        // only entries that there are; the others' sums are not stored
-        auto load_x = [&](int b, u32x4 (&v)[4 * TT]) {
+        for (int q = 0; q < TT; ++q) xr[q] = x + (int64_t)el.list[min(first + 16 * q + mine, en.n - 1)] * ldx + piece * 8;
+        auto load_x = [&](int b, u32x4 (&v)[TT]) {
             const int64_t at = (int64_t)b * Q4_BLOCK;
             if (at + Q4_BLOCK <= dim) {
 #pragma unroll
-                for (int q = 0; q < 4 * TT; ++q)
-                    if (4 * q < here) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at + piece * 8);
+                for (int q = 0; q < TT; ++q)
+                    if (16 * q < here) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at);
             } else {
 #pragma unroll
-                for (int q = 0; q < 4 * TT; ++q)
-                    if (4 * q < here) v[q] = q4_token_piece(xr[q], at + piece * 8, dim);
+                for (int q = 0; q < TT; ++q)
+                    if (16 * q < here) v[q] = q4_token_piece(xr[q] - piece * 8, at + piece * 8, dim);
             }
+        };
+        auto keep_x = [&](u32x4 *to, const u32x4 (&v)[TT]) {
+#pragma unroll
+            for (int q = 0; q < TT; ++q)
+                if (16 * q < here) to[(16 * q + mine) * 16 + (piece ^ mine)] = v[q];
         };
         f32x4 acc[2][TT];
 #pragma unroll
@@ -132,84 +283,30 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES) void k_moe_up(int n_tok, int top_
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         Q4Piece<E, ZP, G, 1> w[2][2];
-        u32x4 v[4 * TT];
+        u32x4 v[TT];
+        load_x(0, v);
 #pragma unroll
-        for (int q = 0; q < 4 * TT; ++q) v[q] = u32x4{0u, 0u, 0u, 0u};
-        load_x(min(part, n_blk - 1), v);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], min(part, n_blk - 1));
-        for (int bb = part; bb < n_blk; bb += 2 * parts) {
+        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
+        keep_x(xt[0], v);
+        __syncthreads();
+        for (int bb = 0; bb < n_blk; bb += 2) {
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                const int b = bb + a * parts;
+                const int b = bb + a;
                 if (b >= n_blk) break;
+                load_x(min(b + 1, n_blk - 1), v);                      // x first: what waits for it does not wait for the codes
 #pragma unroll
-                for (int q = 0; q < 4 * TT; ++q) {
-                    const int t = 4 * q + quarter;
-                    if (4 * q < here) mine[t * 16 + (piece ^ (t & 15))] = v[q];
-                }
-                load_x(min(b + parts, n_blk - 1), v);
-#pragma unroll
-                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + parts, n_blk - 1));
-                f32x4 sum[2][TT];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int g = m / PG;
-                    u32x4 xv[TT];
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) xv[t] = mine[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const u32x4 f = Q4Op<E>::decode(w[a][r].c[0][m], Q4Op<E>::zero(w[a][r].zero(0, g)));
-#pragma unroll
-                        for (int t = 0; t < TT; ++t)
-                            sum[r][t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
-                    }
-                    if ((m + 1) % PG == 0) {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float sc = w[a][r].scale(0, g) * Q4Op<E>::UNIT;
-#pragma unroll
-                            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
-                        }
-                    }
-                }
+                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
+                __builtin_amdgcn_sched_barrier(0);
+                up_block<E, ZP, G, TT>(w[a], xt[a], acc);
+                keep_x(xt[1 - a], v);
+                __syncthreads();
             }
         }
-        f32x4 *sums = reinterpret_cast<f32x4 *>(mine);                 // [2][TT][64] of the wave's 4 TT KB
-        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int t = 0; t < TT; ++t) sums[(r * TT + t) * 64 + lane] = acc[r][t];
-        __syncthreads();
-        if (part == 0) {                                               // the wave of the first columns adds the others'
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                f32x4 gate = acc[0][t], up = acc[1][t];
-                for (int p = 1; p < parts; ++p) {
-                    const f32x4 *other = reinterpret_cast<const f32x4 *>(xt[wv + p]);
-                    gate += other[t * 64 + lane];
-                    up += other[(TT + t) * 64 + lane];
-                }
-                const int row = row0 + (lane & 15);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = 16 * t + 4 * quarter + i;
-                    if (at >= here || row >= h_blk * Q4_BLOCK) continue;
-                    unsigned short o[3] = {0, 0, 0};                    // columns past inter are zeros
-                    if (row < inter) split3(gate[i] / (1.0f + expf(-gate[i])) * up[i], o);
-                    const int tile = (first + at) / 16 * 16, in = min(16, room - tile);
-                    unsigned short *d = h + hidden_tile(base + tile, h_blk) + (first + at - tile) * 8 + row % 8;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        d[hidden_piece(row / Q4_BLOCK, k, row % Q4_BLOCK / 8, in)] = o[k];
-                }
-            }
-        }
-        __syncthreads();
+        for (int t = 0; t < TT; ++t)
+            if (16 * t < here)
+                store_hidden(acc[0][t], acc[1][t], en, first + 16 * t, min(16, here - 16 * t), row0, inter, h_blk, h);
     }
 }
 
@@ -280,65 +377,87 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
         if (lane == 0) count[a] = (unsigned short)n;
     }
     __syncthreads();
-    // several units for each wave, so that waves end together: parts of an expert's columns
+    // units of about as much work for every wave: an expert, or a part of its columns.
+    // A wave goes through its units' steps (U blocks of 16 entries), the next step's codes on their way.
     const int pieces = (n_blk + U - 1) / U;
     const int split = na > 0 ? min(pieces, max(1, (ME_UNITS * waves + na - 1) / na)) : 1;
-    const int row0 = blockIdx.x * rows, r = lane & (rows - 1);
-    for (int unit = wv; unit < na * split; unit += waves) {
-        const int a = unit / split, k0 = unit - a * split;
-        const int e = __builtin_amdgcn_readfirstlane(active[a]), n = __builtin_amdgcn_readfirstlane(count[a]);
-        const int at0 = __builtin_amdgcn_readfirstlane(first_of[e]);
-        const int room = __builtin_amdgcn_readfirstlane(first_of[e + 1]) - at0;
-        const Q4Rows<ZP, G> row = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + r, dim - 1), n_blk);
-        for (int first = 0; first < n; first += 16) {
-            const int in = min(16, room - first);
-            const unsigned short *hr = h + hidden_tile(at0 + first, n_blk) + (quarter * in + min(lane & 15, in - 1)) * 8;
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-            auto block = [&](const auto &w, int u, int b) {
+    const int row0 = blockIdx.x * rows, r = lane & (rows - 1), units = na * split;
+    struct Step {
+        int unit, e, n, at0, room, first, k0, p;
+    };
+    auto begin = [&](int unit) {
+        Step s = {unit, 0, 0, 0, 0, 0, 0, 0};
+        if (unit < units) {
+            const int a = unit / split;
+            s.k0 = s.p = unit - a * split;
+            s.e = __builtin_amdgcn_readfirstlane(active[a]);
+            s.n = __builtin_amdgcn_readfirstlane(count[a]);
+            s.at0 = __builtin_amdgcn_readfirstlane(first_of[s.e]);
+            s.room = __builtin_amdgcn_readfirstlane(first_of[s.e + 1]) - s.at0;
+        }
+        return s;
+    };
+    auto after = [&](Step s) {
+        s.p += split;
+        if (s.p < pieces) return s;
+        s.p = s.k0;
+        s.first += 16;
+        return s.first < s.n ? s : begin(s.unit + waves);
+    };
+    Q4Piece<E, ZP, G, 1> w[2][U];
+    auto load = [&](const Step &s, Q4Piece<E, ZP, G, 1> (&to)[U]) {
+        const Q4Rows<ZP, G> row = Q4Rows<ZP, G>::any(tiles, (int64_t)s.e * dim + min(row0 + r, dim - 1), n_blk);
+#pragma unroll
+        for (int u = 0; u < U; ++u) to[u].load(row, min(s.p * U + u, n_blk - 1));
+    };
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    Step s = begin(wv);
+    if (s.unit < units) load(s, w[0]);
+    while (s.unit < units) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            if (s.unit >= units) break;
+            const Step next = after(s);
+            if (next.unit < units) load(next, w[1 - a]);
+            const int in = min(16, s.room - s.first);
+            const u32x4 *ht = reinterpret_cast<const u32x4 *>(h + hidden_tile(s.at0 + s.first, n_blk));
+            const int hl = quarter * in + min(lane & 15, in - 1);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = s.p * U + u;
+                if (b >= n_blk) break;
                 u32x4 v[3][4];
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        v[i][m] = *reinterpret_cast<const u32x4 *>(hr + hidden_piece(b, i, 4 * m, in));
+                    for (int m = 0; m < 4; ++m) v[i][m] = (ht + hidden_piece(b, i, 4 * m, in) / 8)[hl];
 #pragma unroll
                 for (int g = 0; g < GB; ++g) {
-                    const Op::Zero nz = Op::zero(w.zero(u, g));
+                    const Op::Zero nz = Op::zero(w[a][u].zero(0, g));
                     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int m = g * PG; m < (g + 1) * PG; ++m) {
-                        const u32x4 f = Op::decode(w.c[u][m], nz);
+                        const u32x4 f = Op::decode(w[a][u].c[0][m], nz);
 #pragma unroll
                         for (int i = 2; i >= 0; --i) sum = Op::mfma(v[i][m], f, sum);
                     }
-                    const float sc = w.scale(u, g);
+                    const float sc = w[a][u].scale(0, g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i] = fmaf(sc, sum[i], acc[i]);
                 }
-            };
-            for (int p = k0; p < pieces; p += split) {
-                const int b0 = p * U;
-                if (b0 + U <= n_blk) {
-                    Q4Piece<E, ZP, G, U> w;
-                    w.load(row, b0);
+            }
+            if (next.unit != s.unit || next.first != s.first) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) block(w, u, b0 + u);
-                } else {
-                    for (int b = b0; b < n_blk; ++b) {
-                        Q4Piece<E, ZP, G, 1> w;
-                        w.load(row, b);
-                        block(w, 0, b);
+                for (int i = 0; i < 4; ++i) {
+                    const int at = s.first + quarter * 4 + i;
+                    if (at < s.n && (lane & 15) < rows) {               // a token is once in the list: no two lanes meet
+                        float *d = mine + list[s.at0 + at] * 16 + r;
+                        *d = fmaf(share[s.at0 + at], acc[i], *d);
                     }
+                    acc[i] = 0.0f;
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = first + quarter * 4 + i;
-                if (at < n && (lane & 15) < rows) {                     // a token is once in the list: no two lanes meet
-                    float *d = mine + list[at0 + at] * 16 + r;
-                    *d = fmaf(share[at0 + at], acc[i], *d);
-                }
-            }
+            s = next;
         }
     }
     __syncthreads();
@@ -414,8 +533,10 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     const int up_blk = (int)q4_blocks(dim), down_blk = (int)q4_blocks(inter);
     // parts of the columns in the up product: enough waves for the card
     const int64_t groups = by_slot ? slots : n_experts, up_tiles_n = ld / 16 * groups;
+    // tokens of an expert by their number if the choices are even
+    const bool tile_up = slots > 12 * groups;
     int parts = 1;
-    while (parts < ME_UP_WAVES && parts < up_blk && up_tiles_n * parts < 4096) parts *= 2;
+    while (!tile_up && parts < ME_UP_WAVES && parts < up_blk && up_tiles_n * parts < 4096) parts *= 2;
     const int64_t up_grid = ceil_div(ld / 16, ME_UP_WAVES / parts);
     st = check_grid(up_grid * groups, 64 * ME_UP_WAVES);
     if (st != SPMV_OK) return st;
@@ -433,15 +554,18 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         constexpr bool ZP = decltype(zp)::value;
         constexpr int G = decltype(g)::value;
         auto up = [&](auto tt) {
-            k_moe_up<E, ZP, G, decltype(tt)::value><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
+            k_moe_up_tile<E, ZP, G, decltype(tt)::value><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
+                n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, keys, static_cast<const char *>(up_tiles),
+                static_cast<const T *>(x), ldx, h);
+        };
+        if (!tile_up)
+            k_moe_up<E, ZP, G><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
                 n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, parts, by_slot, keys,
                 static_cast<const char *>(up_tiles), static_cast<const T *>(x), ldx, h);
-        };
-        // tokens of an expert at a time, by their number if the choices are even
-        if (slots <= 12 * groups)
-            up(std::integral_constant<int, 1>{});
         else if (slots <= 24 * groups)
             up(std::integral_constant<int, 2>{});
+        else if (slots <= 40 * groups)
+            up(std::integral_constant<int, 3>{});
         else
             up(std::integral_constant<int, 4>{});
         SPMV_LAUNCHED("k_moe_up");
