@@ -835,8 +835,8 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t inter, size
  * both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A token without an
  * expert gets zeros.  x [n_tok, dim] of type dtype (the scales' type), y [n_tok, dim]
  * of the same type or fp32, rounded once; the products between are kept with fp32's
- * 24 bits.  Only the weights of chosen experts are read.  At most 1024 experts
- * (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
+ * 24 bits.  Only the weights of chosen experts are read.  At most 1024 experts and
+ * a width dim of at least 8 (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
  * overlap; x and y must not overlap.  The same bits on every call.  All pointers
  * device.  Asynchronous. */
 spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,

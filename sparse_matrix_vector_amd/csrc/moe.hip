@@ -182,19 +182,10 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
         const int here = min(16, en.n - first);
         const typename E::T *xr[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) xr[q] = x + (int64_t)el.list[min(first + 4 * q + quarter, en.n - 1)] * ldx + piece * 8;
-        // only entries that there are; the others' sums are not stored
+        for (int q = 0; q < 4; ++q) xr[q] = x + (int64_t)el.list[min(first + 4 * q + quarter, en.n - 1)] * ldx;
         auto load_x = [&](int b, u32x4 (&v)[4]) {
-            const int64_t at = (int64_t)b * Q4_BLOCK;
-            if (at + Q4_BLOCK <= dim) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (4 * q < here) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (4 * q < here) v[q] = q4_token_piece(xr[q] - piece * 8, at + piece * 8, dim);
-            }
+            for (int q = 0; q < 4; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
         };
         f32x4 acc[2][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
         u32x4 v[4];
@@ -208,10 +199,14 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
             for (int a = 0; a < 2; ++a) {
                 const int b = bb + a * parts;
                 if (b >= n_blk) break;
+                if ((int64_t)(b + 1) * Q4_BLOCK > dim) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int t = 4 * q + quarter;
-                    if (4 * q < here) mine[t * 16 + (piece ^ t)] = v[q];
+                    mine[t * 16 + (piece ^ t)] = v[q];
                 }
                 load_x(min(b + parts, n_blk - 1), v);
 #pragma unroll
@@ -259,23 +254,18 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         const int here = min(TN, en.n - first);
         const typename E::T *xr[TT];
 #pragma unroll
-        for (int q = 0; q < TT; ++q) xr[q] = x + (int64_t)el.list[min(first + 16 * q + mine, en.n - 1)] * ldx + piece * 8;
+        for (int q = 0; q < TT; ++q) xr[q] = x + (int64_t)el.list[min(first + 16 * q + mine, en.n - 1)] * ldx;
         auto load_x = [&](int b, u32x4 (&v)[TT]) {
-            const int64_t at = (int64_t)b * Q4_BLOCK;
-            if (at + Q4_BLOCK <= dim) {
 #pragma unroll
-                for (int q = 0; q < TT; ++q)
-                    if (16 * q < here) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at);
-            } else {
-#pragma unroll
-                for (int q = 0; q < TT; ++q)
-                    if (16 * q < here) v[q] = q4_token_piece(xr[q] - piece * 8, at + piece * 8, dim);
-            }
+            for (int q = 0; q < TT; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
         };
-        auto keep_x = [&](u32x4 *to, const u32x4 (&v)[TT]) {
+        auto keep_x = [&](int b, u32x4 *to, u32x4 (&v)[TT]) {
+            if ((int64_t)(b + 1) * Q4_BLOCK > dim) {
 #pragma unroll
-            for (int q = 0; q < TT; ++q)
-                if (16 * q < here) to[(16 * q + mine) * 16 + (piece ^ mine)] = v[q];
+                for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
+            }
+#pragma unroll
+            for (int q = 0; q < TT; ++q) to[(16 * q + mine) * 16 + (piece ^ mine)] = v[q];
         };
         f32x4 acc[2][TT];
 #pragma unroll
@@ -287,7 +277,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         load_x(0, v);
 #pragma unroll
         for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
-        keep_x(xt[0], v);
+        keep_x(0, xt[0], v);
         __syncthreads();
         for (int bb = 0; bb < n_blk; bb += 2) {
 #pragma unroll
@@ -299,7 +289,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
                 for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
                 up_block<E, ZP, G, TT>(w[a], xt[a], acc);
-                keep_x(xt[1 - a], v);
+                keep_x(min(b + 1, n_blk - 1), xt[1 - a], v);
                 __syncthreads();
             }
         }
@@ -513,6 +503,7 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     spmv_status st = moe_workspace_size(n_tok, top_k, inter, &need);
     if (st != SPMV_OK) return st;
     if (n_experts < 1 || dim < 1) return fail(SPMV_ERR_INVALID_VALUE, "n_experts and dim must be >= 1");
+    if (dim < 8) return fail(SPMV_ERR_UNSUPPORTED, "layers of a width below 8 are not supported");
     if (n_experts > ME_MAX_EXPERTS) return fail(SPMV_ERR_UNSUPPORTED, "more than %d experts are not supported", ME_MAX_EXPERTS);
     if (!q4_group_ok(group)) return fail(SPMV_ERR_INVALID_VALUE, "group must be 32, 64 or 128, not %d", group);
     if (!dtype_ok(dtype) || !dtype_ok(y_dtype)) return fail(SPMV_ERR_INVALID_VALUE, "an element type is not a spmv_dtype");

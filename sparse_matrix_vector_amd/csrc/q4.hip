@@ -115,14 +115,8 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
 #pragma unroll
     for (int q = 0; q < 4 * TT; ++q) xr[q] = x + (int64_t)min(4 * q + quarter, n_tok - 1) * ldx;
     auto load_x = [&](int b, u32x4 (&v)[4 * TT]) {
-        const int64_t at = (int64_t)b * Q4_BLOCK;
-        if (at + Q4_BLOCK <= n_cols) {
 #pragma unroll
-            for (int q = 0; q < 4 * TT; ++q) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at + piece * 8);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_piece(xr[q], at + piece * 8, n_cols);
-        }
+        for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
     };
     f32x4 acc[TT];
 #pragma unroll
@@ -136,6 +130,10 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
         for (int a = 0; a < 2; ++a) {
             const int b = bb + a * waves;
             if (b >= n_blk) break;
+            if ((int64_t)(b + 1) * Q4_BLOCK > n_cols) {
+#pragma unroll
+                for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
+            }
 #pragma unroll
             for (int q = 0; q < 4 * TT; ++q) {
                 const int t = 4 * q + quarter;
@@ -205,24 +203,26 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
 #pragma unroll
     for (int r = 0; r < RT; ++r)                     // tiles past the end: not stored
         rows[r] = Q4Rows<ZP, G>(tiles, min(row0 / 16 + r, (int64_t)(n_rows - 1) / 16), n_blk);
+    const int piece = threadIdx.x % 16;
     const typename E::T *xr[TT];
     int slot[TT];
 #pragma unroll
     for (int q = 0; q < TT; ++q) {
-        const int t = (threadIdx.x + 256 * q) / 16, piece = threadIdx.x % 16;
-        xr[q] = x + (int64_t)min(t0 + t, n_tok - 1) * ldx + piece * 8;
+        const int t = (threadIdx.x + 256 * q) / 16;
+        xr[q] = x + (int64_t)min(t0 + t, n_tok - 1) * ldx;
         slot[q] = t * 16 + (piece ^ (t & 15));
     }
     auto load_x = [&](int b, u32x4 (&v)[TT]) {
-        const int64_t at = (int64_t)b * Q4_BLOCK;
-        if (at + Q4_BLOCK <= n_cols) {
 #pragma unroll
-            for (int q = 0; q < TT; ++q) v[q] = *reinterpret_cast<const u32x4_any *>(xr[q] + at);
-        } else {
-            const int piece = (threadIdx.x % 16) * 8;
+        for (int q = 0; q < TT; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
+    };
+    auto keep_x = [&](int b, u32x4 *to, u32x4 (&v)[TT]) {
+        if ((int64_t)(b + 1) * Q4_BLOCK > n_cols) {
 #pragma unroll
-            for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q] - piece, at + piece, n_cols);
+            for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
         }
+#pragma unroll
+        for (int q = 0; q < TT; ++q) to[slot[q]] = v[q];
     };
     Q4Piece<E, ZP, G, 1> w[A + 1][RT];
     u32x4 v[TT];
@@ -231,8 +231,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     for (int a = 0; a < A; ++a)
 #pragma unroll
         for (int r = 0; r < RT; ++r) w[a][r].load(rows[r], min(b0 + a, b1 - 1));
-#pragma unroll
-    for (int q = 0; q < TT; ++q) xt[0][slot[q]] = v[q];
+    keep_x(b0, xt[0], v);
     f32x4 acc[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -277,8 +276,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 // keeps the fragments of one product in registers at a time
                 __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int q = 0; q < TT; ++q) xt[(b - b0 + 1) & 1][slot[q]] = v[q];
+            keep_x(min(b + 1, b1 - 1), xt[(b - b0 + 1) & 1], v);
             __syncthreads();
         }
     }
@@ -427,8 +425,10 @@ Tiling tiling(int64_t n_rows, int64_t n_cols, int64_t n_tok, bool wide) {
 size_t few_lds(int64_t n_cols, int64_t n_tok, int waves) {
     return std::max<size_t>((size_t)n_tok * (q4_blocks(n_cols) * 16 + 1) * 16, (size_t)waves * 1024);
 }
+// fewer than 8 columns: what reads x ahead takes 8 of them at least
+int few_tokens(int64_t n_cols) { return n_cols < 8 ? 16 : QF_TOKENS; }
 bool few(int64_t n_cols, int64_t n_tok) {
-    return n_tok <= QF_TOKENS && few_lds(n_cols, n_tok, 0) <= QF_LDS;
+    return n_cols < 8 || (n_tok <= QF_TOKENS && few_lds(n_cols, n_tok, 0) <= QF_LDS);
 }
 // Whether k_q4_mid takes the product: every 16 rows read x again, which costs less
 // than a second launch up to about 160 MB (f16, groups of 128: 4096 x 4096, 16
@@ -564,16 +564,18 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
             constexpr bool ZP = decltype(zp)::value;
             constexpr int G = decltype(g)::value;
             const int waves = (int)std::min<int64_t>(QF_WAVES, ceil_div(n_blk, QF_UNROLL));
-            auto run = [&](auto tp) {
+            auto run = [&](auto tp, int t0, int n) {
                 k_q4_few<E, ZP, G, decltype(tp)::value>
-                    <<<(int)ceil_div(n_rows, 16), 64 * waves, few_lds(n_cols, n_tok, waves), s>>>(
-                        n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n_tok, alpha, static_cast<const T *>(x),
-                        ldx, beta, y, f32, ldy);
+                    <<<(int)ceil_div(n_rows, 16), 64 * waves, few_lds(n_cols, n, waves), s>>>(
+                        n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n, alpha,
+                        static_cast<const T *>(x) + t0 * ldx, ldx, beta,
+                        static_cast<char *>(y) + t0 * ldy * (int64_t)dtype_size(y_dtype), f32, ldy);
             };
             if (n_tok == 1)
-                run(std::integral_constant<int, 1>{});
-            else
-                run(std::integral_constant<int, QF_TOKENS>{});
+                run(std::integral_constant<int, 1>{}, 0, 1);
+            else                                           // more than one turn only for fewer than 8 columns
+                for (int t0 = 0; t0 < n_tok; t0 += few_tokens(n_cols))
+                    run(std::integral_constant<int, 16>{}, t0, std::min(n_tok - t0, few_tokens(n_cols)));
             SPMV_LAUNCHED("k_q4_few");
             return SPMV_OK;
         });

@@ -177,4 +177,13 @@ __device__ __forceinline__ u32x4 q4_token_piece(const T *row, int64_t c, int64_t
     return v;
 }
 
+// The same for the loops: always one load (a load under a condition would make every
+// wait behind it wait for all loads), of the row's last 8 elements where c is too
+// far right; the last block is read with q4_token_piece when it is used.  The row
+// has at least 8 elements.
+template <class T>
+__device__ __forceinline__ u32x4 q4_token_ahead(const T *row, int64_t c, int64_t n_cols) {
+    return *reinterpret_cast<const u32x4_any *>(row + min(c, n_cols - 8));
+}
+
 }  // namespace spmv

@@ -62,7 +62,7 @@ def test_types_and_groups(dt, group, zeros, T, k, e):
     m.check(keys, w, x, y)
 
 
-@pytest.mark.parametrize("dim,inter", [(1, 1), (16, 7), (17, 128), (130, 129), (600, 520), (1000, 33)])
+@pytest.mark.parametrize("dim,inter", [(8, 1), (16, 7), (17, 128), (9, 2), (130, 129), (600, 520), (1000, 33)])
 @pytest.mark.parametrize("T", [1, 4])
 def test_sizes(dim, inter, T):
     m = Layer(4, dim, inter, 32, "bf16", True, seed=dim)

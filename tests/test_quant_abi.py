@@ -95,6 +95,7 @@ def test_moe_refusals():
     assert _moe(n=-1) == VALUE and _moe(k=0) == VALUE and _moe(e=0) == VALUE
     assert _moe(dim=0) == VALUE and _moe(inter=0) == VALUE and _moe(group=20) == VALUE
     assert _moe(n=257) == UNSUPPORTED and _moe(n=256, k=17) == UNSUPPORTED and _moe(e=1025) == UNSUPPORTED
+    assert _moe(dim=7, ldx=7, ldy=7) == UNSUPPORTED
     assert _moe(dt=F32) == UNSUPPORTED and _moe(dt=9) == VALUE and _moe(ydt=9) == VALUE and _moe(ydt=BF16) == UNSUPPORTED
     assert _moe(ldx=63) == VALUE and _moe(ldy=63) == VALUE
     for p in ("keys", "up", "dn", "x", "y", "ws"):
