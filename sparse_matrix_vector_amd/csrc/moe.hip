@@ -185,7 +185,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
         for (int q = 0; q < 4; ++q) xr[q] = x + (int64_t)el.list[min(first + 4 * q + quarter, en.n - 1)] * ldx;
         auto load_x = [&](int b, u32x4 (&v)[4]) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
+            for (int q = 0; q < 4; ++q) v[q] = q4_token_ahead(xr[q], b * Q4_BLOCK + piece * 8, dim);
         };
         f32x4 acc[2][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
         u32x4 v[4];
@@ -199,9 +199,9 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
             for (int a = 0; a < 2; ++a) {
                 const int b = bb + a * parts;
                 if (b >= n_blk) break;
-                if ((int64_t)(b + 1) * Q4_BLOCK > dim) {
+                if (b == dim / Q4_BLOCK) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
+                    for (int q = 0; q < 4; ++q) v[q] = q4_token_placed(v[q], b * Q4_BLOCK + piece * 8, dim);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -257,12 +257,12 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         for (int q = 0; q < TT; ++q) xr[q] = x + (int64_t)el.list[min(first + 16 * q + mine, en.n - 1)] * ldx;
         auto load_x = [&](int b, u32x4 (&v)[TT]) {
 #pragma unroll
-            for (int q = 0; q < TT; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
+            for (int q = 0; q < TT; ++q) v[q] = q4_token_ahead(xr[q], b * Q4_BLOCK + piece * 8, dim);
         };
         auto keep_x = [&](int b, u32x4 *to, u32x4 (&v)[TT]) {
-            if ((int64_t)(b + 1) * Q4_BLOCK > dim) {
+            if (b == dim / Q4_BLOCK) {
 #pragma unroll
-                for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, dim);
+                for (int q = 0; q < TT; ++q) v[q] = q4_token_placed(v[q], b * Q4_BLOCK + piece * 8, dim);
             }
 #pragma unroll
             for (int q = 0; q < TT; ++q) to[(16 * q + mine) * 16 + (piece ^ mine)] = v[q];
@@ -408,19 +408,19 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
         for (int a = 0; a < 2; ++a) {
             if (s.unit >= units) break;
             const Step next = after(s);
-            if (next.unit < units) load(next, w[1 - a]);
+            load(next.unit < units ? next : s, w[1 - a]);               // always, for the waits behind it
             const int in = min(16, s.room - s.first);
             const u32x4 *ht = reinterpret_cast<const u32x4 *>(h + hidden_tile(s.at0 + s.first, n_blk));
             const int hl = quarter * in + min(lane & 15, in - 1);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int b = s.p * U + u;
-                if (b >= n_blk) break;
                 u32x4 v[3][4];
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) v[i][m] = (ht + hidden_piece(b, i, 4 * m, in) / 8)[hl];
+                    for (int m = 0; m < 4; ++m) v[i][m] = (ht + hidden_piece(min(b, n_blk - 1), i, 4 * m, in) / 8)[hl];
+                if (b >= n_blk) continue;
 #pragma unroll
                 for (int g = 0; g < GB; ++g) {
                     const Op::Zero nz = Op::zero(w[a][u].zero(0, g));

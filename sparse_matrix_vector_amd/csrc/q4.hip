@@ -116,7 +116,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
     for (int q = 0; q < 4 * TT; ++q) xr[q] = x + (int64_t)min(4 * q + quarter, n_tok - 1) * ldx;
     auto load_x = [&](int b, u32x4 (&v)[4 * TT]) {
 #pragma unroll
-        for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
+        for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_ahead(xr[q], b * Q4_BLOCK + piece * 8, n_cols);
     };
     f32x4 acc[TT];
 #pragma unroll
@@ -130,9 +130,9 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
         for (int a = 0; a < 2; ++a) {
             const int b = bb + a * waves;
             if (b >= n_blk) break;
-            if ((int64_t)(b + 1) * Q4_BLOCK > n_cols) {
+            if (b == n_cols / Q4_BLOCK) {
 #pragma unroll
-                for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
+                for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_placed(v[q], b * Q4_BLOCK + piece * 8, n_cols);
             }
 #pragma unroll
             for (int q = 0; q < 4 * TT; ++q) {
@@ -214,12 +214,12 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     }
     auto load_x = [&](int b, u32x4 (&v)[TT]) {
 #pragma unroll
-        for (int q = 0; q < TT; ++q) v[q] = q4_token_ahead(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
+        for (int q = 0; q < TT; ++q) v[q] = q4_token_ahead(xr[q], b * Q4_BLOCK + piece * 8, n_cols);
     };
     auto keep_x = [&](int b, u32x4 *to, u32x4 (&v)[TT]) {
-        if ((int64_t)(b + 1) * Q4_BLOCK > n_cols) {
+        if (b == n_cols / Q4_BLOCK) {
 #pragma unroll
-            for (int q = 0; q < TT; ++q) v[q] = q4_token_piece(xr[q], (int64_t)b * Q4_BLOCK + piece * 8, n_cols);
+            for (int q = 0; q < TT; ++q) v[q] = q4_token_placed(v[q], b * Q4_BLOCK + piece * 8, n_cols);
         }
 #pragma unroll
         for (int q = 0; q < TT; ++q) to[slot[q]] = v[q];

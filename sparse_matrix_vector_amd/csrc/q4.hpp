@@ -177,13 +177,23 @@ __device__ __forceinline__ u32x4 q4_token_piece(const T *row, int64_t c, int64_t
     return v;
 }
 
-// The same for the loops: always one load (a load under a condition would make every
-// wait behind it wait for all loads), of the row's last 8 elements where c is too
-// far right; the last block is read with q4_token_piece when it is used.  The row
-// has at least 8 elements.
+// The same for the loops, in two steps (n_cols is at least 8): always one load, of
+// the row's last 8 elements where column c is too far right, since a load under a
+// condition makes every wait behind it wait for all loads; and, for the last block
+// when it is used, what has been loaded moved to its place.
 template <class T>
-__device__ __forceinline__ u32x4 q4_token_ahead(const T *row, int64_t c, int64_t n_cols) {
+__device__ __forceinline__ u32x4 q4_token_ahead(const T *row, int c, int n_cols) {
     return *reinterpret_cast<const u32x4_any *>(row + min(c, n_cols - 8));
+}
+__device__ __forceinline__ u32x4 q4_token_placed(u32x4 v, int c, int n_cols) {
+    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+    const int drop = c - (n_cols - 8);                   // elements of columns before c
+    if (drop <= 0) return v;
+    u64x2 w = __builtin_bit_cast(u64x2, v);
+    if (drop >= 4) w = u64x2{w[1], 0ull};
+    const int s = 16 * (drop & 3);
+    if (s) w = u64x2{w[0] >> s | w[1] << (64 - s), w[1] >> s};
+    return drop >= 8 ? u32x4{0u, 0u, 0u, 0u} : __builtin_bit_cast(u32x4, w);
 }
 
 }  // namespace spmv
