@@ -823,9 +823,10 @@ spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, int32_t wit
 
 /* Bytes of the workspace of moe_apply.  Host only.  At most 256 tokens and 4096
  * choices n_tok * top_k (SPMV_ERR_UNSUPPORTED). */
-spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t inter, size_t *bytes);
+spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t dim, int32_t inter, size_t *bytes);
 
-/* A layer of gated experts for a few tokens, in two launches:
+/* A layer of gated experts for a few tokens, in two launches (three beyond 64
+ * choices n_tok * top_k, whose results are added by token in the third):
  *   y[t] = sum_c weights[t, c] * Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])), e = keys[t, c]
  * with silu(v) = v / (1 + exp(-v)).  Weights as q4_tiles arranges them, the experts
  * stacked: up_tiles of [n_experts * 2 * inter, dim], an expert's inter gate rows

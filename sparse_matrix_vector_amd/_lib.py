@@ -102,7 +102,7 @@ SIGNATURES = {
     "q4_tiles_size": [c_i32, c_i32, c_i32, c_i32, P_sz],
     "q4_tiles": [c_i32, c_i32, c_i32, vp, vp, vp, vp, c_sz, vp],
     "q4_matmul": [c_i32, c_i32, c_i32, c_i32, vp, c_i32, c_i32, c_f32, vp, c_i64, c_f32, vp, c_i32, c_i64, vp, c_sz, vp],
-    "moe_workspace_size": [c_i32, c_i32, c_i32, P_sz],
+    "moe_workspace_size": [c_i32, c_i32, c_i32, c_i32, P_sz],
     "moe_apply": [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, vp, vp, vp, vp, c_i32, vp, c_i64, vp, c_i32, c_i64, vp,
                   c_sz, vp],
     "embed_lookup": [c_i32, c_i32, c_i32, c_i32, vp, vp, c_i64, c_f32, vp, c_i32, c_i64, vp],

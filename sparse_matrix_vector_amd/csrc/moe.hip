@@ -31,15 +31,16 @@ namespace {
 constexpr int ME_MAX_TOK = 256;
 constexpr int ME_MAX_SLOTS = 4096;
 constexpr int ME_MAX_EXPERTS = 1024;
-constexpr size_t ME_LDS = 160 * 1024 - 64;
 constexpr int ME_UP_WAVES = 4;
+constexpr int ME_DOWN_ROWS = 4;      // row tiles of a wave of the down product by experts
+constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
 constexpr int ME_UNROLL = 2;         // blocks whose codes a wave of the down product loads at once
 constexpr int ME_UNITS = 2;          // units of a wave of the down product, about
 
 // Where the tile of entries first .. first + n - 1 of all entries begins, and a
-// piece of 8 columns in it (in 16-bit numbers).
+// part of a piece of 8 columns in it (in 16-bit numbers).
 __device__ __forceinline__ int64_t hidden_tile(int first, int n_blk) { return (int64_t)first * n_blk * (Q4_BLOCK * 3); }
-__device__ __forceinline__ int hidden_piece(int b, int part, int piece, int n) { return ((b * 3 + part) * 16 + piece) * n * 8; }
+__device__ __forceinline__ int hidden_piece(int b, int part, int piece, int n) { return ((b * 16 + piece) * 3 + part) * n * 8; }
 
 // v = a + b + c with 8 bits each; an infinity or NaN is whole in the first.
 __device__ __forceinline__ void split3(float v, unsigned short (&o)[3]) {
@@ -103,6 +104,14 @@ __device__ __forceinline__ Entries find_entries(int n_tok, int top_k, int e, con
     return r;
 }
 
+// Where the results of this expert's choices will be: place[slot] = entry.
+__device__ __forceinline__ void store_places(int top_k, int e, const Entries &en, const EntryLds &l,
+                                             const int *__restrict__ keys, int *__restrict__ place) {
+    for (int i = threadIdx.x; i < en.n; i += 64 * ME_UP_WAVES)
+        for (int s = l.list[i] * top_k, c = 0; c < top_k; ++c, ++s)
+            if (keys[s] == e) place[s] = en.base + i;
+}
+
 // One block's products of gate and up rows with TT tiles of x, as they lie in LDS.
 template <class E, bool ZP, int G, int TT>
 __device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G, 1> (&w)[2], const u32x4 *xt, f32x4 (&acc)[2][TT]) {
@@ -160,7 +169,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
                                                                 const int *__restrict__ keys,
                                                                 const char *__restrict__ tiles,
                                                                 const typename E::T *__restrict__ x, int64_t ldx,
-                                                                unsigned short *__restrict__ h) {
+                                                                unsigned short *__restrict__ h, int *__restrict__ place) {
     __shared__ u32x4 xt[ME_UP_WAVES][16 * 16];                         // a wave's block of x, then its sums
     __shared__ EntryLds el;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
@@ -176,6 +185,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
     }
     const Entries en = find_entries(n_tok, top_k, e, keys, el);
     if (en.n == 0) return;
+    if (place && blockIdx.x == 0) store_places(top_k, e, en, el, keys, place);
     u32x4 *mine = xt[wv];
     const int piece = lane % 16;
     for (int first = 0; first < en.n; first += 16) {
@@ -238,13 +248,14 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
                                                                      const int *__restrict__ keys,
                                                                      const char *__restrict__ tiles,
                                                                      const typename E::T *__restrict__ x, int64_t ldx,
-                                                                     unsigned short *__restrict__ h) {
+                                                                     unsigned short *__restrict__ h, int *__restrict__ place) {
     constexpr int TN = 16 * TT;
     __shared__ u32x4 xt[2][TN * 16];
     __shared__ EntryLds el;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int e = blockIdx.y, row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 16;
     const Entries en = find_entries(n_tok, top_k, e, keys, el);
+    if (place && blockIdx.x == 0) store_places(top_k, e, en, el, keys, place);
     Q4Rows<ZP, G> rows[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -411,7 +422,7 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
             load(next.unit < units ? next : s, w[1 - a]);               // always, for the waits behind it
             const int in = min(16, s.room - s.first);
             const u32x4 *ht = reinterpret_cast<const u32x4 *>(h + hidden_tile(s.at0 + s.first, n_blk));
-            const int hl = quarter * in + min(lane & 15, in - 1);
+            const int hl = quarter * 3 * in + min(lane & 15, in - 1);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int b = s.p * U + u;
@@ -465,6 +476,155 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
     }
 }
 
+// More choices: an expert's rows of W times its entries, 64 rows for a wave, into
+// z [entries][dim]; k_moe_sum weights and adds them by token.  Up to 5 entries lie
+// with all their parts in one operand of 16 (3 n rows of it, added at the end).
+template <class E, bool ZP, int G, int TT>
+__global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok, int top_k, int n_experts, int dim,
+                                                                       int n_blk, bool by_slot,
+                                                                       const int *__restrict__ keys,
+                                                                       const char *__restrict__ tiles,
+                                                                       const unsigned short *__restrict__ h,
+                                                                       float *__restrict__ z) {
+    constexpr int RT = ME_DOWN_ROWS, PG = G / 32;
+    typedef Q4Op<BF16> Op;
+    __shared__ EntryLds el;
+    __shared__ f32x4 scratch[ME_UP_WAVES][64];
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
+    const int e = __builtin_amdgcn_readfirstlane(expert_of(n_experts, by_slot, keys));
+    if (e < 0) return;
+    const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * (16 * RT);
+    Q4Rows<ZP, G> rows[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        rows[r] = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + 16 * r + (lane & 15), dim - 1), n_blk);
+    const Entries en = find_entries(n_tok, top_k, e, keys, el);
+    // sets of operands: one of 3 n rows, or the three parts of TT tiles
+    auto products = [&](auto sets, const u32x4 *(&at)[decltype(sets)::value],
+                        const int (&step)[(decltype(sets)::value + 2) / 3],
+                        f32x4 (&acc)[RT][(decltype(sets)::value + 2) / 3]) {
+        constexpr int S = decltype(sets)::value, T = (S + 2) / 3;
+        Q4Piece<E, ZP, G, 1> w[2][RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[0][r].load(rows[r], 0);
+        for (int bb = 0; bb < n_blk; bb += 2) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int b = bb + a;
+                if (b >= n_blk) break;
+                u32x4 v[4][S];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int i = 0; i < S; ++i) v[m][i] = at[i][(int64_t)(b * 4 + m) * step[i / 3]];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
+                f32x4 sum[RT][T];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int g = m / PG;
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const u32x4 f = Op::decode(w[a][r].c[0][m], Op::zero(w[a][r].zero(0, g)));
+#pragma unroll
+                        for (int t = 0; t < T; ++t) {
+                            if (m % PG == 0) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int i = (S == 1 ? 0 : 2); i >= 0; --i) sum[r][t] = Op::mfma(v[m][S == 1 ? 0 : 3 * t + i], f, sum[r][t]);
+                        }
+                    }
+                    if ((m + 1) % PG == 0) {
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const float sc = w[a][r].scale(0, g);
+#pragma unroll
+                            for (int t = 0; t < T; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+                        }
+                    }
+                }
+            }
+        }
+    };
+    for (int first = 0; first < en.n; first += 16 * TT) {
+        float *zt = z + (int64_t)(en.base + first) * dim;
+        const int in = min(16, en.room - first);
+        if (in <= 5) {
+            const u32x4 *at[1] = {reinterpret_cast<const u32x4 *>(h + hidden_tile(en.base + first, n_blk)) +
+                                  quarter * 3 * in + min(lane & 15, 3 * in - 1)};
+            f32x4 acc[RT][1];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[r][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const int step[1] = {12 * in};                              // 16-byte pieces of a product's columns
+            products(std::integral_constant<int, 1>{}, at, step, acc);
+            const float *s = reinterpret_cast<const float *>(scratch[wv]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                scratch[wv][lane] = acc[r][0];                          // row i of the operand at lane 16 (i / 4) + column, i % 4
+                auto part = [&](int i, int col) { return s[((i / 4) * 16 + col) * 4 + i % 4]; };
+                for (int o = lane; o < 16 * (en.n - first); o += 64) {
+                    const int i = o / 16, col = o % 16;
+                    if (row0 + 16 * r + col < dim)
+                        zt[(int64_t)i * dim + row0 + 16 * r + col] = (part(2 * in + i, col) + part(in + i, col)) + part(i, col);
+                }
+            }
+        } else {
+            const u32x4 *at[3 * TT];
+            int step[TT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                // a tile that is not there: the one before again, whose sums are not stored
+                const int f = first + 16 * t < en.n ? first + 16 * t : first, nt = min(16, en.room - f);
+                step[t] = 12 * nt;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    at[3 * t + i] = reinterpret_cast<const u32x4 *>(h + hidden_tile(en.base + f, n_blk)) +
+                                    (quarter * 3 + i) * nt + min(lane & 15, nt - 1);
+            }
+            f32x4 acc[RT][TT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            products(std::integral_constant<int, 3 * TT>{}, at, step, acc);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int row = row0 + 16 * r + (lane & 15);
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = 16 * t + 4 * quarter + i;
+                        if (row < dim && first + k < en.n) zt[(int64_t)k * dim + row] = acc[r][t][i];
+                    }
+            }
+        }
+    }
+}
+
+// y[t] = sum over c (ascending) of weights[t, c] * z[place[t, c]].
+template <class E>
+__global__ __launch_bounds__(256) void k_moe_sum(int n_tok, int top_k, int n_experts, int dim, int pieces,
+                                                 const int *__restrict__ keys, const float *__restrict__ weights,
+                                                 const int *__restrict__ place, const float *__restrict__ z,
+                                                 void *__restrict__ y, bool f32, int64_t ldy) {
+    const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int t = (int)(id / pieces), col = (int)(id - (int64_t)t * pieces) * 64 + __lane_id();
+    if (t >= n_tok) return;
+    const int c0 = min(col, dim - 1);
+    float v = 0.0f;
+    for (int s = t * top_k, c = 0; c < top_k; ++c, ++s) {
+        const int e = keys[s];
+        if ((unsigned)e < (unsigned)n_experts) v = fmaf(weights ? weights[s] : 1.0f, z[(int64_t)place[s] * dim + c0], v);
+    }
+    if (col >= dim) return;
+    if (f32)
+        static_cast<float *>(y)[t * ldy + col] = v;
+    else
+        static_cast<typename E::T *>(y)[t * ldy + col] = (typename E::T)v;
+}
+
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
@@ -477,6 +637,21 @@ spmv_status check_slots(int32_t n_tok, int32_t top_k, int32_t inter) {
 }
 int64_t hidden_ld(int32_t inter) { return q4_blocks(inter) * Q4_BLOCK; }
 
+// The workspace's parts: h; beyond ME_FEW_SLOTS choices also z and every choice's place in it.
+struct Parts {
+    size_t z, place, total;
+};
+Parts parts_of(int64_t n_tok, int64_t top_k, int64_t dim, int64_t inter) {
+    const size_t slots = (size_t)(n_tok * top_k);
+    Parts p = {slots * (size_t)hidden_ld((int32_t)inter) * 6, 0, 0};
+    p.total = p.z;
+    if (slots > ME_FEW_SLOTS) {
+        p.place = p.z + slots * (size_t)dim * 4;
+        p.total = p.place + slots * 4;
+    }
+    return p;
+}
+
 size_t down_lds(int waves, int n_tok, int top_k, int n_experts) {
     const size_t slots = (size_t)n_tok * top_k;
     return (size_t)waves * n_tok * 64 + slots * 8 + ((size_t)n_experts + 1) * 4 + std::min<size_t>(slots, n_experts) * 4;
@@ -487,11 +662,13 @@ size_t down_lds(int waves, int n_tok, int top_k, int n_experts) {
 
 using namespace spmv;
 
-extern "C" spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t inter, size_t *bytes) {
+extern "C" spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t dim, int32_t inter, size_t *bytes) {
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
     const spmv_status st = check_slots(n_tok, top_k, inter);
     if (st != SPMV_OK) return st;
-    *bytes = (size_t)n_tok * top_k * hidden_ld(inter) * 3 * 2;
+    if (dim < 1) return fail(SPMV_ERR_INVALID_VALUE, "dim must be >= 1");
+    const Parts p = parts_of(n_tok, top_k, dim, inter);
+    *bytes = p.total;
     return SPMV_OK;
 }
 
@@ -500,9 +677,9 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
                                  const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x, int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, void *stream) {
     size_t need = 0;
-    spmv_status st = moe_workspace_size(n_tok, top_k, inter, &need);
+    spmv_status st = moe_workspace_size(n_tok, top_k, dim, inter, &need);
     if (st != SPMV_OK) return st;
-    if (n_experts < 1 || dim < 1) return fail(SPMV_ERR_INVALID_VALUE, "n_experts and dim must be >= 1");
+    if (n_experts < 1) return fail(SPMV_ERR_INVALID_VALUE, "n_experts must be >= 1");
     if (dim < 8) return fail(SPMV_ERR_UNSUPPORTED, "layers of a width below 8 are not supported");
     if (n_experts > ME_MAX_EXPERTS) return fail(SPMV_ERR_UNSUPPORTED, "more than %d experts are not supported", ME_MAX_EXPERTS);
     if (!q4_group_ok(group)) return fail(SPMV_ERR_INVALID_VALUE, "group must be 32, 64 or 128, not %d", group);
@@ -535,8 +712,13 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     const int rows = ceil_div(dim, 16) < 256 ? 8 : 16;
     st = check_grid(ceil_div(dim, rows), 1024);
     if (st != SPMV_OK) return st;
-    // a wave's sums take 64 bytes per token
-    const int waves = n_tok <= 64 ? 16 : n_tok <= 128 || down_lds(8, n_tok, top_k, n_experts) <= ME_LDS ? 8 : 4;
+    const Parts p = parts_of(n_tok, top_k, dim, inter);
+    const bool tile_down = slots > ME_FEW_SLOTS;
+    const int64_t down_grid = ceil_div(dim, 16 * ME_DOWN_ROWS * ME_UP_WAVES), pieces = ceil_div(dim, 64);
+    st = check_grid(down_grid * groups, 64 * ME_UP_WAVES);
+    if (st != SPMV_OK) return st;
+    float *z = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.z);
+    int *place = tile_down ? reinterpret_cast<int *>(static_cast<char *>(workspace) + p.place) : nullptr;
     hipStream_t s = as_stream(stream);
     unsigned short *h = static_cast<unsigned short *>(workspace);
     auto launch = [&](auto e, auto zp, auto g) -> spmv_status {
@@ -547,12 +729,12 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         auto up = [&](auto tt) {
             k_moe_up_tile<E, ZP, G, decltype(tt)::value><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
                 n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, keys, static_cast<const char *>(up_tiles),
-                static_cast<const T *>(x), ldx, h);
+                static_cast<const T *>(x), ldx, h, place);
         };
         if (!tile_up)
             k_moe_up<E, ZP, G><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
                 n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, parts, by_slot, keys,
-                static_cast<const char *>(up_tiles), static_cast<const T *>(x), ldx, h);
+                static_cast<const char *>(up_tiles), static_cast<const T *>(x), ldx, h, place);
         else if (slots <= 24 * groups)
             up(std::integral_constant<int, 2>{});
         else if (slots <= 40 * groups)
@@ -560,10 +742,26 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         else
             up(std::integral_constant<int, 4>{});
         SPMV_LAUNCHED("k_moe_up");
-        k_moe_down<E, ZP, G><<<(int)ceil_div(dim, rows), 64 * waves, down_lds(waves, n_tok, top_k, n_experts), s>>>(
-            n_tok, top_k, n_experts, dim, rows, down_blk, keys, weights, static_cast<const char *>(down_tiles), h, y,
-            y_dtype == SPMV_F32, ldy);
-        SPMV_LAUNCHED("k_moe_down");
+        if (!tile_down) {
+            k_moe_down<E, ZP, G><<<(int)ceil_div(dim, rows), 1024, down_lds(16, n_tok, top_k, n_experts), s>>>(
+                n_tok, top_k, n_experts, dim, rows, down_blk, keys, weights, static_cast<const char *>(down_tiles), h, y,
+                y_dtype == SPMV_F32, ldy);
+            SPMV_LAUNCHED("k_moe_down");
+            return SPMV_OK;
+        }
+        auto down = [&](auto tt) {
+            k_moe_down_tile<E, ZP, G, decltype(tt)::value>
+                <<<dim3((unsigned)down_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
+                    n_tok, top_k, n_experts, dim, down_blk, by_slot, keys, static_cast<const char *>(down_tiles), h, z);
+        };
+        if (slots <= 12 * groups)
+            down(std::integral_constant<int, 1>{});
+        else
+            down(std::integral_constant<int, 2>{});
+        SPMV_LAUNCHED("k_moe_down_tile");
+        k_moe_sum<E><<<(int)ceil_div(n_tok * pieces, 4), 256, 0, s>>>(n_tok, top_k, n_experts, dim, (int)pieces, keys,
+                                                                   weights, place, z, y, y_dtype == SPMV_F32, ldy);
+        SPMV_LAUNCHED("k_moe_sum");
         return SPMV_OK;
     };
     auto by_group = [&](auto e, auto z) {

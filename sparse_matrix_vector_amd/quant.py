@@ -143,8 +143,8 @@ class Q4Matrix:
 # ---------------------------------------------------------------------------
 # A layer of experts for a few tokens
 # ---------------------------------------------------------------------------
-def moe_workspace_size(n_tok, top_k, inter) -> int:
-    return _size("moe_workspace_size", ctypes.c_size_t, n_tok, top_k, inter)
+def moe_workspace_size(n_tok, top_k, dim, inter) -> int:
+    return _size("moe_workspace_size", ctypes.c_size_t, n_tok, top_k, dim, inter)
 
 
 def moe_apply(keys, weights, gate_up, down, x, y, workspace, stream=None):

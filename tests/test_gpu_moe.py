@@ -27,7 +27,7 @@ class Layer:
 
     def __call__(self, keys, w, x, y=None):
         y = torch.full((x.shape[0], self.dim), float("nan"), device="cuda") if y is None else y
-        ws = torch.empty(S.moe_workspace_size(keys.shape[0], keys.shape[1], self.inter), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(S.moe_workspace_size(keys.shape[0], keys.shape[1], self.dim, self.inter), dtype=torch.uint8, device="cuda")
         ws.fill_(255)
         return S.moe_apply(keys, w, self.gu, self.dn, x, y, ws)
 
@@ -148,7 +148,7 @@ def test_captured_and_replayed():
     m = Layer(8, 256, 192, 64, "f16", True, seed=2)
     keys, w, x = _batch(24, 2, 8, 256, "f16", 1)
     y = torch.empty(24, 256, dtype=torch.float16, device="cuda")
-    ws = torch.empty(S.moe_workspace_size(24, 2, 192), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(S.moe_workspace_size(24, 2, 256, 192), dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):

@@ -86,7 +86,7 @@ def _moe(n=4, k=2, e=8, dim=64, inter=96, group=32, zp=0, keys=P, w=None, up=P, 
          ldy=64, ws=P, wsb=None):
     if wsb is None:
         z = ctypes.c_size_t()
-        S.lib().moe_workspace_size(n, k, inter, ctypes.byref(z))
+        S.lib().moe_workspace_size(n, k, dim, inter, ctypes.byref(z))
         wsb = z.value
     return S.lib().moe_apply(n, k, e, dim, inter, group, zp, keys, w, up, dn, dt, x, ldx, y, ydt, ldy, ws, wsb, None)
 
@@ -101,15 +101,15 @@ def test_moe_refusals():
     for p in ("keys", "up", "dn", "x", "y", "ws"):
         assert _moe(**{p: None}) == VALUE, p
     assert _moe(up=P + 8) == UNSUPPORTED and _moe(dn=P + 8) == UNSUPPORTED and _moe(ws=P + 8) == UNSUPPORTED
-    assert _moe(wsb=S.moe_workspace_size(4, 2, 96) - 1) == VALUE
+    assert _moe(wsb=S.moe_workspace_size(4, 2, 64, 96) - 1) == VALUE
     assert b"workspace" in S.lib().spmv_last_error()
     assert _moe(dim=2 ** 31 - 1, ldx=2 ** 31, ldy=2 ** 31) == OVERFLOW
     assert _moe(n=0, keys=None, x=None, y=None, ws=None) == OK
     z = ctypes.c_size_t()
     L = S.lib()
-    assert L.moe_workspace_size(4, 2, 96, None) == VALUE and L.moe_workspace_size(-1, 2, 96, ctypes.byref(z)) == VALUE
-    assert L.moe_workspace_size(4, 0, 96, ctypes.byref(z)) == VALUE and L.moe_workspace_size(4, 2, 0, ctypes.byref(z)) == VALUE
-    assert S.moe_workspace_size(0, 1, 5) == 0
+    assert L.moe_workspace_size(4, 2, 64, 96, None) == VALUE and L.moe_workspace_size(-1, 2, 64, 96, ctypes.byref(z)) == VALUE
+    assert L.moe_workspace_size(4, 0, 64, 96, ctypes.byref(z)) == VALUE and L.moe_workspace_size(4, 2, 64, 0, ctypes.byref(z)) == VALUE
+    assert S.moe_workspace_size(0, 1, 9, 5) == 0 and L.moe_workspace_size(4, 2, 0, 8, ctypes.byref(z)) == VALUE
 
 
 def _lookup(n=4, v=10, dim=8, dt=F16, ids=P, t=P, ldt=8, y=P, ydt=F16, ldy=8):
