@@ -158,7 +158,7 @@ def prepare(case, seed):
         if own:
             s["gu"] = S.Q4Matrix(2 * f, d, *s["gate_up"], group=case["group"], n_groups=e)
             s["dn"] = S.Q4Matrix(d, f, *s["down"], group=case["group"], n_groups=e)
-            s["ws"] = torch.empty(S.moe_workspace_size(t, k, f), dtype=torch.uint8, device=dev)
+            s["ws"] = torch.empty(S.moe_workspace_size(t, k, d, f), dtype=torch.uint8, device=dev)
         return s
     s["ids"] = _ids(case, g, dev)
     s["scale"] = math.sqrt(case["dim"])
