@@ -32,7 +32,6 @@ constexpr int ME_MAX_TOK = 256;
 constexpr int ME_MAX_SLOTS = 4096;
 constexpr int ME_MAX_EXPERTS = 1024;
 constexpr int ME_UP_WAVES = 4;
-constexpr int ME_DOWN_ROWS = 4;      // row tiles of a wave of the down product by experts
 constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
 constexpr int ME_UNROLL = 2;         // blocks whose codes a wave of the down product loads at once
 constexpr int ME_UNITS = 2;          // units of a wave of the down product, about
@@ -476,9 +475,11 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
     }
 }
 
-// More choices: an expert's rows of W times its entries, 64 rows for a wave, into
-// z [entries][dim]; k_moe_sum weights and adds them by token.  Up to 5 entries lie
-// with all their parts in one operand of 16 (3 n rows of it, added at the end).
+// More choices: an expert's rows of W times its entries, 32 rows for a wave, into
+// z [entries][dim]; k_moe_sum weights and adds them by token.  The waves of a
+// workgroup share the block of h of 16 TT entries, which lies in memory as it is
+// read.  Up to 5 entries lie with all their parts in one operand of 16 (3 n rows of
+// it, added at the end).
 template <class E, bool ZP, int G, int TT>
 __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok, int top_k, int n_experts, int dim,
                                                                        int n_blk, bool by_slot,
@@ -486,110 +487,143 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                                                                        const char *__restrict__ tiles,
                                                                        const unsigned short *__restrict__ h,
                                                                        float *__restrict__ z) {
-    constexpr int RT = ME_DOWN_ROWS, PG = G / 32;
+    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT;  // 48 pieces of 16 bytes of an entry's block
     typedef Q4Op<BF16> Op;
+    __shared__ u32x4 ht[2][48 * 16 * TT];
     __shared__ EntryLds el;
-    __shared__ f32x4 scratch[ME_UP_WAVES][64];
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
     const int e = __builtin_amdgcn_readfirstlane(expert_of(n_experts, by_slot, keys));
     if (e < 0) return;
-    const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * (16 * RT);
-    Q4Rows<ZP, G> rows[RT];
+    const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 32;
+    Q4Rows<ZP, G> rows[2];
+    Q4Piece<E, ZP, G, 1> w[2][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < 2; ++r) {
         rows[r] = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + 16 * r + (lane & 15), dim - 1), n_blk);
+        w[0][r].load(rows[r], 0);                                       // on its way while the entries are found
+    }
     const Entries en = find_entries(n_tok, top_k, e, keys, el);
-    // sets of operands: one of 3 n rows, or the three parts of TT tiles
-    auto products = [&](auto sets, const u32x4 *(&at)[decltype(sets)::value],
-                        const int (&step)[(decltype(sets)::value + 2) / 3],
-                        f32x4 (&acc)[RT][(decltype(sets)::value + 2) / 3]) {
-        constexpr int S = decltype(sets)::value, T = (S + 2) / 3;
-        Q4Piece<E, ZP, G, 1> w[2][RT];
+    for (int first = 0; first < en.n; first += 16 * TT) {
+        // the pieces of this turn's tiles: a block of a tile of n entries is 48 n of them in a row
+        int n_of[TT], from[TT + 1];
+        from[0] = 0;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) w[0][r].load(rows[r], 0);
+        for (int t = 0; t < TT; ++t) {
+            n_of[t] = first + 16 * t < en.n ? min(16, en.room - first - 16 * t) : 0;
+            from[t + 1] = from[t] + 48 * n_of[t];
+        }
+        const u32x4 *src[Q];
+        int step[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int c = min((int)threadIdx.x + THREADS * q, from[TT] - 1);
+            int t = 0;
+#pragma unroll
+            for (int k = 1; k < TT; ++k) t += c >= from[k];
+            int n = n_of[0], f = from[0];
+#pragma unroll
+            for (int k = 1; k < TT; ++k)
+                if (t == k) n = n_of[k], f = from[k];
+            src[q] = reinterpret_cast<const u32x4 *>(h + hidden_tile(en.base + first + 16 * t, n_blk)) + (c - f);
+            step[q] = 48 * n;
+        }
+        auto load_h = [&](int b, u32x4 (&v)[Q]) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) v[q] = src[q][(int64_t)b * step[q]];
+        };
+        auto keep_h = [&](u32x4 *to, const u32x4 (&v)[Q]) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if ((int)threadIdx.x + THREADS * q < from[TT]) to[threadIdx.x + THREADS * q] = v[q];
+        };
+        const bool packed = from[TT] <= 48 * 5;
+        f32x4 acc[2][TT];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        u32x4 v[Q];
+        load_h(0, v);
+        if (first > 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
+        }
+        keep_h(ht[0], v);
+        __syncthreads();
         for (int bb = 0; bb < n_blk; bb += 2) {
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
-                u32x4 v[4][S];
+                load_h(min(b + 1, n_blk - 1), v);
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int i = 0; i < S; ++i) v[m][i] = at[i][(int64_t)(b * 4 + m) * step[i / 3]];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
-                f32x4 sum[RT][T];
+                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4 sum[2][TT];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const int g = m / PG;
+                    const int g = m / PG, p = 3 * (4 * m + quarter);
+                    u32x4 f[2];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const u32x4 f = Op::decode(w[a][r].c[0][m], Op::zero(w[a][r].zero(0, g)));
+                    for (int r = 0; r < 2; ++r) {
+                        f[r] = Op::decode(w[a][r].c[0][m], Op::zero(w[a][r].zero(0, g)));
+                        if (m % PG == 0) {
 #pragma unroll
-                        for (int t = 0; t < T; ++t) {
-                            if (m % PG == 0) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                            for (int i = (S == 1 ? 0 : 2); i >= 0; --i) sum[r][t] = Op::mfma(v[m][S == 1 ? 0 : 3 * t + i], f, sum[r][t]);
+                            for (int t = 0; t < TT; ++t) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                         }
+                    }
+                    if (packed) {
+                        const u32x4 x = ht[a][p * n_of[0] + min(lane & 15, 3 * n_of[0] - 1)];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) sum[r][0] = Op::mfma(x, f[r], sum[r][0]);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+                            if (n_of[t] > 0) {
+                                const u32x4 *at = ht[a] + from[t] + p * n_of[t] + min(lane & 15, n_of[t] - 1);
+#pragma unroll
+                                for (int i = 2; i >= 0; --i) {
+                                    const u32x4 x = at[i * n_of[t]];
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) sum[r][t] = Op::mfma(x, f[r], sum[r][t]);
+                                }
+                            }
                     }
                     if ((m + 1) % PG == 0) {
 #pragma unroll
-                        for (int r = 0; r < RT; ++r) {
+                        for (int r = 0; r < 2; ++r) {
                             const float sc = w[a][r].scale(0, g);
 #pragma unroll
-                            for (int t = 0; t < T; ++t)
+                            for (int t = 0; t < TT; ++t)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
                         }
                     }
                 }
+                keep_h(ht[1 - a], v);
+                __syncthreads();
             }
         }
-    };
-    for (int first = 0; first < en.n; first += 16 * TT) {
         float *zt = z + (int64_t)(en.base + first) * dim;
-        const int in = min(16, en.room - first);
-        if (in <= 5) {
-            const u32x4 *at[1] = {reinterpret_cast<const u32x4 *>(h + hidden_tile(en.base + first, n_blk)) +
-                                  quarter * 3 * in + min(lane & 15, 3 * in - 1)};
-            f32x4 acc[RT][1];
+        if (packed) {
+            // row i of the operand, column col: lane 16 (i / 4) + col, i % 4
+            f32x4 *mine = reinterpret_cast<f32x4 *>(ht[0]) + wv * 64;
+            const float *s = reinterpret_cast<const float *>(mine);
+            const int n = n_of[0];
+            auto part = [&](int i, int col) { return s[((i / 4) * 16 + col) * 4 + i % 4]; };
 #pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            const int step[1] = {12 * in};                              // 16-byte pieces of a product's columns
-            products(std::integral_constant<int, 1>{}, at, step, acc);
-            const float *s = reinterpret_cast<const float *>(scratch[wv]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                scratch[wv][lane] = acc[r][0];                          // row i of the operand at lane 16 (i / 4) + column, i % 4
-                auto part = [&](int i, int col) { return s[((i / 4) * 16 + col) * 4 + i % 4]; };
+            for (int r = 0; r < 2; ++r) {
+                mine[lane] = acc[r][0];
                 for (int o = lane; o < 16 * (en.n - first); o += 64) {
                     const int i = o / 16, col = o % 16;
                     if (row0 + 16 * r + col < dim)
-                        zt[(int64_t)i * dim + row0 + 16 * r + col] = (part(2 * in + i, col) + part(in + i, col)) + part(i, col);
+                        zt[(int64_t)i * dim + row0 + 16 * r + col] = (part(2 * n + i, col) + part(n + i, col)) + part(i, col);
                 }
             }
+            __syncthreads();
         } else {
-            const u32x4 *at[3 * TT];
-            int step[TT];
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                // a tile that is not there: the one before again, whose sums are not stored
-                const int f = first + 16 * t < en.n ? first + 16 * t : first, nt = min(16, en.room - f);
-                step[t] = 12 * nt;
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    at[3 * t + i] = reinterpret_cast<const u32x4 *>(h + hidden_tile(en.base + f, n_blk)) +
-                                    (quarter * 3 + i) * nt + min(lane & 15, nt - 1);
-            }
-            f32x4 acc[RT][TT];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            products(std::integral_constant<int, 3 * TT>{}, at, step, acc);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < 2; ++r) {
                 const int row = row0 + 16 * r + (lane & 15);
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
@@ -714,7 +748,7 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     if (st != SPMV_OK) return st;
     const Parts p = parts_of(n_tok, top_k, dim, inter);
     const bool tile_down = slots > ME_FEW_SLOTS;
-    const int64_t down_grid = ceil_div(dim, 16 * ME_DOWN_ROWS * ME_UP_WAVES), pieces = ceil_div(dim, 64);
+    const int64_t down_grid = ceil_div(dim, 32 * ME_UP_WAVES), pieces = ceil_div(dim, 64);
     st = check_grid(down_grid * groups, 64 * ME_UP_WAVES);
     if (st != SPMV_OK) return st;
     float *z = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.z);
@@ -756,8 +790,10 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         };
         if (slots <= 12 * groups)
             down(std::integral_constant<int, 1>{});
-        else
+        else if (slots <= 24 * groups)
             down(std::integral_constant<int, 2>{});
+        else
+            down(std::integral_constant<int, 3>{});
         SPMV_LAUNCHED("k_moe_down_tile");
         k_moe_sum<E><<<(int)ceil_div(n_tok * pieces, 4), 256, 0, s>>>(n_tok, top_k, n_experts, dim, (int)pieces, keys,
                                                                    weights, place, z, y, y_dtype == SPMV_F32, ldy);
