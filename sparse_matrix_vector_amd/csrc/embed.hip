@@ -15,9 +15,22 @@ namespace spmv {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Lookup: a wave moves one piece of a token's row, 16 bytes per lane and access
-// (the last access of a row starts early where the width is no multiple of it).
+// Lookup: a wave moves one piece of a token's row, 16 bytes of the result per lane
+// and access, so that every store of a wave fills whole cache lines (the last
+// access of a row starts early where the width is no multiple of it).
 // ---------------------------------------------------------------------------
+// N elements at any element's address.
+template <typename E, int N>
+__device__ __forceinline__ Vec<E, N> load_row(const typename E::T *p) {
+    if constexpr (sizeof(Vec<E, N>) == 16) {
+        return load_any<E, N>(p);
+    } else {
+        Vec<E, N> v;
+        __builtin_memcpy(&v, __builtin_assume_aligned(p, sizeof(typename E::T)), sizeof v);
+        return v;
+    }
+}
+
 template <typename E, typename Y, int VEC>
 __global__ __launch_bounds__(256) void k_embed_lookup(int n_tok, int n_vocab, int dim, int pieces,
                                                       const int *__restrict__ ids,
@@ -36,25 +49,17 @@ __global__ __launch_bounds__(256) void k_embed_lookup(int n_tok, int n_vocab, in
     Vec<E, VEC> v[U];
     if (known) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = load_any<E, VEC>(src + min(c0 + u * 64 * VEC, dim - VEC));
+        for (int u = 0; u < U; ++u) v[u] = load_row<E, VEC>(src + min(c0 + u * 64 * VEC, dim - VEC));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int c = c0 + u * 64 * VEC;
         if (c >= dim) continue;
         typename Y::T *d = dst + min(c, dim - VEC);
-        if constexpr (VEC == 1) {
-            *d = (typename Y::T)(known ? scale * (float)v[u].v[0] : 0.0f);
-        } else {
-            constexpr int N = 16 / sizeof(typename Y::T);            // elements of a store
+        Vec<Y, VEC> o;
 #pragma unroll
-            for (int p = 0; p < VEC; p += N) {
-                Vec<Y, N> o;
-#pragma unroll
-                for (int i = 0; i < N; ++i) o.v[i] = (typename Y::T)(known ? scale * (float)v[u].v[p + i] : 0.0f);
-                store_once<Y, N>(d + p, o);
-            }
-        }
+        for (int i = 0; i < VEC; ++i) o.v[i] = (typename Y::T)(known ? scale * (float)v[u].v[i] : 0.0f);
+        store_once<Y, VEC>(d, o);
     }
 }
 
@@ -68,7 +73,7 @@ constexpr int ER_BITS = 8;
 constexpr int ER_BINS = 1 << ER_BITS;
 constexpr int ER_MAX_TOK = 1 << 22;
 
-__device__ __forceinline__ int id_key(int id, int n_vocab) { return (unsigned)id < (unsigned)n_vocab ? id : n_vocab; }
+__device__ __forceinline__ int id_key(int id, int n_vocab) { return (int)min((unsigned)id, (unsigned)n_vocab); }
 
 // A token's place is the number of tokens with a smaller id, or with its id and
 // before it.  A workgroup ranks 64 tokens, and its waves compare them with a part
@@ -82,14 +87,23 @@ __global__ __launch_bounds__(1024) void k_embed_rank(int n_tok, int n_vocab, con
     const int per = (n_tok + 15) / 16;
     const int a = min(wv * per, n_tok), b = min(a + per, n_tok);
     int c = 0;
-    // tokens before the 64 count if their id is at most the lane's, those after if it is smaller
+    // tokens before the 64 count if their id is at most the lane's, those after if it is
+    // smaller, that is, at most the lane's less 1; 16 ids at a time, in scalar registers
+    auto at_most = [&](int from, int to, int limit) {
+        int i = from;
+        for (; i + 16 <= to; i += 16) {
+            int k[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) k[j] = id_key(ids[i + j], n_vocab);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) c += k[j] <= limit;
+        }
+        for (; i < to; ++i) c += id_key(ids[i], n_vocab) <= limit;
+    };
     const int b1 = max(a, min(b, t0)), a2 = min(b, max(a, t0 + 64));
-    for (int i = a; i < b1; ++i) c += id_key(ids[i], n_vocab) <= key;
-    for (int i = b1; i < a2; ++i) {
-        const int k = id_key(ids[i], n_vocab);
-        c += k < key || (k == key && i < t);
-    }
-    for (int i = a2; i < b; ++i) c += id_key(ids[i], n_vocab) < key;
+    at_most(a, b1, key);
+    for (int i = b1; i < a2; ++i) c += id_key(ids[i], n_vocab) <= (i < t ? key : key - 1);
+    at_most(a2, b, key - 1);
     count[wv][lane] = c;
     __syncthreads();
     if (wv == 0 && t < n_tok) {
@@ -269,35 +283,41 @@ __global__ __launch_bounds__(256) void k_embed_sum(int n_tok, int n_vocab, int d
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
     bool begun = p0 > 0 && sorted[p0 - 1] == sorted[p0];           // the run began before the block
-    for (int p = p0; p < p1; p += U) {
-        Vec<E, VEC> v[U];
-        int key[U + 1];
+    for (int q0 = p0; q0 < p1; q0 += 64) {
+        // a lane holds one of 64 positions: its id, its token, whether its run ends there
+        const int q = min(q0 + lane, n_tok - 1);
+        const int key = sorted[q], tok = order[q];
+        const int after = q + 1 < n_tok ? sorted[q + 1] : -1;
+        const unsigned long long last = __ballot(after != key);
+        // ids outside the vocabulary come last, and their rows are not read
+        const int n = __popcll(__ballot(q0 + lane < p1 && key < n_vocab));
+        for (int j = 0; j < n; j += U) {
+            Vec<E, VEC> v[U];
 #pragma unroll
-        for (int u = 0; u <= U; ++u) key[u] = p + u < n_tok ? sorted[min(p + u, n_tok - 1)] : -1;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int q = min(p + u, p1 - 1);
-            // the rows of dropped tokens are not read
-            if (in && p + u < p1 && key[u] < n_vocab) v[u] = load_once<E, VEC>(src + (int64_t)order[q] * lddy);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (p + u >= p1 || key[u] >= n_vocab) continue;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] += (float)v[u].v[i];
-            const bool last = p + u + 1 == p1, ends = key[u + 1] != key[u];
-            if (!ends && !last) continue;
-            if (in) {
-                if (begun || !ends) {
-                    float *d = heads + ((int64_t)(begun ? 0 : n_blocks) + blk) * dim + at;
-                    add_row<VEC>(d, acc, c - at, 1.0f, false);
-                } else {
-                    add_row<VEC>(table + (int64_t)key[u] * ldt + at, acc, c - at, scale, add);
-                }
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = __builtin_amdgcn_readlane(tok, min(j + u, n - 1));
+                v[u] = load_once<E, VEC>(src + t * lddy);
             }
-            begun = false;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+            for (int u = 0; u < U; ++u) {
+                if (j + u >= n) break;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] += (float)v[u].v[i];
+                const bool ends = (last >> (j + u)) & 1;
+                if (!ends && q0 + j + u + 1 < p1) continue;
+                if (in) {
+                    if (begun || !ends) {
+                        float *d = heads + ((int64_t)(begun ? 0 : n_blocks) + blk) * dim + at;
+                        add_row<VEC>(d, acc, c - at, 1.0f, false);
+                    } else {
+                        const int64_t row = __builtin_amdgcn_readlane(key, j + u);
+                        add_row<VEC>(table + row * ldt + at, acc, c - at, scale, add);
+                    }
+                }
+                begun = false;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+            }
         }
     }
 }
@@ -403,7 +423,7 @@ extern "C" spmv_status embed_lookup(int32_t n_tok, int32_t n_vocab, int32_t dim,
     if (dtype == SPMV_F32) return dim >= 4 ? run(F32{}, F32{}, four) : run(F32{}, F32{}, one);
     auto half = [&](auto e) {
         typedef decltype(e) E;
-        if (y_dtype == SPMV_F32) return dim >= 8 ? run(E{}, F32{}, eight) : run(E{}, F32{}, one);
+        if (y_dtype == SPMV_F32) return dim >= 4 ? run(E{}, F32{}, four) : run(E{}, F32{}, one);
         return dim >= 8 ? run(E{}, E{}, eight) : run(E{}, E{}, one);
     };
     return dtype == SPMV_F16 ? half(F16{}) : half(BF16{});

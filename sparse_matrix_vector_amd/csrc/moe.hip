@@ -773,8 +773,10 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
             up(std::integral_constant<int, 2>{});
         else if (slots <= 40 * groups)
             up(std::integral_constant<int, 3>{});
-        else
+        else if constexpr (G == 128 && !ZP)
             up(std::integral_constant<int, 4>{});
+        else                                               // more need more registers than there are
+            up(std::integral_constant<int, 3>{});
         SPMV_LAUNCHED("k_moe_up");
         if (!tile_down) {
             k_moe_down<E, ZP, G><<<(int)ceil_div(dim, rows), 1024, down_lds(16, n_tok, top_k, n_experts), s>>>(
@@ -792,8 +794,10 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
             down(std::integral_constant<int, 1>{});
         else if (slots <= 24 * groups)
             down(std::integral_constant<int, 2>{});
-        else
+        else if constexpr (G == 128 && !ZP)
             down(std::integral_constant<int, 3>{});
+        else
+            down(std::integral_constant<int, 2>{});
         SPMV_LAUNCHED("k_moe_down_tile");
         k_moe_sum<E><<<(int)ceil_div(n_tok * pieces, 4), 256, 0, s>>>(n_tok, top_k, n_experts, dim, (int)pieces, keys,
                                                                    weights, place, z, y, y_dtype == SPMV_F32, ldy);
