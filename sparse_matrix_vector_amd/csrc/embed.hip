@@ -75,12 +75,43 @@ constexpr int ER_MAX_TOK = 1 << 22;
 
 __device__ __forceinline__ int id_key(int id, int n_vocab) { return (int)min((unsigned)id, (unsigned)n_vocab); }
 
+// The gradient's table is cleared beside the sort, by workgroups of the sort's first
+// launch that have no part in it: writing the table takes longer than sorting, and
+// the rows that have tokens are few.
+constexpr int EG_CLEAR = 16384;      // numbers that a workgroup clears
+struct Fill {
+    float *table;
+    int64_t ld, rows;
+    int dim, first, blocks;       // the first of those workgroups, and how many there are
+};
+__device__ __forceinline__ void clear_rows(const Fill &f) {
+    const int64_t blk = (int)blockIdx.x - f.first;
+    if (f.ld == f.dim || f.rows <= 1) {
+        // EG_CLEAR numbers for a workgroup, one after another
+        const int64_t n = f.rows * f.dim, from = blk * EG_CLEAR, to = min(n, from + EG_CLEAR);
+        for (int64_t i = from + 4 * (int64_t)threadIdx.x; i < to; i += 4096) {
+            if (i + 4 <= to)
+                store_any<F32, 4>(f.table + i, Vec<F32, 4>{{0.0f, 0.0f, 0.0f, 0.0f}});
+            else
+                for (int64_t k = i; k < to; ++k) f.table[k] = 0.0f;
+        }
+    } else {
+        // a wave clears a row at a time
+        for (int64_t r = blk * 16 + threadIdx.x / 64; r < f.rows; r += (int64_t)f.blocks * 16)
+            for (int c = (int)(threadIdx.x % 64); c < f.dim; c += 64) f.table[r * f.ld + c] = 0.0f;
+    }
+}
+
 // A token's place is the number of tokens with a smaller id, or with its id and
 // before it.  A workgroup ranks 64 tokens, and its waves compare them with a part
 // of all tokens each; the other side of a comparison is the same for all lanes.
 __global__ __launch_bounds__(1024) void k_embed_rank(int n_tok, int n_vocab, const int *__restrict__ ids,
-                                                     int *__restrict__ sorted, int *__restrict__ order) {
+                                                     int *__restrict__ sorted, int *__restrict__ order, Fill fill) {
     __shared__ int count[16][64];
+    if ((int)blockIdx.x >= fill.first) {
+        clear_rows(fill);
+        return;
+    }
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int t0 = blockIdx.x * 64, t = t0 + lane;
     const int key = id_key(ids[min(t, n_tok - 1)], n_vocab);
@@ -118,8 +149,12 @@ __global__ __launch_bounds__(1024) void k_embed_rank(int n_tok, int n_vocab, con
 // More tokens: a stable sort by digits of 8 bits, lowest first.  counts[digit][chunk].
 template <bool FIRST>
 __global__ __launch_bounds__(1024) void k_embed_count(int n_tok, int n_vocab, int shift, int chunks,
-                                                      const int *__restrict__ keys, int *__restrict__ counts) {
+                                                      const int *__restrict__ keys, int *__restrict__ counts, Fill fill) {
     __shared__ int hist[ER_BINS];
+    if ((int)blockIdx.x >= fill.first) {
+        clear_rows(fill);
+        return;
+    }
     if (threadIdx.x < ER_BINS) hist[threadIdx.x] = 0;
     __syncthreads();
     const int s0 = blockIdx.x * ER_CHUNK, s1 = min(n_tok, s0 + ER_CHUNK);
@@ -208,7 +243,6 @@ __global__ __launch_bounds__(1024) void k_embed_scatter(int n_tok, int n_vocab, 
 // ---------------------------------------------------------------------------
 constexpr int EG_MIN = 16;           // sorted positions of a block at least
 constexpr int EG_BLOCKS = 4096;      // blocks at most
-constexpr int EG_FILL = 4;           // table rows that a wave looks up and clears
 
 // d[0 .. VEC) (+)= scale * v; the first `skip` elements, which the lane before has, are left out.
 template <int VEC>
@@ -229,22 +263,6 @@ __device__ __forceinline__ void add_row(float *d, const float (&v)[VEC], int ski
     }
 }
 
-// Where v is first found in sorted[0 .. n), by 16 lanes each for a v of its own.
-__device__ __forceinline__ int first_at(const int *__restrict__ sorted, int n, int v) {
-    const int l = __lane_id() & 15;
-    int lo = 0, hi = n;
-    while (__ballot(lo < hi)) {
-        const int s = max(1, (hi - lo + 15) / 16);
-        const int64_t i = (int64_t)lo + (int64_t)(l + 1) * s - 1;
-        const bool below = i < hi && sorted[i] < v;
-        const int c = __popcll((__ballot(below) >> (__lane_id() & 48)) & 0xFFFFull);
-        lo += c * s;
-        hi = min(hi, lo + s - 1);
-        lo = min(lo, hi);
-    }
-    return lo;
-}
-
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void k_embed_sum(int n_tok, int n_vocab, int dim, int per, int n_blocks, int pieces,
                                                    const int *__restrict__ sorted, const int *__restrict__ order,
@@ -253,26 +271,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(int n_tok, int n_vocab, int d
                                                    float *__restrict__ heads) {
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t id = (int64_t)blockIdx.x * 4 + wv;
-    if (id >= (int64_t)n_blocks * pieces) {             // rows without a token
-        const int64_t first = (id - (int64_t)n_blocks * pieces) * EG_FILL;
-        if (first >= n_vocab || add) return;
-        const int64_t v = first + lane / 16;
-        const int at = first_at(sorted, n_tok, (int)min(v, (int64_t)n_vocab - 1));
-        const bool empty = v < n_vocab && !(at < n_tok && sorted[at] == v);
-        const unsigned long long rows = __ballot(empty);
-#pragma unroll
-        for (int r = 0; r < EG_FILL; ++r) {
-            if (!((rows >> (16 * r)) & 1)) continue;
-            float *d = table + (first + r) * ldt;
-            if (dim < 4) {
-                if (lane < dim) d[lane] = 0.0f;
-            } else {
-                const Vec<F32, 4> o = {{0.0f, 0.0f, 0.0f, 0.0f}};
-                for (int c = lane * 4; c < dim; c += 256) store_once<F32, 4>(d + min(c, dim - 4), o);
-            }
-        }
-        return;
-    }
+    if (id >= (int64_t)n_blocks * pieces) return;
     const int blk = (int)(id / pieces), piece = (int)(id - (int64_t)blk * pieces);
     const int c = (piece * 64 + lane) * VEC, at = min(c, dim - VEC);
     const bool in = c < dim;
@@ -458,8 +457,10 @@ extern "C" spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, i
     const bool wide = dtype == SPMV_F32 ? dim >= 4 : dim >= 8;
     const int vec = wide ? (dtype == SPMV_F32 ? 4 : 8) : 1;
     const int per = (int)per_block(n_tok), n_blocks = (int)ceil_div(n_tok, per), pieces = (int)ceil_div(dim, 64 * vec);
-    const int64_t waves = (int64_t)n_blocks * pieces + (add ? 0 : ceil_div(n_vocab, EG_FILL));
+    const int64_t waves = (int64_t)n_blocks * pieces;
     st = check_grid(ceil_div(waves, 4));
+    if (st != SPMV_OK) return st;
+    st = check_grid(ceil_div((int64_t)n_vocab * dim, EG_CLEAR) + ceil_div(n_tok, 64), 1024);
     if (st != SPMV_OK) return st;
     if (pieces > 65535) return fail(SPMV_ERR_UNSUPPORTED, "rows of %d elements are not supported", dim);
     const Parts p = parts_of(n_tok, dim);
@@ -467,6 +468,9 @@ extern "C" spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, i
     int *sorted = reinterpret_cast<int *>(base), *order = reinterpret_cast<int *>(base + p.ints);
     float *heads = reinterpret_cast<float *>(base + p.ints * (p.digits ? 4 : 2) + p.counts);
     hipStream_t s = as_stream(stream);
+    const int sort_blocks = p.digits ? p.chunks : (int)ceil_div(n_tok, 64);
+    Fill fill = {dtable, lddt, n_vocab, dim, sort_blocks, 0};
+    if (!add) fill.blocks = (int)ceil_div((int64_t)n_vocab * dim, EG_CLEAR);
     if (p.digits) {
         int *other = reinterpret_cast<int *>(base + 2 * p.ints), *other_order = reinterpret_cast<int *>(base + 3 * p.ints);
         int *counts = reinterpret_cast<int *>(base + 4 * p.ints);
@@ -479,10 +483,10 @@ extern "C" spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, i
             int *ko = to ? sorted : other, *oo = to ? order : other_order;
             const int *ki = to ? other : sorted, *oi = to ? other_order : order;
             if (i == 0) {
-                k_embed_count<true><<<p.chunks, 1024, 0, s>>>(n_tok, n_vocab, 0, p.chunks, ids, counts);
+                k_embed_count<true><<<p.chunks + fill.blocks, 1024, 0, s>>>(n_tok, n_vocab, 0, p.chunks, ids, counts, fill);
                 SPMV_LAUNCHED("k_embed_count");
             } else {
-                k_embed_count<false><<<p.chunks, 1024, 0, s>>>(n_tok, n_vocab, ER_BITS * i, p.chunks, ki, counts);
+                k_embed_count<false><<<p.chunks, 1024, 0, s>>>(n_tok, n_vocab, ER_BITS * i, p.chunks, ki, counts, fill);
                 SPMV_LAUNCHED("k_embed_count");
             }
             k_embed_scan<<<1, 1024, 0, s>>>(p.chunks * ER_BINS, counts);
@@ -493,8 +497,8 @@ extern "C" spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, i
                 k_embed_scatter<false><<<p.chunks, 1024, 0, s>>>(n_tok, n_vocab, ER_BITS * i, p.chunks, ki, oi, counts, ko, oo);
             SPMV_LAUNCHED("k_embed_scatter");
         }
-    } else if (n_tok > 0) {
-        k_embed_rank<<<(int)ceil_div(n_tok, 64), 1024, 0, s>>>(n_tok, n_vocab, ids, sorted, order);
+    } else {
+        k_embed_rank<<<sort_blocks + fill.blocks, 1024, 0, s>>>(n_tok, n_vocab, ids, sorted, order, fill);
         SPMV_LAUNCHED("k_embed_rank");
     }
     if (waves > 0) {
