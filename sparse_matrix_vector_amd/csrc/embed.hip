@@ -122,12 +122,19 @@ __global__ __launch_bounds__(1024) void k_embed_rank(int n_tok, int n_vocab, con
     // smaller, that is, at most the lane's less 1; 16 ids at a time, in scalar registers
     auto at_most = [&](int from, int to, int limit) {
         int i = from;
+        int k[16], next[16];
+        if (i + 16 <= to) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) next[j] = ids[i + j];
+        }
         for (; i + 16 <= to; i += 16) {
-            int k[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) k[j] = id_key(ids[i + j], n_vocab);
+            for (int j = 0; j < 16; ++j) k[j] = next[j];
+            const int ahead = min(i + 16, n_tok - 16);               // there are 16 at least
 #pragma unroll
-            for (int j = 0; j < 16; ++j) c += k[j] <= limit;
+            for (int j = 0; j < 16; ++j) next[j] = ids[ahead + j];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) c += id_key(k[j], n_vocab) <= limit;
         }
         for (; i < to; ++i) c += id_key(ids[i], n_vocab) <= limit;
     };
@@ -243,6 +250,7 @@ __global__ __launch_bounds__(1024) void k_embed_scatter(int n_tok, int n_vocab, 
 // ---------------------------------------------------------------------------
 constexpr int EG_MIN = 16;           // sorted positions of a block at least
 constexpr int EG_BLOCKS = 4096;      // blocks at most
+constexpr int EJ_WAVES = 8;
 
 // d[0 .. VEC) (+)= scale * v; the first `skip` elements, which the lane before has, are left out.
 template <int VEC>
@@ -277,7 +285,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(int n_tok, int n_vocab, int d
     const bool in = c < dim;
     const int p0 = blk * per, p1 = min(n_tok, p0 + per);
     const typename E::T *src = dy + at;
-    constexpr int U = 8;
+    constexpr int U = 16;
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
@@ -295,7 +303,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(int n_tok, int n_vocab, int d
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t t = __builtin_amdgcn_readlane(tok, min(j + u, n - 1));
-                v[u] = load_once<E, VEC>(src + t * lddy);
+                v[u] = load_row<E, VEC>(src + t * lddy);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -321,36 +329,59 @@ __global__ __launch_bounds__(256) void k_embed_sum(int n_tok, int n_vocab, int d
     }
 }
 
+// The first position past the run of `key` in sorted[lo .. n), by the whole wave.
+__device__ __forceinline__ int run_end(const int *__restrict__ sorted, int lo, int n, int key) {
+    int hi = n;
+    while (lo < hi) {
+        const int s = (hi - lo + 63) / 64;
+        const int64_t i = (int64_t)lo + (int64_t)(__lane_id() + 1) * s - 1;
+        const int c = __popcll(__ballot(i < hi && sorted[min(i, (int64_t)n - 1)] <= key));
+        lo = min(hi, lo + c * s);
+        hi = min(hi, lo + s - 1);
+    }
+    return lo;
+}
+
 // The sum of a run that crosses blocks, from the block that it begins in: its
-// tail, and the heads of the blocks after it, every 16th by one wave.
+// tail, and the heads of the blocks after it, every EJ_WAVES-th by one wave.
 template <int VEC>
-__global__ __launch_bounds__(1024) void k_embed_join(int n_tok, int n_vocab, int dim, int per, int n_blocks,
-                                                     const int *__restrict__ sorted, float scale, bool add,
-                                                     float *__restrict__ table, int64_t ldt,
-                                                     const float *__restrict__ heads) {
-    __shared__ float part[16][64 * VEC];
+__global__ __launch_bounds__(64 * EJ_WAVES) void k_embed_join(int n_tok, int n_vocab, int dim, int per, int n_blocks,
+                                                              const int *__restrict__ sorted, float scale, bool add,
+                                                              float *__restrict__ table, int64_t ldt,
+                                                              const float *__restrict__ heads) {
+    constexpr int U = 8;
+    __shared__ float part[EJ_WAVES][64 * VEC];
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int blk = blockIdx.x, p0 = blk * per, p1 = p0 + per;
     if (p1 >= n_tok) return;
     const int key = sorted[p1];
     if (key >= n_vocab || sorted[p1 - 1] != key || (p0 > 0 && sorted[p0 - 1] == key)) return;
     const int c = ((int)blockIdx.y * 64 + lane) * VEC, at = min(c, dim - VEC);
+    const int last = (run_end(sorted, p1, n_tok, key) - 1) / per;       // the block that the run ends in
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
     if (wv == 0) {
+        const Vec<F32, VEC> v = load_row<F32, VEC>(heads + ((int64_t)n_blocks + blk) * dim + at);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = heads[((int64_t)n_blocks + blk) * dim + at + i];
+        for (int i = 0; i < VEC; ++i) acc[i] = v.v[i];
     }
-    for (int64_t b = (int64_t)blk + 1 + wv; b < n_blocks && sorted[b * per] == key; b += 16) {
+    for (int b0 = blk + 1 + wv; b0 <= last; b0 += U * EJ_WAVES) {
+        Vec<F32, VEC> v[U];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] += heads[b * dim + at + i];
+        for (int u = 0; u < U; ++u) v[u] = load_row<F32, VEC>(heads + (int64_t)min(b0 + u * EJ_WAVES, last) * dim + at);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (b0 + u * EJ_WAVES <= last) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] += v[u].v[i];
+            }
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) part[wv][lane * VEC + i] = acc[i];
     __syncthreads();
     if (wv == 0 && c < dim) {
-        for (int w = 1; w < 16; ++w)
+        for (int w = 1; w < EJ_WAVES; ++w)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] += part[w][lane * VEC + i];
         add_row<VEC>(table + (int64_t)key * ldt + at, acc, c - at, scale, add);
@@ -454,8 +485,8 @@ extern "C" spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, i
         return fail(SPMV_ERR_INVALID_VALUE, "workspace of %zu bytes is smaller than %zu", workspace_bytes, need);
     if (!aligned16(workspace)) return fail(SPMV_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
     const bool add = accumulate != 0;
-    const bool wide = dtype == SPMV_F32 ? dim >= 4 : dim >= 8;
-    const int vec = wide ? (dtype == SPMV_F32 ? 4 : 8) : 1;
+    const bool wide = dim >= 4;
+    const int vec = wide ? 4 : 1;
     const int per = (int)per_block(n_tok), n_blocks = (int)ceil_div(n_tok, per), pieces = (int)ceil_div(dim, 64 * vec);
     const int64_t waves = (int64_t)n_blocks * pieces;
     st = check_grid(ceil_div(waves, 4));
@@ -509,23 +540,19 @@ extern "C" spmv_status embed_grad(int32_t n_tok, int32_t n_vocab, int32_t dim, i
                 n_tok, n_vocab, dim, per, n_blocks, pieces, sorted, order, static_cast<const typename E::T *>(dy), lddy,
                 scale, add, dtable, lddt, heads);
         };
-        const std::integral_constant<int, 1> one;
-        if (dtype == SPMV_F32)
-            wide ? sum(F32{}, std::integral_constant<int, 4>{}) : sum(F32{}, one);
-        else if (dtype == SPMV_F16)
-            wide ? sum(F16{}, std::integral_constant<int, 8>{}) : sum(F16{}, one);
-        else
-            wide ? sum(BF16{}, std::integral_constant<int, 8>{}) : sum(BF16{}, one);
+        // 4 columns for a lane: 16 bytes of the table
+        auto by_width = [&](auto e) {
+            wide ? sum(e, std::integral_constant<int, 4>{}) : sum(e, std::integral_constant<int, 1>{});
+        };
+        dtype == SPMV_F32 ? by_width(F32{}) : dtype == SPMV_F16 ? by_width(F16{}) : by_width(BF16{});
         SPMV_LAUNCHED("k_embed_sum");
     }
     if (n_blocks > 1) {
         const dim3 grid(n_blocks - 1, pieces);
-        if (vec == 8)
-            k_embed_join<8><<<grid, 1024, 0, s>>>(n_tok, n_vocab, dim, per, n_blocks, sorted, scale, add, dtable, lddt, heads);
-        else if (vec == 4)
-            k_embed_join<4><<<grid, 1024, 0, s>>>(n_tok, n_vocab, dim, per, n_blocks, sorted, scale, add, dtable, lddt, heads);
+        if (vec == 4)
+            k_embed_join<4><<<grid, 64 * EJ_WAVES, 0, s>>>(n_tok, n_vocab, dim, per, n_blocks, sorted, scale, add, dtable, lddt, heads);
         else
-            k_embed_join<1><<<grid, 1024, 0, s>>>(n_tok, n_vocab, dim, per, n_blocks, sorted, scale, add, dtable, lddt, heads);
+            k_embed_join<1><<<grid, 64 * EJ_WAVES, 0, s>>>(n_tok, n_vocab, dim, per, n_blocks, sorted, scale, add, dtable, lddt, heads);
         SPMV_LAUNCHED("k_embed_join");
     }
     return SPMV_OK;
