@@ -32,6 +32,7 @@ constexpr int ME_MAX_TOK = 256;
 constexpr int ME_MAX_SLOTS = 4096;
 constexpr int ME_MAX_EXPERTS = 1024;
 constexpr int ME_UP_WAVES = 4;
+constexpr int ME_AHEAD = 2;          // blocks whose codes are on their way in the tiles
 constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
 constexpr int ME_UNROLL = 2;         // blocks whose codes a wave of the down product loads at once
 constexpr int ME_UNITS = 2;          // units of a wave of the down product, about
@@ -282,24 +283,27 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        Q4Piece<E, ZP, G, 1> w[2][2];
+        Q4Piece<E, ZP, G, 1> w[ME_AHEAD + 1][2];
         u32x4 v[TT];
         load_x(0, v);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
+        for (int a = 0; a < ME_AHEAD; ++a)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
         keep_x(0, xt[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += 2) {
+        for (int bb = 0; bb < n_blk; bb += ME_AHEAD + 1) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a = 0; a <= ME_AHEAD; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
                 load_x(min(b + 1, n_blk - 1), v);                      // x first: what waits for it does not wait for the codes
 #pragma unroll
-                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
+                for (int r = 0; r < 2; ++r)
+                    w[(a + ME_AHEAD) % (ME_AHEAD + 1)][r].load(rows[r], min(b + ME_AHEAD, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
-                up_block<E, ZP, G, TT>(w[a], xt[a], acc);
-                keep_x(min(b + 1, n_blk - 1), xt[1 - a], v);
+                up_block<E, ZP, G, TT>(w[a], xt[b & 1], acc);
+                keep_x(min(b + 1, n_blk - 1), xt[1 - (b & 1)], v);
                 __syncthreads();
             }
         }
@@ -496,12 +500,17 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
     if (e < 0) return;
     const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 32;
     Q4Rows<ZP, G> rows[2];
-    Q4Piece<E, ZP, G, 1> w[2][2];
+    Q4Piece<E, ZP, G, 1> w[ME_AHEAD + 1][2];
+    auto load_first = [&]() {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+        for (int a = 0; a < ME_AHEAD; ++a)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
+    };
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
         rows[r] = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + 16 * r + (lane & 15), dim - 1), n_blk);
-        w[0][r].load(rows[r], 0);                                       // on its way while the entries are found
-    }
+    load_first();                                                       // on their way while the entries are found
     const Entries en = find_entries(n_tok, top_k, e, keys, el);
     for (int first = 0; first < en.n; first += 16 * TT) {
         // the pieces of this turn's tiles: a block of a tile of n entries is 48 n of them in a row
@@ -544,21 +553,20 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         u32x4 v[Q];
         load_h(0, v);
-        if (first > 0) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
-        }
+        if (first > 0) load_first();
         keep_h(ht[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += 2) {
+        for (int bb = 0; bb < n_blk; bb += ME_AHEAD + 1) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a = 0; a <= ME_AHEAD; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
                 load_h(min(b + 1, n_blk - 1), v);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
+                for (int r = 0; r < 2; ++r)
+                    w[(a + ME_AHEAD) % (ME_AHEAD + 1)][r].load(rows[r], min(b + ME_AHEAD, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
+                const u32x4 *now = ht[b & 1];
                 f32x4 sum[2][TT];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -573,14 +581,14 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                         }
                     }
                     if (packed) {
-                        const u32x4 x = ht[a][p * n_of[0] + min(lane & 15, 3 * n_of[0] - 1)];
+                        const u32x4 x = now[p * n_of[0] + min(lane & 15, 3 * n_of[0] - 1)];
 #pragma unroll
                         for (int r = 0; r < 2; ++r) sum[r][0] = Op::mfma(x, f[r], sum[r][0]);
                     } else {
 #pragma unroll
                         for (int t = 0; t < TT; ++t)
                             if (n_of[t] > 0) {
-                                const u32x4 *at = ht[a] + from[t] + p * n_of[t] + min(lane & 15, n_of[t] - 1);
+                                const u32x4 *at = now + from[t] + p * n_of[t] + min(lane & 15, n_of[t] - 1);
 #pragma unroll
                                 for (int i = 2; i >= 0; --i) {
                                     const u32x4 x = at[i * n_of[t]];
@@ -600,7 +608,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                         }
                     }
                 }
-                keep_h(ht[1 - a], v);
+                keep_h(ht[1 - (b & 1)], v);
                 __syncthreads();
             }
         }
