@@ -776,6 +776,7 @@ spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adap
 /* is not NULL, a zero point (uint8, its low four bits); both are arrays         */
 /* [n_rows, ceil(n_cols / 128) * 128 / group].  The weight is                    */
 /*   W[i, j] = scale * (code - zero), zero = 8 where zeros is NULL.              */
+/* More than 2^30 columns are SPMV_ERR_UNSUPPORTED.                               */
 /* ======================================================================== */
 
 /* Codes, scales and (unless zeros is NULL) zero points of w [n_rows, n_cols] of
@@ -836,8 +837,8 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t dim, int32_
  * both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A token without an
  * expert gets zeros.  x [n_tok, dim] of type dtype (the scales' type), y [n_tok, dim]
  * of the same type or fp32, rounded once; the products between are kept with fp32's
- * 24 bits.  Only the weights of chosen experts are read.  At most 1024 experts and
- * a width dim of at least 8 (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
+ * 24 bits.  Only the weights of chosen experts are read.  At most 1024 experts,
+ * a width dim of 8 to 2^24 and inter of at most 2^24 (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
  * overlap; x and y must not overlap.  The same bits on every call.  All pointers
  * device.  Asynchronous. */
 spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,

@@ -31,11 +31,14 @@ namespace {
 constexpr int ME_MAX_TOK = 256;
 constexpr int ME_MAX_SLOTS = 4096;
 constexpr int ME_MAX_EXPERTS = 1024;
+constexpr int ME_MAX_WIDTH = 1 << 24;
 constexpr int ME_UP_WAVES = 4;
-constexpr int ME_AHEAD = 2;          // blocks whose codes are on their way in the tiles
+constexpr int ME_UP_AHEAD = 2;       // blocks whose codes are on their way in the tiles
+constexpr int ME_DOWN_AHEAD = 1;
 constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
-constexpr int ME_UNROLL = 2;         // blocks whose codes a wave of the down product loads at once
-constexpr int ME_UNITS = 2;          // units of a wave of the down product, about
+constexpr int ME_DOWN_WAVES = 16;
+constexpr int ME_UNROLL = 2;         // blocks of a step of the down product
+constexpr int ME_UNITS = 1;          // units of a wave of the down product, about
 
 // Where the tile of entries first .. first + n - 1 of all entries begins, and a
 // part of a piece of 8 columns in it (in 16-bit numbers).
@@ -283,24 +286,24 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        Q4Piece<E, ZP, G, 1> w[ME_AHEAD + 1][2];
+        Q4Piece<E, ZP, G, 1> w[ME_UP_AHEAD + 1][2];
         u32x4 v[TT];
         load_x(0, v);
 #pragma unroll
-        for (int a = 0; a < ME_AHEAD; ++a)
+        for (int a = 0; a < ME_UP_AHEAD; ++a)
 #pragma unroll
             for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
         keep_x(0, xt[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += ME_AHEAD + 1) {
+        for (int bb = 0; bb < n_blk; bb += ME_UP_AHEAD + 1) {
 #pragma unroll
-            for (int a = 0; a <= ME_AHEAD; ++a) {
+            for (int a = 0; a <= ME_UP_AHEAD; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
                 load_x(min(b + 1, n_blk - 1), v);                      // x first: what waits for it does not wait for the codes
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    w[(a + ME_AHEAD) % (ME_AHEAD + 1)][r].load(rows[r], min(b + ME_AHEAD, n_blk - 1));
+                    w[(a + ME_UP_AHEAD) % (ME_UP_AHEAD + 1)][r].load(rows[r], min(b + ME_UP_AHEAD, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
                 up_block<E, ZP, G, TT>(w[a], xt[b & 1], acc);
                 keep_x(min(b + 1, n_blk - 1), xt[1 - (b & 1)], v);
@@ -314,90 +317,59 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
     }
 }
 
+// Up to 64 choices: a lane holds one, and everything about an expert is ballots over
+// them, without a barrier before the sums at the end.
 template <class E, bool ZP, int G>
-__global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_experts, int dim, int rows, int n_blk,
-                                                   const int *__restrict__ keys, const float *__restrict__ weights,
-                                                   const char *__restrict__ tiles,
-                                                   const unsigned short *__restrict__ h, void *__restrict__ y, bool f32,
-                                                   int64_t ldy) {
-    constexpr int GB = Q4_BLOCK / G, PG = G / 32, U = ME_UNROLL;
+__global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int top_k, int n_experts, int dim, int rows,
+                                                                 int n_blk, const int *__restrict__ keys,
+                                                                 const float *__restrict__ weights,
+                                                                 const char *__restrict__ tiles,
+                                                                 const unsigned short *__restrict__ h,
+                                                                 void *__restrict__ y, bool f32, int64_t ldy) {
+    constexpr int GB = Q4_BLOCK / G, PG = G / 32, U = ME_UNROLL, W = ME_DOWN_WAVES;
     typedef Q4Op<BF16> Op;
-    extern __shared__ __attribute__((aligned(16))) float sums[];        // [waves][n_tok][16], then what follows
-    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
-    const int quarter = lane / 16, slots = n_tok * top_k;
-    float *mine = sums + (size_t)wv * n_tok * 16;
-    float *share = sums + (size_t)waves * n_tok * 16;                   // an entry's weight [slots] ..
-    int *first_of = reinterpret_cast<int *>(share + slots);             // entries of smaller experts [n_experts + 1]
-    short *key = reinterpret_cast<short *>(first_of + n_experts + 1);   // [slots]
-    unsigned short *list = reinterpret_cast<unsigned short *>(key + slots);   // .. and its token [slots]
-    unsigned short *active = list + slots, *count = active + min(slots, n_experts);
-    __shared__ int n_active;
-    for (int i = threadIdx.x; i <= n_experts; i += blockDim.x) first_of[i] = 0;
-    for (int i = threadIdx.x; i < waves * n_tok * 16; i += blockDim.x) sums[i] = 0.0f;
-    __syncthreads();
-    for (int i = threadIdx.x; i < slots; i += blockDim.x) {
-        const int e = keys[i];
-        const bool in = (unsigned)e < (unsigned)n_experts;
-        key[i] = (short)(in ? e : -1);
-        if (in) atomicAdd(&first_of[e], 1);
+    typedef unsigned long long u64;
+    extern __shared__ __attribute__((aligned(16))) float sums[];        // [W][n_tok][16]
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
+    const int slots = n_tok * top_k;
+    const int key = lane < slots ? keys[lane] : -1;
+    const float weight = weights && lane < slots ? weights[lane] : 1.0f;
+    float *mine = sums + wv * n_tok * 16;
+    for (int i = lane; i < n_tok * 16; i += 64) mine[i] = 0.0f;
+    const bool valid = (unsigned)key < (unsigned)n_experts;
+    const u64 below = (1ull << lane) - 1;
+    const int tok0 = lane / top_k * top_k;                              // first choice of this lane's token
+    // first choices of an expert
+    u64 firsts = 0, left = __ballot(valid);
+    while (left) {
+        const int j = __ffsll(left) - 1;
+        firsts |= 1ull << j;
+        left &= ~__ballot(valid && key == __builtin_amdgcn_readlane(key, j));
     }
-    __syncthreads();
-    if (wv == 0) {
-        int n = 0, before = 0;
-        for (int e0 = 0; e0 < n_experts; e0 += 64) {
-            const int e = e0 + lane, c = e < n_experts ? first_of[e] : 0;
-            const unsigned long long has = __ballot(c > 0);
-            if (c > 0) active[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)e;
-            n += __popcll(has);
-            const int incl = wave_inclusive_scan(c);
-            if (e < n_experts) first_of[e] = before + incl - c;
-            before += __builtin_amdgcn_readlane(incl, 63);
-        }
-        if (lane == 0) first_of[n_experts] = before, n_active = n;
-    }
-    __syncthreads();
-    const int na = n_active;
-    for (int a = wv; a < na; a += waves) {
-        const int e = active[a], at0 = first_of[e];
-        int n = 0;
-        for (int t0 = 0; t0 < n_tok; t0 += 64) {
-            const int t = t0 + lane;
-            bool has = false;
-            float w = 0.0f;
-            if (t < n_tok)
-                for (int c = 0; c < top_k; ++c)                         // an expert chosen twice counts with both weights
-                    if (key[t * top_k + c] == e) {
-                        has = true;
-                        w += weights ? weights[t * top_k + c] : 1.0f;
-                    }
-            const unsigned long long all = __ballot(has);
-            if (has) {
-                const int at = at0 + n + __popcll(all & ((1ull << lane) - 1));
-                list[at] = (unsigned short)t;
-                share[at] = w;
-            }
-            n += __popcll(all);
-        }
-        if (lane == 0) count[a] = (unsigned short)n;
-    }
-    __syncthreads();
+    const int na = __popcll(firsts);
     // units of about as much work for every wave: an expert, or a part of its columns.
     // A wave goes through its units' steps (U blocks of 16 entries), the next step's codes on their way.
     const int pieces = (n_blk + U - 1) / U;
-    const int split = na > 0 ? min(pieces, max(1, (ME_UNITS * waves + na - 1) / na)) : 1;
+    const int split = na > 0 ? min(pieces, max(1, (ME_UNITS * W + na - 1) / na)) : 1;
     const int row0 = blockIdx.x * rows, r = lane & (rows - 1), units = na * split;
     struct Step {
-        int unit, e, n, at0, room, first, k0, p;
+        int unit, e, n, base, room, first, k0, p;
+        u64 same, lead;
     };
     auto begin = [&](int unit) {
-        Step s = {unit, 0, 0, 0, 0, 0, 0, 0};
+        Step s = {unit, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         if (unit < units) {
             const int a = unit / split;
+            u64 m = firsts;
+            for (int i = 0; i < a; ++i) m &= m - 1;
             s.k0 = s.p = unit - a * split;
-            s.e = __builtin_amdgcn_readfirstlane(active[a]);
-            s.n = __builtin_amdgcn_readfirstlane(count[a]);
-            s.at0 = __builtin_amdgcn_readfirstlane(first_of[s.e]);
-            s.room = __builtin_amdgcn_readfirstlane(first_of[s.e + 1]) - s.at0;
+            s.e = __builtin_amdgcn_readlane(key, __ffsll(m) - 1);
+            s.same = __ballot(valid && key == s.e);
+            // one entry for each token, at its first choice of the expert
+            s.lead = __ballot(valid && key == s.e && !(s.same & below & ~((1ull << tok0) - 1)));
+            s.n = __popcll(s.lead);
+            s.room = __popcll(s.same);
+            s.base = __popcll(__ballot(valid && key < s.e));
         }
         return s;
     };
@@ -406,7 +378,7 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
         if (s.p < pieces) return s;
         s.p = s.k0;
         s.first += 16;
-        return s.first < s.n ? s : begin(s.unit + waves);
+        return s.first < s.n ? s : begin(s.unit + W);
     };
     Q4Piece<E, ZP, G, 1> w[2][U];
     auto load = [&](const Step &s, Q4Piece<E, ZP, G, 1> (&to)[U]) {
@@ -423,18 +395,24 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
             if (s.unit >= units) break;
             const Step next = after(s);
             load(next.unit < units ? next : s, w[1 - a]);               // always, for the waits behind it
+            // up to 5 entries lie with all their parts in one operand of 16 (row part * in + entry)
             const int in = min(16, s.room - s.first);
-            const u32x4 *ht = reinterpret_cast<const u32x4 *>(h + hidden_tile(s.at0 + s.first, n_blk));
-            const int hl = quarter * 3 * in + min(lane & 15, in - 1);
+            const bool packed = in <= 5;
+            const u32x4 *ht = reinterpret_cast<const u32x4 *>(h + hidden_tile(s.base + s.first, n_blk));
+            const int hl = quarter * 3 * in + min(lane & 15, (packed ? 3 * in : in) - 1);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int b = s.p * U + u;
+                if (b >= n_blk) continue;
                 u32x4 v[3][4];
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
+                for (int m = 0; m < 4; ++m) v[0][m] = (ht + hidden_piece(b, 0, 4 * m, in) / 8)[hl];
+                if (!packed) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) v[i][m] = (ht + hidden_piece(min(b, n_blk - 1), i, 4 * m, in) / 8)[hl];
-                if (b >= n_blk) continue;
+                    for (int i = 1; i < 3; ++i)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) v[i][m] = (ht + hidden_piece(b, i, 4 * m, in) / 8)[hl];
+                }
 #pragma unroll
                 for (int g = 0; g < GB; ++g) {
                     const Op::Zero nz = Op::zero(w[a][u].zero(0, g));
@@ -442,8 +420,11 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
 #pragma unroll
                     for (int m = g * PG; m < (g + 1) * PG; ++m) {
                         const u32x4 f = Op::decode(w[a][u].c[0][m], nz);
-#pragma unroll
-                        for (int i = 2; i >= 0; --i) sum = Op::mfma(v[i][m], f, sum);
+                        if (!packed) {
+                            sum = Op::mfma(v[2][m], f, sum);
+                            sum = Op::mfma(v[1][m], f, sum);
+                        }
+                        sum = Op::mfma(v[0][m], f, sum);
                     }
                     const float sc = w[a][u].scale(0, g);
 #pragma unroll
@@ -451,24 +432,32 @@ __global__ __launch_bounds__(1024) void k_moe_down(int n_tok, int top_k, int n_e
                 }
             }
             if (next.unit != s.unit || next.first != s.first) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = s.first + quarter * 4 + i;
-                    if (at < s.n && (lane & 15) < rows) {               // a token is once in the list: no two lanes meet
-                        float *d = mine + list[s.at0 + at] * 16 + r;
-                        *d = fmaf(share[s.at0 + at], acc[i], *d);
-                    }
-                    acc[i] = 0.0f;
+                // row i of the result, for all quarters
+                auto result = [&](int i) {
+                    const float x = (i & 2) ? ((i & 1) ? acc[3] : acc[2]) : ((i & 1) ? acc[1] : acc[0]);
+                    return __shfl(x, i / 4 * 16 + (lane & 15));
+                };
+                for (u64 left = s.same; left; left &= left - 1) {       // an expert chosen twice counts with both weights
+                    const int j = __ffsll(left) - 1;
+                    const int entry = __popcll(s.lead & ((2ull << j) - 1)) - 1 - s.first;
+                    if (entry < 0 || entry >= 16) continue;
+                    const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j));
+                    float x = result(entry);
+                    if (packed) x = (result(2 * in + entry) + result(in + entry)) + x;
+                    float *d = mine + j / top_k * 16 + r;
+                    if (lane < rows) *d = fmaf(wj, x, *d);
                 }
+                acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
             s = next;
         }
     }
     __syncthreads();
-    for (int o = threadIdx.x; o < n_tok * rows; o += blockDim.x) {
+    for (int o = threadIdx.x; o < n_tok * rows; o += 64 * W) {
         const int in = o % rows, t = o / rows, row = row0 + in;
         float v = 0.0f;
-        for (int w = 0; w < waves; ++w) v += sums[((size_t)w * n_tok + t) * 16 + in];
+#pragma unroll
+        for (int k = 0; k < W; ++k) v += sums[(k * n_tok + t) * 16 + in];
         if (row < dim) {
             const int64_t at = (int64_t)t * ldy + row;
             if (f32)
@@ -491,7 +480,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                                                                        const char *__restrict__ tiles,
                                                                        const unsigned short *__restrict__ h,
                                                                        float *__restrict__ z) {
-    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT;  // 48 pieces of 16 bytes of an entry's block
+    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT, A = ME_DOWN_AHEAD;  // 48 pieces of 16 bytes of an entry's block
     typedef Q4Op<BF16> Op;
     __shared__ u32x4 ht[2][48 * 16 * TT];
     __shared__ EntryLds el;
@@ -500,10 +489,10 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
     if (e < 0) return;
     const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 32;
     Q4Rows<ZP, G> rows[2];
-    Q4Piece<E, ZP, G, 1> w[ME_AHEAD + 1][2];
+    Q4Piece<E, ZP, G, 1> w[A + 1][2];
     auto load_first = [&]() {
 #pragma unroll
-        for (int a = 0; a < ME_AHEAD; ++a)
+        for (int a = 0; a < A; ++a)
 #pragma unroll
             for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
     };
@@ -556,15 +545,15 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
         if (first > 0) load_first();
         keep_h(ht[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += ME_AHEAD + 1) {
+        for (int bb = 0; bb < n_blk; bb += A + 1) {
 #pragma unroll
-            for (int a = 0; a <= ME_AHEAD; ++a) {
+            for (int a = 0; a <= A; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
                 load_h(min(b + 1, n_blk - 1), v);
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    w[(a + ME_AHEAD) % (ME_AHEAD + 1)][r].load(rows[r], min(b + ME_AHEAD, n_blk - 1));
+                    w[(a + A) % (A + 1)][r].load(rows[r], min(b + A, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
                 const u32x4 *now = ht[b & 1];
                 f32x4 sum[2][TT];
@@ -694,11 +683,6 @@ Parts parts_of(int64_t n_tok, int64_t top_k, int64_t dim, int64_t inter) {
     return p;
 }
 
-size_t down_lds(int waves, int n_tok, int top_k, int n_experts) {
-    const size_t slots = (size_t)n_tok * top_k;
-    return (size_t)waves * n_tok * 64 + slots * 8 + ((size_t)n_experts + 1) * 4 + std::min<size_t>(slots, n_experts) * 4;
-}
-
 }  // namespace
 }  // namespace spmv
 
@@ -723,6 +707,8 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     if (st != SPMV_OK) return st;
     if (n_experts < 1) return fail(SPMV_ERR_INVALID_VALUE, "n_experts must be >= 1");
     if (dim < 8) return fail(SPMV_ERR_UNSUPPORTED, "layers of a width below 8 are not supported");
+    if (dim > ME_MAX_WIDTH || inter > ME_MAX_WIDTH)
+        return fail(SPMV_ERR_UNSUPPORTED, "widths above %d are not supported", ME_MAX_WIDTH);
     if (n_experts > ME_MAX_EXPERTS) return fail(SPMV_ERR_UNSUPPORTED, "more than %d experts are not supported", ME_MAX_EXPERTS);
     if (!q4_group_ok(group)) return fail(SPMV_ERR_INVALID_VALUE, "group must be 32, 64 or 128, not %d", group);
     if (!dtype_ok(dtype) || !dtype_ok(y_dtype)) return fail(SPMV_ERR_INVALID_VALUE, "an element type is not a spmv_dtype");
@@ -742,17 +728,17 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     const bool by_slot = slots <= n_experts;
     const int up_blk = (int)q4_blocks(dim), down_blk = (int)q4_blocks(inter);
     // parts of the columns in the up product: enough waves for the card
-    const int64_t groups = by_slot ? slots : n_experts, up_tiles_n = ld / 16 * groups;
+    const int64_t groups = by_slot ? slots : n_experts, up_row_tiles = ld / 16 * groups;
     // tokens of an expert by their number if the choices are even
     const bool tile_up = slots > 12 * groups;
     int parts = 1;
-    while (!tile_up && parts < ME_UP_WAVES && parts < up_blk && up_tiles_n * parts < 4096) parts *= 2;
+    while (!tile_up && parts < ME_UP_WAVES && parts < up_blk && up_row_tiles * parts < 4096) parts *= 2;
     const int64_t up_grid = ceil_div(ld / 16, ME_UP_WAVES / parts);
     st = check_grid(up_grid * groups, 64 * ME_UP_WAVES);
     if (st != SPMV_OK) return st;
     // 8 rows for a workgroup of the down product where 16 would leave compute units without one
     const int rows = ceil_div(dim, 16) < 256 ? 8 : 16;
-    st = check_grid(ceil_div(dim, rows), 1024);
+    st = check_grid(ceil_div(dim, rows), 64 * ME_DOWN_WAVES);
     if (st != SPMV_OK) return st;
     const Parts p = parts_of(n_tok, top_k, dim, inter);
     const bool tile_down = slots > ME_FEW_SLOTS;
@@ -787,7 +773,7 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
             up(std::integral_constant<int, 3>{});
         SPMV_LAUNCHED("k_moe_up");
         if (!tile_down) {
-            k_moe_down<E, ZP, G><<<(int)ceil_div(dim, rows), 1024, down_lds(16, n_tok, top_k, n_experts), s>>>(
+            k_moe_down<E, ZP, G><<<(int)ceil_div(dim, rows), 64 * ME_DOWN_WAVES, (size_t)ME_DOWN_WAVES * n_tok * 64, s>>>(
                 n_tok, top_k, n_experts, dim, rows, down_blk, keys, weights, static_cast<const char *>(down_tiles), h, y,
                 y_dtype == SPMV_F32, ldy);
             SPMV_LAUNCHED("k_moe_down");

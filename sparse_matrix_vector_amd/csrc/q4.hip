@@ -383,8 +383,11 @@ __global__ __launch_bounds__(256) void k_q4_quantize(int64_t n_groups, int n_col
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+constexpr int Q4_MAX_COLS = 1 << 30;
+
 spmv_status check_weight(int32_t n_rows, int32_t n_cols, int32_t group, int32_t dtype) {
     if (n_rows < 0 || n_cols < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
+    if (n_cols > Q4_MAX_COLS) return fail(SPMV_ERR_UNSUPPORTED, "more than %d columns are not supported", Q4_MAX_COLS);
     if (!q4_group_ok(group)) return fail(SPMV_ERR_INVALID_VALUE, "group must be 32, 64 or 128, not %d", group);
     if (!dtype_ok(dtype)) return fail(SPMV_ERR_INVALID_VALUE, "element type %d is not a spmv_dtype", dtype);
     if (dtype == SPMV_F32) return fail(SPMV_ERR_UNSUPPORTED, "scales and x are fp16 or bf16");
@@ -521,6 +524,7 @@ extern "C" spmv_status q4_tiles(int32_t n_rows, int32_t n_cols, int32_t group, c
 extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, size_t *bytes) {
     if (!bytes) return fail(SPMV_ERR_INVALID_VALUE, "bytes is NULL");
     if (n_rows < 0 || n_cols < 0 || n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
+    if (n_cols > Q4_MAX_COLS) return fail(SPMV_ERR_UNSUPPORTED, "more than %d columns are not supported", Q4_MAX_COLS);
     // the most that any batch of up to n_tok tokens needs: full tiles of tokens, as long as there is a split
     size_t most = split_bytes(n_rows, n_cols, n_tok);
     for (int64_t t = QF_TOKENS; t < n_tok; t = t < 16 ? 16 : t < 64 ? t + 16 : t + 64) {
@@ -557,6 +561,8 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         return SPMV_OK;
     }
     const int n_blk = (int)q4_blocks(n_cols);
+    st = check_grid(ceil_div(n_rows, 16), 64 * QF_WAVES);
+    if (st != SPMV_OK) return st;
     if (few(n_cols, n_tok))
         return by_weight(dtype, with_zeros != 0, group, [&](auto e, auto zp, auto g) -> spmv_status {
             typedef decltype(e) E;

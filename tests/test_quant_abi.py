@@ -61,6 +61,8 @@ def test_matmul_refusals():
     assert _matmul(group=48) == VALUE and _matmul(dt=5) == VALUE and _matmul(ydt=5) == VALUE
     assert _matmul(dt=F32) == UNSUPPORTED and _matmul(dt=F16, ydt=BF16) == UNSUPPORTED
     assert _matmul(ldx=99) == VALUE and _matmul(ldy=39) == VALUE
+    assert _matmul(cols=2 ** 30 + 1, ldx=2 ** 31) == UNSUPPORTED
+    assert _matmul(rows=2 ** 31 - 1, cols=4, ldx=4, ldy=2 ** 31) == OVERFLOW
     for k in ("tiles", "x", "y"):
         assert _matmul(**{k: None}) == VALUE, k
     assert _matmul(tiles=P + 8) == UNSUPPORTED
@@ -103,7 +105,8 @@ def test_moe_refusals():
     assert _moe(up=P + 8) == UNSUPPORTED and _moe(dn=P + 8) == UNSUPPORTED and _moe(ws=P + 8) == UNSUPPORTED
     assert _moe(wsb=S.moe_workspace_size(4, 2, 64, 96) - 1) == VALUE
     assert b"workspace" in S.lib().spmv_last_error()
-    assert _moe(dim=2 ** 31 - 1, ldx=2 ** 31, ldy=2 ** 31) == OVERFLOW
+    assert _moe(dim=2 ** 24 + 1, ldx=2 ** 31, ldy=2 ** 31) == UNSUPPORTED and _moe(inter=2 ** 24 + 1) == UNSUPPORTED
+    assert _moe(e=1024, n=256, k=16, inter=2 ** 24) == OVERFLOW
     assert _moe(n=0, keys=None, x=None, y=None, ws=None) == OK
     z = ctypes.c_size_t()
     L = S.lib()
