@@ -810,9 +810,10 @@ def fem_assemble_csr(n_elem, n_dof, edof, rho, penalty, Ke, stream=None):
 # ---------------------------------------------------------------------------
 def __getattr__(name):
     if name in _TOKENS:
-        from . import tokens
-        return getattr(tokens, name)
-    if name in _QUANT:
-        from . import quant
-        return getattr(quant, name)
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import tokens as module
+    elif name in _QUANT:
+        from . import quant as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(module, name)          # found without this function from now on
+    return value

@@ -98,6 +98,8 @@ class Q4Matrix:
         self.n_rows, self.n_cols, self.n_groups, self.group = int(n_rows), int(n_cols), int(n_groups), _group(group)
         self.with_zeros = int(zeros is not None)
         d, total = _device(codes, "codes"), self.n_rows * self.n_groups
+        if total > 0x7fffffff:
+            raise ValueError(f"{total} rows in all do not fit int32")
         with _stream_scope(stream, d):
             self.tiles = torch.empty(q4_tiles_size(total, n_cols, group, self.with_zeros), dtype=torch.uint8, device=d)
         q4_tiles(total, n_cols, codes, scales, zeros, self.tiles, group, stream)
@@ -131,13 +133,22 @@ class Q4Matrix:
         is allocated for the call, in the order of the stream it runs on."""
         if self.n_groups != 1:
             raise ValueError("apply takes a single weight; stacked ones are moe_apply's")
-        if x.dtype is not self.dtype:
-            raise TypeError(f"x must be {self.dtype} like the scales, got {x.dtype}")
-        if workspace is None and x.dim() == 2:
-            with _stream_scope(stream, self.tiles.device):
-                workspace = self.workspace(x.shape[0])
-        return q4_matmul(self.n_rows, self.n_cols, self.tiles, alpha, x, beta, y, workspace, self.group, self.with_zeros,
-                         stream)
+        d, n, width, xp, ldx = _matrix(x, "x")
+        dt = x.dtype
+        if dt is not self.dtype:
+            raise TypeError(f"x must be {self.dtype} like the scales, got {dt}")
+        if width != self.n_cols:
+            raise ValueError(f"x must have {self.n_cols} columns, got {width}")
+        if d != self.tiles.device:
+            raise ValueError(f"x is on {d}, not on {self.tiles.device}")
+        if workspace is None:
+            with _stream_scope(stream, d):
+                workspace = self.workspace(n)
+        yp, ldy = _rows(y, (dt, _F32), "y", n, self.n_rows, d)
+        wp, wb = _ws(workspace, d)
+        _launch(d, stream, "q4_matmul", self.n_rows, width, self.group, self.with_zeros, self.tiles.data_ptr(), _CODE[dt],
+                n, alpha, xp, ldx, beta, yp, _CODE[y.dtype], ldy, wp, wb)
+        return y
 
 
 # ---------------------------------------------------------------------------

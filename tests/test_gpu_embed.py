@@ -164,6 +164,27 @@ def test_grad_against_differences():
             assert (look(a) - look(b)) / 0.5 == grad[v, j].item()
 
 
+def test_refusals():
+    ids, table, y = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(9, 16, device="cuda").half(), torch.zeros(4, 16, device="cuda")
+    for i, t, o in ((ids, table, y[:3]), (ids, table, y[:, :15]), (ids[::2], table, y[:2]), (ids, table[0], y), (ids, table.t(), y)):
+        with pytest.raises(ValueError):
+            S.embed_lookup(i, t, o)
+    for i, t, o in ((ids.long(), table, y), (ids, table.double(), y), (ids, table, y.bfloat16()), (ids, table.cpu(), y)):
+        with pytest.raises(TypeError):
+            S.embed_lookup(i, t, o)
+    dy, ws = torch.zeros(4, 16, device="cuda"), torch.empty(S.embed_grad_workspace_size(4, 9, 16), dtype=torch.uint8, device="cuda")
+    dt = torch.zeros(9, 16, device="cuda")
+    for i, d, o in ((ids[:3], dy, dt), (ids, dy, dt[:, :15]), (ids, dy, dt[0]), (ids, dy.t(), dt)):
+        with pytest.raises(ValueError):
+            S.embed_grad(i, d, o, ws)
+    for i, d, o in ((ids.long(), dy, dt), (ids, dy, dt.half()), (ids, dy.double(), dt)):
+        with pytest.raises(TypeError):
+            S.embed_grad(i, d, o, ws)
+    for bad in (None, ws[:-16]):
+        with pytest.raises(S.SpmvError):
+            S.embed_grad(ids, dy, dt, bad)
+
+
 def test_captured_and_replayed():
     n, v, d = 500, 90, 128
     ids, dy = torch.from_numpy(_ids("skewed", n, v, 1)).cuda(), torch.randn(n, d, device="cuda").bfloat16()

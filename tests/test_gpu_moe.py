@@ -144,6 +144,30 @@ def test_large_hidden_values():
         assert ((y[t] - ref[t]).abs() <= ref[t].abs() * 2.0 ** -20).all()
 
 
+def test_refusals():
+    m = Layer(4, 72, 40, 64, "f16", False, seed=1)
+    keys, w, x = _batch(5, 2, 4, 72, "f16", 1)
+    y, ws = torch.empty(5, 72, device="cuda"), torch.empty(S.moe_workspace_size(5, 2, 72, 40), dtype=torch.uint8, device="cuda")
+    ok = dict(keys=keys, weights=w, gate_up=m.gu, down=m.dn, x=x, y=y, workspace=ws)
+    S.moe_apply(**ok)
+    for name, bad in (("keys", keys.reshape(-1)), ("keys", keys[:4]), ("weights", w[:, :1]), ("x", x[:, :71]), ("y", y[:4]),
+                      ("y", y[:, :71]), ("gate_up", m.dn), ("down", m.gu), ("workspace", ws[::2])):
+        with pytest.raises(ValueError):
+            S.moe_apply(**{**ok, name: bad})
+    for name, bad in (("keys", keys.long()), ("weights", w.half()), ("x", x.bfloat16()), ("x", x.float()), ("y", y.bfloat16())):
+        with pytest.raises(TypeError):
+            S.moe_apply(**{**ok, name: bad})
+    for bad in (None, ws[:-16]):
+        with pytest.raises(S.SpmvError):
+            S.moe_apply(**{**ok, "workspace": bad})
+    other = Layer(4, 72, 40, 32, "f16", False, seed=1)
+    with pytest.raises(ValueError):                          # another group size
+        S.moe_apply(**{**ok, "down": other.dn})
+    zeros = Layer(4, 72, 40, 64, "f16", True, seed=1)
+    with pytest.raises(ValueError):                          # zero points in one of them
+        S.moe_apply(**{**ok, "down": zeros.dn})
+
+
 def test_captured_and_replayed():
     m = Layer(8, 256, 192, 64, "f16", True, seed=2)
     keys, w, x = _batch(24, 2, 8, 256, "f16", 1)

@@ -88,7 +88,6 @@ def test_nothing_to_do_and_no_columns():
 def test_infinities_and_nan_stay_in_their_row(dt, tok, cols):
     """What the definition gives in float64, sign of infinity and NaN included."""
     m, w = _matrix(90, cols, 64, dt, False, 5)
-    w[:, 3:5] = w[:, 3:5]
     x = torch.randn(tok, cols, generator=torch.Generator().manual_seed(1)).to(F[dt])
     x[1, 3], x[2, cols - 1] = float("inf"), float("nan")
     x[3, 3], x[3, 4] = float("inf"), float("-inf")
@@ -102,6 +101,47 @@ def test_infinities_and_nan_stay_in_their_row(dt, tok, cols):
     keep = [t for t in range(tok) if t not in (1, 2, 3)]
     ref, bound = Q.matmul(w, x[keep], 1.0, 0.0, None, torch.float32, 64)
     R.check(y[keep], ref, bound, "other tokens")
+
+
+@pytest.mark.parametrize("tok", [1, 9, 80])
+def test_subnormal_x(tok):
+    """fp16's smallest numbers are multiplied as they are."""
+    m, w = _matrix(50, 700, 128, "f16", True, 8)
+    x = (torch.randint(-1023, 1024, (tok, 700)).double() * 2.0 ** -24).half()
+    y = m.apply(x.cuda(), torch.empty(tok, 50, device="cuda"))
+    ref, bound = Q.matmul(w, x, 1.0, 0.0, None, torch.float32, 128)
+    R.check(y, ref, bound)
+
+
+def test_refusals():
+    m, _ = _matrix(40, 256, 64, "f16", True, 1)
+    x, y = torch.zeros(3, 256, device="cuda").half(), torch.zeros(3, 40, device="cuda")
+    for bad in (x.bfloat16(), x.float()):
+        with pytest.raises(TypeError):
+            m.apply(bad, y)
+    for bx, by in ((x[:, :255], y), (x, y[:2]), (x, y[:, :39]), (x[0], y), (x.t(), y)):
+        with pytest.raises(ValueError):
+            m.apply(bx, by)
+    with pytest.raises(TypeError):
+        m.apply(x, y.bfloat16())
+    with pytest.raises(TypeError):
+        m.apply(x.cpu(), y)
+    with pytest.raises(ValueError):
+        S.q4_matmul(40, 256, m.tiles[:-16], 1.0, x, 0.0, y, group=64, with_zeros=True)
+    stack = S.Q4Matrix.quantize(torch.randn(2, 20, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        stack.apply(torch.zeros(1, 64, device="cuda").half(), torch.zeros(1, 20, device="cuda"))
+    codes, scales = torch.zeros(40, 32, dtype=torch.int32, device="cuda"), torch.ones(40, 4, device="cuda").half()
+    for c, s in ((codes[:-1], scales), (codes, scales[:-1]), (codes, scales.t())):
+        with pytest.raises(ValueError):
+            S.Q4Matrix(40, 256, c, s, group=64)
+    with pytest.raises(TypeError):
+        S.Q4Matrix(40, 256, codes, scales.float(), group=64)
+    with pytest.raises(ValueError):
+        S.Q4Matrix(40, 256, codes, scales, group=48)
+    big = S.Q4Matrix.quantize(torch.randn(2048, 12288, device="cuda").half())
+    with pytest.raises(S.SpmvError):                         # the workspace of one token for 64
+        big.apply(torch.zeros(64, 12288, device="cuda").half(), torch.zeros(64, 2048, device="cuda"), workspace=big.workspace(1))
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
