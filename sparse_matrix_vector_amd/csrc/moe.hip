@@ -33,8 +33,6 @@ constexpr int ME_MAX_SLOTS = 4096;
 constexpr int ME_MAX_EXPERTS = 1024;
 constexpr int ME_MAX_WIDTH = 1 << 24;
 constexpr int ME_UP_WAVES = 4;
-constexpr int ME_UP_AHEAD = 2;       // blocks whose codes are on their way in the tiles
-constexpr int ME_DOWN_AHEAD = 1;
 constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
 constexpr int ME_DOWN_WAVES = 16;
 constexpr int ME_UNROLL = 2;         // blocks of a step of the down product
@@ -286,27 +284,25 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        Q4Piece<E, ZP, G, 1> w[ME_UP_AHEAD + 1][2];
-        u32x4 v[TT];
-        load_x(0, v);
+        Q4Piece<E, ZP, G, 1> w[2][2];
+        u32x4 v[2][TT];                                                // x of the next block and of the one after it
+        load_x(0, v[0]);
+        load_x(min(1, n_blk - 1), v[1]);
 #pragma unroll
-        for (int a = 0; a < ME_UP_AHEAD; ++a)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
-        keep_x(0, xt[0], v);
+        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
+        keep_x(0, xt[0], v[0]);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += ME_UP_AHEAD + 1) {
+        for (int bb = 0; bb < n_blk; bb += 2) {
 #pragma unroll
-            for (int a = 0; a <= ME_UP_AHEAD; ++a) {
+            for (int a = 0; a < 2; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
-                load_x(min(b + 1, n_blk - 1), v);                      // x first: what waits for it does not wait for the codes
+                load_x(min(b + 2, n_blk - 1), v[a]);                   // x first: what waits for it does not wait for the codes
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    w[(a + ME_UP_AHEAD) % (ME_UP_AHEAD + 1)][r].load(rows[r], min(b + ME_UP_AHEAD, n_blk - 1));
+                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
-                up_block<E, ZP, G, TT>(w[a], xt[b & 1], acc);
-                keep_x(min(b + 1, n_blk - 1), xt[1 - (b & 1)], v);
+                up_block<E, ZP, G, TT>(w[a], xt[a], acc);
+                keep_x(min(b + 1, n_blk - 1), xt[1 - a], v[1 - a]);
                 __syncthreads();
             }
         }
@@ -480,7 +476,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                                                                        const char *__restrict__ tiles,
                                                                        const unsigned short *__restrict__ h,
                                                                        float *__restrict__ z) {
-    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT, A = ME_DOWN_AHEAD;  // 48 pieces of 16 bytes of an entry's block
+    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT, A = 1;  // 48 pieces of 16 bytes of an entry's block
     typedef Q4Op<BF16> Op;
     __shared__ u32x4 ht[2][48 * 16 * TT];
     __shared__ EntryLds el;
@@ -634,20 +630,38 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
     }
 }
 
-// y[t] = sum over c (ascending) of weights[t, c] * z[place[t, c]].
+// y[t] = sum over c (ascending) of weights[t, c] * z[place[t, c]]; a lane holds one
+// of 64 choices, and the rows of 8 choices are on their way together.
 template <class E>
 __global__ __launch_bounds__(256) void k_moe_sum(int n_tok, int top_k, int n_experts, int dim, int pieces,
                                                  const int *__restrict__ keys, const float *__restrict__ weights,
                                                  const int *__restrict__ place, const float *__restrict__ z,
                                                  void *__restrict__ y, bool f32, int64_t ldy) {
+    constexpr int U = 8;
     const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int t = (int)(id / pieces), col = (int)(id - (int64_t)t * pieces) * 64 + __lane_id();
+    const int lane = __lane_id(), t = (int)(id / pieces), col = (int)(id - (int64_t)t * pieces) * 64 + lane;
     if (t >= n_tok) return;
-    const int c0 = min(col, dim - 1);
+    const float *zc = z + min(col, dim - 1);
     float v = 0.0f;
-    for (int s = t * top_k, c = 0; c < top_k; ++c, ++s) {
-        const int e = keys[s];
-        if ((unsigned)e < (unsigned)n_experts) v = fmaf(weights ? weights[s] : 1.0f, z[(int64_t)place[s] * dim + c0], v);
+    for (int c0 = 0; c0 < top_k; c0 += 64) {
+        const int s = t * top_k + min(c0 + lane, top_k - 1);
+        const bool in = c0 + lane < top_k && (unsigned)keys[s] < (unsigned)n_experts;
+        const int at = place[s];                                        // of a dropped choice: not used
+        const float w = weights ? weights[s] : 1.0f;
+        unsigned long long left = __ballot(in);
+        while (left) {
+            float x[U], f[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = left ? __ffsll(left) - 1 : -1;
+                left &= left - 1;
+                f[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j & 63));
+                x[u] = j >= 0 ? zc[(int64_t)__builtin_amdgcn_readlane(at, j & 63) * dim] : 0.0f;
+                if (j < 0) f[u] = 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) v = fmaf(f[u], x[u], v);
+        }
     }
     if (col >= dim) return;
     if (f32)

@@ -183,13 +183,13 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
 // different banks).  Every fragment of W is decoded once and used TT times; its
 // codes go straight to registers, a block ahead.  With few tiles the columns are
 // split over workgroups, whose sums k_q4_join adds.
-template <class E, bool ZP, int G, int RT, int TT>
+template <class E, bool ZP, int G, int RT, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int n_blk, int row_tiles, int tok_tiles,
                                                     int split, const char *__restrict__ tiles, int n_tok, float alpha,
                                                     const typename E::T *__restrict__ x, int64_t ldx, float beta,
                                                     void *__restrict__ y, bool f32, int64_t ldy,
                                                     float *__restrict__ parts) {
-    constexpr int PG = G / 32, TN = 16 * TT, A = RT == 4 || (G == 32 && TT == 4) ? 1 : 2;
+    constexpr int PG = G / 32, TN = 16 * TT, XA = RT == 4 || TT == 4 ? 1 : 2;
     __shared__ u32x4 xt[2][TN * 16];
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
     // neighbouring workgroups run on different XCDs; every 8th one shares a row tile, whose codes one L2 then holds
@@ -224,30 +224,29 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
 #pragma unroll
         for (int q = 0; q < TT; ++q) to[slot[q]] = v[q];
     };
-    Q4Piece<E, ZP, G, 1> w[A + 1][RT];
-    u32x4 v[TT];
-    load_x(b0, v);
+    Q4Piece<E, ZP, G, 1> w[2][RT];
+    u32x4 v[XA][TT];                                 // x of the next block, and of the one after it where there is room
+    load_x(b0, v[0]);
+    if constexpr (XA == 2) load_x(min(b0 + 1, b1 - 1), v[1]);
 #pragma unroll
-    for (int a = 0; a < A; ++a)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) w[a][r].load(rows[r], min(b0 + a, b1 - 1));
-    keep_x(b0, xt[0], v);
+    for (int r = 0; r < RT; ++r) w[0][r].load(rows[r], b0);
+    keep_x(b0, xt[0], v[0]);
     f32x4 acc[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    for (int bb = b0; bb < b1; bb += A + 1) {
+    for (int bb = b0; bb < b1; bb += 2) {
 #pragma unroll
-        for (int a = 0; a <= A; ++a) {
+        for (int a = 0; a < 2; ++a) {
             const int b = bb + a;
             if (b >= b1) break;
-            const u32x4 *now = xt[(b - b0) & 1];
+            const u32x4 *now = xt[a];
             // x first: what waits for it does not wait for the codes behind it
-            load_x(min(b + 1, b1 - 1), v);
+            load_x(min(b + XA, b1 - 1), v[XA == 2 ? a : 0]);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) w[(a + A) % (A + 1)][r].load(rows[r], min(b + A, b1 - 1));
+            for (int r = 0; r < RT; ++r) w[1 - a][r].load(rows[r], min(b + 1, b1 - 1));
             __builtin_amdgcn_sched_barrier(0);
             f32x4 sum[RT][TT];
 #pragma unroll
@@ -276,7 +275,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 // keeps the fragments of one product in registers at a time
                 __builtin_amdgcn_sched_barrier(0);
             }
-            keep_x(min(b + 1, b1 - 1), xt[(b - b0 + 1) & 1], v);
+            keep_x(min(b + 1, b1 - 1), xt[1 - a], v[XA == 2 ? 1 - a : 0]);
             __syncthreads();
         }
     }
@@ -284,29 +283,56 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     for (int r = 0; r < RT; ++r) {
         const int64_t row = row0 + 16 * r + (lane & 15);
         if (row >= n_rows) continue;
+        // the lane's token of each tile is 16 rows of the result further
+        float *part = SPLIT ? parts + ((int64_t)blockIdx.y * n_tok + t0 + 4 * quarter) * n_rows + row : nullptr;
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tok = t0 + 16 * t + 4 * quarter + i;
                 if (tok >= n_tok) continue;
-                if (split > 1)
-                    parts[((int64_t)blockIdx.y * n_tok + tok) * n_rows + row] = acc[r][t][i];
+                if constexpr (SPLIT)
+                    part[(int64_t)(16 * t + i) * n_rows] = acc[r][t][i];
                 else
                     q4_store<E>(y, f32, (int64_t)tok * ldy + row, alpha * acc[r][t][i], beta);
             }
     }
 }
 
+// Adds the parts, in order: 4 results for a thread, 8 parts on their way together.
 template <class E>
 __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int split, float alpha, float beta,
                                                  const float *__restrict__ parts, void *__restrict__ y, bool f32,
                                                  int64_t ldy) {
-    const int64_t n = (int64_t)n_rows * n_tok, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    constexpr int U = 8;
+    const int64_t n = (int64_t)n_rows * n_tok, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
-    float v = 0.0f;
-    for (int k = 0; k < split; ++k) v += parts[k * n + i];
-    q4_store<E>(y, f32, i / n_rows * ldy + i % n_rows, alpha * v, beta);
+    const int64_t from = min(i, max((int64_t)0, n - 4));         // the last thread starts early
+    if (n < 4) {
+        for (int64_t j = i; j < n; ++j) {
+            float v = 0.0f;
+            for (int k = 0; k < split; ++k) v += parts[k * n + j];
+            q4_store<E>(y, f32, j / n_rows * ldy + j % n_rows, alpha * v, beta);
+        }
+        return;
+    }
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < split; k0 += U) {
+        f32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = __builtin_bit_cast(f32x4, load_any<F32, 4>(parts + min(k0 + u, split - 1) * n + from));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u < split) sum += v[u];
+    }
+    int64_t t = from / n_rows;
+    int row = (int)(from - t * n_rows);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (from + j >= i) q4_store<E>(y, f32, t * ldy + row, alpha * sum[j], beta);
+        if (++row == n_rows) row = 0, ++t;
+    }
 }
 
 // y = beta * y where W has no columns.
@@ -414,13 +440,14 @@ Tiling tiling(int64_t n_rows, int64_t n_cols, int64_t n_tok, bool wide) {
     Tiling t;
     t.tt = (int)std::min<int64_t>(4, ceil_div(n_tok, 16));
     // 64 rows of a wave share a fragment of x, where their sums fit the registers: 513
-    // tokens of 12288 x 12288 206 us against 230 with 32 rows (groups of 128); 1300
-    // against 295 with groups of 32 and zero points, whose code needs more registers
+    // tokens of 12288 x 12288 192 us against 230 with 32 rows (fp16, groups of 128);
+    // 1300 against 295 with groups of 32 and zero points, whose code needs more registers
     t.rt = n_tok > 64 && wide ? 4 : 2;
     t.row_tiles = (int)ceil_div(n_rows, 64 * t.rt);
     t.tok_tiles = (int)ceil_div(n_tok, 16 * t.tt);
-    // as many workgroups as run at once: 48 tokens of 12288 x 12288 40 us with 768 (3 per CU), 47 with 512, 48 with 1024
-    const int64_t tiles = (int64_t)t.row_tiles * t.tok_tiles, groups = t.rt == 4 || t.tt == 4 ? 512 : 768;
+    // two workgroups on each CU: 48 tokens of 12288 x 12288 (bf16, groups of 64, zero
+    // points) 35.9 us with 512 and 38.9 with 768, whose parts take longer to add
+    const int64_t tiles = (int64_t)t.row_tiles * t.tok_tiles, groups = 512;
     t.split = (int)std::max<int64_t>(1, std::min(groups / tiles, q4_blocks(n_cols) / QT_MIN_BLOCKS));
     return t;
 }
@@ -622,11 +649,14 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         typedef typename E::T T;
         constexpr bool ZP = decltype(zp)::value;
         constexpr int G = decltype(g)::value;
-        auto run = [&](auto rt, auto tt) {
-            k_q4_tile<E, ZP, G, decltype(rt)::value, decltype(tt)::value>
+        auto launch = [&](auto rt, auto tt, auto split) {
+            k_q4_tile<E, ZP, G, decltype(rt)::value, decltype(tt)::value, decltype(split)::value>
                 <<<dim3((unsigned)(t.row_tiles * t.tok_tiles), (unsigned)t.split), 256, 0, s>>>(
                     n_rows, n_cols, n_blk, t.row_tiles, t.tok_tiles, t.split, static_cast<const char *>(tiles), n_tok,
                     alpha, static_cast<const T *>(x), ldx, beta, y, f32, ldy, static_cast<float *>(workspace));
+        };
+        auto run = [&](auto rt, auto tt) {
+            t.split > 1 ? launch(rt, tt, std::true_type{}) : launch(rt, tt, std::false_type{});
         };
         const std::integral_constant<int, 2> two;
         const std::integral_constant<int, 4> four;
@@ -644,7 +674,7 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
         return SPMV_OK;
     });
     if (st != SPMV_OK || t.split == 1) return st;
-    const int grid = (int)ceil_div((int64_t)n_rows * n_tok, 256);
+    const int grid = (int)ceil_div((int64_t)n_rows * n_tok, 1024);
     if (dtype == SPMV_F16)
         k_q4_join<F16><<<grid, 256, 0, s>>>(n_rows, n_tok, t.split, alpha, beta, static_cast<const float *>(workspace), y,
                                             f32, ldy);
