@@ -63,8 +63,9 @@ struct Entries {
 };
 struct EntryLds {
     unsigned short list[ME_MAX_TOK];
-    int n, below[ME_UP_WAVES], equal[ME_UP_WAVES];
+    int count[ME_UP_WAVES], below[ME_UP_WAVES], equal[ME_UP_WAVES];
 };
+static_assert(ME_MAX_TOK <= 64 * ME_UP_WAVES, "a thread looks at one token's choices");
 // The expert of this workgroup, or -1 if another one does its work.
 __device__ __forceinline__ int expert_of(int n_experts, bool by_slot, const int *__restrict__ keys) {
     if (!by_slot) return blockIdx.y;
@@ -74,32 +75,34 @@ __device__ __forceinline__ int expert_of(int n_experts, bool by_slot, const int 
     return __syncthreads_or(before) || (unsigned)e >= (unsigned)n_experts ? -1 : e;
 }
 __device__ __forceinline__ Entries find_entries(int n_tok, int top_k, int e, const int *__restrict__ keys, EntryLds &l) {
-    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int slots = n_tok * top_k;
+    constexpr int U = 8;
+    const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), t = threadIdx.x;
     int lo = 0, eq = 0;
-    for (int i0 = wv * 64; i0 < slots; i0 += 64 * ME_UP_WAVES) {
-        const int k = i0 + lane < slots ? keys[i0 + lane] : -1;
-        lo += __popcll(__ballot(k >= 0 && k < e));
-        eq += __popcll(__ballot(k == e));
-    }
-    if (lane == 0) l.below[wv] = lo, l.equal[wv] = eq;
-    if (wv == 0) {
-        int n = 0;
-        for (int t0 = 0; t0 < n_tok; t0 += 64) {
-            const int t = t0 + lane;
-            bool mine = false;
-            if (t < n_tok)
-                for (int c = 0; c < top_k; ++c) mine |= keys[t * top_k + c] == e;
-            const unsigned long long has = __ballot(mine);
-            if (mine) l.list[n + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)t;
-            n += __popcll(has);
-        }
-        if (lane == 0) l.n = n;
-    }
-    __syncthreads();
-    Entries r = {__builtin_amdgcn_readfirstlane(l.n), 0, 0};
+    bool mine = false;
+    for (int c0 = 0; c0 < top_k; c0 += U) {
+        int k[U];
 #pragma unroll
-    for (int w = 0; w < ME_UP_WAVES; ++w) r.base += l.below[w], r.room += l.equal[w];
+        for (int u = 0; u < U; ++u) k[u] = t < n_tok && c0 + u < top_k ? keys[t * top_k + c0 + u] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            lo += __popcll(__ballot(k[u] >= 0 && k[u] < e));
+            eq += __popcll(__ballot(k[u] == e));
+            mine |= k[u] == e;
+        }
+    }
+    const unsigned long long has = __ballot(mine);
+    if (lane == 0) l.count[wv] = __popcll(has), l.below[wv] = lo, l.equal[wv] = eq;
+    __syncthreads();
+    Entries r = {0, 0, 0};
+    int at = 0;
+#pragma unroll
+    for (int w = 0; w < ME_UP_WAVES; ++w) {
+        if (w < wv) at += l.count[w];
+        r.n += l.count[w], r.base += l.below[w], r.room += l.equal[w];
+    }
+    if (mine) l.list[at + __popcll(has & ((1ull << lane) - 1))] = (unsigned short)t;
+    __syncthreads();
+    r.n = __builtin_amdgcn_readfirstlane(r.n);
     r.base = __builtin_amdgcn_readfirstlane(r.base);
     r.room = __builtin_amdgcn_readfirstlane(r.room);
     return r;
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
                                                                      const char *__restrict__ tiles,
                                                                      const typename E::T *__restrict__ x, int64_t ldx,
                                                                      unsigned short *__restrict__ h, int *__restrict__ place) {
-    constexpr int TN = 16 * TT;
+    constexpr int TN = 16 * TT, A = 2;                                 // A blocks of codes on their way
     __shared__ u32x4 xt[2][TN * 16];
     __shared__ EntryLds el;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -284,25 +287,26 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        Q4Piece<E, ZP, G, 1> w[2][2];
-        u32x4 v[2][TT];                                                // x of the next block and of the one after it
-        load_x(0, v[0]);
-        load_x(min(1, n_blk - 1), v[1]);
+        Q4Piece<E, ZP, G, 1> w[A + 1][2];
+        u32x4 v[TT];
+        load_x(0, v);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
-        keep_x(0, xt[0], v[0]);
+        for (int a = 0; a < A; ++a)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
+        keep_x(0, xt[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += 2) {
+        for (int bb = 0; bb < n_blk; bb += A + 1) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a = 0; a <= A; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
-                load_x(min(b + 2, n_blk - 1), v[a]);                   // x first: what waits for it does not wait for the codes
+                load_x(min(b + 1, n_blk - 1), v);                      // x first: what waits for it does not wait for the codes
 #pragma unroll
-                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
+                for (int r = 0; r < 2; ++r) w[(a + A) % (A + 1)][r].load(rows[r], min(b + A, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
-                up_block<E, ZP, G, TT>(w[a], xt[a], acc);
-                keep_x(min(b + 1, n_blk - 1), xt[1 - a], v[1 - a]);
+                up_block<E, ZP, G, TT>(w[a], xt[b & 1], acc);
+                keep_x(min(b + 1, n_blk - 1), xt[1 - (b & 1)], v);
                 __syncthreads();
             }
         }
@@ -476,7 +480,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                                                                        const char *__restrict__ tiles,
                                                                        const unsigned short *__restrict__ h,
                                                                        float *__restrict__ z) {
-    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT, A = 1;  // 48 pieces of 16 bytes of an entry's block
+    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT;  // 48 pieces of 16 bytes of an entry's block
     typedef Q4Op<BF16> Op;
     __shared__ u32x4 ht[2][48 * 16 * TT];
     __shared__ EntryLds el;
@@ -485,12 +489,10 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
     if (e < 0) return;
     const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 32;
     Q4Rows<ZP, G> rows[2];
-    Q4Piece<E, ZP, G, 1> w[A + 1][2];
+    Q4Piece<E, ZP, G, 1> w[2][2];
     auto load_first = [&]() {
 #pragma unroll
-        for (int a = 0; a < A; ++a)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) w[a][r].load(rows[r], min(a, n_blk - 1));
+        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
     };
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -541,17 +543,16 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
         if (first > 0) load_first();
         keep_h(ht[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += A + 1) {
+        for (int bb = 0; bb < n_blk; bb += 2) {
 #pragma unroll
-            for (int a = 0; a <= A; ++a) {
+            for (int a = 0; a < 2; ++a) {
                 const int b = bb + a;
                 if (b >= n_blk) break;
                 load_h(min(b + 1, n_blk - 1), v);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    w[(a + A) % (A + 1)][r].load(rows[r], min(b + A, n_blk - 1));
+                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
                 __builtin_amdgcn_sched_barrier(0);
-                const u32x4 *now = ht[b & 1];
+                const u32x4 *now = ht[a];
                 f32x4 sum[2][TT];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                         }
                     }
                 }
-                keep_h(ht[1 - (b & 1)], v);
+                keep_h(ht[1 - a], v);
                 __syncthreads();
             }
         }
