@@ -774,7 +774,8 @@ spmv_status lora_grad(int32_t n_tok, int32_t n_in, int32_t n_out, int32_t n_adap
 /* e = 0 .. 7, column e in bits 4 i .. 4 i + 3 with i = e / 2 + 4 (e % 2).       */
 /* group (32, 64 or 128) columns share a scale (fp16 or bf16) and, where zeros   */
 /* is not NULL, a zero point (uint8, its low four bits); both are arrays         */
-/* [n_rows, ceil(n_cols / 128) * 128 / group].  The weight is                    */
+/* [n_rows, ceil(n_cols / 128) * 128 / group], those of groups past the last      */
+/* column not used.  The weight is                                               */
 /*   W[i, j] = scale * (code - zero), zero = 8 where zeros is NULL.              */
 /* More than 2^30 columns are SPMV_ERR_UNSUPPORTED.                               */
 /* ======================================================================== */
@@ -832,19 +833,21 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t dim, int32_
  * with silu(v) = v / (1 + exp(-v)).  Weights as q4_tiles arranges them, the experts
  * stacked: up_tiles of [n_experts * 2 * inter, dim], an expert's inter gate rows
  * before its inter up rows, and down_tiles of [n_experts * dim, inter]; one group
- * size, and zero points in both (with_zeros != 0) or in neither.  keys int32 [n_tok * top_k]: a choice
- * outside [0, n_experts) is dropped; an expert chosen twice by a token counts with
- * both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A token without an
- * expert gets zeros.  x [n_tok, dim] of type dtype (the scales' type), y [n_tok, dim]
- * of the same type or fp32, rounded once; the products between are kept with fp32's
- * 24 bits.  Only the weights of chosen experts are read.  At most 1024 experts,
- * a width dim of 8 to 2^24 and inter of at most 2^24 (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
- * overlap; x and y must not overlap.  The same bits on every call.  All pointers
- * device.  Asynchronous. */
+ * size, and zero points in both (with_zeros != 0) or in neither.  keys int32
+ * [n_tok * top_k]: a choice outside [0, n_experts) is dropped; an expert chosen twice
+ * by a token counts with both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A
+ * token without an expert gets zeros.  x [n_tok, dim] of type dtype (the scales'
+ * type), y [n_tok, dim] of the same type or fp32, rounded once; the products between
+ * are kept with fp32's 24 bits.  Of an expert without a token no more than the first
+ * block of its rows is read.  At most 1024 experts, a width dim of 8 to 2^24 and
+ * inter of at most 2^24 (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not
+ * shared by calls that may overlap; x and y must not overlap.  The same bits on every
+ * call.  All pointers device.  Asynchronous. */
 spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,
                       int32_t group, int32_t with_zeros, const int32_t *keys, const float *weights,
                       const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x,
-                      int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
+                      int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace,
+                      size_t workspace_bytes, void *stream);
 
 /* ======================================================================== */
 /* Rows of a table by token id, and the table's gradient: the products of the   */

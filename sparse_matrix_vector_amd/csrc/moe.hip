@@ -36,7 +36,6 @@ constexpr int ME_UP_WAVES = 4;
 constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
 constexpr int ME_DOWN_WAVES = 16;
 constexpr int ME_UNROLL = 2;         // blocks of a step of the down product
-constexpr int ME_UNITS = 1;          // units of a wave of the down product, about
 
 // Where the tile of entries first .. first + n - 1 of all entries begins, and a
 // part of a piece of 8 columns in it (in 16-bit numbers).
@@ -118,7 +117,7 @@ __device__ __forceinline__ void store_places(int top_k, int e, const Entries &en
 
 // One block's products of gate and up rows with TT tiles of x, as they lie in LDS.
 template <class E, bool ZP, int G, int TT>
-__device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G, 1> (&w)[2], const u32x4 *xt, f32x4 (&acc)[2][TT]) {
+__device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G> (&w)[2], const u32x4 *xt, f32x4 (&acc)[2][TT]) {
     constexpr int PG = G / 32;
     const int lane = __lane_id(), quarter = lane / 16;
     f32x4 sum[2][TT];
@@ -130,7 +129,7 @@ __device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G, 1> (&w)[2], con
         for (int t = 0; t < TT; ++t) xv[t] = xt[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const u32x4 f = Q4Op<E>::decode(w[r].c[0][m], Q4Op<E>::zero(w[r].zero(0, g)));
+            const u32x4 f = Q4Op<E>::decode(w[r].c[m], Q4Op<E>::zero(w[r].zero(g)));
 #pragma unroll
             for (int t = 0; t < TT; ++t)
                 sum[r][t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
@@ -138,7 +137,7 @@ __device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G, 1> (&w)[2], con
         if ((m + 1) % PG == 0) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float sc = w[r].scale(0, g) * Q4Op<E>::UNIT;
+                const float sc = w[r].scale(g) * Q4Op<E>::UNIT;
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -181,7 +180,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
     if (e < 0) return;
     const int part = wv % parts, row0 = ((int)blockIdx.x * (ME_UP_WAVES / parts) + wv / parts) * 16;
     Q4Rows<ZP, G> rows[2];
-    Q4Piece<E, ZP, G, 1> w[2][2];
+    Q4Piece<E, ZP, G> w[2][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         rows[r] = Q4Rows<ZP, G>::any(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk);
@@ -287,7 +286,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        Q4Piece<E, ZP, G, 1> w[A + 1][2];
+        Q4Piece<E, ZP, G> w[A + 1][2];
         u32x4 v[TT];
         load_x(0, v);
 #pragma unroll
@@ -347,10 +346,10 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
         left &= ~__ballot(valid && key == __builtin_amdgcn_readlane(key, j));
     }
     const int na = __popcll(firsts);
-    // units of about as much work for every wave: an expert, or a part of its columns.
+    // a unit of work for about every wave: an expert, or a part of its columns.
     // A wave goes through its units' steps (U blocks of 16 entries), the next step's codes on their way.
     const int pieces = (n_blk + U - 1) / U;
-    const int split = na > 0 ? min(pieces, max(1, (ME_UNITS * W + na - 1) / na)) : 1;
+    const int split = na > 0 ? min(pieces, (W + na - 1) / na) : 1;
     const int row0 = blockIdx.x * rows, r = lane & (rows - 1), units = na * split;
     struct Step {
         int unit, e, n, base, room, first, k0, p;
@@ -380,8 +379,8 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
         s.first += 16;
         return s.first < s.n ? s : begin(s.unit + W);
     };
-    Q4Piece<E, ZP, G, 1> w[2][U];
-    auto load = [&](const Step &s, Q4Piece<E, ZP, G, 1> (&to)[U]) {
+    Q4Piece<E, ZP, G> w[2][U];
+    auto load = [&](const Step &s, Q4Piece<E, ZP, G> (&to)[U]) {
         const Q4Rows<ZP, G> row = Q4Rows<ZP, G>::any(tiles, (int64_t)s.e * dim + min(row0 + r, dim - 1), n_blk);
 #pragma unroll
         for (int u = 0; u < U; ++u) to[u].load(row, min(s.p * U + u, n_blk - 1));
@@ -415,18 +414,18 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
                 }
 #pragma unroll
                 for (int g = 0; g < GB; ++g) {
-                    const Op::Zero nz = Op::zero(w[a][u].zero(0, g));
+                    const Op::Zero nz = Op::zero(w[a][u].zero(g));
                     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int m = g * PG; m < (g + 1) * PG; ++m) {
-                        const u32x4 f = Op::decode(w[a][u].c[0][m], nz);
+                        const u32x4 f = Op::decode(w[a][u].c[m], nz);
                         if (!packed) {
                             sum = Op::mfma(v[2][m], f, sum);
                             sum = Op::mfma(v[1][m], f, sum);
                         }
                         sum = Op::mfma(v[0][m], f, sum);
                     }
-                    const float sc = w[a][u].scale(0, g);
+                    const float sc = w[a][u].scale(g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i] = fmaf(sc, sum[i], acc[i]);
                 }
@@ -489,7 +488,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
     if (e < 0) return;
     const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 32;
     Q4Rows<ZP, G> rows[2];
-    Q4Piece<E, ZP, G, 1> w[2][2];
+    Q4Piece<E, ZP, G> w[2][2];
     auto load_first = [&]() {
 #pragma unroll
         for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
@@ -560,7 +559,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                     u32x4 f[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        f[r] = Op::decode(w[a][r].c[0][m], Op::zero(w[a][r].zero(0, g)));
+                        f[r] = Op::decode(w[a][r].c[m], Op::zero(w[a][r].zero(g)));
                         if (m % PG == 0) {
 #pragma unroll
                             for (int t = 0; t < TT; ++t) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -586,7 +585,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                     if ((m + 1) % PG == 0) {
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float sc = w[a][r].scale(0, g);
+                            const float sc = w[a][r].scale(g);
 #pragma unroll
                             for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -715,7 +714,8 @@ extern "C" spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t 
 
 extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,
                                  int32_t group, int32_t with_zeros, const int32_t *keys, const float *weights,
-                                 const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x, int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace,
+                                 const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x,
+                                 int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, void *stream) {
     size_t need = 0;
     spmv_status st = moe_workspace_size(n_tok, top_k, dim, inter, &need);

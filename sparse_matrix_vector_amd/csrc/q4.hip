@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
     const int64_t row0 = (int64_t)blockIdx.x * 16;
     const int ld = n_blk * 16 + 1;                  // 16-byte pieces of a token: the odd one spreads tokens over the banks
     const Q4Rows<ZP, G> row(tiles, blockIdx.x, n_blk);
-    Q4Piece<E, ZP, G, 1> w[A + 1][U];
+    Q4Piece<E, ZP, G> w[A + 1][U];
     const int step = waves * U;
 #pragma unroll
     for (int a = 0; a < A; ++a)
@@ -69,12 +69,12 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
                 if (b + u >= n_blk) break;
 #pragma unroll
                 for (int g = 0; g < GB; ++g) {
-                    const typename Q4Op<E>::Zero nz = Q4Op<E>::zero(w[a][u].zero(0, g));
+                    const typename Q4Op<E>::Zero nz = Q4Op<E>::zero(w[a][u].zero(g));
                     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int m = g * PG; m < (g + 1) * PG; ++m)
-                        sum = Q4Op<E>::mfma(xr[(b + u) * 16 + 4 * m], Q4Op<E>::decode(w[a][u].c[0][m], nz), sum);
-                    const float s = w[a][u].scale(0, g) * Q4Op<E>::UNIT;
+                        sum = Q4Op<E>::mfma(xr[(b + u) * 16 + 4 * m], Q4Op<E>::decode(w[a][u].c[m], nz), sum);
+                    const float s = w[a][u].scale(g) * Q4Op<E>::UNIT;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, sum[i], acc[i]);
                 }
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
     f32x4 acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Q4Piece<E, ZP, G, 1> w[2];
+    Q4Piece<E, ZP, G> w[2];
     u32x4 v[4 * TT];
     load_x(min(wv, n_blk - 1), v);
     w[0].load(row, min(wv, n_blk - 1));
@@ -148,12 +148,12 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
                 u32x4 xv[TT];
 #pragma unroll
                 for (int t = 0; t < TT; ++t) xv[t] = mine[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
-                const u32x4 f = Q4Op<E>::decode(w[a].c[0][m], Q4Op<E>::zero(w[a].zero(0, g)));
+                const u32x4 f = Q4Op<E>::decode(w[a].c[m], Q4Op<E>::zero(w[a].zero(g)));
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
                     sum[t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[t]);
                 if ((m + 1) % PG == 0) {
-                    const float sc = w[a].scale(0, g) * Q4Op<E>::UNIT;
+                    const float sc = w[a].scale(g) * Q4Op<E>::UNIT;
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
 #pragma unroll
         for (int q = 0; q < TT; ++q) to[slot[q]] = v[q];
     };
-    Q4Piece<E, ZP, G, 1> w[2][RT];
+    Q4Piece<E, ZP, G> w[2][RT];
     u32x4 v[XA][TT];                                 // x of the next block, and of the one after it where there is room
     load_x(b0, v[0]);
     if constexpr (XA == 2) load_x(min(b0 + 1, b1 - 1), v[1]);
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 for (int t = 0; t < TT; ++t) xv[t] = now[(16 * t + (lane & 15)) * 16 + ((4 * m + quarter) ^ (lane & 15))];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const u32x4 f = Q4Op<E>::decode(w[a][r].c[0][m], Q4Op<E>::zero(w[a][r].zero(0, g)));
+                    const u32x4 f = Q4Op<E>::decode(w[a][r].c[m], Q4Op<E>::zero(w[a][r].zero(g)));
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
                         sum[r][t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t]);
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 if ((m + 1) % PG == 0) {
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const float sc = w[a][r].scale(0, g) * Q4Op<E>::UNIT;
+                        const float sc = w[a][r].scale(g) * Q4Op<E>::UNIT;
 #pragma unroll
                         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -344,9 +344,11 @@ __global__ __launch_bounds__(256) void k_q4_scale(int n_rows, int64_t n, float b
 }
 
 // The records from the rows: a workgroup writes the records of four blocks, a wave
-// each; words and groups past the last row are zeros.
-__global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_blk, int gb, int64_t n_rec, int rec_bytes,
-                                                  const u32x4 *__restrict__ codes,
+// each.  What lies past the last row is zeros, and so are the scales of groups past the
+// last column, whatever the caller's arrays hold there: x is zero in them, and a NaN
+// for a scale would come through.
+__global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_cols, int n_blk, int gb, int64_t n_rec,
+                                                  int rec_bytes, const u32x4 *__restrict__ codes,
                                                   const unsigned short *__restrict__ scales,
                                                   const unsigned char *__restrict__ zeros, char *__restrict__ tiles) {
     const int lane = __lane_id();
@@ -359,7 +361,8 @@ __global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_blk, int
     reinterpret_cast<u32x4 *>(out)[lane] = row < n_rows ? codes[(row * n_blk + b) * 4 + lane / 16] : none;
     for (int i = lane; i < 16 * gb; i += 64) {
         const int64_t r = tile * 16 + i / gb, at = (r * n_blk + b) * gb + i % gb;
-        reinterpret_cast<unsigned short *>(out + Q4_SCALES)[i] = r < n_rows ? scales[at] : (unsigned short)0;
+        const bool in = r < n_rows && b * Q4_BLOCK + i % gb * (Q4_BLOCK / gb) < n_cols;
+        reinterpret_cast<unsigned short *>(out + Q4_SCALES)[i] = in ? scales[at] : (unsigned short)0;
         if (zeros) reinterpret_cast<unsigned char *>(out + Q4_SCALES + 32 * gb)[i] = r < n_rows ? zeros[at] : (unsigned char)0;
     }
 }
@@ -541,7 +544,7 @@ extern "C" spmv_status q4_tiles(int32_t n_rows, int32_t n_cols, int32_t group, c
     st = check_grid(ceil_div(n_rec, 4));
     if (st != SPMV_OK) return st;
     k_q4_tiles<<<(int)ceil_div(n_rec, 4), 256, 0, as_stream(stream)>>>(
-        n_rows, (int)n_blk, Q4_BLOCK / group, n_rec, (int)q4_record(group, zeros != nullptr),
+        n_rows, n_cols, (int)n_blk, Q4_BLOCK / group, n_rec, (int)q4_record(group, zeros != nullptr),
         reinterpret_cast<const u32x4 *>(codes), static_cast<const unsigned short *>(scales), zeros,
         static_cast<char *>(tiles));
     SPMV_LAUNCHED("k_q4_tiles");
@@ -564,8 +567,9 @@ extern "C" spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t
 }
 
 extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, int32_t with_zeros, const void *tiles,
-                                 int32_t dtype, int32_t n_tok, float alpha, const void *x, int64_t ldx, float beta, void *y, int32_t y_dtype, int64_t ldy,
-                                 void *workspace, size_t workspace_bytes, void *stream) {
+                                 int32_t dtype, int32_t n_tok, float alpha, const void *x, int64_t ldx, float beta,
+                                 void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
     spmv_status st = check_weight(n_rows, n_cols, group, dtype);
     if (st != SPMV_OK) return st;
     if (n_tok < 0) return fail(SPMV_ERR_INVALID_VALUE, "negative size");
@@ -597,18 +601,18 @@ extern "C" spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, 
             constexpr bool ZP = decltype(zp)::value;
             constexpr int G = decltype(g)::value;
             const int waves = (int)std::min<int64_t>(QF_WAVES, ceil_div(n_blk, QF_UNROLL));
-            auto run = [&](auto tp, int t0, int n) {
+            auto run = [&](auto tp, int64_t t0, int n) {
                 k_q4_few<E, ZP, G, decltype(tp)::value>
                     <<<(int)ceil_div(n_rows, 16), 64 * waves, few_lds(n_cols, n, waves), s>>>(
                         n_rows, n_cols, n_blk, static_cast<const char *>(tiles), n, alpha,
                         static_cast<const T *>(x) + t0 * ldx, ldx, beta,
-                        static_cast<char *>(y) + t0 * ldy * (int64_t)dtype_size(y_dtype), f32, ldy);
+                        static_cast<char *>(y) + t0 * ldy * dtype_size(y_dtype), f32, ldy);
             };
             if (n_tok == 1)
                 run(std::integral_constant<int, 1>{}, 0, 1);
             else                                           // more than one turn only for fewer than 8 columns
-                for (int t0 = 0; t0 < n_tok; t0 += few_tokens(n_cols))
-                    run(std::integral_constant<int, 16>{}, t0, std::min(n_tok - t0, few_tokens(n_cols)));
+                for (int64_t t0 = 0; t0 < n_tok; t0 += few_tokens(n_cols))
+                    run(std::integral_constant<int, 16>{}, t0, (int)std::min<int64_t>(n_tok - t0, few_tokens(n_cols)));
             SPMV_LAUNCHED("k_q4_few");
             return SPMV_OK;
         });

@@ -133,30 +133,26 @@ struct Q4Rows {
     }
 };
 
-// U blocks of one row as a lane holds them: its quarter's codes, and the scales
-// and zero points of all their groups.
-template <class E, bool ZP, int G, int U>
+// A block of one row as a lane holds it: its quarter's codes, and the scales and zero
+// points of all its groups.
+template <class E, bool ZP, int G>
 struct Q4Piece {
     static constexpr int GB = Q4_BLOCK / G;
-    typedef typename E::T T;
-    u32x4 c[U];
-    Vec<E, GB> s[U];
-    Bytes<ZP ? GB : 1> z[U];
+    u32x4 c;
+    Vec<E, GB> s;
+    Bytes<ZP ? GB : 1> z;
 
     __device__ __forceinline__ void load(const Q4Rows<ZP, G> &rows, int b) {
         typedef Q4Rec<ZP, G> Rec;
         const char *rec = rows.base + (int64_t)b * Rec::SIZE;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(rec + u * Rec::SIZE) + rows.lane);
-            s[u] = *(reinterpret_cast<const Vec<E, GB> *>(rec + u * Rec::SIZE + Q4_SCALES) + rows.row);
-            if constexpr (ZP) z[u] = load_bytes<GB>(rec + u * Rec::SIZE + Rec::ZEROS + rows.row * GB);
-        }
+        c = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(rec) + rows.lane);
+        s = *(reinterpret_cast<const Vec<E, GB> *>(rec + Q4_SCALES) + rows.row);
+        if constexpr (ZP) z = load_bytes<GB>(rec + Rec::ZEROS + rows.row * GB);
     }
-    __device__ __forceinline__ float scale(int u, int g) const { return (float)s[u].v[g]; }
-    __device__ __forceinline__ int zero(int u, int g) const {
+    __device__ __forceinline__ float scale(int g) const { return (float)s.v[g]; }
+    __device__ __forceinline__ int zero(int g) const {
         if constexpr (ZP)
-            return z[u].b[g] & 15;
+            return z.b[g] & 15;
         else
             return 8;
     }

@@ -225,11 +225,13 @@ def test_quantized_weight_is_near_the_weight():
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("rows,cols,group", [(1, 1, 128), (16, 128, 64), (35, 300, 32), (48, 129, 128)])
 def test_tiles(rows, cols, group, zeros):
-    """The records word for word."""
+    """The records word for word; scales of groups past the last column are zeros."""
     w, s, z = Q.weight(rows, cols, group, torch.float16, zeros, rows)
     m = S.Q4Matrix(rows, cols, w.cuda(), s.cuda(), None if z is None else z.cuda(), group=group)
     nb, gb = Q.blocks(cols), 128 // group
     rec = m.tiles.cpu().numpy().reshape(-1, 1024 + gb * (48 if zeros else 32))
+    s = s.clone()
+    s[:, (cols + group - 1) // group:] = 0
     pad = lambda t: np.pad(t.numpy(), ((0, -rows % 16), (0, 0)))  # noqa: E731
     for i in range((rows + 15) // 16):
         for b in range(nb):
@@ -240,6 +242,17 @@ def test_tiles(rows, cols, group, zeros):
             assert np.array_equal(r[1024:1024 + 32 * gb].view(np.float16).reshape(16, gb), sc)
             if zeros:
                 assert np.array_equal(r[1024 + 32 * gb:].reshape(16, gb), pad(z)[16 * i:16 * i + 16, gb * b:gb * b + gb])
+
+
+@pytest.mark.parametrize("tok", [1, 12, 300])
+@pytest.mark.parametrize("cols,group", [(300, 32), (129, 64)])
+def test_scales_past_the_last_column_are_not_used(tok, cols, group):
+    w, s, z = Q.weight(40, cols, group, torch.float16, True, 2)
+    x = torch.randn(tok, cols, generator=torch.Generator().manual_seed(3)).half()
+    ref, bound = Q.matmul(Q.dense(w, s, z, group, cols), x, 1.0, 0.0, None, torch.float32, group)
+    s[:, (cols + group - 1) // group:] = float("nan")
+    m = S.Q4Matrix(40, cols, w.cuda(), s.cuda(), z.cuda(), group=group)
+    R.check(m.apply(x.cuda(), torch.empty(tok, 40, device="cuda")), ref, bound)
 
 
 @pytest.mark.parametrize("tok", [1, 12, 40, 300])
