@@ -1,17 +1,22 @@
 // A layer of gated experts with 4-bit weights for the few tokens of a decoding
-// step, on gfx950, in two launches:
+// step, on gfx950, in two launches, or three beyond 64 choices:
 //   h[t, c] = silu(Wg x[t]) * (Wu x[t]),  y[t] = sum_c w[t, c] Wd h[t, c]
 // with the weights of token t's c-th expert.  The bound is reading each used
-// expert's weights once.
+// expert's weights once.  Every kernel finds its expert's tokens among the keys
+// itself: no sort comes before it.  Where there are fewer choices than experts the
+// grid counts choices, and the first choice of an expert does its work.
 //
-// Up (k_moe_up): a wave owns 16 gate rows and the same 16 up rows of one expert, or
-// a part of their columns, and the workgroup finds the expert's tokens among the
-// keys itself: no sort comes before it.  Where there are fewer slots than experts
-// the grid counts slots, and the first slot of an expert does its work.
-// Down (k_moe_down): a workgroup owns 16 (or 8) rows of y for all experts; its waves
-// take an expert, or a part of its columns, each, add the weighted results to sums
-// of their own in LDS, and these are added in order at the end: no atomics on
-// results, the same bits on every call.
+// Up (k_moe_up, k_moe_up_tile): a wave owns 16 gate rows and the same 16 up rows of an
+// expert, so that silu and the product are its own registers' work.
+// Down, up to 64 choices (k_moe_down): a workgroup owns 16 (or 8) rows of y for all
+// experts, and the weighted results are added in LDS, in order.  More (k_moe_down_tile):
+// by experts, as the up product, results per choice, which k_moe_sum weights and adds
+// by token.  No atomics on results: the same bits on every call.
+//
+// Measured, and what the weights' bytes take at the rate of a large copy: one token,
+// 2 of 8 experts of 2048 x 4096 17 us (26 MB: 5), 9 up and 9 down, each a chain of
+// launch, keys, codes and sums; 16 tokens, 8 of 64 of 2048 x 1024 59 us (190 MB: 37),
+// 35 + 24 + 5; 200 tokens, 4 of 24 of 4096 x 1500 124 us (230 MB: 44), 60 + 68 + 6.
 //
 // h is kept as three bf16 numbers whose sum has all of fp32's 24 bits (cut, not
 // rounded, so that the largest numbers stay finite): the down product is
@@ -34,6 +39,7 @@ constexpr int ME_MAX_EXPERTS = 1024;
 constexpr int ME_MAX_WIDTH = 1 << 24;
 constexpr int ME_UP_WAVES = 4;
 constexpr int ME_FEW_SLOTS = 64;     // choices up to which the down product adds by token itself
+constexpr int ME_TURNS = 3;          // workgroups of an expert's rows where its tokens may need several turns
 constexpr int ME_DOWN_WAVES = 16;
 constexpr int ME_UNROLL = 2;         // blocks of a step of the down product
 
@@ -165,7 +171,10 @@ __device__ __forceinline__ void store_hidden(const f32x4 &gate, const f32x4 &up,
 }
 
 // Few tokens of an expert: a wave brings its block of x into LDS of its own and
-// takes every parts-th block of its rows.
+// takes every parts-th block of its rows, so that no wave waits for another before the
+// sums at the end (a row of x per lane, straight to registers, is 64 cache accesses for
+// a load).  16 tokens, 8 of 64 experts, zero points: 127 MB of weights in 35 us, 3.6 TB/s;
+// the vector unit is busy a quarter of the time, waiting for codes the rest.
 template <class E, bool ZP, int G>
 __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int top_k, int n_experts, int dim, int inter,
                                                                 int n_blk, int h_blk, int parts, bool by_slot,
@@ -244,27 +253,33 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
     }
 }
 
-// More: the waves of a workgroup share the block of x of 16 TT tokens.
+// More: the waves of a workgroup share the block of x of 16 TT tokens, and a fragment
+// of W is decoded once for all of them.  Experts with more tokens than that have their
+// turns in workgroups of their own, up to ME_TURNS (200 tokens over 24 uneven experts,
+// up to 3 turns: 60 us; 77 when one workgroup takes them all).  With groups of 128 and
+// no zero points three workgroups fit a CU if one block of codes is on its way, not two:
+// 60 us against 75.  Decoding is a third of the vector unit's time there; the rest is
+// waiting, at 2.5 TB/s of weights.
 template <class E, bool ZP, int G, int TT>
-__global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, int top_k, int n_experts, int dim,
+__global__ __launch_bounds__(64 * ME_UP_WAVES, TT <= 3 && G == 128 && !ZP ? 3 : 2) void k_moe_up_tile(int n_tok, int top_k, int n_experts, int dim,
                                                                      int inter, int n_blk, int h_blk,
                                                                      const int *__restrict__ keys,
                                                                      const char *__restrict__ tiles,
                                                                      const typename E::T *__restrict__ x, int64_t ldx,
                                                                      unsigned short *__restrict__ h, int *__restrict__ place) {
-    constexpr int TN = 16 * TT, A = 2;                                 // A blocks of codes on their way
+    constexpr int TN = 16 * TT, A = TT <= 3 && G == 128 && !ZP ? 1 : 2;                                // A blocks of codes on their way
     __shared__ u32x4 xt[2][TN * 16];
     __shared__ EntryLds el;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int e = blockIdx.y, row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 16;
     const Entries en = find_entries(n_tok, top_k, e, keys, el);
-    if (place && blockIdx.x == 0) store_places(top_k, e, en, el, keys, place);
+    if (place && blockIdx.x == 0 && blockIdx.z == 0) store_places(top_k, e, en, el, keys, place);
     Q4Rows<ZP, G> rows[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
         rows[r] = Q4Rows<ZP, G>::any(tiles, ((int64_t)e * 2 + r) * inter + min(row0 + (lane & 15), inter - 1), n_blk);
     const int piece = threadIdx.x % 16, mine = threadIdx.x / 16;       // this thread's pieces: of entries mine + 16 q
-    for (int first = 0; first < en.n; first += TN) {
+    for (int first = blockIdx.z * TN; first < en.n; first += TN * gridDim.z) {
         const int here = min(TN, en.n - first);
         const typename E::T *xr[TT];
 #pragma unroll
@@ -317,7 +332,9 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_up_tile(int n_tok, 
 }
 
 // Up to 64 choices: a lane holds one, and everything about an expert is ballots over
-// them, without a barrier before the sums at the end.
+// them, without a barrier before the sums at the end (found in LDS by all waves: 12 us
+// against 9 for one token and 2 experts).  A unit of work is an expert, or a part of its
+// columns: 16 waves have one each.
 template <class E, bool ZP, int G>
 __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int top_k, int n_experts, int dim, int rows,
                                                                  int n_blk, const int *__restrict__ keys,
@@ -471,7 +488,11 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
 // z [entries][dim]; k_moe_sum weights and adds them by token.  The waves of a
 // workgroup share the block of h of 16 TT entries, which lies in memory as it is
 // read.  Up to 5 entries lie with all their parts in one operand of 16 (3 n rows of
-// it, added at the end).
+// it, added at the end).  Three tiles take half a block at a time and fixed places in
+// LDS: with whole blocks and places that depend on the entries the addresses do not fit
+// the registers (200 tokens, 24 experts of 4096 x 1500: 68 us against 89, turns in
+// workgroups of their own included; the matrix instructions alone take 14).
+// Bound by waits between barriers, at 1.2 TB/s of weights.
 template <class E, bool ZP, int G, int TT>
 __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok, int top_k, int n_experts, int dim,
                                                                        int n_blk, bool by_slot,
@@ -479,39 +500,44 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                                                                        const char *__restrict__ tiles,
                                                                        const unsigned short *__restrict__ h,
                                                                        float *__restrict__ z) {
-    constexpr int PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = 3 * TT;  // 48 pieces of 16 bytes of an entry's block
+    // SEG segments of a block, one at a time: SP pieces of 16 bytes of an entry
+    constexpr int SEG = TT == 3 ? 2 : 1, SP = 48 / SEG, SM = 4 / SEG;
+    constexpr int RT = 2, PG = G / 32, THREADS = 64 * ME_UP_WAVES, Q = (SP * 16 * TT + THREADS - 1) / THREADS;
     typedef Q4Op<BF16> Op;
-    __shared__ u32x4 ht[2][48 * 16 * TT];
+    __shared__ u32x4 ht[2][SP * 16 * TT];
     __shared__ EntryLds el;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), quarter = lane / 16;
     const int e = __builtin_amdgcn_readfirstlane(expert_of(n_experts, by_slot, keys));
     if (e < 0) return;
-    const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 32;
-    Q4Rows<ZP, G> rows[2];
-    Q4Piece<E, ZP, G> w[2][2];
+    const int row0 = ((int)blockIdx.x * ME_UP_WAVES + wv) * 16 * RT;
+    Q4Rows<ZP, G> rows[RT];
+    Q4Piece<E, ZP, G> w[2][RT];
     auto load_first = [&]() {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) w[0][r].load(rows[r], 0);
+        for (int r = 0; r < RT; ++r) w[0][r].load(rows[r], 0);
     };
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < RT; ++r)
         rows[r] = Q4Rows<ZP, G>::any(tiles, (int64_t)e * dim + min(row0 + 16 * r + (lane & 15), dim - 1), n_blk);
-    load_first();                                                       // on their way while the entries are found
+    if (blockIdx.z == 0) load_first();                                  // on their way while the entries are found
     const Entries en = find_entries(n_tok, top_k, e, keys, el);
-    for (int first = 0; first < en.n; first += 16 * TT) {
-        // the pieces of this turn's tiles: a block of a tile of n entries is 48 n of them in a row
+    for (int first = blockIdx.z * 16 * TT; first < en.n; first += 16 * TT * gridDim.z) {
+        // the pieces of this turn's tiles: a segment of a tile of n entries is SP n of them in a row
         int n_of[TT], from[TT + 1];
         from[0] = 0;
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             n_of[t] = first + 16 * t < en.n ? min(16, en.room - first - 16 * t) : 0;
-            from[t + 1] = from[t] + 48 * n_of[t];
+            from[t + 1] = from[t] + SP * n_of[t];
         }
+        // in LDS 48 places for the 8 columns of a tile's entries: 16 part + entry, or, packed,
+        // n part + entry; what is not written there reaches rows that are not used
+        const bool packed = from[TT] <= SP * 5;
         const u32x4 *src[Q];
-        int step[Q];
+        int step[Q], dst[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const int c = min((int)threadIdx.x + THREADS * q, from[TT] - 1);
+            const int c = min((int)threadIdx.x + THREADS * q, from[TT] - 1);       // past the end: the last one again
             int t = 0;
 #pragma unroll
             for (int k = 1; k < TT; ++k) t += c >= from[k];
@@ -520,21 +546,21 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
             for (int k = 1; k < TT; ++k)
                 if (t == k) n = n_of[k], f = from[k];
             src[q] = reinterpret_cast<const u32x4 *>(h + hidden_tile(en.base + first + 16 * t, n_blk)) + (c - f);
-            step[q] = 48 * n;
+            step[q] = SP * n;
+            const int place = (c - f) / n, piece = place / 3;
+            dst[q] = (t * 4 * SM + piece) * 48 + (place - 3 * piece) * (packed ? n : 16) + (c - f) - place * n;
         }
-        auto load_h = [&](int b, u32x4 (&v)[Q]) {
+        auto load_h = [&](int seg, u32x4 (&v)[Q]) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) v[q] = src[q][(int64_t)b * step[q]];
+            for (int q = 0; q < Q; ++q) v[q] = src[q][(int64_t)seg * step[q]];
         };
         auto keep_h = [&](u32x4 *to, const u32x4 (&v)[Q]) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-                if ((int)threadIdx.x + THREADS * q < from[TT]) to[threadIdx.x + THREADS * q] = v[q];
+            for (int q = 0; q < Q; ++q) to[dst[q]] = v[q];
         };
-        const bool packed = from[TT] <= 48 * 5;
-        f32x4 acc[2][TT];
+        f32x4 acc[RT][TT];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         u32x4 v[Q];
@@ -542,61 +568,78 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
         if (first > 0) load_first();
         keep_h(ht[0], v);
         __syncthreads();
-        for (int bb = 0; bb < n_blk; bb += 2) {
+        // NT tiles, or (0) one whose parts lie in one operand: without branches inside
+        auto products = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value, N = NT ? NT : 1;
+            for (int bb = 0; bb < n_blk; bb += 2) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const int b = bb + a;
-                if (b >= n_blk) break;
-                load_h(min(b + 1, n_blk - 1), v);
+                for (int a = 0; a < 2; ++a) {
+                    const int b = bb + a;
+                    if (b >= n_blk) break;
+                    f32x4 sum[RT][N];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
-                __builtin_amdgcn_sched_barrier(0);
-                const u32x4 *now = ht[a];
-                f32x4 sum[2][TT];
+                    for (int seg = 0; seg < SEG; ++seg) {
+                        load_h(min(SEG * b + seg + 1, SEG * n_blk - 1), v);   // h first: what waits for it does not wait for the codes
+                        if (seg == 0) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int g = m / PG, p = 3 * (4 * m + quarter);
-                    u32x4 f[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        f[r] = Op::decode(w[a][r].c[m], Op::zero(w[a][r].zero(g)));
-                        if (m % PG == 0) {
-#pragma unroll
-                            for (int t = 0; t < TT; ++t) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                            for (int r = 0; r < RT; ++r) w[1 - a][r].load(rows[r], min(b + 1, n_blk - 1));
                         }
-                    }
-                    if (packed) {
-                        const u32x4 x = now[p * n_of[0] + min(lane & 15, 3 * n_of[0] - 1)];
+                        __builtin_amdgcn_sched_barrier(0);
+                        const int at = SEG == 2 ? seg : a;
+                        const u32x4 *now = ht[at] + quarter * 48 + (lane & 15);
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) sum[r][0] = Op::mfma(x, f[r], sum[r][0]);
-                    } else {
+                        for (int m = SM * seg; m < SM * seg + SM; ++m) {
+                            const int g = m / PG, p = 4 * (m - SM * seg) * 48;
+                            u32x4 f[RT];
 #pragma unroll
-                        for (int t = 0; t < TT; ++t)
-                            if (n_of[t] > 0) {
-                                const u32x4 *at = now + from[t] + p * n_of[t] + min(lane & 15, n_of[t] - 1);
+                            for (int r = 0; r < RT; ++r) {
+                                f[r] = Op::decode(w[a][r].c[m], Op::zero(w[a][r].zero(g)));
+                                if (m % PG == 0) {
 #pragma unroll
-                                for (int i = 2; i >= 0; --i) {
-                                    const u32x4 x = at[i * n_of[t]];
-#pragma unroll
-                                    for (int r = 0; r < 2; ++r) sum[r][t] = Op::mfma(x, f[r], sum[r][t]);
+                                    for (int t = 0; t < N; ++t) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                                 }
                             }
-                    }
-                    if ((m + 1) % PG == 0) {
+                            if constexpr (NT == 0) {
+                                const u32x4 x = now[p];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float sc = w[a][r].scale(g);
+                                for (int r = 0; r < RT; ++r) sum[r][0] = Op::mfma(x, f[r], sum[r][0]);
+                            } else {
 #pragma unroll
-                            for (int t = 0; t < TT; ++t)
+                                for (int t = 0; t < N; ++t)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+                                    for (int i = 2; i >= 0; --i) {
+                                        const u32x4 x = now[t * 4 * SM * 48 + p + 16 * i];
+#pragma unroll
+                                        for (int r = 0; r < RT; ++r) sum[r][t] = Op::mfma(x, f[r], sum[r][t]);
+                                    }
+                            }
+                            if ((m + 1) % PG == 0) {
+#pragma unroll
+                                for (int r = 0; r < RT; ++r) {
+                                    const float sc = w[a][r].scale(g);
+#pragma unroll
+                                    for (int t = 0; t < N; ++t)
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sc, sum[r][t][i], acc[r][t][i]);
+                                }
+                            }
+                            // keeps the fragments of one product in registers at a time
+                            __builtin_amdgcn_sched_barrier(0);
                         }
+                        keep_h(ht[1 - at], v);
+                        __syncthreads();
                     }
                 }
-                keep_h(ht[1 - a], v);
-                __syncthreads();
             }
-        }
+        };
+        if (packed)
+            products(std::integral_constant<int, 0>{});
+        else if (TT == 1 || n_of[TT > 1 ? 1 : 0] == 0)
+            products(std::integral_constant<int, 1>{});
+        else if (TT == 2 || n_of[TT - 1] == 0)
+            products(std::integral_constant<int, TT < 2 ? TT : 2>{});
+        else
+            products(std::integral_constant<int, TT>{});
         float *zt = z + (int64_t)(en.base + first) * dim;
         if (packed) {
             // row i of the operand, column col: lane 16 (i / 4) + col, i % 4
@@ -605,7 +648,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
             const int n = n_of[0];
             auto part = [&](int i, int col) { return s[((i / 4) * 16 + col) * 4 + i % 4]; };
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < RT; ++r) {
                 mine[lane] = acc[r][0];
                 for (int o = lane; o < 16 * (en.n - first); o += 64) {
                     const int i = o / 16, col = o % 16;
@@ -616,7 +659,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
             __syncthreads();
         } else {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < RT; ++r) {
                 const int row = row0 + 16 * r + (lane & 15);
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
@@ -631,7 +674,8 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
 }
 
 // y[t] = sum over c (ascending) of weights[t, c] * z[place[t, c]]; a lane holds one
-// of 64 choices, and the rows of 8 choices are on their way together.
+// of 64 choices, and the rows of 8 choices are on their way together (800 rows of 4096:
+// 13 MB in 5.7 us, most of it the launch and one chain of loads).
 template <class E>
 __global__ __launch_bounds__(256) void k_moe_sum(int n_tok, int top_k, int n_experts, int dim, int pieces,
                                                  const int *__restrict__ keys, const float *__restrict__ weights,
@@ -749,7 +793,7 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     int parts = 1;
     while (!tile_up && parts < ME_UP_WAVES && parts < up_blk && up_row_tiles * parts < 4096) parts *= 2;
     const int64_t up_grid = ceil_div(ld / 16, ME_UP_WAVES / parts);
-    st = check_grid(up_grid * groups, 64 * ME_UP_WAVES);
+    st = check_grid(up_grid * groups * ME_TURNS, 64 * ME_UP_WAVES);
     if (st != SPMV_OK) return st;
     // 8 rows for a workgroup of the down product where 16 would leave compute units without one
     const int rows = ceil_div(dim, 16) < 256 ? 8 : 16;
@@ -758,7 +802,7 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
     const Parts p = parts_of(n_tok, top_k, dim, inter);
     const bool tile_down = slots > ME_FEW_SLOTS;
     const int64_t down_grid = ceil_div(dim, 32 * ME_UP_WAVES), pieces = ceil_div(dim, 64);
-    st = check_grid(down_grid * groups, 64 * ME_UP_WAVES);
+    st = check_grid(down_grid * groups * ME_TURNS, 64 * ME_UP_WAVES);
     if (st != SPMV_OK) return st;
     float *z = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.z);
     int *place = tile_down ? reinterpret_cast<int *>(static_cast<char *>(workspace) + p.place) : nullptr;
@@ -769,10 +813,13 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
         typedef typename E::T T;
         constexpr bool ZP = decltype(zp)::value;
         constexpr int G = decltype(g)::value;
+        auto turns = [&](int tt) { return (unsigned)std::min<int64_t>(ME_TURNS, ceil_div(n_tok, 16 * tt)); };
         auto up = [&](auto tt) {
-            k_moe_up_tile<E, ZP, G, decltype(tt)::value><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
-                n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, keys, static_cast<const char *>(up_tiles),
-                static_cast<const T *>(x), ldx, h, place);
+            constexpr int TT = decltype(tt)::value;
+            k_moe_up_tile<E, ZP, G, TT>
+                <<<dim3((unsigned)up_grid, (unsigned)groups, turns(TT)), 64 * ME_UP_WAVES, 0, s>>>(
+                    n_tok, top_k, n_experts, dim, inter, up_blk, down_blk, keys, static_cast<const char *>(up_tiles),
+                    static_cast<const T *>(x), ldx, h, place);
         };
         if (!tile_up)
             k_moe_up<E, ZP, G><<<dim3((unsigned)up_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
@@ -795,8 +842,9 @@ extern "C" spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts
             return SPMV_OK;
         }
         auto down = [&](auto tt) {
-            k_moe_down_tile<E, ZP, G, decltype(tt)::value>
-                <<<dim3((unsigned)down_grid, (unsigned)groups), 64 * ME_UP_WAVES, 0, s>>>(
+            constexpr int TT = decltype(tt)::value;
+            k_moe_down_tile<E, ZP, G, TT>
+                <<<dim3((unsigned)down_grid, (unsigned)groups, turns(TT)), 64 * ME_UP_WAVES, 0, s>>>(
                     n_tok, top_k, n_experts, dim, down_blk, by_slot, keys, static_cast<const char *>(down_tiles), h, z);
         };
         if (slots <= 12 * groups)

@@ -3,8 +3,15 @@
 // The codes go from memory straight to the registers that decode them, and the
 // matrix cores serve one token as well as 16: the product of a fragment costs the
 // same, and decoding is what the vector unit does.  Up to 4 tokens (k_q4_few) the
-// waves of a workgroup split the columns of 16 rows and the bound is HBM; more
-// (k_q4_tile) share tiles of x through LDS.
+// waves of a workgroup split the columns of 16 rows and the bound is HBM; up to 64 of
+// smaller weights (k_q4_mid) they also bring x themselves; more (k_q4_tile) share
+// tiles of x through LDS.
+//
+// Measured, with what the bytes take at the rate of a large copy (5.2 TB/s) or the
+// products at the rate of a large fp16 product (1.15 PFLOP/s): 12288 x 12288, one token
+// 14.8 us (15.0; reads alone reach 7.1 TB/s here), 48 tokens 35 (16), 513 tokens 187
+// (135); 5003 x 4100 in groups of 32 with zero points, 7 tokens 7.8 (2.4); 2048 x 2048,
+// one token 7.0, of which the GPU has 3.5.
 #include "q4.hpp"
 
 #include <algorithm>
@@ -31,7 +38,9 @@ __device__ __forceinline__ void q4_store(void *y, bool f32, int64_t at, float v,
 
 // Up to TP tokens: a workgroup owns 16 rows and keeps x whole in LDS (padded with
 // zeros to whole blocks); its waves take QF_UNROLL blocks in turn, whose codes are
-// loaded QF_AHEAD turns before they are used.
+// loaded QF_AHEAD turns before they are used.  12288 x 12288, one token: 77.9 MB in 14
+// us, 5.4 TB/s, bound by HBM (24 us with x from memory in every wave); three turns
+// ahead took as long as one.
 template <class E, bool ZP, int G, int TP>
 __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols, int n_blk,
                                                               const char *__restrict__ tiles, int n_tok, float alpha,
@@ -97,7 +106,10 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
 // Up to 64 tokens of smaller weights: as above, for 16 TT tokens, but a wave brings x
 // block by block into LDS of its own (16-byte pieces exchanged within a row by the
 // token's number, so that 16 tokens' pieces lie in different banks): no waiting for
-// other waves before the sums at the end.
+// other waves before the sums at the end.  Bound by the latency of a chain of 4 or 5
+// loads where there are few blocks (5003 x 4100, 7 tokens: 13 MB in 7.8 us), by x from
+// L2, once for every 16 rows, where there are many (4096 x 4096, 48 tokens: 134 MB of x
+// and 9 of weights in 9 us).
 template <class E, bool ZP, int G, int TT>
 __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols, int n_blk,
                                                           const char *__restrict__ tiles, int n_tok, float alpha,
@@ -182,7 +194,13 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
 // exchanged within a row by the token's number, so that 16 tokens' pieces lie in
 // different banks).  Every fragment of W is decoded once and used TT times; its
 // codes go straight to registers, a block ahead.  With few tiles the columns are
-// split over workgroups, whose sums k_q4_join adds.
+// split over workgroups, whose sums k_q4_join adds.  12288 x 12288, bf16, groups of 64,
+// zero points, 48 tokens: 32 us, of which 2.6 are the start, 2.9 the stores; the vector
+// unit (17 instructions to decode 8 codes) and the matrix cores are busy a third of the
+// time each, and codes arrive at 2.6 TB/s.  fp16, groups of 128, 513 tokens: 187 us, 830
+// TFLOP/s, 432 workgroups on 512 places, vector unit 82 us and matrix cores 70, which
+// overlap in part.  TT of 8 with sums in accumulation registers, 16 rows of a wave, and
+// codes two blocks ahead were slower.
 template <class E, bool ZP, int G, int RT, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int n_blk, int row_tiles, int tok_tiles,
                                                     int split, const char *__restrict__ tiles, int n_tok, float alpha,
@@ -299,7 +317,8 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
     }
 }
 
-// Adds the parts, in order: 4 results for a thread, 8 parts on their way together.
+// Adds the parts, in order: 4 results for a thread, 8 parts on their way together
+// (5 parts of 48 x 12288, 12 MB: 4.5 us; one result for a thread took 7).
 template <class E>
 __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int split, float alpha, float beta,
                                                  const float *__restrict__ parts, void *__restrict__ y, bool f32,
@@ -346,7 +365,7 @@ __global__ __launch_bounds__(256) void k_q4_scale(int n_rows, int64_t n, float b
 // The records from the rows: a workgroup writes the records of four blocks, a wave
 // each.  What lies past the last row is zeros, and so are the scales of groups past the
 // last column, whatever the caller's arrays hold there: x is zero in them, and a NaN
-// for a scale would come through.
+// for a scale would come through.  Bound by HBM: 12288 x 12288 in 30 us, 5.2 TB/s.
 __global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_cols, int n_blk, int gb, int64_t n_rec,
                                                   int rec_bytes, const u32x4 *__restrict__ codes,
                                                   const unsigned short *__restrict__ scales,
@@ -370,7 +389,8 @@ __global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_cols, in
 // Codes of a dense weight, one thread per group.  Symmetric: s = max |w| / 7,
 // q = w / s rounded to even + 8.  With zero points: s = (max(w, 0) - min(w, 0)) / 15,
 // z = -min(w, 0) / s and q = w / s + z, each rounded to even and kept in 0 .. 15.
-// s is rounded to its type (at most its largest number) before it divides.
+// s is rounded to its type (at most its largest number) before it divides.  Once per
+// weight, and as simple as that: a lane reads its group twice, the second time from L2.
 template <class S, class W>
 __global__ __launch_bounds__(256) void k_q4_quantize(int64_t n_groups, int n_cols, int gpr, int group,
                                                      const typename W::T *__restrict__ w, int64_t ldw,

@@ -83,6 +83,18 @@ def test_choices(kind, T, k, e):
     assert torch.equal(y, m(keys, w, x))                     # the same bits again
 
 
+@pytest.mark.parametrize("group,zeros", [(128, False), (128, True), (32, True)])
+@pytest.mark.parametrize("T,k,e", [(200, 4, 24), (250, 3, 40), (256, 4, 16), (90, 2, 24)])
+def test_uneven_experts(T, k, e, group, zeros):
+    """From no token to almost all of them: every number of turns and of tiles in a turn."""
+    m = Layer(e, 300, 420, group, "f16", zeros, seed=e)
+    keys, w, x = _batch(T, k, e, 300, "f16", T)
+    g = torch.Generator().manual_seed(T)
+    p = torch.pow(0.8, torch.arange(e - 1).double()).repeat(T, 1)
+    keys = torch.multinomial(p, k, generator=g).to(torch.int32).to(keys.device)
+    m.check(keys, w, x, m(keys, w, x))
+
+
 def test_without_weights_and_strided():
     m = Layer(6, 136, 100, 128, "bf16", True, seed=3)
     keys, _, x = _batch(9, 2, 6, 136, "bf16", 4)
