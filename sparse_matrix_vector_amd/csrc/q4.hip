@@ -10,7 +10,7 @@
 // Measured, with what the bytes take at the rate of a large copy (5.2 TB/s) or the
 // products at the rate of a large fp16 product (1.15 PFLOP/s): 12288 x 12288, one token
 // 14.8 us (15.0; reads alone reach 7.1 TB/s here), 48 tokens 35 (16), 513 tokens 187
-// (135); 5003 x 4100 in groups of 32 with zero points, 7 tokens 7.8 (2.4); 2048 x 2048,
+// to 195 (135); 5003 x 4100 in groups of 32 with zero points, 7 tokens 7.8 (2.4); 2048 x 2048,
 // one token 7.0, of which the GPU has 3.5.
 #include "q4.hpp"
 
