@@ -16,7 +16,7 @@
 // Measured, and what the weights' bytes take at the rate of a large copy: one token,
 // 2 of 8 experts of 2048 x 4096 17 us (26 MB: 5), 9 up and 9 down, each a chain of
 // launch, keys, codes and sums; 16 tokens, 8 of 64 of 2048 x 1024 59 us (190 MB: 37),
-// 35 + 24 + 5; 200 tokens, 4 of 24 of 4096 x 1500 124 to 134 us (230 MB: 44), 60 + 68 + 6.
+// 35 + 24 + 5; 200 tokens, 4 of 24 of 4096 x 1500 124 to 142 us (230 MB: 44), 60 + 68 + 6.
 //
 // h is kept as three bf16 numbers whose sum has all of fp32's 24 bits (cut, not
 // rounded, so that the largest numbers stay finite): the down product is
@@ -267,7 +267,10 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, TT <= 3 && G == 128 && !ZP ? 3 : 
                                                                      const char *__restrict__ tiles,
                                                                      const typename E::T *__restrict__ x, int64_t ldx,
                                                                      unsigned short *__restrict__ h, int *__restrict__ place) {
-    constexpr int TN = 16 * TT, A = TT <= 3 && G == 128 && !ZP ? 1 : 2;                                // A blocks of codes on their way
+    // blocks of codes on their way: one where three workgroups fit a CU with it, and where
+    // scales and zero points of 32 columns leave no registers for two
+    constexpr bool THREE = TT <= 3 && G == 128 && !ZP;
+    constexpr int TN = 16 * TT, A = THREE || (TT == 3 && G == 32 && ZP) ? 1 : 2;
     __shared__ u32x4 xt[2][TN * 16];
     __shared__ EntryLds el;
     const int lane = __lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
 // other waves before the sums at the end.  Bound by the latency of a chain of 4 or 5
 // loads where there are few blocks (5003 x 4100, 7 tokens: 13 MB in 7.8 us), by x from
 // L2, once for every 16 rows, where there are many (4096 x 4096, 48 tokens: 134 MB of x
-// and 9 of weights in 9 us).
+// and 9 of weights in 9.7 us).
 template <class E, bool ZP, int G, int TT>
 __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols, int n_blk,
                                                           const char *__restrict__ tiles, int n_tok, float alpha,
@@ -318,7 +318,8 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
 }
 
 // Adds the parts, in order: 4 results for a thread, 8 parts on their way together
-// (5 parts of 48 x 12288, 12 MB: 4.5 us; one result for a thread took 7).
+// (5 parts of 48 x 12288, 12 MB from the second-level caches: 4.5 us, half of it the
+// launch and one chain of loads).
 template <class E>
 __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int split, float alpha, float beta,
                                                  const float *__restrict__ parts, void *__restrict__ y, bool f32,
