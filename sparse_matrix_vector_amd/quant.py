@@ -90,9 +90,9 @@ def q4_matmul(n_rows, n_cols, tiles, alpha, x, beta, y, workspace=None, group=12
 class Q4Matrix:
     """One 4-bit weight, or n_groups stacked ones (the experts of moe_apply), arranged
     for the products from codes, scales and zero points (or None) in the layout of
-    include/spmv.h, which may be freed afterwards.  It is made on `stream`: other
-    streams wait for it before they use the matrix, and it is kept until their calls
-    are done."""
+    include/spmv.h, which may be freed afterwards.  It is made on `stream`: before
+    another stream uses the matrix the caller makes it wait, and keeps the matrix until
+    the calls there are done."""
 
     def __init__(self, n_rows, n_cols, codes, scales, zeros=None, group=128, n_groups=1, stream=None):
         self.n_rows, self.n_cols, self.n_groups, self.group = int(n_rows), int(n_cols), int(n_groups), _group(group)
@@ -109,14 +109,14 @@ class Q4Matrix:
     def quantize(cls, w, group=128, dtype=None, zeros=False, stream=None):
         """The weight w [rows, cols], or [n_groups, rows, cols], in 4 bits, with zero
         points if `zeros`; dtype: the scales' type (w's, or float16 for fp32)."""
-        if w.dim() == 3:
-            n_groups, rows, cols = w.shape
-            w = w.reshape(n_groups * rows, cols)
-        else:
-            n_groups, (rows, cols) = 1, w.shape
+        d = _device(w, "w")
+        if w.dim() not in (2, 3):
+            raise ValueError(f"w must be 2-D or 3-D, got shape {tuple(w.shape)}")
+        n_groups, (rows, cols) = w.shape[0] if w.dim() == 3 else 1, w.shape[-2:]
         dtype = dtype or (w.dtype if w.dtype in _HALF_TYPES else torch.float16)
-        shape = (w.shape[0], _groups(cols, _group(group)))
-        with _stream_scope(stream, _device(w, "w")):
+        shape = (n_groups * rows, _groups(cols, _group(group)))
+        with _stream_scope(stream, d):
+            w = w.reshape(n_groups * rows, cols) if w.dim() == 3 else w      # a copy if strided, in the stream's order
             codes = torch.empty(w.shape[0], (cols + 127) // 128 * 16, dtype=_I32, device=w.device)
             scales = torch.empty(shape, dtype=dtype, device=w.device)
             zp = torch.empty(shape, dtype=torch.uint8, device=w.device) if zeros else None

@@ -209,6 +209,17 @@ def test_quantize(src, dt, group, zeros):
     assert np.array_equal(Q.unpack(codes), q.reshape(rows, n).astype(np.int64))
 
 
+def test_quantize_of_a_strided_stack_on_another_stream():
+    w = torch.randn(3, 20, 200, device="cuda").half()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    m, ref = S.Q4Matrix.quantize(w[:, :, 30:190], stream=side), S.Q4Matrix.quantize(w[:, :, 30:190].contiguous())
+    torch.cuda.synchronize()
+    assert (m.n_groups, m.n_rows, m.n_cols) == (3, 20, 160) and torch.equal(m.tiles, ref.tiles)
+    with pytest.raises(ValueError):
+        S.Q4Matrix.quantize(w[0, 0])
+
+
 def test_quantized_weight_is_near_the_weight():
     """Half a step of the scale per weight (symmetric: the scale is at most max / 7 rounded)."""
     w = torch.randn(64, 500, device="cuda")
