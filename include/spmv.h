@@ -814,10 +814,13 @@ spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, siz
  * type dtype (the scales' type) and y [n_tok, n_rows] of the same type or fp32,
  * rounded once; tiles as q4_tiles wrote them, with zero points if with_zeros != 0.
  * A group's products with code - zero are exact and summed in fp32, and so are the
- * groups' sums times their scales.  Row strides ldx, ldy in elements.  tiles and
- * workspace: 16-byte aligned; the workspace is not shared by calls that may overlap.
- * x and y must not overlap.  The same bits on every call; an infinity or NaN
- * reaches its own token's row only.  All pointers device.  Asynchronous. */
+ * groups' sums times their scales.  For bf16 the sums are held at 2^-11 of the result,
+ * so that those of the largest finite x stay finite until their scale brings them
+ * back; below 2^-115 a result is a sum of multiples of 2^-138.  Row strides ldx, ldy in
+ * elements.  tiles and workspace: 16-byte aligned; the workspace is not shared by calls
+ * that may overlap.  x and y must not overlap.  The same bits on every call; an
+ * infinity or NaN reaches its own token's row only.  All pointers device.
+ * Asynchronous. */
 spmv_status q4_matmul(int32_t n_rows, int32_t n_cols, int32_t group, int32_t with_zeros, const void *tiles,
                       int32_t dtype, int32_t n_tok, float alpha, const void *x, int64_t ldx, float beta,
                       void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t workspace_bytes,
@@ -838,11 +841,12 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t dim, int32_
  * by a token counts with both weights.  weights fp32 [n_tok * top_k] or NULL (1).  A
  * token without an expert gets zeros.  x [n_tok, dim] of type dtype (the scales'
  * type), y [n_tok, dim] of the same type or fp32, rounded once; the products between
- * are kept with fp32's 24 bits.  Of an expert without a token no more than the first
- * block of its rows is read.  At most 1024 experts, a width dim of 8 to 2^24 and
- * inter of at most 2^24 (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not
- * shared by calls that may overlap; x and y must not overlap.  The same bits on every
- * call.  All pointers device.  Asynchronous. */
+ * are kept with fp32's 24 bits (from 2^-110 on) and its whole range, as in q4_matmul
+ * for bf16.  Of an expert without a token no more than the first block of its rows is
+ * read.  At most 1024 experts, a width dim of 8 to 2^24 and inter of at most 2^24
+ * (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
+ * overlap; x and y must not overlap.  The same bits on every call.  All pointers
+ * device.  Asynchronous. */
 spmv_status moe_apply(int32_t n_tok, int32_t top_k, int32_t n_experts, int32_t dim, int32_t inter,
                       int32_t group, int32_t with_zeros, const int32_t *keys, const float *weights,
                       const void *up_tiles, const void *down_tiles, int32_t dtype, const void *x,

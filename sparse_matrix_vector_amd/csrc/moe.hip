@@ -143,7 +143,7 @@ __device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G> (&w)[2], const 
         if ((m + 1) % PG == 0) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float sc = w[r].scale(g) * Q4Op<E>::UNIT;
+                const float sc = w[r].scale(g);
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -154,6 +154,7 @@ __device__ __forceinline__ void up_block(const Q4Piece<E, ZP, G> (&w)[2], const 
 }
 
 // h of the 16 columns from row0 on and the 16 entries from `first` on, of which `here` are there.
+template <class E>
 __device__ __forceinline__ void store_hidden(const f32x4 &gate, const f32x4 &up, const Entries &en, int first, int here,
                                              int row0, int inter, int h_blk, unsigned short *__restrict__ h) {
     const int lane = __lane_id(), row = row0 + (lane & 15), in = min(16, en.room - first);
@@ -163,7 +164,10 @@ __device__ __forceinline__ void store_hidden(const f32x4 &gate, const f32x4 &up,
         const int at = 4 * (lane / 16) + i;
         if (at >= here) continue;
         unsigned short o[3] = {0, 0, 0};                                // columns past inter are zeros
-        if (row < inter) split3(gate[i] / (1.0f + expf(-gate[i])) * up[i], o);
+        if (row < inter) {
+            const float g = Q4Op<E>::UNIT * gate[i], u = Q4Op<E>::UNIT * up[i];
+            split3(g / (1.0f + expf(-g)) * u, o);
+        }
         unsigned short *d = h + hidden_tile(en.base + first, h_blk) + at * 8 + row % 8;
 #pragma unroll
         for (int k = 0; k < 3; ++k) d[hidden_piece(row / Q4_BLOCK, k, row % Q4_BLOCK / 8, in)] = o[k];
@@ -247,7 +251,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
                 gate += other[lane];
                 up += other[64 + lane];
             }
-            store_hidden(gate, up, en, first, here, row0, inter, h_blk, h);
+            store_hidden<E>(gate, up, en, first, here, row0, inter, h_blk, h);
         }
         __syncthreads();
     }
@@ -330,7 +334,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, TT <= 3 && G == 128 && !ZP ? 3 : 
 #pragma unroll
         for (int t = 0; t < TT; ++t)
             if (16 * t < here)
-                store_hidden(acc[0][t], acc[1][t], en, first + 16 * t, min(16, here - 16 * t), row0, inter, h_blk, h);
+                store_hidden<E>(acc[0][t], acc[1][t], en, first + 16 * t, min(16, here - 16 * t), row0, inter, h_blk, h);
     }
 }
 
@@ -464,7 +468,7 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
                     float x = result(entry);
                     if (packed) x = (result(2 * in + entry) + result(in + entry)) + x;
                     float *d = mine + j / top_k * 16 + r;
-                    if (lane < rows) *d = fmaf(wj, x, *d);
+                    if (lane < rows) *d = fmaf(wj, Op::UNIT * x, *d);
                 }
                 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
@@ -656,7 +660,8 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                 for (int o = lane; o < 16 * (en.n - first); o += 64) {
                     const int i = o / 16, col = o % 16;
                     if (row0 + 16 * r + col < dim)
-                        zt[(int64_t)i * dim + row0 + 16 * r + col] = (part(2 * n + i, col) + part(n + i, col)) + part(i, col);
+                        zt[(int64_t)i * dim + row0 + 16 * r + col] =
+                            Op::UNIT * ((part(2 * n + i, col) + part(n + i, col)) + part(i, col));
                 }
             }
             __syncthreads();
@@ -669,7 +674,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int k = 16 * t + 4 * quarter + i;
-                        if (row < dim && first + k < en.n) zt[(int64_t)k * dim + row] = acc[r][t][i];
+                        if (row < dim && first + k < en.n) zt[(int64_t)k * dim + row] = Op::UNIT * acc[r][t][i];
                     }
             }
         }

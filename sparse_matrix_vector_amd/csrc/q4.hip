@@ -83,7 +83,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
 #pragma unroll
                     for (int m = g * PG; m < (g + 1) * PG; ++m)
                         sum = Q4Op<E>::mfma(xr[(b + u) * 16 + 4 * m], Q4Op<E>::decode(w[a][u].c[m], nz), sum);
-                    const float s = w[a][u].scale(g) * Q4Op<E>::UNIT;
+                    const float s = w[a][u].scale(g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, sum[i], acc[i]);
                 }
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
         const int r = o % 16, t = o / 16, at = ((t / 4) * 16 + r) * 4 + t % 4;
         float v = 0.0f;
         for (int k = 0; k < waves; ++k) v += sums[k * 256 + at];
-        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * v, beta);
+        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * (Q4Op<E>::UNIT * v), beta);
     }
 }
 
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
                 for (int t = 0; t < TT; ++t)
                     sum[t] = Q4Op<E>::mfma(xv[t], f, m % PG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[t]);
                 if ((m + 1) % PG == 0) {
-                    const float sc = w[a].scale(g) * Q4Op<E>::UNIT;
+                    const float sc = w[a].scale(g);
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
         const int at = (t / 16 * 64 + (t % 16 / 4) * 16 + r) * 4 + t % 4;
         float s = 0.0f;
         for (int k = 0; k < waves; ++k) s += sums[k * TT * 256 + at];
-        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * s, beta);
+        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * (Q4Op<E>::UNIT * s), beta);
     }
 }
 
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 if ((m + 1) % PG == 0) {
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const float sc = w[a][r].scale(g) * Q4Op<E>::UNIT;
+                        const float sc = w[a][r].scale(g);
 #pragma unroll
                         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 if constexpr (SPLIT)
                     part[(int64_t)(16 * t + i) * n_rows] = acc[r][t][i];
                 else
-                    q4_store<E>(y, f32, (int64_t)tok * ldy + row, alpha * acc[r][t][i], beta);
+                    q4_store<E>(y, f32, (int64_t)tok * ldy + row, alpha * (Q4Op<E>::UNIT * acc[r][t][i]), beta);
             }
     }
 }
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int spli
         for (int64_t j = i; j < n; ++j) {
             float v = 0.0f;
             for (int k = 0; k < split; ++k) v += parts[k * n + j];
-            q4_store<E>(y, f32, j / n_rows * ldy + j % n_rows, alpha * v, beta);
+            q4_store<E>(y, f32, j / n_rows * ldy + j % n_rows, alpha * (Q4Op<E>::UNIT * v), beta);
         }
         return;
     }
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int spli
     int row = (int)(from - t * n_rows);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (from + j >= i) q4_store<E>(y, f32, t * ldy + row, alpha * sum[j], beta);
+        if (from + j >= i) q4_store<E>(y, f32, t * ldy + row, alpha * (Q4Op<E>::UNIT * sum[j]), beta);
         if (++row == n_rows) row = 0, ++t;
     }
 }

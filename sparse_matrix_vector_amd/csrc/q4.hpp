@@ -14,10 +14,15 @@
 // W), the tokens' the first: a lane then decodes the row whose scale it multiplies
 // with.
 //
-// Codes become exact 16-bit numbers q - z (fp16: (q - z) 2^-9; a code masked out
-// of a word is the fp16 subnormal q 2^-24 or 16 q 2^-24, and one fused
-// multiply-add brings it to q - z).  The products of a group are summed in fp32
-// and multiplied with the group's scale in fp32: no weight is rounded.
+// Codes become exact 16-bit numbers (q - z) / UNIT (a code masked out of a word is
+// the fp16 subnormal q 2^-24 or 16 q 2^-24, and one fused multiply-add brings it
+// there).  The products of a group are summed in fp32 and multiplied with the
+// group's scale in fp32: no weight is rounded.  The sums stay 1 / UNIT of the result
+// until all are added, which costs one multiplication per result.  For fp16 UNIT is
+// what that multiply-add leaves.  For bf16 it is 2^11: 128 products of the largest x
+// with factors of 15, 1920 of them, stay finite where the scale brings the result
+// back.  Such a sum is subnormal where the result is below 2^-115, and is rounded to
+// multiples of 2^-138 of the result there; x, down to bf16's smallest number, is not.
 #pragma once
 
 #include "elem.hpp"
@@ -48,7 +53,7 @@ struct Q4Op;
 template <>
 struct Q4Op<F16> {
     typedef q4_h2 Zero;
-    static constexpr float UNIT = 512.0f;      // what the group's sum is short of
+    static constexpr float UNIT = 512.0f;      // what the sums are short of
     static __device__ __forceinline__ Zero zero(int z) {
         // z as the fp16 subnormal z 2^-24, times -2^15
         const q4_h2 s = __builtin_bit_cast(q4_h2, (unsigned)z * 0x00010001u);
@@ -72,8 +77,11 @@ struct Q4Op<F16> {
 template <>
 struct Q4Op<BF16> {
     typedef float Zero;
-    static constexpr float UNIT = 1.0f;
-    static __device__ __forceinline__ Zero zero(int z) { return -(float)z; }
+    static constexpr float UNIT = 2048.0f;
+    static __device__ __forceinline__ Zero zero(int z) {
+        // z as the fp16 subnormal z 2^-24, converted and multiplied by one instruction
+        return __builtin_fmaf((float)__builtin_bit_cast(_Float16, (unsigned short)z), -16777216.0f / UNIT, 0.0f);
+    }
     static __device__ __forceinline__ unsigned pair(unsigned bits, float k, Zero nz) {
         const q4_h2 h = __builtin_bit_cast(q4_h2, bits);
         q4_b2 r;
@@ -84,10 +92,10 @@ struct Q4Op<BF16> {
     static __device__ __forceinline__ u32x4 decode(unsigned w, Zero nz) {
         const unsigned v = w >> 8;
         u32x4 o;
-        o[0] = pair(w & 0x000F000Fu, 16777216.0f, nz);
-        o[1] = pair(w & 0x00F000F0u, 1048576.0f, nz);
-        o[2] = pair(v & 0x000F000Fu, 16777216.0f, nz);
-        o[3] = pair(v & 0x00F000F0u, 1048576.0f, nz);
+        o[0] = pair(w & 0x000F000Fu, 8192.0f, nz);
+        o[1] = pair(w & 0x00F000F0u, 512.0f, nz);
+        o[2] = pair(v & 0x000F000Fu, 8192.0f, nz);
+        o[3] = pair(v & 0x00F000F0u, 512.0f, nz);
         return o;
     }
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
