@@ -110,6 +110,15 @@ __device__ __forceinline__ int wave_inclusive_scan(int v) {
     return v;
 }
 
+// Orders the LDS accesses of a wave's lanes with one another: what some wrote before
+// it is what others read after it.  The hardware runs them in order, so this costs no
+// instruction; it keeps the compiler from moving them.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Sum over the 64 lanes (all lanes active), as a wave-uniform value.
 __device__ __forceinline__ int wave_sum_int(int v) {
     return __builtin_amdgcn_readlane(wave_inclusive_scan(v), 63);

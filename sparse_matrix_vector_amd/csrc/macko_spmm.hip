@@ -405,12 +405,6 @@ __device__ __forceinline__ void clear_tile(unsigned short *tile, int lane) {
     for (int i = 0; i < SM_ROWS; i += 2) *reinterpret_cast<u32x4 *>(p + i * SM_LDW) = u32x4{0u, 0u, 0u, 0u};
 }
 
-__device__ __forceinline__ void wave_lds_order() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Few tokens, 32 at most.  Workgroup: rows 16 blockIdx.x .. of group blockIdx.y and
 // that group's tokens, slabs wave, wave + WAVES, ...; the waves add their sums at
 // the end.  Bound by the latency of a slab's chain (plan word,

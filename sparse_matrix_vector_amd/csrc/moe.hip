@@ -229,11 +229,13 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = q4_token_placed(v[q], b * Q4_BLOCK + piece * 8, dim);
                 }
+                wave_lds_order();                                      // after the reads of the block before
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int t = 4 * q + quarter;
                     mine[t * 16 + (piece ^ t)] = v[q];
                 }
+                wave_lds_order();
                 load_x(min(b + parts, n_blk - 1), v);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) w[1 - a][r].load(rows[r], min(b + parts, n_blk - 1));
@@ -241,6 +243,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 4) void k_moe_up(int n_tok, int t
             }
         }
         f32x4 *sums = reinterpret_cast<f32x4 *>(mine);                 // [2][64] of the wave's 4 KB
+        wave_lds_order();
 #pragma unroll
         for (int r = 0; r < 2; ++r) sums[r * 64 + lane] = acc[r][0];
         __syncthreads();
@@ -359,6 +362,7 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
     const float weight = weights && lane < slots ? weights[lane] : 1.0f;
     float *mine = sums + wv * n_tok * 16;
     for (int i = lane; i < n_tok * 16; i += 64) mine[i] = 0.0f;
+    wave_lds_order();
     const bool valid = (unsigned)key < (unsigned)n_experts;
     const u64 below = (1ull << lane) - 1;
     const int tok0 = lane / top_k * top_k;                              // first choice of this lane's token
@@ -656,7 +660,9 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
             auto part = [&](int i, int col) { return s[((i / 4) * 16 + col) * 4 + i % 4]; };
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
+                wave_lds_order();                                      // after the reads of the rows before
                 mine[lane] = acc[r][0];
+                wave_lds_order();
                 for (int o = lane; o < 16 * (en.n - first); o += 64) {
                     const int i = o / 16, col = o % 16;
                     if (row0 + 16 * r + col < dim)

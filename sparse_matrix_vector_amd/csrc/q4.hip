@@ -146,11 +146,13 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
 #pragma unroll
                 for (int q = 0; q < 4 * TT; ++q) v[q] = q4_token_placed(v[q], b * Q4_BLOCK + piece * 8, n_cols);
             }
+            wave_lds_order();                        // after the reads of the block before
 #pragma unroll
             for (int q = 0; q < 4 * TT; ++q) {
                 const int t = 4 * q + quarter;
                 mine[t * 16 + (piece ^ (t & 15))] = v[q];
             }
+            wave_lds_order();
             load_x(min(b + waves, n_blk - 1), v);
             w[1 - a].load(row, min(b + waves, n_blk - 1));
             f32x4 sum[TT];
