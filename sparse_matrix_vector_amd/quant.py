@@ -22,6 +22,12 @@ def _groups(n_cols, group):
     return (n_cols + 127) // 128 * (128 // group)
 
 
+def _tensor(t, name):
+    """Before a tensor's shape or type is asked for: the rest is checked with its pointer."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+
+
 def _group(group):
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
@@ -37,6 +43,7 @@ def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
     has ceil(cols / 128) blocks of 128 / group groups."""
     d, n, width, wp, ldw = _matrix(w, "w")
     blocks, per = (width + 127) // 128, _groups(width, _group(group))
+    _tensor(scales, "scales")
     if scales.dtype not in _HALF_TYPES:
         raise TypeError(f"scales must be float16 or bfloat16, got {scales.dtype}")
     _launch(d, stream, "q4_quantize", n, width, group, wp, _code(w, "w"), ldw, _CODE[scales.dtype],
@@ -165,10 +172,15 @@ def moe_apply(keys, weights, gate_up, down, x, y, workspace, stream=None):
     (2 inter x dim), down: one of dim x inter.  At most 256 tokens."""
     d, n, dim, xp, ldx = _matrix(x, "x")
     dt = x.dtype
+    _tensor(keys, "keys")
     if keys.dim() != 2 or keys.shape[0] != n or keys.shape[1] < 1:
         raise ValueError(f"keys must have shape ({n}, top_k), got {tuple(keys.shape)}")
-    if weights is not None and weights.shape != keys.shape:
-        raise ValueError(f"weights must have the shape of keys, got {tuple(weights.shape)}")
+    if weights is not None:
+        _tensor(weights, "weights")
+        if weights.shape != keys.shape:
+            raise ValueError(f"weights must have the shape of keys, got {tuple(weights.shape)}")
+    if not isinstance(gate_up, Q4Matrix) or not isinstance(down, Q4Matrix):
+        raise TypeError("gate_up and down must be Q4Matrix")
     k, e, inter = keys.shape[1], gate_up.n_groups, down.n_cols
     if gate_up.n_cols != dim or gate_up.n_rows != 2 * inter or down.n_rows != dim or down.n_groups != e:
         raise ValueError(f"{e} x {gate_up.n_rows} x {gate_up.n_cols} and {down.n_groups} x {down.n_rows} x {down.n_cols} "
@@ -192,6 +204,7 @@ def embed_lookup(ids, table, y, scale=1.0, stream=None):
     """y[t] = scale * table[ids[t]], zeros for ids outside the table.  ids: int32
     [tokens]; y [tokens, dim] of the table's type or fp32."""
     d, v, dim, tp, ldt = _matrix(table, "table")
+    _tensor(ids, "ids")
     n = ids.numel()
     yp, ldy = _rows(y, (table.dtype, _F32), "y", n, dim, d)
     _launch(d, stream, "embed_lookup", n, v, dim, _code(table, "table"), _ptr(ids, _I32, "ids", n, d), tp, ldt, scale, yp,
@@ -207,6 +220,8 @@ def embed_grad(ids, dy, dtable, workspace, scale=1.0, accumulate=False, stream=N
     """dtable[v] = scale * sum of dy[t] over ids[t] = v (fp32 [vocabulary, dim]), or
     added to it with `accumulate`."""
     d, n, dim, gp, ldg = _matrix(dy, "dy")
+    _tensor(ids, "ids")
+    _tensor(dtable, "dtable")
     if ids.numel() != n:
         raise ValueError(f"ids must have {n} elements, got {ids.numel()}")
     if dtable.dim() != 2:

@@ -145,6 +145,8 @@ def _ws(workspace, device):
     """(pointer, bytes) of a workspace tensor (None: NULL, 0)."""
     if workspace is None:
         return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a CUDA tensor")
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
