@@ -842,8 +842,8 @@ spmv_status moe_workspace_size(int32_t n_tok, int32_t top_k, int32_t dim, int32_
  * token without an expert gets zeros.  x [n_tok, dim] of type dtype (the scales'
  * type), y [n_tok, dim] of the same type or fp32, rounded once; the products between
  * are kept with fp32's 24 bits (from 2^-110 on) and its whole range, as in q4_matmul
- * for bf16.  Of an expert without a token no more than the first block of its rows is
- * read.  At most 1024 experts, a width dim of 8 to 2^24 and inter of at most 2^24
+ * for bf16.  Of an expert without a token no more than the first four blocks of its up
+ * rows and the first of its down rows are read.  At most 1024 experts, a width dim of 8 to 2^24 and inter of at most 2^24
  * (SPMV_ERR_UNSUPPORTED).  workspace: 16-byte aligned, not shared by calls that may
  * overlap; x and y must not overlap.  The same bits on every call.  All pointers
  * device.  Asynchronous. */

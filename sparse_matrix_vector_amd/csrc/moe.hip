@@ -15,7 +15,7 @@
 //
 // Measured, and what the weights' bytes take at the rate of a large copy: one token,
 // 2 of 8 experts of 2048 x 4096 17 us (26 MB: 5), 9 up and 9 down, each a chain of
-// launch, keys, codes and sums; 16 tokens, 8 of 64 of 2048 x 1024 59 us (190 MB: 37),
+// launch, keys, codes and sums; 16 tokens, 8 of 64 of 2048 x 1024 60 us (190 MB: 37),
 // 35 + 24 + 5; 200 tokens, 4 of 24 of 4096 x 1500 124 to 142 us (230 MB: 44), 60 + 68 + 6.
 //
 // h is kept as three bf16 numbers whose sum has all of fp32's 24 bits (cut, not

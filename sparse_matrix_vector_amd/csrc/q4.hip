@@ -7,11 +7,13 @@
 // smaller weights (k_q4_mid) they also bring x themselves; more (k_q4_tile) share
 // tiles of x through LDS.
 //
-// Measured, with what the bytes take at the rate of a large copy (5.2 TB/s) or the
-// products at the rate of a large fp16 product (1.15 PFLOP/s): 12288 x 12288, one token
-// 14.8 us (15.0; reads alone reach 7.1 TB/s here), 48 tokens 35 (16), 513 tokens 187
-// to 195 (135); 5003 x 4100 in groups of 32 with zero points, 7 tokens 7.8 (2.4); 2048 x 2048,
-// one token 7.0, of which the GPU has 3.5.
+// Measured, a pass among others, with what the bytes take at the rate of a large copy
+// (5.2 TB/s) or the products at the rate of a large fp16 product (1.15 PFLOP/s): 12288 x
+// 12288, one token 14.9 us (15.0; reads alone reach 7.1 TB/s here), 48 tokens 35 to 37
+// (16), 513 tokens 185 to 190 (135); 5003 x 4100 in groups of 32 with zero points, 7
+// tokens 7.8 (2.4); 2048 x 2048, one token 6.8, of which the GPU has 3.5.  A kernel trace
+// has the kernels longer: k_q4_mid 8.4 to 8.8 for the 7 tokens, k_q4_tile 204 to 207 for
+// the 513.
 #include "q4.hpp"
 
 #include <algorithm>
@@ -23,7 +25,10 @@ constexpr int QF_UNROLL = 2;         // blocks of a wave's turn
 constexpr int QF_AHEAD = 1;          // turns whose codes are on their way
 constexpr int QF_WAVES = 8;
 constexpr int QF_TOKENS = 4;
-constexpr int QF_LDS = 65536;        // bytes of x at most
+// Bytes of x at most, so that a CU has two workgroups.  With 128 KB (f16, groups of 128)
+// 3 tokens of 4096 x 12288 take 8.4 us against 10.4 by tiles, but 4 tokens of 12288 x
+// 12288 25.4 against 19.4.
+constexpr int QF_LDS = 65536;
 
 template <class E>
 __device__ __forceinline__ void q4_store(void *y, bool f32, int64_t at, float v, float beta) {
@@ -107,9 +112,9 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
 // block by block into LDS of its own (16-byte pieces exchanged within a row by the
 // token's number, so that 16 tokens' pieces lie in different banks): no waiting for
 // other waves before the sums at the end.  Bound by the latency of a chain of 4 or 5
-// loads where there are few blocks (5003 x 4100, 7 tokens: 13 MB in 7.8 us), by x from
-// L2, once for every 16 rows, where there are many (4096 x 4096, 48 tokens: 134 MB of x
-// and 9 of weights in 9.7 us).
+// loads, since a wave has one block ahead, where there are few blocks (5003 x 4100, 7
+// tokens: 13 MB in 7.8 us), by x from L2, once for every 16 rows, where there are many
+// (4096 x 4096, 48 tokens: 101 MB of x and 9 of weights in 9.8 us).
 template <class E, bool ZP, int G, int TT>
 __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols, int n_blk,
                                                           const char *__restrict__ tiles, int n_tok, float alpha,
@@ -199,9 +204,9 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
 // split over workgroups, whose sums k_q4_join adds.  12288 x 12288, bf16, groups of 64,
 // zero points, 48 tokens: 32 us, of which 2.6 are the start, 2.9 the stores; the vector
 // unit (17 instructions to decode 8 codes) and the matrix cores are busy a third of the
-// time each, and codes arrive at 2.6 TB/s.  fp16, groups of 128, 513 tokens: 187 us, 830
-// TFLOP/s, 432 workgroups on 512 places, vector unit 82 us and matrix cores 70, which
-// overlap in part.  TT of 8 with sums in accumulation registers, 16 rows of a wave, and
+// time each, and codes arrive at 2.6 TB/s.  fp16, groups of 128, 513 tokens: 185 to 190
+// us, 816 to 837 TFLOP/s, 432 workgroups on 512 places, vector unit 82 us and matrix
+// cores 70, which overlap in part.  TT of 8 with sums in accumulation registers, 16 rows of a wave, and
 // codes two blocks ahead were slower.
 template <class E, bool ZP, int G, int RT, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int n_blk, int row_tiles, int tok_tiles,
@@ -393,7 +398,9 @@ __global__ __launch_bounds__(256) void k_q4_tiles(int64_t n_rows, int n_cols, in
 // q = w / s rounded to even + 8.  With zero points: s = (max(w, 0) - min(w, 0)) / 15,
 // z = -min(w, 0) / s and q = w / s + z, each rounded to even and kept in 0 .. 15.
 // s is rounded to its type (at most its largest number) before it divides.  Once per
-// weight, and as simple as that: a lane reads its group twice, the second time from L2.
+// weight, and as simple as that: a lane reads its group twice, an element at a time, far
+// from its neighbours' (12288 x 12288: 0.6 ms from fp16 in groups of 32, 4.7 in groups of
+// 128, 5.5 from fp32; its bytes take 0.07 to 0.13).
 template <class S, class W>
 __global__ __launch_bounds__(256) void k_q4_quantize(int64_t n_groups, int n_cols, int gpr, int group,
                                                      const typename W::T *__restrict__ w, int64_t ldw,
@@ -466,8 +473,10 @@ Tiling tiling(int64_t n_rows, int64_t n_cols, int64_t n_tok, bool wide) {
     Tiling t;
     t.tt = (int)std::min<int64_t>(4, ceil_div(n_tok, 16));
     // 64 rows of a wave share a fragment of x, where their sums fit the registers: 513
-    // tokens of 12288 x 12288 192 us against 230 with 32 rows (fp16, groups of 128);
-    // 1300 against 295 with groups of 32 and zero points, whose code needs more registers
+    // tokens of 12288 x 12288 192 us against 230 with 32 rows (fp16, groups of 128).  With
+    // zero points 3 (fp16) to 20 registers (bf16) spill: 214 against 227 and 304 against
+    // 256, 200 tokens of 4096 x 12288 in fp16 43 against 40; groups of 64 spill 140 and
+    // more: 775 to 1160 against 252 to 290; groups of 32 with zero points 1300 against 295
     t.rt = n_tok > 64 && wide ? 4 : 2;
     t.row_tiles = (int)ceil_div(n_rows, 64 * t.rt);
     t.tok_tiles = (int)ceil_div(n_tok, 16 * t.tt);
@@ -487,9 +496,13 @@ bool few(int64_t n_cols, int64_t n_tok) {
     return n_cols < 8 || (n_tok <= QF_TOKENS && few_lds(n_cols, n_tok, 0) <= QF_LDS);
 }
 // Whether k_q4_mid takes the product: every 16 rows read x again, which costs less
-// than a second launch up to about 160 MB (f16, groups of 128: 4096 x 4096, 16
-// tokens, 34 MB, 6.3 us against 10.1 by tiles; 48 tokens, 134 MB, 11.5 against 14.9;
-// 12288 x 12288, 16 tokens, 302 MB, 31 against 24).
+// than a second launch up to 130 to 160 MB (f16, groups of 128: 4096 x 4096, 16
+// tokens, 34 MB, 8.0 us against 10.6 by tiles; 64 tokens, 134 MB, 11.6 against 12.1; 4096 x
+// 4608, 64 tokens, 151 MB, 12.2 against 14.0; 12288 x 12288, 16 tokens, 302 MB, 29 against
+// 20.5).  The bytes do not say all: with 33 tokens and more a CU has one workgroup, and
+// where the row tiles leave CUs without one or need a second round the tiles are faster
+// from less on (2048 x 8704, 64 tokens, 143 MB, 19.5 against 14.4; 4608 x 4608, 48 tokens,
+// 127 MB, 17.6 against 13.5).
 constexpr int64_t QM_BYTES = 160000000;
 bool mid(int64_t n_rows, int64_t n_cols, int64_t n_tok) {
     return n_tok <= 64 && ceil_div(n_rows, 16) * (ceil_div(n_tok, 16) * 16) * n_cols * 2 <= QM_BYTES;
