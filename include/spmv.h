@@ -815,8 +815,8 @@ spmv_status q4_workspace_size(int32_t n_rows, int32_t n_cols, int32_t n_tok, siz
  * rounded once; tiles as q4_tiles wrote them, with zero points if with_zeros != 0.
  * A group's products with code - zero are exact and summed in fp32, and so are the
  * groups' sums times their scales.  For bf16 the sums are held at 2^-11 of the result,
- * so that those of the largest finite x stay finite until their scale brings them
- * back; below 2^-115 a result is a sum of multiples of 2^-138.  Row strides ldx, ldy in
+ * so that those of the largest finite x stay finite until their scale or alpha brings
+ * them back; below 2^-115 a result is a sum of multiples of 2^-138.  Row strides ldx, ldy in
  * elements.  tiles and workspace: 16-byte aligned; the workspace is not shared by calls
  * that may overlap.  x and y must not overlap.  The same bits on every call; an
  * infinity or NaN reaches its own token's row only.  All pointers device.

@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
                     float x = result(entry);
                     if (packed) x = (result(2 * in + entry) + result(in + entry)) + x;
                     float *d = mine + j / top_k * 16 + r;
-                    if (lane < rows) *d = fmaf(wj, Op::UNIT * x, *d);
+                    if (lane < rows) *d = fmaf(wj, x, *d);
                 }
                 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
@@ -485,6 +485,7 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < W; ++k) v += sums[(k * n_tok + t) * 16 + in];
+        v *= Op::UNIT;
         if (row < dim) {
             const int64_t at = (int64_t)t * ldy + row;
             if (f32)
@@ -495,8 +496,8 @@ __global__ __launch_bounds__(64 * ME_DOWN_WAVES) void k_moe_down(int n_tok, int 
     }
 }
 
-// More choices: an expert's rows of W times its entries, 32 rows for a wave, into
-// z [entries][dim]; k_moe_sum weights and adds them by token.  The waves of a
+// More choices: an expert's rows of W times its entries, 32 rows for a wave, 1 / UNIT of
+// them into z [entries][dim]; k_moe_sum weights and adds them by token.  The waves of a
 // workgroup share the block of h of 16 TT entries, which lies in memory as it is
 // read.  Up to 5 entries lie with all their parts in one operand of 16 (3 n rows of
 // it, added at the end).  Three tiles take half a block at a time and fixed places in
@@ -666,8 +667,7 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
                 for (int o = lane; o < 16 * (en.n - first); o += 64) {
                     const int i = o / 16, col = o % 16;
                     if (row0 + 16 * r + col < dim)
-                        zt[(int64_t)i * dim + row0 + 16 * r + col] =
-                            Op::UNIT * ((part(2 * n + i, col) + part(n + i, col)) + part(i, col));
+                        zt[(int64_t)i * dim + row0 + 16 * r + col] = (part(2 * n + i, col) + part(n + i, col)) + part(i, col);
                 }
             }
             __syncthreads();
@@ -680,14 +680,14 @@ __global__ __launch_bounds__(64 * ME_UP_WAVES, 2) void k_moe_down_tile(int n_tok
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int k = 16 * t + 4 * quarter + i;
-                        if (row < dim && first + k < en.n) zt[(int64_t)k * dim + row] = Op::UNIT * acc[r][t][i];
+                        if (row < dim && first + k < en.n) zt[(int64_t)k * dim + row] = acc[r][t][i];
                     }
             }
         }
     }
 }
 
-// y[t] = sum over c (ascending) of weights[t, c] * z[place[t, c]]; a lane holds one
+// y[t] = UNIT * sum over c (ascending) of weights[t, c] * z[place[t, c]]; a lane holds one
 // of 64 choices, and the rows of 8 choices are on their way together (800 rows of 4096:
 // 13 MB in 5.7 us, most of it the launch and one chain of loads).
 template <class E>
@@ -722,6 +722,7 @@ __global__ __launch_bounds__(256) void k_moe_sum(int n_tok, int top_k, int n_exp
         }
     }
     if (col >= dim) return;
+    v *= Q4Op<BF16>::UNIT;
     if (f32)
         static_cast<float *>(y)[t * ldy + col] = v;
     else

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_few(int n_rows, int n_cols
         const int r = o % 16, t = o / 16, at = ((t / 4) * 16 + r) * 4 + t % 4;
         float v = 0.0f;
         for (int k = 0; k < waves; ++k) v += sums[k * 256 + at];
-        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * (Q4Op<E>::UNIT * v), beta);
+        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, Q4Op<E>::UNIT * (alpha * v), beta);
     }
 }
 
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(64 * QF_WAVES) void k_q4_mid(int n_rows, int n_cols
         const int at = (t / 16 * 64 + (t % 16 / 4) * 16 + r) * 4 + t % 4;
         float s = 0.0f;
         for (int k = 0; k < waves; ++k) s += sums[k * TT * 256 + at];
-        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, alpha * (Q4Op<E>::UNIT * s), beta);
+        if (row0 + r < n_rows) q4_store<E>(y, f32, t * ldy + row0 + r, Q4Op<E>::UNIT * (alpha * s), beta);
     }
 }
 
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256, 2) void k_q4_tile(int n_rows, int n_cols, int 
                 if constexpr (SPLIT)
                     part[(int64_t)(16 * t + i) * n_rows] = acc[r][t][i];
                 else
-                    q4_store<E>(y, f32, (int64_t)tok * ldy + row, alpha * (Q4Op<E>::UNIT * acc[r][t][i]), beta);
+                    q4_store<E>(y, f32, (int64_t)tok * ldy + row, Q4Op<E>::UNIT * (alpha * acc[r][t][i]), beta);
             }
     }
 }
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int spli
         for (int64_t j = i; j < n; ++j) {
             float v = 0.0f;
             for (int k = 0; k < split; ++k) v += parts[k * n + j];
-            q4_store<E>(y, f32, j / n_rows * ldy + j % n_rows, alpha * (Q4Op<E>::UNIT * v), beta);
+            q4_store<E>(y, f32, j / n_rows * ldy + j % n_rows, Q4Op<E>::UNIT * (alpha * v), beta);
         }
         return;
     }
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(256) void k_q4_join(int n_rows, int n_tok, int spli
     int row = (int)(from - t * n_rows);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (from + j >= i) q4_store<E>(y, f32, t * ldy + row, alpha * (Q4Op<E>::UNIT * sum[j]), beta);
+        if (from + j >= i) q4_store<E>(y, f32, t * ldy + row, Q4Op<E>::UNIT * (alpha * sum[j]), beta);
         if (++row == n_rows) row = 0, ++t;
     }
 }

@@ -18,11 +18,12 @@
 // the fp16 subnormal q 2^-24 or 16 q 2^-24, and one fused multiply-add brings it
 // there).  The products of a group are summed in fp32 and multiplied with the
 // group's scale in fp32: no weight is rounded.  The sums stay 1 / UNIT of the result
-// until all are added, which costs one multiplication per result.  For fp16 UNIT is
-// what that multiply-add leaves.  For bf16 it is 2^11: 128 products of the largest x
-// with factors of 15, 1920 of them, stay finite where the scale brings the result
-// back.  Such a sum is subnormal where the result is below 2^-115, and is rounded to
-// multiples of 2^-138 of the result there; x, down to bf16's smallest number, is not.
+// until all are added and weighted, which costs one multiplication per result.  For
+// fp16 UNIT is what that multiply-add leaves.  For bf16 it is 2^11: 128 products of
+// the largest x with factors of 15, 1920 of them, stay finite where the scale brings
+// the result back.  Such a sum is subnormal where the result is below 2^-115, and is
+// rounded to multiples of 2^-138 of the result there; x, down to bf16's smallest
+// number, is not.
 #pragma once
 
 #include "elem.hpp"

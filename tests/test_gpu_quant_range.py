@@ -135,3 +135,43 @@ def test_experts_with_large_x(T, experts, group, zeros):
     ref, bound = Q.moe(keys, None, Q.dense(*up, group, dim).view(experts, 2 * inter, dim),
                        Q.dense(*down, group, inter).view(experts, dim, inter), x, torch.float32, group)
     R.check(y, ref, bound, f"{T} {experts}")
+
+
+@pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
+@pytest.mark.parametrize("tok,cols", FORMS)
+def test_sums_that_alpha_brings_back(tok, cols, group, zeros):
+    rows = 40
+    w = _weight(rows, cols, group, zeros, tok, 2.0 ** -4)
+    x = torch.full((tok, cols), TOP * 0.75, dtype=torch.float64).to(BF)
+    m = S.Q4Matrix(rows, cols, *[None if t is None else t.cuda() for t in w], group=group)
+    ref, bound = Q.matmul(Q.dense(*w, group, cols), x, 2.0 ** -11, 0.0, None, torch.float32, group)
+    # of these rows the sum, before alpha, is past fp32's largest number, and less than 2^11 times it
+    some = (ref.abs() * 2.0 ** 11 > 2.0 ** 128) & (ref.abs() < 2.0 ** 127)
+    assert some[:, :2].all()
+    y = m.apply(x.cuda(), torch.full((tok, rows), float("nan"), device="cuda"), alpha=2.0 ** -11).cpu().double()
+    assert ((y - ref).abs() <= bound)[some].all()
+
+
+@pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
+@pytest.mark.parametrize("T,experts", LAYERS)
+def test_experts_whose_results_the_weights_bring_back(T, experts, group, zeros):
+    dim, inter = 40, 200
+    n, m = Q.blocks(dim) * 128, Q.blocks(inter) * 128
+    q = torch.full((experts * 2 * inter, n), 8)
+    q[:, 0] = 9
+    up = Q.pack(q.numpy()), torch.ones(q.shape[0], n // group, dtype=BF), \
+        torch.full((q.shape[0], n // group), 8, dtype=torch.uint8) if zeros else None
+    q = torch.full((experts * dim, m), 9)                    # the sum of 200 hidden values
+    down = Q.pack(q.numpy()), torch.ones(q.shape[0], m // group, dtype=BF), \
+        torch.full((q.shape[0], m // group), 8, dtype=torch.uint8) if zeros else None
+    gu, dn = _layer(experts, dim, inter, group, zeros, up, down)
+    x = torch.zeros(T, dim, dtype=BF)
+    x[:, 0] = (2.0 ** 63 * (0.5 + 0.5 * torch.rand(T, generator=torch.Generator().manual_seed(T)))).to(BF)
+    keys = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), 2.0 ** -9, device="cuda")
+    ws = torch.empty(S.moe_workspace_size(T, 1, dim, inter), dtype=torch.uint8, device="cuda")
+    y = S.moe_apply(keys, w, gu, dn, x.cuda(), torch.full((T, dim), float("nan"), device="cuda"), ws)
+    ref, bound = Q.moe(keys.cpu(), w.cpu(), Q.dense(*up, group, dim).view(experts, 2 * inter, dim),
+                       Q.dense(*down, group, inter).view(experts, dim, inter), x, torch.float32, group)
+    assert float(ref.min()) * 2.0 ** 9 > 2.0 ** 128
+    R.check(y, ref, bound, f"{T} {experts}")
